@@ -189,6 +189,29 @@ ESM_API esm_status esm_encoder_forward_padded(esm_encoder_t* h, const esm_weight
  * forward; default: every layer in the handle's precision. */
 ESM_API esm_status esm_encoder_set_layer_precision(esm_encoder_t* h, const esm_precision* per_layer, int num_layers);
 
+/* ---- attention window ----
+ * No counterpart on the pages, whose attention is full: a window for sequences that full
+ * attention makes too long, with the first tokens (<cls>) kept visible.  Query i of a sequence
+ * sees key j of the same sequence if
+ *   j <= i + right  and  (j >= i - left  or  j < sinks)
+ * (positions in the sequence, from 0).  A side of -1 is unlimited: {-1, -1, 0} is full attention,
+ * {-1, 0, 0} causal, {w, w, s} a band with s sinks.  The sinks reopen the left side only; a
+ * limited right side holds for them too.  0 <= sinks <= ESM_MAX_SINKS. */
+#define ESM_MAX_SINKS 128
+typedef struct {
+  int left;
+  int right;
+  int sinks;
+} esm_attn_window;
+
+/* The window of every layer's attention, from the next forward on (packed, padded, host-buffer
+ * and training forwards, in every precision); NULL restores full attention, the default.
+ * esm_encoder_backward uses the window its forward ran with.  A training buffer is sized for the
+ * window that is set when esm_encoder_train_buffer_size is called.  In the padded forward a
+ * padding query that sees no key attends to nothing (zero).
+ * ESM_ERR_INVALID_ARG: a side below -1, or sinks out of range. */
+ESM_API esm_status esm_encoder_set_attention_window(esm_encoder_t* h, const esm_attn_window* window);
+
 /* The NVFP4 tensor scales S of the last forward's FP4 layers (ESM_FP8_E4M3 handles): host_buf
  * float32 [num_layers * 8] in the tensor order {x_qkv, w_qkv, x_o, w_o, x_1, w_1, x_2, w_2}
  * (zero for layers that did not run in FP4); n must equal num_layers * 8.  Synchronises the
@@ -267,6 +290,21 @@ ESM_API esm_status esm_encoder_lm_head_backward(esm_encoder_t* h, const esm_lm_h
                                                 const int* loss_count, void* workspace, size_t workspace_bytes,
                                                 esm_stream_t stream);
 
+/* ---- masked-LM head backward from a teacher's top logits ----
+ * esm_encoder_lm_head_backward with the distillation loss of esm_op_distill_loss (below) on the
+ * head's logits in place of the cross-entropy: a training step of a student from a larger
+ * model's stored top logits.  teacher_ids (device int32), teacher_logits (device float32): [T, K];
+ * loss_sum, count: this call's sum and number of scored rows; the gradients are those of the mean
+ * over loss_count (NULL: this call's count).  Everything else, the workspace size included, as
+ * for esm_encoder_lm_head_backward. */
+ESM_API esm_status esm_encoder_lm_head_distill_backward(esm_encoder_t* h, const esm_lm_head* head, const void* hidden,
+                                                        int total_tokens, const int32_t* teacher_ids,
+                                                        const float* teacher_logits, int K, float temperature,
+                                                        float* d_hidden, const esm_lm_head_grads* grads,
+                                                        float* loss_sum, int* count, const int* loss_count,
+                                                        void* workspace, size_t workspace_bytes,
+                                                        esm_stream_t stream);
+
 /* Synchronise `stream` and return (and clear) the first error the kernels latched
  * since the last check: ESM_ERR_BAD_CU_SEQLENS, ESM_ERR_TOKEN_RANGE, ESM_ERR_TIMEOUT
  * or ESM_OK. */
@@ -333,6 +371,21 @@ ESM_API esm_status esm_op_gemm_fp8(esm_encoder_t* h, esm_epilogue epi, const uin
 ESM_API esm_status esm_op_attention(esm_encoder_t* h, const void* qkv, const int32_t* cu_seqlens,
                             int num_seqs, int total_tokens, int max_seqlen, void* o,
                             void* workspace, size_t workspace_bytes, esm_stream_t stream);
+
+/* esm_op_attention with a window, given in the call (the handle's own window plays no part).
+ * qkv device [T, 3*hidden] in the activation dtype, o device [T, hidden], both 16-byte aligned.
+ * lse: device float32 [heads, T], head-major, or NULL: the natural-log softmax normaliser of
+ * every row over the keys it sees, which the backward needs (bf16 activations only: an ESM_FP32
+ * handle with lse is ESM_ERR_UNSUPPORTED).  Every row sees itself, so no row is empty.  Keys and
+ * values that a row does not see have no influence on it, infinite and NaN ones included.
+ * Workspace: esm_op_attention_window_workspace_size bytes (backward: 1 for the backward below),
+ * 256-byte aligned, of this call alone while it runs.  cu_seqlens and max_seqlen as for
+ * esm_encoder_forward; total_tokens == 0 is a no-op. */
+ESM_API esm_status esm_op_attention_window_workspace_size(const esm_encoder_t* h, int total_tokens, int num_seqs,
+                                                          const esm_attn_window* window, int backward, size_t* bytes);
+ESM_API esm_status esm_op_attention_window(esm_encoder_t* h, const void* qkv, const int32_t* cu_seqlens, int num_seqs,
+                                           int total_tokens, int max_seqlen, const esm_attn_window* window, void* o,
+                                           float* lse, void* workspace, size_t workspace_bytes, esm_stream_t stream);
 
 /* ---- attention without any allocation ----
  * No counterpart on the pages: this entry point exists for callers that cannot allocate
@@ -503,6 +556,56 @@ ESM_API esm_status esm_op_attention_backward(esm_encoder_t* h, const void* qkv, 
                                              const void* d_o, const int32_t* cu_seqlens, int num_seqs,
                                              int total_tokens, int max_seqlen, void* dqkv, void* workspace,
                                              size_t workspace_bytes, esm_stream_t stream);
+
+/* esm_op_attention_backward with a window (bf16, head_dim 64): dqkv = dL/d(q | k | v) from qkv, o
+ * and lse of esm_op_attention_window with the same window, and d_o = dL/do.  qkv, d_o and o must
+ * be finite.  The float32 sums over key tiles behind dq, and only those, are added in no fixed
+ * order. */
+ESM_API esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, const void* o, const float* lse,
+                                                    const void* d_o, const int32_t* cu_seqlens, int num_seqs,
+                                                    int total_tokens, int max_seqlen, const esm_attn_window* window,
+                                                    void* dqkv, void* workspace, size_t workspace_bytes,
+                                                    esm_stream_t stream);
+
+/* ---- distillation from a teacher's top logits ----
+ * No counterpart on the pages.  For every token, K entries of a teacher's output are given: ids
+ * and logits (its K largest, say).  With temperature t, q = softmax(logits / t) over the
+ * vocabulary and p = softmax(teacher_logits / t) over the row's usable entries,
+ *   token_loss = t^2 sum_k p_k (log p_k - log q_{id_k}),   lse = log sum_v exp(logits_v / t),
+ *   d token_loss / d logits_v = t (q_v - sum_{k: id_k = v} p_k).
+ * An entry is usable if its id is in [0, vocab) and its logit is not -inf; id -1 marks an unused
+ * entry, any other id outside [0, vocab) is unused and latches ESM_ERR_TOKEN_RANGE (see
+ * esm_encoder_check).  An id may stand in a row more than once.  A row without a usable entry is
+ * not scored: its loss, its lse and its gradient are 0, whatever its logits are.
+ * logits: device, float32 (logits_type ESM_FP32) or bfloat16 (ESM_BF16; other types:
+ *   ESM_ERR_UNSUPPORTED) [T, vocab], rows logits_stride >= vocab elements apart; any vocab >= 1
+ * teacher_ids, teacher_logits: device int32 and float32 [T, K], 1 <= K <= ESM_DISTILL_MAX_K
+ * temperature: > 0, it and its inverse finite
+ * token_loss: device float32 [T]; lse: device float32 [T] or NULL (the backward needs it);
+ * loss_sum, count: device float32 and int32 scalars, each may be NULL: the sum of token_loss, in a
+ *   fixed order, and the number of scored rows.  The workspace (the size query's bytes, 256-byte
+ *   aligned) may be NULL when both are NULL.
+ * T == 0 sets loss_sum and count to 0.  Sums are float32 whatever the logits' type. */
+#define ESM_DISTILL_MAX_K 256
+ESM_API esm_status esm_op_distill_loss_workspace_size(const esm_encoder_t* h, int total_tokens, int vocab,
+                                                      size_t* bytes);
+ESM_API esm_status esm_op_distill_loss(esm_encoder_t* h, const void* logits, esm_precision logits_type,
+                                       long long logits_stride, const int32_t* teacher_ids,
+                                       const float* teacher_logits, int K, int total_tokens, int vocab,
+                                       float temperature, float* token_loss, float* lse, float* loss_sum, int* count,
+                                       void* workspace, size_t workspace_bytes, esm_stream_t stream);
+
+/* d_logits = d(sum of token_loss / n) / d logits, n = *loss_count (device int32 scalar: the
+ * forward's count, or the global batch's in data-parallel training; with n <= 0 every gradient is
+ * 0) or 1 if loss_count is NULL.  lse: of esm_op_distill_loss for the same logits and temperature.
+ * d_logits: of the logits' type, rows d_stride >= vocab elements apart; it may be the logits
+ * themselves (then with the same stride), and must not overlap them otherwise.  Elements between
+ * the rows are left as they are. */
+ESM_API esm_status esm_op_distill_loss_backward(esm_encoder_t* h, const void* logits, esm_precision logits_type,
+                                                long long logits_stride, const int32_t* teacher_ids,
+                                                const float* teacher_logits, int K, int total_tokens, int vocab,
+                                                float temperature, const float* lse, const int* loss_count,
+                                                void* d_logits, long long d_stride, esm_stream_t stream);
 
 /* ---- measurement hooks ----
  * Kernel classes of the forward: 0 QKV GEMM (+bias, RoPE), 1 attention, 2 output-projection

@@ -34,7 +34,10 @@ EXPORTS = ("esm_encoder_create", "esm_encoder_destroy", "esm_encoder_workspace_s
            "esm_op_layernorm_backward_workspace_size", "esm_op_layernorm_backward", "esm_op_attention_train",
            "esm_op_attention_backward_workspace_size", "esm_op_attention_backward",
            "esm_encoder_lm_head_backward_workspace_size", "esm_encoder_lm_head_backward",
-           "esm_op_quantize_nvfp4", "esm_op_gemm_nvfp4", "esm_encoder_get_fp4_scales", "esm_status_string")
+           "esm_op_quantize_nvfp4", "esm_op_gemm_nvfp4", "esm_encoder_get_fp4_scales", "esm_status_string",
+           "esm_encoder_set_attention_window", "esm_op_attention_window_workspace_size", "esm_op_attention_window",
+           "esm_op_attention_window_backward", "esm_op_distill_loss_workspace_size", "esm_op_distill_loss",
+           "esm_op_distill_loss_backward", "esm_encoder_lm_head_distill_backward")
 PROFILE_CLASSES = ("gemm_qkv", "attention", "gemm_oproj", "gemm_fc1", "gemm_fc2", "layernorm", "other",
                    "gemm_backward")
 
@@ -75,6 +78,10 @@ class EsmGrads(ctypes.Structure):
         [("lnf_g", ctypes.c_void_p), ("lnf_b", ctypes.c_void_p)]
 
 
+class EsmAttnWindow(ctypes.Structure):
+    _fields_ = [("left", ctypes.c_int), ("right", ctypes.c_int), ("sinks", ctypes.c_int)]
+
+
 LM_HEAD_NAMES = ("dense_w", "dense_b", "ln_g", "ln_b", "emb", "bias")
 
 
@@ -98,6 +105,7 @@ def load_library() -> ctypes.CDLL:
                            "(run python -m transformer_esm_layer_gb300.build)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    i64, f32 = ctypes.c_longlong, ctypes.c_float
     sig = {
         "esm_encoder_create": (i32, [ctypes.POINTER(EsmConfig), ctypes.POINTER(vp)]),
         "esm_encoder_destroy": (None, [vp]),
@@ -141,6 +149,18 @@ def load_library() -> ctypes.CDLL:
         "esm_encoder_lm_head_backward_workspace_size": (i32, [vp, i32, ctypes.POINTER(sz)]),
         "esm_encoder_lm_head_backward": (i32, [vp, ctypes.POINTER(EsmLmHead), vp, i32, vp, vp,
                                                ctypes.POINTER(EsmLmHeadGrads), vp, vp, vp, vp, sz, vp]),
+        "esm_encoder_lm_head_distill_backward": (i32, [vp, ctypes.POINTER(EsmLmHead), vp, i32, vp, vp, i32, f32, vp,
+                                                       ctypes.POINTER(EsmLmHeadGrads), vp, vp, vp, vp, sz, vp]),
+        "esm_encoder_set_attention_window": (i32, [vp, ctypes.POINTER(EsmAttnWindow)]),
+        "esm_op_attention_window_workspace_size": (i32, [vp, i32, i32, ctypes.POINTER(EsmAttnWindow), i32,
+                                                         ctypes.POINTER(sz)]),
+        "esm_op_attention_window": (i32, [vp, vp, vp, i32, i32, i32, ctypes.POINTER(EsmAttnWindow), vp, vp, vp, sz,
+                                          vp]),
+        "esm_op_attention_window_backward": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32,
+                                                   ctypes.POINTER(EsmAttnWindow), vp, vp, sz, vp]),
+        "esm_op_distill_loss_workspace_size": (i32, [vp, i32, i32, ctypes.POINTER(sz)]),
+        "esm_op_distill_loss": (i32, [vp, vp, i32, i64, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp, sz, vp]),
+        "esm_op_distill_loss_backward": (i32, [vp, vp, i32, i64, vp, vp, i32, i32, i32, f32, vp, vp, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -159,6 +179,27 @@ def _stream_ptr(stream) -> Optional[int]:
         import torch
         stream = torch.cuda.current_stream()
     return stream.cuda_stream or None
+
+
+def _need(ok, where: str, what: str):
+    """Arguments the C side cannot check (it sees only addresses)."""
+    if not ok:
+        raise ValueError(f"{where}: {what}")
+
+
+def _check_tensor(t, where: str, name: str, dtype, shape, device):
+    """A contiguous tensor of this type and shape on this CUDA device (shape None: any)."""
+    import torch
+    _need(isinstance(t, torch.Tensor) and t.is_cuda, where, f"{name} must be a CUDA tensor")
+    _need(t.device == device, where, f"{name} must be on {device}")
+    _need(t.dtype == dtype, where, f"{name} must be {dtype}")
+    _need(shape is None or tuple(t.shape) == tuple(shape), where, f"{name} must be {shape and list(shape)}")
+    _need(t.is_contiguous(), where, f"{name} must be contiguous")
+
+
+def _window_struct(window) -> EsmAttnWindow:
+    left, right, sinks = window
+    return EsmAttnWindow(int(left), int(right), int(sinks))
 
 
 class DeviceWeights:
@@ -393,6 +434,149 @@ class EsmEncoder:
                     "esm_op_attention")
         return o
 
+    # ------------------------------------------------------------------ windowed attention
+    def set_attention_window(self, window=None):
+        """esm_encoder_set_attention_window: (left, right, sinks) for every layer, -1 = unlimited;
+        None restores full attention.  Set it before train_buffer()."""
+        w = None if window is None else ctypes.byref(_window_struct(window))
+        self._raise(self.lib.esm_encoder_set_attention_window(self.handle, w), "esm_encoder_set_attention_window")
+
+    def op_attention_window_workspace(self, T: int, B: int, window, backward: bool = False, device="cuda"):
+        import torch
+        n = ctypes.c_size_t()
+        self._raise(self.lib.esm_op_attention_window_workspace_size(self.handle, T, B,
+                                                                    ctypes.byref(_window_struct(window)),
+                                                                    int(backward), ctypes.byref(n)),
+                    "esm_op_attention_window_workspace_size")
+        return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+
+    def _check_packed(self, where: str, qkv, cu_seqlens):
+        import torch
+        _need(isinstance(qkv, torch.Tensor) and qkv.dim() == 2, where, "qkv must be a 2-D tensor")
+        _check_tensor(qkv, where, "qkv", self.out_dtype, (qkv.shape[0], 3 * self.hidden), qkv.device)
+        _check_tensor(cu_seqlens, where, "cu_seqlens", torch.int32, None, qkv.device)
+        _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2, where, "cu_seqlens must hold at least two offsets")
+
+    def op_attention_window(self, qkv, cu_seqlens, max_seqlen: int, window, o, lse=None, workspace=None, stream=None):
+        """esm_op_attention_window: attention of packed q | k | v [T, 3*hidden] under a window
+        (left, right, sinks), -1 = unlimited: query i sees key j of its sequence if j <= i + right
+        and (j >= i - left or j < sinks).  Writes o [T, hidden] and, if given, lse float32 [heads, T]."""
+        import torch
+        where = "op_attention_window"
+        self._check_packed(where, qkv, cu_seqlens)
+        T, B = qkv.shape[0], cu_seqlens.numel() - 1
+        _check_tensor(o, where, "o", self.out_dtype, (T, self.hidden), qkv.device)
+        if lse is not None:
+            _check_tensor(lse, where, "lse", torch.float32, (self.cfg.heads, T), qkv.device)
+        if workspace is None:
+            workspace = self.op_attention_window_workspace(T, B, window, device=qkv.device)
+        self._raise(self.lib.esm_op_attention_window(self.handle, _ptr(qkv), _ptr(cu_seqlens), B, T, int(max_seqlen),
+                                                     ctypes.byref(_window_struct(window)), _ptr(o), _ptr(lse),
+                                                     _ptr(workspace), workspace.numel(), _stream_ptr(stream)),
+                    "esm_op_attention_window")
+        return o
+
+    def op_attention_window_backward(self, qkv, o, lse, d_o, cu_seqlens, max_seqlen: int, window, dqkv,
+                                     workspace=None, stream=None):
+        """esm_op_attention_window_backward: dqkv [T, 3*hidden] (bf16) from the forward's qkv, o and
+        lse under the same window and d_o = dL/do."""
+        import torch
+        where = "op_attention_window_backward"
+        self._check_packed(where, qkv, cu_seqlens)
+        T, B = qkv.shape[0], cu_seqlens.numel() - 1
+        for name, t in (("o", o), ("d_o", d_o)):
+            _check_tensor(t, where, name, torch.bfloat16, (T, self.hidden), qkv.device)
+        _check_tensor(lse, where, "lse", torch.float32, (self.cfg.heads, T), qkv.device)
+        _check_tensor(dqkv, where, "dqkv", torch.bfloat16, (T, 3 * self.hidden), qkv.device)
+        if workspace is None:
+            workspace = self.op_attention_window_workspace(T, B, window, backward=True, device=qkv.device)
+        self._raise(self.lib.esm_op_attention_window_backward(self.handle, _ptr(qkv), _ptr(o), _ptr(lse), _ptr(d_o),
+                                                              _ptr(cu_seqlens), B, T, int(max_seqlen),
+                                                              ctypes.byref(_window_struct(window)), _ptr(dqkv),
+                                                              _ptr(workspace), workspace.numel(), _stream_ptr(stream)),
+                    "esm_op_attention_window_backward")
+        return dqkv
+
+    # ------------------------------------------------------------------ distillation
+    def op_distill_loss_workspace(self, T: int, vocab: int, device="cuda"):
+        import torch
+        n = ctypes.c_size_t()
+        self._raise(self.lib.esm_op_distill_loss_workspace_size(self.handle, T, vocab, ctypes.byref(n)),
+                    "esm_op_distill_loss_workspace_size")
+        return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+
+    @staticmethod
+    def _check_distill(where: str, logits, teacher_ids, teacher_logits):
+        import torch
+        _need(isinstance(logits, torch.Tensor) and logits.is_cuda, where, "logits must be a CUDA tensor")
+        _need(logits.dtype in (torch.float32, torch.bfloat16), where, "logits must be float32 or bfloat16")
+        _need(logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1), where,
+              "logits must be 2-D with contiguous rows")
+        T = logits.shape[0]
+        _need(isinstance(teacher_ids, torch.Tensor) and teacher_ids.dim() == 2, where, "teacher_ids must be [T, K]")
+        shape = (T, teacher_ids.shape[1])
+        _check_tensor(teacher_ids, where, "teacher_ids", torch.int32, shape, logits.device)
+        _check_tensor(teacher_logits, where, "teacher_logits", torch.float32, shape, logits.device)
+
+    @staticmethod
+    def _row_stride(t) -> int:
+        """Elements between rows (a single row may report any stride)."""
+        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+    def op_distill_loss(self, logits, teacher_ids, teacher_logits, temperature: float, token_loss, lse=None,
+                        loss_sum=None, count=None, workspace=None, stream=None):
+        """esm_op_distill_loss: t^2 KL(teacher's top logits || student) per row of logits [T, vocab]
+        (float32 or bf16, rows may be strided), into token_loss [T]; optionally the rows' lse [T]
+        (for the backward) and the sum and number of scored rows (device scalars).  teacher_ids
+        int32, teacher_logits float32 [T, K]; id -1: unused entry."""
+        import torch
+        where = "op_distill_loss"
+        self._check_distill(where, logits, teacher_ids, teacher_logits)
+        T, V = logits.shape
+        _check_tensor(token_loss, where, "token_loss", torch.float32, (T,), logits.device)
+        if lse is not None:
+            _check_tensor(lse, where, "lse", torch.float32, (T,), logits.device)
+        for name, t, dt in (("loss_sum", loss_sum, torch.float32), ("count", count, torch.int32)):
+            if t is not None:
+                _check_tensor(t, where, name, dt, None, logits.device)
+                _need(t.numel() == 1, where, f"{name} must hold one value")
+        if workspace is None and (loss_sum is not None or count is not None):
+            workspace = self.op_distill_loss_workspace(T, V, logits.device)
+        self._raise(self.lib.esm_op_distill_loss(self.handle, _ptr(logits),
+                                                 PRECISIONS["fp32" if logits.dtype == torch.float32 else "bf16"],
+                                                 self._row_stride(logits), _ptr(teacher_ids), _ptr(teacher_logits),
+                                                 teacher_ids.shape[1], T, V, float(temperature), _ptr(token_loss),
+                                                 _ptr(lse), _ptr(loss_sum), _ptr(count), _ptr(workspace),
+                                                 0 if workspace is None else workspace.numel(), _stream_ptr(stream)),
+                    "esm_op_distill_loss")
+        return token_loss
+
+    def op_distill_loss_backward(self, logits, teacher_ids, teacher_logits, temperature: float, lse, d_logits,
+                                 loss_count=None, stream=None):
+        """esm_op_distill_loss_backward: d_logits (the logits' type; may be logits itself) of the
+        sum of token_loss divided by loss_count (device int32 scalar; None: of the sum)."""
+        import torch
+        where = "op_distill_loss_backward"
+        self._check_distill(where, logits, teacher_ids, teacher_logits)
+        T, V = logits.shape
+        _check_tensor(lse, where, "lse", torch.float32, (T,), logits.device)
+        _need(isinstance(d_logits, torch.Tensor) and d_logits.device == logits.device
+              and d_logits.dtype == logits.dtype and d_logits.shape == logits.shape
+              and (d_logits.stride(1) == 1 or V == 1), where,
+              "d_logits must have the type, device and shape of logits, and contiguous rows")
+        if loss_count is not None:
+            _check_tensor(loss_count, where, "loss_count", torch.int32, None, logits.device)
+            _need(loss_count.numel() == 1, where, "loss_count must hold one value")
+        self._raise(self.lib.esm_op_distill_loss_backward(self.handle, _ptr(logits),
+                                                          PRECISIONS["fp32" if logits.dtype == torch.float32
+                                                                     else "bf16"],
+                                                          self._row_stride(logits), _ptr(teacher_ids),
+                                                          _ptr(teacher_logits), teacher_ids.shape[1], T, V,
+                                                          float(temperature), _ptr(lse), _ptr(loss_count),
+                                                          _ptr(d_logits), self._row_stride(d_logits),
+                                                          _stream_ptr(stream)), "esm_op_distill_loss_backward")
+        return d_logits
+
     def set_layer_precision(self, per_layer):
         """esm_encoder_set_layer_precision: one of "fp32", "bf16", "fp8", "fp4" per layer."""
         arr = (ctypes.c_int * max(1, len(per_layer)))(*[PRECISIONS[p] for p in per_layer])
@@ -538,6 +722,32 @@ class EsmEncoder:
                                                           _ptr(loss_sum), _ptr(count), _ptr(loss_count),
                                                           _ptr(workspace), workspace.numel(), _stream_ptr(stream)),
                     "esm_encoder_lm_head_backward")
+        return d_hidden, grads
+
+    def lm_head_distill_backward(self, head: "DeviceLmHead", hidden, teacher_ids, teacher_logits, temperature: float,
+                                 d_hidden=None, grads=None, loss_sum=None, count=None, workspace=None, stream=None,
+                                 loss_count=None):
+        """esm_encoder_lm_head_distill_backward: as lm_head_backward, for the distillation loss
+        against a teacher's top logits (teacher_ids int32, teacher_logits float32 [T, K])."""
+        import torch
+        where = "lm_head_distill_backward"
+        T = hidden.shape[0]
+        dev = hidden.device
+        _need(isinstance(teacher_ids, torch.Tensor) and teacher_ids.dim() == 2, where, "teacher_ids must be [T, K]")
+        _check_tensor(teacher_ids, where, "teacher_ids", torch.int32, (T, teacher_ids.shape[1]), dev)
+        _check_tensor(teacher_logits, where, "teacher_logits", torch.float32, tuple(teacher_ids.shape), dev)
+        if d_hidden is None:
+            d_hidden = torch.empty(T, self.hidden, dtype=torch.float32, device=dev)
+        if grads is None:
+            grads = {k: torch.empty(tuple(head.t[k].shape), dtype=torch.float32, device=dev) for k in LM_HEAD_NAMES}
+        if workspace is None:
+            workspace = self.lm_head_backward_workspace(T, dev)
+        gs = EsmLmHeadGrads(*[grads[k].data_ptr() for k in LM_HEAD_NAMES])
+        self._raise(self.lib.esm_encoder_lm_head_distill_backward(
+            self.handle, ctypes.byref(head.struct), _ptr(hidden), T, _ptr(teacher_ids), _ptr(teacher_logits),
+            teacher_ids.shape[1], float(temperature), _ptr(d_hidden), ctypes.byref(gs), _ptr(loss_sum), _ptr(count),
+            _ptr(loss_count), _ptr(workspace), workspace.numel(), _stream_ptr(stream)),
+            "esm_encoder_lm_head_distill_backward")
         return d_hidden, grads
 
     def op_quantize_nvfp4(self, x, stream=None):

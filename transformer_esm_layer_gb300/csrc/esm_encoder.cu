@@ -69,6 +69,8 @@ struct esm_encoder {
   unsigned* d_err = nullptr;     // device error word
   float2* d_rope = nullptr;      // [16][max_positions][2] (cos, sin)
   std::vector<uint8_t> layer_fp8;  // per layer: 1 = E4M3 GEMMs, 2 = NVFP4 GEMMs (FP8 handles only)
+  AttnWindow window = kFullWindow;        // attention window of every layer
+  AttnWindow train_window = kFullWindow;  // the window the last training forward ran with
   float* d_fp8 = nullptr;        // scales [L*8] | history [L*8*len] | amax [L*8]
   float* d_fp4 = nullptr;        // NVFP4 tensor scales of the last forward [L*8] | amax [L*8]
   size_t fp8_floats = 0;
@@ -257,6 +259,39 @@ esm_status check_ws(esm_encoder* h, int T, int B, void* ws, size_t bytes, WsLayo
 
 esm_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ESM_OK : ESM_ERR_CUDA; }
 
+// The window with its sides in canonical form: a side that reaches past every position is
+// unlimited (so that positions plus a side never overflow), and sinks only matter beside a
+// limited left side.  False for sides below -1 or a bad sink count.
+bool canonical_window(const esm_encoder* h, const esm_attn_window* w, AttnWindow* out) {
+  if (!w || w->left < -1 || w->right < -1 || w->sinks < 0 || w->sinks > kMaxSinks) return false;
+  *out = *w;
+  if (out->left >= h->cfg.max_positions) out->left = -1;
+  if (out->right >= h->cfg.max_positions) out->right = -1;
+  if (out->left < 0) out->sinks = 0;
+  return true;
+}
+bool is_full(const AttnWindow& w) { return w.left < 0 && w.right < 0; }
+
+// Attention of an indexed batch (work items in tiles of kAttnQTileTc rows; fp32: positions and
+// segments): qkv [T, 3d] -> o [T, d] (act_out), with lse [heads, T] if given.
+esm_status run_attention(esm_encoder* h, const AttnWindow& win, const void* qkv, void* o, Act act_out, int T,
+                         int max_items, const PackBuffers& pb, const float* q_scale, float* amax, cudaStream_t st,
+                         float* lse = nullptr) {
+  const int d = h->cfg.hidden, H = h->cfg.heads;
+  if (h->cfg.precision == ESM_FP32) {
+    launch_attention_f32(static_cast<const float*>(qkv), static_cast<float*>(o), d, H, T, pb, st, win);
+    return cuda_status(cudaGetLastError());
+  }
+  const CUtensorMap* tq = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 128, 2);
+  if (!tq) return ESM_ERR_CUDA;
+  if (is_full(win))
+    return cuda_status(launch_attention_tc(tq, o, act_out, d, H, max_items, pb, q_scale, amax, h->d_err, st, lse, T));
+  const CUtensorMap* tq16 = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 16, 2);
+  if (!tq16) return ESM_ERR_CUDA;
+  return cuda_status(launch_attention_window_tc(tq, tq16, win, qkv, o, act_out, d, H, max_items, pb, q_scale, amax,
+                                                h->d_err, st, lse, T));
+}
+
 bool weights_ok(const esm_encoder* h, const esm_weights* w) {
   if (!w || !w->emb) return false;
   const void* const* arrs[] = {w->ln1_g, w->ln1_b, w->w_qkv, w->b_qkv, w->w_o, w->b_o,
@@ -344,7 +379,7 @@ esm_status run_fp4_layer(esm_encoder* h, const esm_weights* w, int l, int T, con
   void* qkv = b + L.qkv;
   void* o = b + L.o;
   void* u = b + L.u;
-  const int d = c.hidden, f = c.ffn, H = c.heads;
+  const int d = c.hidden, f = c.ffn;
   const int tp = (T + 127) / 128 * 128;
   const size_t nf = (size_t)c.num_layers * kNumFp8Tensors;
   float* sc = h->d_fp4 + (size_t)l * kNumFp8Tensors;
@@ -392,11 +427,9 @@ esm_status run_fp4_layer(esm_encoder* h, const esm_weights* w, int l, int T, con
     return s;
   {
     ProfScope _ps(h, P_ATTN, st, 1);
-    const CUtensorMap* tq = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 128, 2);
-    if (!tq) return ESM_ERR_CUDA;
     // the attention output's amax comes from the attention kernel (so its quantisation is one pass)
-    if (launch_attention_tc(tq, o, Act::BF16, d, H, L.max_items, pb, nullptr, am + X_O, h->d_err, st) != cudaSuccess)
-      return ESM_ERR_CUDA;
+    if ((s = run_attention(h, h->window, qkv, o, Act::BF16, T, L.max_items, pb, nullptr, am + X_O, st)) != ESM_OK)
+      return s;
   }
   if ((s = gemm(P_OPROJ, kFp4Residual, o, true, d, w->w_o[l], d, X_O, W_O, w->b_o[l], x, nullptr)) != ESM_OK)
     return s;
@@ -418,7 +451,7 @@ esm_status run_layers(esm_encoder* h, const esm_weights* w, int T, int max_items
   void* qkv = b + L.qkv;
   void* o = b + L.o;
   void* u = b + L.u;
-  const int d = c.hidden, f = c.ffn, H = c.heads;
+  const int d = c.hidden, f = c.ffn;
   const bool pf32 = !h->bf16_params();
   const Act act = h->act();
   esm_status s;
@@ -483,15 +516,10 @@ esm_status run_layers(esm_encoder* h, const esm_weights* w, int T, int max_items
     if (s != ESM_OK) return s;
     {
       ProfScope _ps(h, P_ATTN, st, 1);
-      if (c.precision == ESM_FP32)
-        launch_attention_f32(static_cast<const float*>(qkv), static_cast<float*>(o), d, H, T, pb, st);
-      else {
-        const CUtensorMap* tq = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 128, 2);
-        if (!tq) return ESM_ERR_CUDA;
-        if (launch_attention_tc(tq, o, fp8 ? Act::E4M3 : Act::BF16, d, H, max_items, pb, sc + X_O,
-                                fp8 ? am + X_O : nullptr, h->d_err, st) != cudaSuccess)
-          return ESM_ERR_CUDA;
-      }
+      const Act act_o = c.precision == ESM_FP32 ? Act::F32 : fp8 ? Act::E4M3 : Act::BF16;
+      if ((s = run_attention(h, h->window, qkv, o, act_o, T, max_items, pb, sc + X_O, fp8 ? am + X_O : nullptr, st)) !=
+          ESM_OK)
+        return s;
     }
     LnFoldArgs ln_out;  // out-projection: statistics and bf16(x * gamma2) for fc1
     if (fold) {
@@ -586,13 +614,13 @@ bool config_ok(const esm_config* c) {
 struct TrainLayout {
   size_t tok, x, xmid, y1, qkv, o, lse, y2, z, u;                        // bases
   size_t sx, sy, sqkv, slse, sz;                                         // slab strides
-  size_t dx, dxb, dy, dz, dob, dqkv, dqacc, dsum, partial, split, embp;  // scratch
+  size_t dx, dxb, dy, dz, dob, dqkv, dqacc, dsum, far, partial, split, embp;  // scratch
   size_t split_floats, total;
 };
 
 constexpr int kMaxKSplit = 8;
 
-TrainLayout train_layout(const esm_config& c, int Tm) {
+TrainLayout train_layout(const esm_config& c, int Tm, const AttnWindow& win) {
   TrainLayout L{};
   const size_t T = Tm > 0 ? Tm : 1, d = c.hidden, f = c.ffn, H = c.heads, nl = c.num_layers > 0 ? c.num_layers : 0;
   L.sx = align256(4 * T * d);
@@ -624,6 +652,7 @@ TrainLayout train_layout(const esm_config& c, int Tm) {
   L.dqkv = take(2 * T * 3 * d);
   L.dqacc = take(4 * T * d);
   L.dsum = take(4 * T * H);
+  L.far = take(attention_window_bwd_far_bytes(win, (int)T, (int)H));
   const size_t widest = std::max(3 * d, f);
   L.partial = take(4 * bwd_partial_floats((int)T, (int)widest));
   L.split_floats = (size_t)kMaxKSplit * std::max(f * d, 3 * d * d);
@@ -713,13 +742,13 @@ esm_status train_forward_impl(esm_encoder* h, const esm_weights* w, const int32_
   esm_status s = check_ws(h, T, B, ws, ws_bytes, &L);
   if (s != ESM_OK) return s;
   const esm_config& c = h->cfg;
-  const TrainLayout R = train_layout(c, T);
+  const TrainLayout R = train_layout(c, T, h->window);
   uint8_t* tb = static_cast<uint8_t*>(train);
   PackBuffers pb = pack_buffers(ws, L);
   if (cudaMemsetAsync(pb.pos_id, 0, 4 * (size_t)T, st) != cudaSuccess) return ESM_ERR_CUDA;
   if (cudaMemsetAsync(pb.seg_id, 0, 4 * (size_t)T, st) != cudaSuccess) return ESM_ERR_CUDA;
   if (cudaMemcpyAsync(tb + R.tok, tok, 4 * (size_t)T, cudaMemcpyDeviceToDevice, st) != cudaSuccess) return ESM_ERR_CUDA;
-  const int d = c.hidden, f = c.ffn, H = c.heads;
+  const int d = c.hidden, f = c.ffn;
   {
     ProfScope _ps(h, P_OTHER, st, 3);
     launch_pack_index(cu, B, T, max_seqlen, c.max_positions, pb, h->d_err, st);
@@ -745,11 +774,8 @@ esm_status train_forward_impl(esm_encoder* h, const esm_weights* w, const int32_
     if (s != ESM_OK) return s;
     {
       ProfScope _ps(h, P_ATTN, st, 1);
-      const CUtensorMap* tq = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 128, 2);
-      if (!tq) return ESM_ERR_CUDA;
-      if (launch_attention_tc(tq, o, Act::BF16, d, H, L.max_items, pb, nullptr, nullptr, h->d_err, st, lse, T) !=
-          cudaSuccess)
-        return ESM_ERR_CUDA;
+      if ((s = run_attention(h, h->window, qkv, o, Act::BF16, T, L.max_items, pb, nullptr, nullptr, st, lse)) != ESM_OK)
+        return s;
     }
     s = run_gemm(h, P_OPROJ, ESM_EPI_RESIDUAL, o, w->w_o[l], w->b_o[l], xmid, nullptr, T, d, d, false, Act::F32,
                  nullptr, nullptr, nullptr, nullptr, st, -1, x);
@@ -775,6 +801,7 @@ esm_status train_forward_impl(esm_encoder* h, const esm_weights* w, const int32_
   h->train_T = T;
   h->train_B = B;
   h->train_items = L.max_items;
+  h->train_window = h->window;
   h->train_buf = train;
   h->train_ws = ws;
   return cuda_status(cudaGetLastError());
@@ -784,7 +811,8 @@ esm_status backward_impl(esm_encoder* h, const esm_weights* w, const float* d_ou
                          void* ws, cudaStream_t st) {
   const esm_config& c = h->cfg;
   const int T = h->train_T, d = c.hidden, f = c.ffn, H = c.heads;
-  const TrainLayout R = train_layout(c, T);
+  const AttnWindow& win = h->train_window;
+  const TrainLayout R = train_layout(c, T, win);
   const WsLayout L = h->layout(T, h->train_B);
   PackBuffers pb = pack_buffers(ws, L);
   uint8_t* tb = static_cast<uint8_t*>(train);
@@ -839,10 +867,14 @@ esm_status backward_impl(esm_encoder* h, const esm_weights* w, const float* d_ou
       const CUtensorMap* td = h->map(dob, (uint64_t)T, (uint64_t)d, 128, 2);
       const CUtensorMap* tdq = h->map(dqacc, (uint64_t)T, (uint64_t)d, 32, 4);
       if (!tq || !td || !tdq) return ESM_ERR_CUDA;
-      if (launch_attention_bwd_tc(tq, td, tdq, static_cast<const __nv_bfloat16*>(o), dob, lse, dsum, dqacc, dqkv, T, d, H,
-                                  h->train_items, pb, h->d_rope, c.max_positions, h->num_sms, h->d_err,
-                                  st) != cudaSuccess)
-        return ESM_ERR_CUDA;
+      const __nv_bfloat16* ob = static_cast<const __nv_bfloat16*>(o);
+      const cudaError_t e =
+          is_full(win) ? launch_attention_bwd_tc(tq, td, tdq, ob, dob, lse, dsum, dqacc, dqkv, T, d, H, h->train_items,
+                                                 pb, h->d_rope, c.max_positions, h->num_sms, h->d_err, st)
+                       : launch_attention_window_bwd_tc(tq, td, tdq, win, ob, dob, lse, dsum, dqacc, tb + R.far, dqkv,
+                                                        T, h->train_B, d, H, h->train_items, pb, h->d_rope,
+                                                        c.max_positions, h->num_sms, h->d_err, st);
+      if (e != cudaSuccess) return ESM_ERR_CUDA;
     }
     PROF(h, P_OTHER, st, 2, launch_colsum(dqkv, true, T, 3 * d, g->b_qkv[l], partial, nullptr, st));
     if ((s = run_wgrad(h, dqkv, y1, g->w_qkv[l], T, 3 * d, d, split, R.split_floats, st)) != ESM_OK) return s;
@@ -995,6 +1027,14 @@ esm_status esm_encoder_set_layer_precision(esm_encoder_t* h, const esm_precision
   return ESM_OK;
 }
 
+esm_status esm_encoder_set_attention_window(esm_encoder_t* h, const esm_attn_window* window) {
+  if (!h) return ESM_ERR_INVALID_ARG;
+  AttnWindow w = kFullWindow;
+  if (window && !canonical_window(h, window, &w)) return ESM_ERR_INVALID_ARG;
+  h->window = w;
+  return ESM_OK;
+}
+
 esm_status esm_encoder_lm_head_workspace_size(const esm_encoder_t* h, int total_tokens, size_t* bytes) {
   if (!h || !bytes || total_tokens < 0) return ESM_ERR_INVALID_ARG;
   size_t a, b;
@@ -1081,11 +1121,45 @@ esm_status esm_encoder_lm_head_backward_workspace_size(const esm_encoder_t* h, i
   return ESM_OK;
 }
 
-esm_status esm_encoder_lm_head_backward(esm_encoder_t* h, const esm_lm_head* head, const void* hidden,
-                                        int total_tokens, const int32_t* targets, float* d_hidden,
-                                        const esm_lm_head_grads* grads, float* loss_sum, int* count,
-                                        const int* loss_count, void* workspace, size_t workspace_bytes,
-                                        esm_stream_t stream) {
+// Arguments of the distillation loss that both directions share; false if one is invalid.
+static bool distill_args(esm_encoder* h, const void* logits, esm_precision type, long long stride,
+                         const int32_t* teacher_ids, const float* teacher_logits, int K, int T, int V,
+                         float temperature, DistillArgs* a) {
+  if (T < 0 || V <= 0 || K <= 0 || K > kDistillMaxK || stride < V) return false;
+  if (!(temperature > 0.f) || !(1.f / temperature > 0.f) || !(1.f / temperature <= 3.0e38f)) return false;
+  const size_t es = type == ESM_FP32 ? 4 : 2;
+  if (T > 0 && (!logits || !teacher_ids || !teacher_logits || !aligned(logits, es) || !aligned(teacher_ids, 4) ||
+                !aligned(teacher_logits, 4)))
+    return false;
+  *a = DistillArgs{};
+  a->logits = logits;
+  a->bf16 = type == ESM_BF16;
+  a->stride = stride;
+  a->teacher_ids = teacher_ids;
+  a->teacher_logits = teacher_logits;
+  a->K = K;
+  a->T = T;
+  a->V = V;
+  a->temperature = temperature;
+  a->err = h->d_err;
+  return true;
+}
+
+// What the head's backward differentiates: the masked cross-entropy against targets, or the
+// distillation loss against a teacher's top logits.
+struct LmLoss {
+  const int32_t* targets = nullptr;
+  const int32_t* teacher_ids = nullptr;
+  const float* teacher_logits = nullptr;
+  int K = 0;
+  float temperature = 1.f;
+  bool distill() const { return K > 0; }
+};
+
+static esm_status lm_head_backward_impl(esm_encoder* h, const esm_lm_head* head, const void* hidden, int total_tokens,
+                                        const LmLoss& loss, float* d_hidden, const esm_lm_head_grads* grads,
+                                        float* loss_sum, int* count, const int* loss_count, void* workspace,
+                                        size_t workspace_bytes, esm_stream_t stream) {
   if (!h || !head || !grads || total_tokens <= 0 || !hidden || !d_hidden) return ESM_ERR_INVALID_ARG;
   if (h->cfg.precision != ESM_BF16) return ESM_ERR_UNSUPPORTED;
   const void* p[6] = {head->dense_w, head->dense_b, head->ln_g, head->ln_b, head->emb, head->bias};
@@ -1094,7 +1168,7 @@ esm_status esm_encoder_lm_head_backward(esm_encoder_t* h, const esm_lm_head* hea
   float* gp[6] = {grads->dense_w, grads->dense_b, grads->ln_g, grads->ln_b, grads->emb, grads->bias};
   for (float* q : gp)
     if (!q || !aligned(q, 16)) return ESM_ERR_INVALID_ARG;
-  if (!aligned(hidden, 16) || !aligned(d_hidden, 16)) return ESM_ERR_INVALID_ARG;
+  if (!aligned(hidden, 16) || !aligned(d_hidden, 16) || !aligned(loss_count, 4)) return ESM_ERR_INVALID_ARG;
   const int d = h->cfg.hidden, V = h->cfg.vocab, T = total_tokens;
   if (!lm_logits_supported(V, d, true) || d % 256) return ESM_ERR_UNSUPPORTED;
   const LmBwdLayout L = lm_bwd_layout(h->cfg, T);
@@ -1119,23 +1193,76 @@ esm_status esm_encoder_lm_head_backward(esm_encoder_t* h, const esm_lm_head* hea
                           Act::BF16, nullptr, nullptr, nullptr, nullptr, st, -1, nullptr, a);
   if (s != ESM_OK) return s;
   launch_layernorm_bf16in(u, head->ln_g, head->ln_b, false, z, Act::BF16, T, d, h->cfg.ln_eps, st);
-  if (launch_lm_logits(z, true, head->emb, head->bias, T, d, V, targets, logits, tl, lsum, cnt, h->num_sms, h->d_err,
-                       st) != cudaSuccess)
+  DistillArgs dist;
+  if (loss.distill()) {
+    // the distillation loss of the logits; its row lse is kept in the first T floats of dz, which
+    // is written only after the gradient of the logits has been taken
+    if (launch_lm_logits(z, true, head->emb, head->bias, T, d, V, nullptr, logits, nullptr, nullptr, nullptr, h->num_sms,
+                         h->d_err, st) != cudaSuccess)
+      return ESM_ERR_CUDA;
+    if (!distill_args(h, logits, ESM_FP32, V, loss.teacher_ids, loss.teacher_logits, loss.K, T, V, loss.temperature,
+                      &dist))
+      return ESM_ERR_INVALID_ARG;
+    dist.token_loss = tl;
+    dist.lse = dz;
+    if (launch_distill_loss(dist, lsum, cnt, dl, h->num_sms, st) != cudaSuccess) return ESM_ERR_CUDA;
+  } else if (launch_lm_logits(z, true, head->emb, head->bias, T, d, V, loss.targets, logits, tl, lsum, cnt, h->num_sms,
+                              h->d_err, st) != cudaSuccess) {
     return ESM_ERR_CUDA;
+  }
   if (loss_sum && cudaMemcpyAsync(loss_sum, lsum, 4, cudaMemcpyDeviceToDevice, st) != cudaSuccess) return ESM_ERR_CUDA;
   if (count && cudaMemcpyAsync(count, cnt, 4, cudaMemcpyDeviceToDevice, st) != cudaSuccess) return ESM_ERR_CUDA;
-  // backward of the mean masked cross-entropy (over this call's scored tokens, or over the
-  // caller's global count)
-  if (loss_count && !aligned(loss_count, 4)) return ESM_ERR_INVALID_ARG;
-  if (launch_lm_backward_head(logits, targets, loss_count ? loss_count : cnt, head->emb, z, T, d, V, dl, dz, grads->emb, grads->bias, partial,
-                              h->num_sms, st) != cudaSuccess)
+  // backward of the mean loss (over this call's scored tokens, or over the caller's global count)
+  const int* over = loss_count ? loss_count : cnt;
+  if (loss.distill()) {
+    dist.loss_count = over;
+    dist.d_logits = dl;
+    dist.d_stride = V;
+    if (launch_distill_loss_backward(dist, h->num_sms, st) != cudaSuccess ||
+        launch_lm_backward_from_dlogits(dl, head->emb, z, T, d, V, dz, grads->emb, grads->bias, partial, st) !=
+            cudaSuccess)
+      return ESM_ERR_CUDA;
+  } else if (launch_lm_backward_head(logits, loss.targets, over, head->emb, z, T, d, V, dl, dz, grads->emb, grads->bias,
+                                     partial, h->num_sms, st) != cudaSuccess) {
     return ESM_ERR_CUDA;
+  }
   launch_ln_bwd_bf16in(u, head->ln_g, false, dz, du, grads->ln_g, grads->ln_b, partial, T, d, h->cfg.ln_eps, st);
   launch_gelu_bwd(du, a, da, (size_t)T * d, st);
   launch_colsum(da, true, T, d, grads->dense_b, partial, nullptr, st);
   if ((s = run_wgrad(h, da, hidden, grads->dense_w, T, d, d, split, L.split_floats, st)) != ESM_OK) return s;
   if ((s = run_dgrad(h, da, head->dense_w, d_hidden, false, T, d, d, st)) != ESM_OK) return s;
   return cuda_status(cudaGetLastError());
+}
+
+esm_status esm_encoder_lm_head_backward(esm_encoder_t* h, const esm_lm_head* head, const void* hidden,
+                                        int total_tokens, const int32_t* targets, float* d_hidden,
+                                        const esm_lm_head_grads* grads, float* loss_sum, int* count,
+                                        const int* loss_count, void* workspace, size_t workspace_bytes,
+                                        esm_stream_t stream) {
+  LmLoss loss;
+  loss.targets = targets;
+  return lm_head_backward_impl(h, head, hidden, total_tokens, loss, d_hidden, grads, loss_sum, count, loss_count,
+                               workspace, workspace_bytes, stream);
+}
+
+esm_status esm_encoder_lm_head_distill_backward(esm_encoder_t* h, const esm_lm_head* head, const void* hidden,
+                                                int total_tokens, const int32_t* teacher_ids,
+                                                const float* teacher_logits, int K, float temperature, float* d_hidden,
+                                                const esm_lm_head_grads* grads, float* loss_sum, int* count,
+                                                const int* loss_count, void* workspace, size_t workspace_bytes,
+                                                esm_stream_t stream) {
+  LmLoss loss;
+  loss.teacher_ids = teacher_ids;
+  loss.teacher_logits = teacher_logits;
+  loss.K = K;
+  loss.temperature = temperature;
+  DistillArgs da;
+  if (!h || K <= 0 || total_tokens <= 0 || !teacher_ids || !teacher_logits) return ESM_ERR_INVALID_ARG;
+  const int V = h->cfg.vocab;  // (a stand-in for the logits' address, which the call allots itself)
+  if (!distill_args(h, teacher_logits, ESM_FP32, V, teacher_ids, teacher_logits, K, total_tokens, V, temperature, &da))
+    return ESM_ERR_INVALID_ARG;
+  return lm_head_backward_impl(h, head, hidden, total_tokens, loss, d_hidden, grads, loss_sum, count, loss_count,
+                               workspace, workspace_bytes, stream);
 }
 
 namespace {
@@ -1161,6 +1288,7 @@ std::vector<uintptr_t> host_graph_key(const esm_encoder* h, const esm_weights* w
   for (const void* const* a : arrs)
     for (int l = 0; l < h->cfg.num_layers; ++l) k.push_back((uintptr_t)a[l]);
   for (uint8_t p : h->layer_fp8) k.push_back(p);
+  for (int v : {h->window.left, h->window.right, h->window.sinks}) k.push_back((uintptr_t)(intptr_t)v);
   return k;
 }
 
@@ -1435,11 +1563,173 @@ esm_status esm_op_attention(esm_encoder_t* h, const void* qkv, const int32_t* cu
   return cuda_status(cudaGetLastError());
 }
 
+// Workspace of the windowed attention hooks: the batch's index (positions and segments only for
+// the fp32 kernel), then the backward's scratch.
+struct WindowWs {
+  size_t pos, seg, seg_start, seg_qlen, seg_klen, work, work_count, dsum, dq, far, total;
+  int max_items;
+};
+static WindowWs window_ws(const esm_encoder* h, int Tm, int Bm, const AttnWindow& win, bool backward) {
+  WindowWs L{};
+  const size_t T = Tm > 0 ? Tm : 1, B = Bm > 0 ? Bm : 1;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    size_t o = off;
+    off += align256(bytes);
+    return o;
+  };
+  L.max_items = (int)((T + kAttnQTileTc - 1) / kAttnQTileTc + B);
+  const bool f32 = h->cfg.precision == ESM_FP32;
+  L.pos = take(f32 ? 4 * T : 0);
+  L.seg = take(f32 ? 4 * T : 0);
+  L.seg_start = take(4 * B);
+  L.seg_qlen = take(4 * B);
+  L.seg_klen = take(4 * B);
+  L.work = take(16 * (size_t)L.max_items);
+  L.work_count = take(16);
+  L.dsum = take(backward ? 4 * T * h->cfg.heads : 0);
+  L.dq = take(backward ? 4 * T * h->cfg.hidden : 0);
+  L.far = take(backward ? attention_window_bwd_far_bytes(win, (int)T, h->cfg.heads) : 0);
+  L.total = off;
+  return L;
+}
+
+// Index of the batch in the workspace, for the windowed attention hooks.
+static esm_status window_index(esm_encoder* h, const int32_t* cu, int B, int T, int max_seqlen, const WindowWs& L,
+                               void* ws, PackBuffers* pb, cudaStream_t st) {
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  auto at = [&](size_t off) { return reinterpret_cast<int32_t*>(b + off); };
+  *pb = PackBuffers{at(L.pos),      at(L.seg),  at(L.seg_start), at(L.seg_qlen),
+                    at(L.seg_klen), at(L.work), at(L.work_count)};
+  if (h->cfg.precision == ESM_FP32) {
+    if (cudaMemsetAsync(pb->pos_id, 0, 4 * (size_t)T, st) != cudaSuccess ||
+        cudaMemsetAsync(pb->seg_id, 0, 4 * (size_t)T, st) != cudaSuccess)
+      return ESM_ERR_CUDA;
+    launch_pack_index(cu, B, T, max_seqlen, h->cfg.max_positions, *pb, h->d_err, st);
+  } else {
+    launch_attn_plan(cu, B, T, max_seqlen, h->cfg.max_positions, kAttnQTileTc, L.max_items, *pb, h->d_err, st);
+  }
+  return cuda_status(cudaGetLastError());
+}
+
+esm_status esm_op_attention_window_workspace_size(const esm_encoder_t* h, int total_tokens, int num_seqs,
+                                                  const esm_attn_window* window, int backward, size_t* bytes) {
+  AttnWindow win;
+  if (!h || !bytes || total_tokens < 0 || num_seqs < 0 || !canonical_window(h, window, &win)) return ESM_ERR_INVALID_ARG;
+  if (backward && h->cfg.precision == ESM_FP32) return ESM_ERR_UNSUPPORTED;
+  *bytes = window_ws(h, total_tokens, num_seqs, win, backward != 0).total;
+  return ESM_OK;
+}
+
+esm_status esm_op_attention_window(esm_encoder_t* h, const void* qkv, const int32_t* cu_seqlens, int num_seqs,
+                                   int total_tokens, int max_seqlen, const esm_attn_window* window, void* o, float* lse,
+                                   void* workspace, size_t workspace_bytes, esm_stream_t stream) {
+  AttnWindow win;
+  if (!h || num_seqs < 0 || total_tokens < 0 || !canonical_window(h, window, &win)) return ESM_ERR_INVALID_ARG;
+  if (h->cfg.precision == ESM_FP32 && lse) return ESM_ERR_UNSUPPORTED;
+  if (total_tokens == 0) return ESM_OK;
+  if (!qkv || !cu_seqlens || !o || num_seqs == 0 || max_seqlen <= 0 || max_seqlen > h->cfg.max_positions)
+    return ESM_ERR_INVALID_ARG;
+  if (!aligned(qkv, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(cu_seqlens, 4)) return ESM_ERR_INVALID_ARG;
+  const WindowWs L = window_ws(h, total_tokens, num_seqs, win, false);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return ESM_ERR_WORKSPACE;
+  if (workspace == h->train_ws) h->train_buf = nullptr;  // as check_ws: the pending backward's index is overwritten
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  PackBuffers pb;
+  const esm_status s = window_index(h, cu_seqlens, num_seqs, total_tokens, max_seqlen, L, workspace, &pb, st);
+  if (s != ESM_OK) return s;
+  return run_attention(h, win, qkv, o, h->act(), total_tokens, L.max_items, pb, nullptr, nullptr, st, lse);
+}
+
+esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, const void* o, const float* lse,
+                                            const void* d_o, const int32_t* cu_seqlens, int num_seqs, int total_tokens,
+                                            int max_seqlen, const esm_attn_window* window, void* dqkv, void* workspace,
+                                            size_t workspace_bytes, esm_stream_t stream) {
+  AttnWindow win;
+  if (!h || num_seqs < 0 || total_tokens < 0 || !canonical_window(h, window, &win)) return ESM_ERR_INVALID_ARG;
+  if (h->cfg.precision == ESM_FP32) return ESM_ERR_UNSUPPORTED;
+  if (total_tokens == 0) return ESM_OK;
+  if (!qkv || !o || !lse || !d_o || !cu_seqlens || !dqkv || num_seqs == 0 || max_seqlen <= 0 ||
+      max_seqlen > h->cfg.max_positions)
+    return ESM_ERR_INVALID_ARG;
+  if (!aligned(qkv, 16) || !aligned(o, 16) || !aligned(d_o, 16) || !aligned(dqkv, 16) || !aligned(lse, 4) ||
+      !aligned(cu_seqlens, 4))
+    return ESM_ERR_INVALID_ARG;
+  const WindowWs L = window_ws(h, total_tokens, num_seqs, win, true);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return ESM_ERR_WORKSPACE;
+  if (workspace == h->train_ws) h->train_buf = nullptr;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  PackBuffers pb;
+  const esm_status s = window_index(h, cu_seqlens, num_seqs, total_tokens, max_seqlen, L, workspace, &pb, st);
+  if (s != ESM_OK) return s;
+  const int d = h->cfg.hidden, T = total_tokens;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const CUtensorMap* tq = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 128, 2);
+  const CUtensorMap* td = h->map(d_o, (uint64_t)T, (uint64_t)d, 128, 2);
+  const CUtensorMap* tdq = h->map(ws + L.dq, (uint64_t)T, (uint64_t)d, 32, 4);
+  if (!tq || !td || !tdq) return ESM_ERR_CUDA;
+  return cuda_status(launch_attention_window_bwd_tc(
+      tq, td, tdq, win, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), lse,
+      reinterpret_cast<float*>(ws + L.dsum), reinterpret_cast<float*>(ws + L.dq), ws + L.far,
+      static_cast<__nv_bfloat16*>(dqkv), T, num_seqs, d, h->cfg.heads, L.max_items, pb, nullptr, h->cfg.max_positions,
+      h->num_sms, h->d_err, st));
+}
+
+// ------------------------------------------------------------------ distillation
+esm_status esm_op_distill_loss_workspace_size(const esm_encoder_t* h, int total_tokens, int vocab, size_t* bytes) {
+  if (!h || !bytes || total_tokens < 0 || vocab <= 0) return ESM_ERR_INVALID_ARG;
+  *bytes = distill_workspace_bytes(total_tokens, vocab, h->num_sms);
+  return ESM_OK;
+}
+
+esm_status esm_op_distill_loss(esm_encoder_t* h, const void* logits, esm_precision logits_type, long long logits_stride,
+                               const int32_t* teacher_ids, const float* teacher_logits, int K, int total_tokens,
+                               int vocab, float temperature, float* token_loss, float* lse, float* loss_sum, int* count,
+                               void* workspace, size_t workspace_bytes, esm_stream_t stream) {
+  if (!h) return ESM_ERR_INVALID_ARG;
+  if (logits_type != ESM_FP32 && logits_type != ESM_BF16) return ESM_ERR_UNSUPPORTED;
+  DistillArgs a;
+  if (!distill_args(h, logits, logits_type, logits_stride, teacher_ids, teacher_logits, K, total_tokens, vocab,
+                    temperature, &a))
+    return ESM_ERR_INVALID_ARG;
+  if ((total_tokens > 0 && !token_loss) || !aligned(token_loss, 4) || !aligned(lse, 4) || !aligned(loss_sum, 4) ||
+      !aligned(count, 4))
+    return ESM_ERR_INVALID_ARG;
+  if ((loss_sum || count) && (!workspace || !aligned(workspace, 256) ||
+                              workspace_bytes < distill_workspace_bytes(total_tokens, vocab, h->num_sms)))
+    return ESM_ERR_WORKSPACE;
+  a.token_loss = token_loss;
+  a.lse = lse;
+  return cuda_status(launch_distill_loss(a, loss_sum, count, workspace, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+esm_status esm_op_distill_loss_backward(esm_encoder_t* h, const void* logits, esm_precision logits_type,
+                                        long long logits_stride, const int32_t* teacher_ids,
+                                        const float* teacher_logits, int K, int total_tokens, int vocab,
+                                        float temperature, const float* lse, const int* loss_count, void* d_logits,
+                                        long long d_stride, esm_stream_t stream) {
+  if (!h) return ESM_ERR_INVALID_ARG;
+  if (logits_type != ESM_FP32 && logits_type != ESM_BF16) return ESM_ERR_UNSUPPORTED;
+  DistillArgs a;
+  if (!distill_args(h, logits, logits_type, logits_stride, teacher_ids, teacher_logits, K, total_tokens, vocab,
+                    temperature, &a))
+    return ESM_ERR_INVALID_ARG;
+  if (d_stride < vocab || (d_logits == logits && d_stride != logits_stride)) return ESM_ERR_INVALID_ARG;
+  if ((total_tokens > 0 && (!lse || !d_logits)) || !aligned(lse, 4) || !aligned(loss_count, 4) ||
+      !aligned(d_logits, logits_type == ESM_FP32 ? 4 : 2))
+    return ESM_ERR_INVALID_ARG;
+  a.lse = const_cast<float*>(lse);
+  a.loss_count = loss_count;
+  a.d_logits = d_logits;
+  a.d_stride = d_stride;
+  return cuda_status(launch_distill_loss_backward(a, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 // ------------------------------------------------------------------ training
 esm_status esm_encoder_train_buffer_size(const esm_encoder_t* h, int max_tokens, size_t* bytes) {
   if (!h || !bytes || max_tokens < 0) return ESM_ERR_INVALID_ARG;
   if (h->cfg.precision != ESM_BF16 || h->cfg.hidden > 4096) return ESM_ERR_UNSUPPORTED;
-  *bytes = train_layout(h->cfg, max_tokens).total;
+  *bytes = train_layout(h->cfg, max_tokens, h->window).total;
   return ESM_OK;
 }
 
@@ -1452,7 +1742,7 @@ esm_status esm_encoder_forward_train(esm_encoder_t* h, const esm_weights* w, con
   if (!token_ids || !cu_seqlens || !hidden_out || !aligned(hidden_out, 16)) return ESM_ERR_INVALID_ARG;
   if (max_seqlen <= 0 || max_seqlen > h->cfg.max_positions) return ESM_ERR_INVALID_ARG;
   if (!weights_ok(h, w)) return ESM_ERR_INVALID_ARG;
-  if (!train_buf || !aligned(train_buf, 256) || train_bytes < train_layout(h->cfg, total_tokens).total)
+  if (!train_buf || !aligned(train_buf, 256) || train_bytes < train_layout(h->cfg, total_tokens, h->window).total)
     return ESM_ERR_WORKSPACE;
   h->train_buf = nullptr;  // valid again only once this forward is fully enqueued
   return train_forward_impl(h, w, token_ids, cu_seqlens, num_seqs, total_tokens, max_seqlen, hidden_out, train_buf,
@@ -1466,7 +1756,7 @@ esm_status esm_encoder_backward(esm_encoder_t* h, const esm_weights* w, const fl
   if (h->cfg.precision != ESM_BF16) return ESM_ERR_UNSUPPORTED;
   if (!weights_ok(h, w) || !grads_ok(h, grads)) return ESM_ERR_INVALID_ARG;
   if (h->train_T <= 0 || train_buf != h->train_buf || workspace != h->train_ws) return ESM_ERR_INVALID_ARG;
-  if (train_bytes < train_layout(h->cfg, h->train_T).total) return ESM_ERR_WORKSPACE;
+  if (train_bytes < train_layout(h->cfg, h->train_T, h->train_window).total) return ESM_ERR_WORKSPACE;
   if (workspace_bytes < h->layout(h->train_T, h->train_B).total) return ESM_ERR_WORKSPACE;
   return backward_impl(h, w, d_hidden_out, grads, train_buf, workspace, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -29,6 +29,13 @@ struct PackBuffers {
   int32_t* work_count; // [1]
 };
 
+// Attention window: query i sees key j if j <= i + right and (j >= i - left or j < sinks);
+// -1: that side is unlimited.  kFullWindow is attention to the whole sequence.
+using AttnWindow = esm_attn_window;
+constexpr AttnWindow kFullWindow{-1, -1, 0};
+// Largest number of sinks (they fit one key tile).
+constexpr int kMaxSinks = ESM_MAX_SINKS;
+
 // ---------------------------------------------------------------- launchers (pack.cu)
 void launch_pack_index(const int32_t* cu, int B, int T, int max_seqlen, int max_positions,
                        const PackBuffers& pb, unsigned* err, cudaStream_t st);
@@ -36,6 +43,10 @@ void launch_pad_index(const int32_t* seq_lens, int B, int S, const PackBuffers& 
                       cudaStream_t st);
 // Work items (segment, first query row) in tiles of q_tile rows, longest segments first.
 void launch_attn_worklist(int B, int max_items, int q_tile, const PackBuffers& pb, cudaStream_t st);
+// Segment table (seg_start, seg_qlen, seg_klen) and work items straight from cu_seqlens, validated
+// like launch_pack_index, without positions; items in batch order.
+void launch_attn_plan(const int32_t* cu, int B, int T, int max_seqlen, int max_positions, int q_tile, int max_items,
+                      const PackBuffers& pb, unsigned* err, cudaStream_t st);
 void launch_embed(const int32_t* tok, int T, const void* emb, bool emb_f32, int vocab, int d, float scale,
                   float* x, unsigned* err, cudaStream_t st);
 void launch_rope_table(float2* tab, int max_pos, int half, float base, cudaStream_t st);
@@ -193,8 +204,14 @@ bool encode_attention_qkv_map(const void* qkv, int total_tokens, int hidden, CUt
 cudaError_t launch_attention_tc(const CUtensorMap* tm_qkv, void* o, Act out, int d, int heads, int max_items,
                                 const PackBuffers& pb, const float* q_scale, float* amax, unsigned* err,
                                 cudaStream_t st, float* lse = nullptr, int lse_stride = 0);
+// The same with a window (win.sinks <= kMaxSinks): tm_qkv16 is a map over the same qkv with a
+// 64 x 16 box, qkv the buffer itself (16-byte aligned).
+cudaError_t launch_attention_window_tc(const CUtensorMap* tm_qkv, const CUtensorMap* tm_qkv16, const AttnWindow& win,
+                                       const void* qkv, void* o, Act out, int d, int heads, int max_items,
+                                       const PackBuffers& pb, const float* q_scale, float* amax, unsigned* err,
+                                       cudaStream_t st, float* lse = nullptr, int lse_stride = 0);
 void launch_attention_f32(const float* qkv, float* o, int d, int heads, int T, const PackBuffers& pb,
-                          cudaStream_t st);
+                          cudaStream_t st, const AttnWindow& win = kFullWindow);
 
 // tcgen05 attention backward (attention_bwd_tc.cu): dqkv (bf16 [T, 3d]) from the saved
 // qkv (RoPE applied), O, the forward's lse ([heads, T]) and dO (bf16 [T, d], tm_do a
@@ -207,6 +224,16 @@ cudaError_t launch_attention_bwd_tc(const CUtensorMap* tm_qkv, const CUtensorMap
                                     const __nv_bfloat16* dout, const float* lse, float* dsum, float* dq_acc,
                                     __nv_bfloat16* dqkv, int T, int d, int heads, int max_items, const PackBuffers& pb,
                                     const float2* rope, int max_pos, int num_sms, unsigned* err, cudaStream_t st);
+
+// The same with a window (win.sinks <= kMaxSinks); B sequences (pb.seg_*).  far: scratch of
+// attention_window_bwd_far_bytes bytes, 16-byte aligned (may be NULL when that is 0).
+size_t attention_window_bwd_far_bytes(const AttnWindow& w, int T, int heads);
+cudaError_t launch_attention_window_bwd_tc(const CUtensorMap* tm_qkv, const CUtensorMap* tm_do,
+                                           const CUtensorMap* tm_dq, const AttnWindow& win, const __nv_bfloat16* o,
+                                           const __nv_bfloat16* dout, const float* lse, float* dsum, float* dq_acc,
+                                           void* far, __nv_bfloat16* dqkv, int T, int B, int d, int heads,
+                                           int max_items, const PackBuffers& pb, const float2* rope, int max_pos,
+                                           int num_sms, unsigned* err, cudaStream_t st);
 
 // ---------------------------------------------------------------- backward.cu
 // Scratch floats for the column reductions of rows x cols (LayerNorm: two sums per column).
@@ -235,11 +262,42 @@ size_t lm_backward_partial_floats(int T, int V, int d);
 cudaError_t launch_lm_backward_head(const float* logits, const int32_t* targets, const int* count, const void* emb,
                                     const __nv_bfloat16* z, int T, int d, int V, float* dl, float* dz, float* demb,
                                     float* dbias, float* partial, int num_sms, cudaStream_t st);
+// The gradient stages after the logits: dz, demb and dbias from dl = dL/dlogits [T, V].
+cudaError_t launch_lm_backward_from_dlogits(const float* dl, const void* emb, const __nv_bfloat16* z, int T, int d,
+                                            int V, float* dz, float* demb, float* dbias, float* partial,
+                                            cudaStream_t st);
 // out[i] = sum_s partial[s * n + i] (split-K partial products, in split order).
 void launch_reduce_splits(const float* partial, int splits, size_t n, float* out, cudaStream_t st);
 // demb[v] = scale * sum over tokens t with tok[t] == v of dx[t] (float32 [vocab, d]).
 void launch_emb_bwd(const float* dx, const int32_t* tok, int T, int d, int vocab, float scale, float* partial,
                     float* demb, cudaStream_t st);
+
+// ---------------------------------------------------------------- distill.cu
+// Distillation from a teacher's top K <= kDistillMaxK logits per row.  logits [T, V] fp32 or
+// bf16, rows `stride` elements apart; teacher_ids / teacher_logits [T, K].  token_loss, lse
+// [T] (lse may be NULL in the forward).  Backward: lse of the forward, loss_count (device, NULL:
+// 1), d_logits of the logits' type, rows d_stride apart, possibly the logits themselves.
+constexpr int kDistillMaxK = ESM_DISTILL_MAX_K;
+struct DistillArgs {
+  const void* logits;
+  bool bf16;
+  long long stride;
+  const int32_t* teacher_ids;
+  const float* teacher_logits;
+  int K, T, V;
+  float temperature;
+  float* token_loss;
+  float* lse;
+  const int* loss_count;
+  void* d_logits;
+  long long d_stride;
+  unsigned* err;
+};
+// Scratch for the sums (loss_sum, count): 4-byte aligned.
+size_t distill_workspace_bytes(int T, int V, int num_sms);
+cudaError_t launch_distill_loss(const DistillArgs& a, float* loss_sum, int* count, void* workspace, int num_sms,
+                                cudaStream_t st);
+cudaError_t launch_distill_loss_backward(const DistillArgs& a, int num_sms, cudaStream_t st);
 
 // ---------------------------------------------------------------- fp8.cu
 // Quantise a bf16 tensor to e4m3 with *scale; record max|w| into *amax.

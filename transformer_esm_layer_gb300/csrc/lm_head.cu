@@ -443,15 +443,9 @@ size_t lm_backward_partial_floats(int T, int V, int d) {
   return chunks * V * (size_t)d + chunks * V;
 }
 
-cudaError_t launch_lm_backward_head(const float* logits, const int32_t* targets, const int* count, const void* emb,
-                                    const __nv_bfloat16* z, int T, int d, int V, float* dl, float* dz, float* demb,
-                                    float* dbias, float* partial, int num_sms, cudaStream_t st) {
-  if (T <= 0) {
-    cudaMemsetAsync(demb, 0, sizeof(float) * (size_t)V * d, st);
-    cudaMemsetAsync(dbias, 0, sizeof(float) * V, st);
-    return cudaGetLastError();
-  }
-  lm_dlogits_kernel<<<(T + 7) / 8, 256, 0, st>>>(logits, targets, count, T, V, dl);
+cudaError_t launch_lm_backward_from_dlogits(const float* dl, const void* emb, const __nv_bfloat16* z, int T, int d,
+                                            int V, float* dz, float* demb, float* dbias, float* partial,
+                                            cudaStream_t st) {
   const size_t smem = sizeof(float) * (size_t)V * (kDzCols + kDzTStride);
   cudaFuncSetAttribute(lm_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   lm_dz_kernel<<<dim3((d + kDzCols - 1) / kDzCols, (T + kDzTok - 1) / kDzTok), 256, smem, st>>>(
@@ -465,6 +459,18 @@ cudaError_t launch_lm_backward_head(const float* logits, const int32_t* targets,
   reduce_chunks(pe, chunks, (size_t)V * d, (size_t)V * d, 1.f, demb, st);
   reduce_chunks(pb, chunks, (size_t)V, (size_t)V, 1.f, dbias, st);
   return cudaGetLastError();
+}
+
+cudaError_t launch_lm_backward_head(const float* logits, const int32_t* targets, const int* count, const void* emb,
+                                    const __nv_bfloat16* z, int T, int d, int V, float* dl, float* dz, float* demb,
+                                    float* dbias, float* partial, int num_sms, cudaStream_t st) {
+  if (T <= 0) {
+    cudaMemsetAsync(demb, 0, sizeof(float) * (size_t)V * d, st);
+    cudaMemsetAsync(dbias, 0, sizeof(float) * V, st);
+    return cudaGetLastError();
+  }
+  lm_dlogits_kernel<<<(T + 7) / 8, 256, 0, st>>>(logits, targets, count, T, V, dl);
+  return launch_lm_backward_from_dlogits(dl, emb, z, T, d, V, dz, demb, dbias, partial, st);
 }
 
 size_t lm_logits_smem_bytes(int vocab, int hidden, bool bf16) { return (size_t)vocab * hidden * (bf16 ? 2 : 4); }

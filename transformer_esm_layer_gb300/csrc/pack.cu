@@ -134,6 +134,74 @@ __global__ void __launch_bounds__(WL_THREADS) attn_worklist_kernel(int B, int ma
   if (tid == 0) pb.work_count[0] = min(s_base, max_items);
 }
 
+// Single CTA: pack_index_kernel's validated segment table and attn_worklist_kernel's items in
+// one launch, for callers that need no positions.  A chunk of 1024 sequences at a time: their
+// tiles are scanned, then all threads write the chunk's items, each found by bisection.
+__global__ void __launch_bounds__(WL_THREADS) attn_plan_kernel(const int32_t* __restrict__ cu, int B, int T,
+                                                               int max_seqlen, int max_positions, int q_tile,
+                                                               int max_items, PackBuffers pb, unsigned* err) {
+  __shared__ int s_first[WL_THREADS + 1];  // items before the chunk's sequence i, within the chunk
+  __shared__ int s_start[WL_THREADS], s_len[WL_THREADS];
+  __shared__ int s_warp[WL_THREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  int base = 0;
+  for (int b0 = 0; b0 < B; b0 += WL_THREADS) {
+    const int i = b0 + tid;
+    int tiles = 0;
+    if (i < B) {
+      int c0 = cu[i], c1 = cu[i + 1];
+      const bool bad = (i == 0 && c0 != 0) || (i == B - 1 && c1 != T) || c1 < c0 || c1 - c0 > max_seqlen ||
+                       c1 - c0 > max_positions || c0 < 0 || c1 > T;
+      if (bad) {
+        latch_error(err, ERRBIT_CU_SEQLENS);
+        c0 = min(max(c0, 0), T);
+        c1 = min(min(max(c1, c0), T), c0 + max_positions);
+      }
+      const int L = c1 - c0;
+      pb.seg_start[i] = s_start[tid] = c0;
+      pb.seg_qlen[i] = pb.seg_klen[i] = s_len[tid] = L;
+      tiles = (L + q_tile - 1) / q_tile;
+    }
+    int v = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += n;
+    }
+    if (lane == 31) s_warp[wid] = v;
+    __syncthreads();
+    if (wid == 0) {
+      int w = s_warp[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += n;
+      }
+      s_warp[lane] = w;
+    }
+    __syncthreads();
+    v += wid > 0 ? s_warp[wid - 1] : 0;
+    s_first[tid] = v - tiles;
+    if (tid == WL_THREADS - 1) s_first[WL_THREADS] = v;
+    __syncthreads();
+    const int total = s_first[WL_THREADS];
+    for (int k = tid; k < total && base + k < max_items; k += WL_THREADS) {
+      int lo = 0, hi = WL_THREADS;  // the last sequence with s_first <= k (it has tiles)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_first[mid] <= k) lo = mid;
+        else hi = mid;
+      }
+      const int off = (k - s_first[lo]) * q_tile;
+      reinterpret_cast<int4*>(pb.work)[base + k] =
+          make_int4(s_start[lo] + off, min(q_tile, s_len[lo] - off), s_start[lo], s_len[lo]);
+    }
+    base += total;
+    __syncthreads();
+  }
+  if (tid == 0) pb.work_count[0] = min(base, max_items);
+}
+
 // x[t, :] = scale * E[tok[t], :] into the fp32 residual stream; one warp per token,
 // 16-byte loads and stores.  Ids outside [0, vocab) latch ERRBIT_TOKEN and read row 0.
 template <bool F32>
@@ -216,6 +284,11 @@ void launch_pad_index(const int32_t* seq_lens, int B, int S, const PackBuffers& 
 
 void launch_attn_worklist(int B, int max_items, int q_tile, const PackBuffers& pb, cudaStream_t st) {
   attn_worklist_kernel<<<1, WL_THREADS, 0, st>>>(B, max_items, q_tile, pb);
+}
+
+void launch_attn_plan(const int32_t* cu, int B, int T, int max_seqlen, int max_positions, int q_tile, int max_items,
+                      const PackBuffers& pb, unsigned* err, cudaStream_t st) {
+  attn_plan_kernel<<<1, WL_THREADS, 0, st>>>(cu, B, T, max_seqlen, max_positions, q_tile, max_items, pb, err);
 }
 
 void launch_embed(const int32_t* tok, int T, const void* emb, bool emb_f32, int vocab, int d, float scale, float* x,
