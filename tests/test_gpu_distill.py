@@ -73,7 +73,9 @@ def _run(enc, logits, ids, tl, t, **kw):
 
 CASES = [(1, 1, 1, 0, 0), (5, 2, 3, 0, 0), (300, 33, 8, 0, 0), (77, 33, 33, 31, 5), (64, 64, 256, 0, 0), (9, 65, 40, 3, 1),
          (50, 255, 20, 1, 1), (33, 256, 7, 0, 0), (33, 257, 7, 0, 0), (17, 1000, 100, 24, 8), (40, 4099, 64, 0, 0),
-         (3, 32000, 32, 0, 0), (2, 131071, 256, 2, 1), (2000, 40, 1, 0, 0), (1300, 700, 5, 0, 0)]
+         (3, 32000, 32, 0, 0), (2, 131071, 256, 2, 1), (2000, 40, 1, 0, 0), (1300, 700, 5, 0, 0),
+         # more rows than resident blocks: a warp per row, with two and with eight entries per lane
+         (1000, 300, 64, 3, 1), (900, 2049, 65, 0, 0), (700, 16000, 256, 7, 3), (650, 5000, 33, 0, 0)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -260,6 +262,23 @@ def test_streams_graphs_and_repeatability(enc):
             assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(dd, d)
 
 
+def test_a_workspace_of_its_own_on_another_stream(enc):
+    """Calls on a side stream that allocate their scratch themselves, beside work of the current
+    stream that frees and reuses memory of the same sizes."""
+    _, logits, ids, tl = _case(3000, 33, 8, torch.float32, 8)
+    want = _run(enc, logits, ids, tl, 1.0)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [[torch.zeros_like(x) for x in want] for _ in range(20)]
+    torch.cuda.synchronize()
+    for g in got:
+        enc.op_distill_loss(logits, ids, tl, 1.0, g[0], g[1], loss_sum=g[2], count=g[3], stream=st)
+        enc.op_distill_loss_workspace(3000, 33).fill_(255)
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
 def test_refusals(enc):
     from transformer_esm_layer_gb300.binding import EsmError
     _, z, ids, tl = _case(8, 40, 4, torch.float32, 7)
@@ -289,6 +308,9 @@ def test_refusals(enc):
     for dd in (d.bfloat16(), d[:4], d.t().contiguous().t(), d.cpu()):
         with pytest.raises(ValueError):
             enc.op_distill_loss_backward(z, ids, tl, 1.0, lse, dd)
+    for ws in (torch.empty(4096, dtype=torch.uint8), torch.empty(8192, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            enc.op_distill_loss(z, ids, tl, 1.0, loss, count=count, workspace=ws)
     with pytest.raises(ValueError):
         enc.op_distill_loss(z, ids, tl, 1.0, loss[:4])
     with pytest.raises(ValueError):

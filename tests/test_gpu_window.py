@@ -385,6 +385,9 @@ def test_refusals():
         enc.op_attention_window_backward(qkv, o, lse, o, cu, 300, (1, 1, 0), torch.empty_like(qkv),
                                          workspace=enc.op_attention_window_workspace(300, 1, (1, 1, 0)))
     assert e.value.status == 5
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 21, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            enc.op_attention_window(qkv, cu, 300, (1, 1, 0), o, workspace=ws)
     for bad in (dict(o=o.float()), dict(o=o[:299]), dict(o=o.t().contiguous().t()), dict(lse=lse.double()),
                 dict(lse=lse.t().contiguous()), dict(o=o.cpu())):
         args = dict(o=o, lse=lse)

@@ -11,6 +11,7 @@ import os
 from typing import Dict, Optional, Sequence
 
 import numpy as np
+import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libesm_encoder.so")
@@ -176,25 +177,61 @@ def _ptr(t) -> Optional[int]:
 
 def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
-        import torch
         stream = torch.cuda.current_stream()
     return stream.cuda_stream or None
+
+
+def _refuse(where: str, what: str):
+    raise ValueError(f"{where}: {what}")
 
 
 def _need(ok, where: str, what: str):
     """Arguments the C side cannot check (it sees only addresses)."""
     if not ok:
-        raise ValueError(f"{where}: {what}")
+        _refuse(where, what)
 
 
 def _check_tensor(t, where: str, name: str, dtype, shape, device):
-    """A contiguous tensor of this type and shape on this CUDA device (shape None: any)."""
-    import torch
+    """A contiguous tensor of this type and shape (a tuple, or None for any) on this CUDA device.
+
+    One expression decides and the message is put together only for a refusal: an operator of a
+    few microseconds has several tensors to check in every call."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_cuda
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return
     _need(isinstance(t, torch.Tensor) and t.is_cuda, where, f"{name} must be a CUDA tensor")
     _need(t.device == device, where, f"{name} must be on {device}")
     _need(t.dtype == dtype, where, f"{name} must be {dtype}")
-    _need(shape is None or tuple(t.shape) == tuple(shape), where, f"{name} must be {shape and list(shape)}")
-    _need(t.is_contiguous(), where, f"{name} must be contiguous")
+    _need(shape is None or t.shape == shape, where, f"{name} must be {shape and list(shape)}")
+    _refuse(where, f"{name} must be contiguous")
+
+
+def _check_scalar(t, where: str, name: str, dtype, device):
+    _check_tensor(t, where, name, dtype, None, device)
+    if t.numel() != 1:
+        _refuse(where, f"{name} must hold one value")
+
+
+def _launch_stream(where: str, stream, device) -> Optional[int]:
+    """The stream of a launch on `device`'s tensors: the current one unless given.  The kernels run
+    on the current device, so that must be the tensors'."""
+    if torch.cuda.current_device() != device.index:
+        _refuse(where, f"the tensors' device {device} must be the current one")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index) or None
+    _need(stream.device == device, where, "stream must be on the tensors' device")
+    return stream.cuda_stream or None
+
+
+def _allocating(stream):
+    """Context for what a call allocates itself: memory of the launch stream, so that neither its
+    last use (on another stream, perhaps still running) nor its next one overlaps this call's."""
+    return torch.cuda.stream(stream)
+
+
+def _check_workspace(t, where: str, device):
+    if not (isinstance(t, torch.Tensor) and t.device == device and t.is_contiguous()):
+        _refuse(where, f"workspace must be a contiguous tensor on {device}")
 
 
 def _window_struct(window) -> EsmAttnWindow:
@@ -208,7 +245,6 @@ class DeviceWeights:
     ``w`` is the dict returned by synth.model_weights (float32 arrays)."""
 
     def __init__(self, w: Dict, precision: str, device="cuda"):
-        import torch
         dt = torch.float32 if precision == "fp32" else torch.bfloat16
         to = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(device=device, dtype=dt)
         self.emb = to(w["emb"])
@@ -233,7 +269,6 @@ class DeviceGrads:
     struct (esm_encoder_backward overwrites them)."""
 
     def __init__(self, g, num_layers: int, device="cuda"):
-        import torch
         z = lambda *shape: torch.empty(*shape, dtype=torch.float32, device=device)
         d, f = g.hidden, g.ffn
         shapes = {"ln1_g": (d,), "ln1_b": (d,), "w_qkv": (3 * d, d), "b_qkv": (3 * d,), "w_o": (d, d), "b_o": (d,),
@@ -263,7 +298,6 @@ class DeviceLmHead:
     struct; ``w`` is the dict of synth.lm_head_weights (its "emb" is the tied embedding)."""
 
     def __init__(self, w: Dict, precision: str, device="cuda"):
-        import torch
         dt = torch.float32 if precision == "fp32" else torch.bfloat16
         to = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(device=device, dtype=dt)
         self.t = {k: to(w[k]) for k in ("dense_w", "dense_b", "ln_g", "ln_b", "emb", "bias")}
@@ -311,7 +345,6 @@ class EsmEncoder:
     # ------------------------------------------------------------------ buffers
     @property
     def out_dtype(self):
-        import torch
         return torch.float32 if self.precision == "fp32" else torch.bfloat16
 
     def workspace_size(self, max_tokens: int, max_seqs: int) -> int:
@@ -321,13 +354,11 @@ class EsmEncoder:
         return n.value
 
     def workspace(self, max_tokens: int, max_seqs: int, device="cuda"):
-        import torch
         return torch.empty(self.workspace_size(max_tokens, max_seqs), dtype=torch.uint8, device=device)
 
     # ------------------------------------------------------------------ calls
     def forward(self, weights: DeviceWeights, token_ids, cu_seqlens, max_seqlen: int, out=None, workspace=None,
                 stream=None, check: bool = False):
-        import torch
         T = token_ids.numel()
         B = cu_seqlens.numel() - 1
         if out is None:
@@ -356,7 +387,6 @@ class EsmEncoder:
 
     def forward_padded(self, weights: DeviceWeights, token_ids, seq_lens, out=None, workspace=None, stream=None,
                        check: bool = False):
-        import torch
         B, S = token_ids.shape
         if out is None:
             out = torch.empty(B, S, self.hidden, dtype=self.out_dtype, device=token_ids.device)
@@ -380,7 +410,6 @@ class EsmEncoder:
         return self.lib.esm_encoder_check(self.handle, _stream_ptr(stream))
 
     def debug_pack_index(self, cu_seqlens, total_tokens: int, max_seqlen: int, workspace=None, stream=None):
-        import torch
         B = cu_seqlens.numel() - 1
         pos = torch.empty(max(total_tokens, 1), dtype=torch.int32, device=cu_seqlens.device)
         seg = torch.empty_like(pos)
@@ -442,7 +471,6 @@ class EsmEncoder:
         self._raise(self.lib.esm_encoder_set_attention_window(self.handle, w), "esm_encoder_set_attention_window")
 
     def op_attention_window_workspace(self, T: int, B: int, window, backward: bool = False, device="cuda"):
-        import torch
         n = ctypes.c_size_t()
         self._raise(self.lib.esm_op_attention_window_workspace_size(self.handle, T, B,
                                                                     ctypes.byref(_window_struct(window)),
@@ -451,55 +479,61 @@ class EsmEncoder:
         return torch.empty(int(n.value), dtype=torch.uint8, device=device)
 
     def _check_packed(self, where: str, qkv, cu_seqlens):
-        import torch
+        """q | k | v and offsets of a packed batch; returns its tokens and sequences."""
         _need(isinstance(qkv, torch.Tensor) and qkv.dim() == 2, where, "qkv must be a 2-D tensor")
-        _check_tensor(qkv, where, "qkv", self.out_dtype, (qkv.shape[0], 3 * self.hidden), qkv.device)
+        T = qkv.shape[0]
+        _check_tensor(qkv, where, "qkv", self.out_dtype, (T, 3 * self.hidden), qkv.device)
         _check_tensor(cu_seqlens, where, "cu_seqlens", torch.int32, None, qkv.device)
         _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2, where, "cu_seqlens must hold at least two offsets")
+        return T, cu_seqlens.numel() - 1
 
     def op_attention_window(self, qkv, cu_seqlens, max_seqlen: int, window, o, lse=None, workspace=None, stream=None):
         """esm_op_attention_window: attention of packed q | k | v [T, 3*hidden] under a window
         (left, right, sinks), -1 = unlimited: query i sees key j of its sequence if j <= i + right
         and (j >= i - left or j < sinks).  Writes o [T, hidden] and, if given, lse float32 [heads, T]."""
-        import torch
         where = "op_attention_window"
-        self._check_packed(where, qkv, cu_seqlens)
-        T, B = qkv.shape[0], cu_seqlens.numel() - 1
-        _check_tensor(o, where, "o", self.out_dtype, (T, self.hidden), qkv.device)
+        T, B = self._check_packed(where, qkv, cu_seqlens)
+        dev = qkv.device
+        _check_tensor(o, where, "o", qkv.dtype, (T, self.hidden), dev)
         if lse is not None:
-            _check_tensor(lse, where, "lse", torch.float32, (self.cfg.heads, T), qkv.device)
+            _check_tensor(lse, where, "lse", torch.float32, (self.cfg.heads, T), dev)
+        st = _launch_stream(where, stream, dev)
         if workspace is None:
-            workspace = self.op_attention_window_workspace(T, B, window, device=qkv.device)
-        self._raise(self.lib.esm_op_attention_window(self.handle, _ptr(qkv), _ptr(cu_seqlens), B, T, int(max_seqlen),
-                                                     ctypes.byref(_window_struct(window)), _ptr(o), _ptr(lse),
-                                                     _ptr(workspace), workspace.numel(), _stream_ptr(stream)),
-                    "esm_op_attention_window")
+            with _allocating(stream):
+                workspace = self.op_attention_window_workspace(T, B, window, device=dev)
+        _check_workspace(workspace, where, dev)
+        self._raise(self.lib.esm_op_attention_window(self.handle, qkv.data_ptr(), cu_seqlens.data_ptr(), B, T,
+                                                     int(max_seqlen), ctypes.byref(_window_struct(window)),
+                                                     o.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                                                     workspace.nbytes, st), "esm_op_attention_window")
         return o
 
     def op_attention_window_backward(self, qkv, o, lse, d_o, cu_seqlens, max_seqlen: int, window, dqkv,
                                      workspace=None, stream=None):
         """esm_op_attention_window_backward: dqkv [T, 3*hidden] (bf16) from the forward's qkv, o and
         lse under the same window and d_o = dL/do."""
-        import torch
         where = "op_attention_window_backward"
-        self._check_packed(where, qkv, cu_seqlens)
-        T, B = qkv.shape[0], cu_seqlens.numel() - 1
-        for name, t in (("o", o), ("d_o", d_o)):
-            _check_tensor(t, where, name, torch.bfloat16, (T, self.hidden), qkv.device)
-        _check_tensor(lse, where, "lse", torch.float32, (self.cfg.heads, T), qkv.device)
-        _check_tensor(dqkv, where, "dqkv", torch.bfloat16, (T, 3 * self.hidden), qkv.device)
+        T, B = self._check_packed(where, qkv, cu_seqlens)
+        dev, hidden = qkv.device, (T, self.hidden)
+        _check_tensor(o, where, "o", torch.bfloat16, hidden, dev)
+        _check_tensor(d_o, where, "d_o", torch.bfloat16, hidden, dev)
+        _check_tensor(lse, where, "lse", torch.float32, (self.cfg.heads, T), dev)
+        _check_tensor(dqkv, where, "dqkv", torch.bfloat16, (T, 3 * self.hidden), dev)
+        st = _launch_stream(where, stream, dev)
         if workspace is None:
-            workspace = self.op_attention_window_workspace(T, B, window, backward=True, device=qkv.device)
-        self._raise(self.lib.esm_op_attention_window_backward(self.handle, _ptr(qkv), _ptr(o), _ptr(lse), _ptr(d_o),
-                                                              _ptr(cu_seqlens), B, T, int(max_seqlen),
-                                                              ctypes.byref(_window_struct(window)), _ptr(dqkv),
-                                                              _ptr(workspace), workspace.numel(), _stream_ptr(stream)),
+            with _allocating(stream):
+                workspace = self.op_attention_window_workspace(T, B, window, backward=True, device=dev)
+        _check_workspace(workspace, where, dev)
+        self._raise(self.lib.esm_op_attention_window_backward(self.handle, qkv.data_ptr(), o.data_ptr(),
+                                                              lse.data_ptr(), d_o.data_ptr(), cu_seqlens.data_ptr(),
+                                                              B, T, int(max_seqlen),
+                                                              ctypes.byref(_window_struct(window)), dqkv.data_ptr(),
+                                                              workspace.data_ptr(), workspace.nbytes, st),
                     "esm_op_attention_window_backward")
         return dqkv
 
     # ------------------------------------------------------------------ distillation
     def op_distill_loss_workspace(self, T: int, vocab: int, device="cuda"):
-        import torch
         n = ctypes.c_size_t()
         self._raise(self.lib.esm_op_distill_loss_workspace_size(self.handle, T, vocab, ctypes.byref(n)),
                     "esm_op_distill_loss_workspace_size")
@@ -507,16 +541,19 @@ class EsmEncoder:
 
     @staticmethod
     def _check_distill(where: str, logits, teacher_ids, teacher_logits):
-        import torch
+        """Logits and teacher entries; returns the logits' esm_precision, rows, columns, row stride
+        (a single row may report any stride) and the entries per row."""
         _need(isinstance(logits, torch.Tensor) and logits.is_cuda, where, "logits must be a CUDA tensor")
-        _need(logits.dtype in (torch.float32, torch.bfloat16), where, "logits must be float32 or bfloat16")
+        f32 = logits.dtype is torch.float32
+        _need(f32 or logits.dtype is torch.bfloat16, where, "logits must be float32 or bfloat16")
         _need(logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1), where,
               "logits must be 2-D with contiguous rows")
-        T = logits.shape[0]
+        T, V = logits.shape
         _need(isinstance(teacher_ids, torch.Tensor) and teacher_ids.dim() == 2, where, "teacher_ids must be [T, K]")
-        shape = (T, teacher_ids.shape[1])
-        _check_tensor(teacher_ids, where, "teacher_ids", torch.int32, shape, logits.device)
-        _check_tensor(teacher_logits, where, "teacher_logits", torch.float32, shape, logits.device)
+        shape, dev = (T, teacher_ids.shape[1]), logits.device
+        _check_tensor(teacher_ids, where, "teacher_ids", torch.int32, shape, dev)
+        _check_tensor(teacher_logits, where, "teacher_logits", torch.float32, shape, dev)
+        return PRECISIONS["fp32" if f32 else "bf16"], T, V, EsmEncoder._row_stride(logits), shape[1]
 
     @staticmethod
     def _row_stride(t) -> int:
@@ -529,25 +566,26 @@ class EsmEncoder:
         (float32 or bf16, rows may be strided), into token_loss [T]; optionally the rows' lse [T]
         (for the backward) and the sum and number of scored rows (device scalars).  teacher_ids
         int32, teacher_logits float32 [T, K]; id -1: unused entry."""
-        import torch
         where = "op_distill_loss"
-        self._check_distill(where, logits, teacher_ids, teacher_logits)
-        T, V = logits.shape
-        _check_tensor(token_loss, where, "token_loss", torch.float32, (T,), logits.device)
+        kind, T, V, stride, K = self._check_distill(where, logits, teacher_ids, teacher_logits)
+        dev = logits.device
+        _check_tensor(token_loss, where, "token_loss", torch.float32, (T,), dev)
         if lse is not None:
-            _check_tensor(lse, where, "lse", torch.float32, (T,), logits.device)
-        for name, t, dt in (("loss_sum", loss_sum, torch.float32), ("count", count, torch.int32)):
-            if t is not None:
-                _check_tensor(t, where, name, dt, None, logits.device)
-                _need(t.numel() == 1, where, f"{name} must hold one value")
+            _check_tensor(lse, where, "lse", torch.float32, (T,), dev)
+        if loss_sum is not None:
+            _check_scalar(loss_sum, where, "loss_sum", torch.float32, dev)
+        if count is not None:
+            _check_scalar(count, where, "count", torch.int32, dev)
+        st = _launch_stream(where, stream, dev)
         if workspace is None and (loss_sum is not None or count is not None):
-            workspace = self.op_distill_loss_workspace(T, V, logits.device)
-        self._raise(self.lib.esm_op_distill_loss(self.handle, _ptr(logits),
-                                                 PRECISIONS["fp32" if logits.dtype == torch.float32 else "bf16"],
-                                                 self._row_stride(logits), _ptr(teacher_ids), _ptr(teacher_logits),
-                                                 teacher_ids.shape[1], T, V, float(temperature), _ptr(token_loss),
-                                                 _ptr(lse), _ptr(loss_sum), _ptr(count), _ptr(workspace),
-                                                 0 if workspace is None else workspace.numel(), _stream_ptr(stream)),
+            with _allocating(stream):
+                workspace = self.op_distill_loss_workspace(T, V, dev)
+        if workspace is not None:
+            _check_workspace(workspace, where, dev)
+        self._raise(self.lib.esm_op_distill_loss(self.handle, logits.data_ptr(), kind, stride, teacher_ids.data_ptr(),
+                                                 teacher_logits.data_ptr(), K, T, V, float(temperature),
+                                                 token_loss.data_ptr(), _ptr(lse), _ptr(loss_sum), _ptr(count),
+                                                 _ptr(workspace), 0 if workspace is None else workspace.nbytes, st),
                     "esm_op_distill_loss")
         return token_loss
 
@@ -555,26 +593,21 @@ class EsmEncoder:
                                  loss_count=None, stream=None):
         """esm_op_distill_loss_backward: d_logits (the logits' type; may be logits itself) of the
         sum of token_loss divided by loss_count (device int32 scalar; None: of the sum)."""
-        import torch
         where = "op_distill_loss_backward"
-        self._check_distill(where, logits, teacher_ids, teacher_logits)
-        T, V = logits.shape
-        _check_tensor(lse, where, "lse", torch.float32, (T,), logits.device)
-        _need(isinstance(d_logits, torch.Tensor) and d_logits.device == logits.device
-              and d_logits.dtype == logits.dtype and d_logits.shape == logits.shape
-              and (d_logits.stride(1) == 1 or V == 1), where,
+        kind, T, V, stride, K = self._check_distill(where, logits, teacher_ids, teacher_logits)
+        dev = logits.device
+        _check_tensor(lse, where, "lse", torch.float32, (T,), dev)
+        _need(isinstance(d_logits, torch.Tensor) and d_logits.device == dev and d_logits.dtype is logits.dtype
+              and d_logits.shape == logits.shape and (d_logits.stride(1) == 1 or V == 1), where,
               "d_logits must have the type, device and shape of logits, and contiguous rows")
         if loss_count is not None:
-            _check_tensor(loss_count, where, "loss_count", torch.int32, None, logits.device)
-            _need(loss_count.numel() == 1, where, "loss_count must hold one value")
-        self._raise(self.lib.esm_op_distill_loss_backward(self.handle, _ptr(logits),
-                                                          PRECISIONS["fp32" if logits.dtype == torch.float32
-                                                                     else "bf16"],
-                                                          self._row_stride(logits), _ptr(teacher_ids),
-                                                          _ptr(teacher_logits), teacher_ids.shape[1], T, V,
-                                                          float(temperature), _ptr(lse), _ptr(loss_count),
-                                                          _ptr(d_logits), self._row_stride(d_logits),
-                                                          _stream_ptr(stream)), "esm_op_distill_loss_backward")
+            _check_scalar(loss_count, where, "loss_count", torch.int32, dev)
+        self._raise(self.lib.esm_op_distill_loss_backward(self.handle, logits.data_ptr(), kind, stride,
+                                                          teacher_ids.data_ptr(), teacher_logits.data_ptr(), K, T, V,
+                                                          float(temperature), lse.data_ptr(), _ptr(loss_count),
+                                                          d_logits.data_ptr(), self._row_stride(d_logits),
+                                                          _launch_stream(where, stream, dev)),
+                    "esm_op_distill_loss_backward")
         return d_logits
 
     def set_layer_precision(self, per_layer):
@@ -584,7 +617,6 @@ class EsmEncoder:
                     "esm_encoder_set_layer_precision")
 
     def lm_head_workspace(self, T: int, device="cuda"):
-        import torch
         n = ctypes.c_size_t()
         self._raise(self.lib.esm_encoder_lm_head_workspace_size(self.handle, T, ctypes.byref(n)),
                     "esm_encoder_lm_head_workspace_size")
@@ -604,7 +636,6 @@ class EsmEncoder:
 
     # ------------------------------------------------------------------ training
     def train_buffer(self, max_tokens: int, device="cuda"):
-        import torch
         n = ctypes.c_size_t()
         self._raise(self.lib.esm_encoder_train_buffer_size(self.handle, max_tokens, ctypes.byref(n)),
                     "esm_encoder_train_buffer_size")
@@ -613,7 +644,6 @@ class EsmEncoder:
     def forward_train(self, weights: DeviceWeights, token_ids, cu_seqlens, max_seqlen: int, train_buf, workspace,
                       out=None, stream=None):
         """esm_encoder_forward_train: the forward, keeping its activations in train_buf."""
-        import torch
         T = token_ids.numel()
         B = cu_seqlens.numel() - 1
         if out is None:
@@ -634,7 +664,6 @@ class EsmEncoder:
         return grads
 
     def op_gemm_dgrad(self, dY, W, out, stream=None):
-        import torch
         M, N = dY.shape
         K = W.shape[1]
         self._raise(self.lib.esm_op_gemm_dgrad(self.handle, _ptr(dY), _ptr(W), _ptr(out),
@@ -643,7 +672,6 @@ class EsmEncoder:
         return out
 
     def op_gemm_wgrad(self, dY, X, dW, workspace=None, stream=None):
-        import torch
         M, N = dY.shape
         K = X.shape[1]
         if workspace is None:
@@ -657,7 +685,6 @@ class EsmEncoder:
         return dW
 
     def op_layernorm_backward(self, x, gamma, dy, dres, dx, dgamma, dbeta, stream=None):
-        import torch
         rows, cols = x.shape
         n = ctypes.c_size_t()
         self._raise(self.lib.esm_op_layernorm_backward_workspace_size(self.handle, rows, cols, ctypes.byref(n)),
@@ -680,7 +707,6 @@ class EsmEncoder:
 
     def op_attention_backward(self, qkv, o, lse, d_o, cu_seqlens, max_seqlen: int, dqkv, workspace=None,
                               stream=None):
-        import torch
         T = qkv.shape[0]
         B = cu_seqlens.numel() - 1
         if workspace is None:
@@ -695,7 +721,6 @@ class EsmEncoder:
         return dqkv
 
     def lm_head_backward_workspace(self, T: int, device="cuda"):
-        import torch
         n = ctypes.c_size_t()
         self._raise(self.lib.esm_encoder_lm_head_backward_workspace_size(self.handle, T, ctypes.byref(n)),
                     "esm_encoder_lm_head_backward_workspace_size")
@@ -707,7 +732,6 @@ class EsmEncoder:
         gradients (dict of float32 device tensors shaped like the head's parameters) of the
         mean masked-LM loss.  ``loss_count`` (device int32 scalar): the scored-token count the
         mean divides by, e.g. the global batch's in data-parallel training (None: this call's)."""
-        import torch
         T = hidden.shape[0]
         dev = hidden.device
         if d_hidden is None:
@@ -729,24 +753,35 @@ class EsmEncoder:
                                  loss_count=None):
         """esm_encoder_lm_head_distill_backward: as lm_head_backward, for the distillation loss
         against a teacher's top logits (teacher_ids int32, teacher_logits float32 [T, K])."""
-        import torch
         where = "lm_head_distill_backward"
-        T = hidden.shape[0]
-        dev = hidden.device
+        _need(isinstance(hidden, torch.Tensor) and hidden.dim() == 2, where, "hidden must be a 2-D tensor")
+        T, dev = hidden.shape[0], hidden.device
+        _check_tensor(hidden, where, "hidden", self.out_dtype, (T, self.hidden), dev)
         _need(isinstance(teacher_ids, torch.Tensor) and teacher_ids.dim() == 2, where, "teacher_ids must be [T, K]")
-        _check_tensor(teacher_ids, where, "teacher_ids", torch.int32, (T, teacher_ids.shape[1]), dev)
-        _check_tensor(teacher_logits, where, "teacher_logits", torch.float32, tuple(teacher_ids.shape), dev)
-        if d_hidden is None:
-            d_hidden = torch.empty(T, self.hidden, dtype=torch.float32, device=dev)
-        if grads is None:
-            grads = {k: torch.empty(tuple(head.t[k].shape), dtype=torch.float32, device=dev) for k in LM_HEAD_NAMES}
-        if workspace is None:
-            workspace = self.lm_head_backward_workspace(T, dev)
+        K = teacher_ids.shape[1]
+        _check_tensor(teacher_ids, where, "teacher_ids", torch.int32, (T, K), dev)
+        _check_tensor(teacher_logits, where, "teacher_logits", torch.float32, (T, K), dev)
+        for name, t, dt in (("loss_sum", loss_sum, torch.float32), ("count", count, torch.int32),
+                            ("loss_count", loss_count, torch.int32)):
+            if t is not None:
+                _check_scalar(t, where, name, dt, dev)
+        st = _launch_stream(where, stream, dev)
+        with _allocating(stream):
+            if d_hidden is None:
+                d_hidden = torch.empty(T, self.hidden, dtype=torch.float32, device=dev)
+            if grads is None:
+                grads = {k: torch.empty_like(head.t[k], dtype=torch.float32) for k in LM_HEAD_NAMES}
+            if workspace is None:
+                workspace = self.lm_head_backward_workspace(T, dev)
+        _check_tensor(d_hidden, where, "d_hidden", torch.float32, (T, self.hidden), dev)
+        for k in LM_HEAD_NAMES:
+            _check_tensor(grads[k], where, f"grads[{k!r}]", torch.float32, head.t[k].shape, dev)
+        _check_workspace(workspace, where, dev)
         gs = EsmLmHeadGrads(*[grads[k].data_ptr() for k in LM_HEAD_NAMES])
         self._raise(self.lib.esm_encoder_lm_head_distill_backward(
-            self.handle, ctypes.byref(head.struct), _ptr(hidden), T, _ptr(teacher_ids), _ptr(teacher_logits),
-            teacher_ids.shape[1], float(temperature), _ptr(d_hidden), ctypes.byref(gs), _ptr(loss_sum), _ptr(count),
-            _ptr(loss_count), _ptr(workspace), workspace.numel(), _stream_ptr(stream)),
+            self.handle, ctypes.byref(head.struct), hidden.data_ptr(), T, teacher_ids.data_ptr(),
+            teacher_logits.data_ptr(), K, float(temperature), d_hidden.data_ptr(), ctypes.byref(gs), _ptr(loss_sum),
+            _ptr(count), _ptr(loss_count), workspace.data_ptr(), workspace.nbytes, st),
             "esm_encoder_lm_head_distill_backward")
         return d_hidden, grads
 
@@ -754,7 +789,6 @@ class EsmEncoder:
         """esm_op_quantize_nvfp4 of a contiguous bf16 [rows, cols] CUDA tensor: returns (codes uint8
         [rows, cols/2], scales uint8 [rows * cols / 16] in the tensor-core atom order, amax and
         scale as float32 one-element tensors)."""
-        import torch
         rows, cols = x.shape
         codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
         scales = torch.empty(rows * cols // 16, dtype=torch.uint8, device=x.device)
@@ -769,7 +803,6 @@ class EsmEncoder:
         v = (A B^T) / (S_A S_B) + bias, then the epilogue `epi` ("bias_f32": float32 out = v;
         "residual": float32 out += v; "gelu": bf16 out = GELU(v); "qkv_rope": bf16 out = v with
         RoPE at the rows' positions pos_id)."""
-        import torch
         (ac, asf, _, asc), (bc, bsf, _, bsc) = a, b
         M, N, K = ac.shape[0], bc.shape[0], 2 * ac.shape[1]
         if out is None:
@@ -833,7 +866,6 @@ def op_attention_noalloc(qkv, cu_seqlens, max_seqlen: int, hidden: int, heads: i
     tensor of one element that receives the call's device-side outcome (ESM_OK,
     ESM_ERR_BAD_CU_SEQLENS or ESM_ERR_TIMEOUT).  Raises ValueError on tensors the C side
     cannot check (wrong dtype, device, layout or shape); returns the call's status code."""
-    import torch
 
     def need(ok, what):
         if not ok:
@@ -858,7 +890,6 @@ def op_attention_noalloc(qkv, cu_seqlens, max_seqlen: int, hidden: int, heads: i
 
 def packed_inputs(tokens: np.ndarray, lengths: Sequence[int], device="cuda"):
     """Device token ids and cu_seqlens (int32) for a packed batch."""
-    import torch
     from .synth import cu_seqlens_from_lengths
     tok = torch.from_numpy(np.ascontiguousarray(tokens, dtype=np.int32)).to(device)
     cu = torch.from_numpy(cu_seqlens_from_lengths(lengths)).to(device)
