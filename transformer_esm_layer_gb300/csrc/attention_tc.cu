@@ -31,14 +31,6 @@
 //               back to the TMA warp.
 // Tensor memory: S 128 columns, P 64 (bf16 pairs), O 64 -> 256 columns per CTA.  Every
 // mbarrier wait is bounded.
-//
-// Windowed form (WIN): query i of a sequence sees key j if j <= i + right and (j >= i - left
-// or j < sinks).  A query tile's keys are then the list [sinks | lo .. hi), with lo .. hi the
-// band that any of its rows sees: first the sink rows, padded to a multiple of 16, then the
-// band.  The key tiles are 128 consecutive entries of that list, so a few sinks cost their
-// 16-row groups and not a tile of their own; the one tile that holds both is fetched as eight
-// 16-row boxes.  A tile that every row of a warp sees whole takes the unmasked path; in the
-// others each row's visible columns are two runs, [0, cs) and [cl, ch), applied as bits.
 #include "common.cuh"
 #include "internal.h"
 
@@ -102,68 +94,30 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 
 struct Item {
   int qrow0, qrows, krow0, klen, nkb, h;
-  // windowed: position of the first query in its sequence, sink rows and their padded count
-  // at the front of the key list, first band key (all positions in the sequence)
-  int qpos0, nsink, s16, lo;
 };
 
 // Work item `it` = (work-list entry it / heads, head it % heads); one 16-byte load.
 __device__ __forceinline__ int4 load_item(const PackBuffers& pb, int it, int heads) {
   return __ldg(reinterpret_cast<const int4*>(pb.work) + it / heads);
 }
-template <bool WIN>
-__device__ __forceinline__ Item make_item(int4 w, int it, int heads, const AttnWindow& win) {
+__device__ __forceinline__ Item make_item(int4 w, int it, int heads) {
   Item x;
   x.h = it % heads;
   x.qrow0 = w.x;
   x.qrows = w.y;
   x.krow0 = w.z;
   x.klen = w.w;
-  if constexpr (WIN) {
-    x.qpos0 = x.qrow0 - x.krow0;
-    x.lo = win.left < 0 ? 0 : max(0, x.qpos0 - win.left);
-    // sinks that reach the band make one run with it
-    if (win.sinks >= x.lo) x.lo = 0;
-    x.nsink = x.lo > 0 ? min(win.sinks, x.klen) : 0;
-    x.s16 = (x.nsink + 15) & ~15;
-    const int hi = win.right < 0 ? x.klen : min(x.klen, x.qpos0 + x.qrows + win.right);
-    // at least one tile, so that rows that see nothing (padding queries far past the last key)
-    // pass through the same pipeline
-    x.nkb = max(1, (x.s16 + max(0, hi - x.lo) + KT - 1) / KT);
-  } else {
-    x.nkb = (x.klen + KT - 1) / KT;
-  }
+  x.nkb = (x.klen + KT - 1) / KT;
   return x;
-}
-
-// The low n bits set (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t low_bits(int n) {
-  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
-// Key tile j of a windowed item: entries 128 j .. of [sinks (s16 rows) | band from lo].
-__device__ __forceinline__ void load_window_tile(uint8_t* dst, const CUtensorMap* tm, const CUtensorMap* tm16, int xcol,
-                                                 const Item& x, int j, uint64_t* bar) {
-  const int c0 = j * KT;
-  if (c0 >= x.s16) {
-    tma_load_2d(dst, tm, xcol, x.krow0 + x.lo + c0 - x.s16, bar);
-  } else if (c0 + KT <= x.s16) {
-    tma_load_2d(dst, tm, xcol, x.krow0 + c0, bar);
-  } else {  // c0 == 0 (at most 128 sinks): s16 sink rows, then the band's first rows
-#pragma unroll 1
-    for (int r = 0; r < KT; r += 16)
-      tma_load_2d(dst + r * 128, tm16, xcol, x.krow0 + (r < x.s16 ? r : x.lo + r - x.s16), bar);
-  }
 }
 
 // AMAX: a bf16 output also records its max |value| into amax_out (compiled only into the
 // instantiation that needs it, so the others keep their registers).
-template <Act OUT, bool AMAX, bool WIN>
-__device__ __forceinline__ void attention_tc_body(const CUtensorMap& tm, const CUtensorMap& tm16,
-                                                  const AttnWindow& win, const __nv_bfloat16* __restrict__ qkv,
-                                                  void* __restrict__ o, int d, int heads,
-                                                  const PackBuffers& pb, const float* q_scale, float* amax_out,
-                                                  float* __restrict__ lse, int lse_stride, unsigned* err) {
+template <Act OUT, bool AMAX = false>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
+    attention_tc_kernel(const __grid_constant__ CUtensorMap tm, void* __restrict__ o, int d, int heads,
+                        PackBuffers pb, const float* q_scale, float* amax_out, float* __restrict__ lse,
+                        int lse_stride, unsigned* err) {
   const int n_items = *pb.work_count * heads;
   if ((int)blockIdx.x >= n_items) return;  // whole CTA, before any barrier or TMEM use
 
@@ -217,7 +171,7 @@ __device__ __forceinline__ void attention_tc_body(const CUtensorMap& tm, const C
       int g = 0, qi = 0;
       int4 nxt = load_item(pb, item_at(0), heads);
       for (int rnd = 0, it = item_at(0); it < n_items && !sm->abort; it = item_at(++rnd), ++qi) {
-        const Item x = make_item<WIN>(nxt, it, heads, win);
+        const Item x = make_item(nxt, it, heads);
         if (item_at(rnd + 1) < n_items) nxt = load_item(pb, item_at(rnd + 1), heads);  // prefetch
         if (kq) {
           const int qb = qi & 1;
@@ -241,10 +195,7 @@ __device__ __forceinline__ void attention_tc_body(const CUtensorMap& tm, const C
             break;
           }
           mbar_arrive_expect_tx(&full[st], TILE_BYTES);
-          if constexpr (WIN)
-            load_window_tile(dst0 + 2 * st * TILE_BYTES, &tm, &tm16, xcol, x, j, &full[st]);
-          else
-            tma_load_2d(dst0 + 2 * st * TILE_BYTES, &tm, xcol, x.krow0 + j * KT, &full[st]);
+          tma_load_2d(dst0 + 2 * st * TILE_BYTES, &tm, xcol, x.krow0 + j * KT, &full[st]);
         }
       }
       // Copies still in flight can only exist if a consumer gave up early: then the last
@@ -273,7 +224,7 @@ __device__ __forceinline__ void attention_tc_body(const CUtensorMap& tm, const C
       int g = 0, qi = 0;
       int4 nxt = load_item(pb, item_at(0), heads);
       for (int rnd = 0, it = item_at(0); it < n_items && ok && !sm->abort; it = item_at(++rnd), ++qi) {
-        const Item x = make_item<WIN>(nxt, it, heads, win);
+        const Item x = make_item(nxt, it, heads);
         if (item_at(rnd + 1) < n_items) nxt = load_item(pb, item_at(rnd + 1), heads);  // prefetch
         const int qb = qi & 1;
         for (int j = 0; j < x.nkb; ++j, ++g) {
@@ -338,7 +289,7 @@ __device__ __forceinline__ void attention_tc_body(const CUtensorMap& tm, const C
     int g = 0, qi = 0;
     int4 nxt = load_item(pb, item_at(0), heads);
     for (int rnd = 0, it = item_at(0); it < n_items && ok; it = item_at(++rnd), ++qi) {
-      const Item x = make_item<WIN>(nxt, it, heads, win);
+      const Item x = make_item(nxt, it, heads);
       if (item_at(rnd + 1) < n_items) nxt = load_item(pb, item_at(rnd + 1), heads);  // prefetch
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < x.nkb; ++j, ++g) {
@@ -358,24 +309,8 @@ __device__ __forceinline__ void attention_tc_body(const CUtensorMap& tm, const C
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->s_free);
-        if constexpr (WIN) {
-          // columns [0, cs) (sinks) and [cl, ch) (band) of this row's tile are visible
-          const int q = x.qpos0 + r;
-          const int base = x.s16 - x.lo - j * KT;  // column of key position 0
-          const int end = win.right < 0 ? x.klen : min(x.klen, q + win.right + 1);
-          const int cl = (win.left < 0 ? 0 : max(x.lo, q - win.left)) + base, ch = end + base;
-          const int cs = x.lo > 0 ? x.nsink - j * KT : min(win.sinks, end) - j * KT;
-          if (!__all_sync(0xffffffffu, cl <= 0 && ch >= KT)) {
-#pragma unroll
-            for (int w = 0; w < KT / 32; ++w) {
-              const uint32_t vis = low_bits(cs - 32 * w) | (low_bits(ch - 32 * w) & ~low_bits(cl - 32 * w));
-#pragma unroll
-              for (int i = 0; i < 32; ++i) sv[32 * w + i] = (vis >> i & 1u) ? sv[32 * w + i] : -INFINITY;
-            }
-          }
-        }
         const int kvalid = x.klen - j * KT;  // keys >= kvalid lie past the sequence end
-        if (!WIN && kvalid < KT) {
+        if (kvalid < KT) {
 #pragma unroll
           for (int i = 0; i < KT; ++i) sv[i] = i < kvalid ? sv[i] : -INFINITY;
         }
@@ -396,9 +331,7 @@ __device__ __forceinline__ void attention_tc_body(const CUtensorMap& tm, const C
         // P = 2^(s*c - m) (hardware ex2) as bf16 pairs, computed while the previous P V may
         // still be reading the P columns
         // (scale-subtract and row sums two scores per f32x2 instruction)
-        // (a row that has seen no key yet has m = -inf: 2^(-inf - 0) = 0 for all its keys)
-        const float nm = WIN && m_ref == -INFINITY ? 0.f : -m_ref;
-        const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(nm, nm);
+        const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_ref, -m_ref);
         uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
         uint32_t w[KT / 32][16];
 #pragma unroll
@@ -453,22 +386,7 @@ __device__ __forceinline__ void attention_tc_body(const CUtensorMap& tm, const C
       tmem_ld_wait_regs(u[0]);
       tmem_ld_wait_regs(u[1]);
       tc_fence_before();
-      float inv = 1.f / l;
-      bool redo = false;
-      if constexpr (WIN) {
-        // A row that sees no key is zero.  A zero weight times an infinite or NaN value is NaN,
-        // so values that a row does not see could reach it through the tile's product: a row
-        // whose sum is not finite is set aside and summed over its visible keys alone below.
-        float probe = 0.f;
-#pragma unroll
-        for (int i = 0; i < DH; ++i) probe = fmaf(__uint_as_float(u[i >> 5][i & 31]), 0.f, probe);
-        redo = probe != 0.f && l != 0.f && r < x.qrows;
-        if (probe != 0.f || l == 0.f) {
-#pragma unroll
-          for (int i = 0; i < DH; ++i) u[i >> 5][i & 31] = 0u;
-        }
-        if (l == 0.f) inv = 0.f;
-      }
+      const float inv = 1.f / l;
       // training forward: the natural-log softmax normaliser of this row and head (scores
       // scaled by 1/sqrt(dh)), ln 2 * (m + log2 l) in the base-2 units used above
       if (lse != nullptr && r < x.qrows) lse[(size_t)x.h * lse_stride + x.qrow0 + r] = 0.6931471805599453f * (m_ref + log2f(l));
@@ -508,40 +426,6 @@ __device__ __forceinline__ void attention_tc_body(const CUtensorMap& tm, const C
         }
       }
       __syncwarp();
-      if constexpr (WIN) {
-        // (rare) whole warp per set-aside row: lane c holds head columns 2c and 2c + 1
-        for (unsigned todo = __ballot_sync(0xffffffffu, redo); todo != 0u; todo &= todo - 1) {
-          const int src = __ffs(todo) - 1, row = wq * 32 + src, q = x.qpos0 + row;
-          const float m = __shfl_sync(0xffffffffu, m_ref, src), scale = __shfl_sync(0xffffffffu, inv, src);
-          const int end = win.right < 0 ? x.klen : min(x.klen, q + win.right + 1);
-          const int lo = win.left < 0 ? 0 : max(0, q - win.left), ns = min(win.sinks, min(lo, end));
-          const __nv_bfloat16* seq = qkv + (size_t)x.krow0 * 3 * d + x.h * DH + 2 * lane;
-          const float2 qv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(seq + (size_t)q * 3 * d));
-          float2 acc = make_float2(0.f, 0.f);
-          for (int j = 0; j < ns + max(0, end - lo); ++j) {
-            const __nv_bfloat16* kr = seq + (size_t)(j < ns ? j : lo + j - ns) * 3 * d + d;
-            const float2 kv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(kr));
-            const float2 vv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(kr + d));
-            float s = fmaf(qv.x, kv.x, qv.y * kv.y);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            const float p = fast_exp2(fmaf(s, c, -m));
-            acc.x = fmaf(p, vv.x, acc.x);
-            acc.y = fmaf(p, vv.y, acc.y);
-          }
-          acc.x *= scale;
-          acc.y *= scale;
-          if constexpr (OUT == Act::E4M3 || AMAX) amax = fmaxf(amax, fmaxf(fabsf(acc.x), fabsf(acc.y)));
-          if constexpr (OUT == Act::BF16) {
-            *reinterpret_cast<uint32_t*>(stage + stage_off(row, lane >> 2) + 4 * (lane & 3)) = pack_bf16x2(acc.x, acc.y);
-          } else {
-            __nv_fp8x2_e4m3 qv8(make_float2(acc.x * qs, acc.y * qs));
-            *reinterpret_cast<uint16_t*>(stage + stage_off(row, lane >> 3) + 2 * (lane & 7)) =
-                *reinterpret_cast<uint16_t*>(&qv8);
-          }
-        }
-        __syncwarp();
-      }
       {
         constexpr int kRowsPerInst = 32 / kUnits;
         constexpr size_t kElem = (OUT == Act::BF16) ? 2 : 1;
@@ -581,88 +465,47 @@ __device__ __forceinline__ void attention_tc_body(const CUtensorMap& tm, const C
   }
 }
 
-template <Act OUT, bool AMAX = false>
-__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
-    attention_tc_kernel(const __grid_constant__ CUtensorMap tm, void* __restrict__ o, int d, int heads,
-                        PackBuffers pb, const float* q_scale, float* amax_out, float* __restrict__ lse,
-                        int lse_stride, unsigned* err) {
-  attention_tc_body<OUT, AMAX, false>(tm, tm, AttnWindow{-1, -1, 0}, nullptr, o, d, heads, pb, q_scale, amax_out, lse,
-                                      lse_stride, err);
-}
-
-template <Act OUT, bool AMAX = false>
-__global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
-    attention_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm16,
-                               AttnWindow win, const __nv_bfloat16* __restrict__ qkv, void* __restrict__ o, int d,
-                               int heads, PackBuffers pb, const float* q_scale, float* amax_out,
-                               float* __restrict__ lse, int lse_stride, unsigned* err) {
-  attention_tc_body<OUT, AMAX, true>(tm, tm16, win, qkv, o, d, heads, pb, q_scale, amax_out, lse, lse_stride, err);
-}
-
 }  // namespace
 
 int attention_tc_smem_bytes() { return SMEM_BYTES; }
 
-namespace {
-
-// Persistent grid: at most CTAS_PER_SM CTAs per SM; CTAs past the (device-side) item count exit.
-unsigned attention_grid(int max_items, int heads) {
+cudaError_t launch_attention_tc(const CUtensorMap* tm_qkv, void* o, Act out, int d, int heads, int max_items,
+                                const PackBuffers& pb, const float* q_scale, float* amax, unsigned* err,
+                                cudaStream_t st, float* lse, int lse_stride) {
+  if (max_items <= 0) return cudaSuccess;
   static int num_sms = 0;
+  static bool configured[3] = {false, false, false};
+  const int which = out == Act::E4M3 ? 1 : (amax != nullptr ? 2 : 0);
+  if (!configured[which]) {
+    cudaError_t e = which == 1 ? cudaFuncSetAttribute(attention_tc_kernel<Act::E4M3>,
+                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)
+                    : which == 2 ? cudaFuncSetAttribute(attention_tc_kernel<Act::BF16, true>,
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)
+                                 : cudaFuncSetAttribute(attention_tc_kernel<Act::BF16>,
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    configured[which] = true;
+  }
   if (num_sms == 0) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || num_sms <= 0)
       num_sms = 148;
   }
+  // persistent: at most CTAS_PER_SM CTAs per SM; CTAs past the (device-side) item count exit
   const long long items = (long long)max_items * heads;
   const long long cap = (long long)CTAS_PER_SM * num_sms;
-  return (unsigned)(items < cap ? items : cap);
-}
-
-template <typename K>
-cudaError_t configure_smem(K kernel, bool* done) {
-  if (*done) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  *done = e == cudaSuccess;
-  return e;
-}
-
-}  // namespace
-
-cudaError_t launch_attention_tc(const CUtensorMap* tm_qkv, void* o, Act out, int d, int heads, int max_items,
-                                const PackBuffers& pb, const float* q_scale, float* amax, unsigned* err,
-                                cudaStream_t st, float* lse, int lse_stride) {
-  if (max_items <= 0) return cudaSuccess;
-  static bool configured[3] = {false, false, false};
-  const unsigned grid = attention_grid(max_items, heads);
-  auto run = [&](auto kernel, int which) -> cudaError_t {
-    const cudaError_t e = configure_smem(kernel, &configured[which]);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, THREADS, SMEM_BYTES, st>>>(*tm_qkv, o, d, heads, pb, q_scale, amax, lse, lse_stride, err);
-    return cudaGetLastError();
-  };
-  if (out == Act::E4M3) return run(attention_tc_kernel<Act::E4M3>, 1);
-  if (amax != nullptr) return run(attention_tc_kernel<Act::BF16, true>, 2);
-  return run(attention_tc_kernel<Act::BF16>, 0);
-}
-
-cudaError_t launch_attention_window_tc(const CUtensorMap* tm_qkv, const CUtensorMap* tm_qkv16, const AttnWindow& win,
-                                       const void* qkv, void* o, Act out, int d, int heads, int max_items,
-                                       const PackBuffers& pb, const float* q_scale, float* amax, unsigned* err,
-                                       cudaStream_t st, float* lse, int lse_stride) {
-  if (max_items <= 0) return cudaSuccess;
-  static bool configured[3] = {false, false, false};
-  const unsigned grid = attention_grid(max_items, heads);
-  auto run = [&](auto kernel, int which) -> cudaError_t {
-    const cudaError_t e = configure_smem(kernel, &configured[which]);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, THREADS, SMEM_BYTES, st>>>(*tm_qkv, *tm_qkv16, win, static_cast<const __nv_bfloat16*>(qkv), o, d,
-                                              heads, pb, q_scale, amax, lse, lse_stride, err);
-    return cudaGetLastError();
-  };
-  if (out == Act::E4M3) return run(attention_window_tc_kernel<Act::E4M3>, 1);
-  if (amax != nullptr) return run(attention_window_tc_kernel<Act::BF16, true>, 2);
-  return run(attention_window_tc_kernel<Act::BF16>, 0);
+  const unsigned grid = (unsigned)(items < cap ? items : cap);
+  if (which == 1)
+    attention_tc_kernel<Act::E4M3><<<grid, THREADS, SMEM_BYTES, st>>>(*tm_qkv, o, d, heads, pb, q_scale, amax, lse,
+                                                                      lse_stride, err);
+  else if (which == 2)
+    attention_tc_kernel<Act::BF16, true><<<grid, THREADS, SMEM_BYTES, st>>>(*tm_qkv, o, d, heads, pb, q_scale, amax,
+                                                                            lse, lse_stride, err);
+  else
+    attention_tc_kernel<Act::BF16><<<grid, THREADS, SMEM_BYTES, st>>>(*tm_qkv, o, d, heads, pb, q_scale, amax, lse,
+                                                                      lse_stride, err);
+  return cudaGetLastError();
 }
 
 }  // namespace esm
