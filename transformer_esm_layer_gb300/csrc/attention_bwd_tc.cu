@@ -33,17 +33,6 @@
 //                memory and adds it into an fp32 accumulator in global memory with TMA
 //                reduce-add (several key tiles contribute to each query row).
 // Every mbarrier wait is bounded; on timeout the kernel latches an error bit and stops.
-//
-// Windowed form (WIN; key j visible to query i if j <= i + right and (j >= i - left or
-// j < sinks)): a key tile's query tiles start at the first query that sees any of its keys and
-// end behind the last, so each key row's visible queries are one run of columns.  The keys
-// of the first tile that are sinks are seen by every later query.  The tile itself goes on
-// kFarStart queries past its band; the queries behind that, of a long sequence, are cut into
-// chunks of kFarQueries, each a work item of its own with the same key tile, so that no one
-// CTA walks the whole sequence.  Such chunks and the tile itself leave the sinks' dK and dV as
-// fp32 partial sums in slots, which a last kernel adds in slot order.  Slot 0 of a sequence
-// that starts at row s0 is s0 / kFarSlotTokens: a sequence long enough to have chunks spans more
-// slots than it uses, so no list of them is needed.
 #include "common.cuh"
 #include "internal.h"
 
@@ -125,77 +114,27 @@ __device__ __forceinline__ float ld_nc_early(const float* p) {
   return v;
 }
 
-// Windowed form: queries past the first key tile's band that its own item still takes, queries
-// of a chunk item, and tokens per slot.  A sequence has chunks from length
-// 128 + left + 1 + kFarStart on, and 1 + ceil((L - kFarStart) / kFarQueries) <= L / kFarSlotTokens
-// slots from there.
-constexpr int kFarStart = 1024, kFarQueries = 2048, kFarSlotTokens = 512;
-
-// Keys k0 .. k0 + krows - 1 (rows of the packed batch) of the sequence at row s0; its queries
-// q0 .. q1 - 1 (positions in the sequence) in nq tiles.  slot: where the sinks' fp32 partial
-// sums go (-1: nowhere, the gradients are written whole); far: a chunk item.
 struct BItem {
-  int k0, krows, s0, h, q0, q1, nq, slot;
-  bool far;
+  int k0, krows, s0, slen, h, nq;
 };
-
-// Far chunks of the batch: count, then (s0, length, first query, slot) each.
-struct FarList {
-  const int32_t* count;
-  const int4* item;
-  float* partial;  // [slot][heads][sinks][dK 64 | dV 64]
-};
-
-template <bool WIN>
-__device__ __forceinline__ BItem bitem(const PackBuffers& pb, int it, int heads, const AttnWindow& win,
-                                       const FarList& fl, int n_far) {
+__device__ __forceinline__ BItem bitem(const PackBuffers& pb, int it, int heads) {
+  const int4 w = __ldg(reinterpret_cast<const int4*>(pb.work) + it / heads);
   BItem x;
   x.h = it % heads;
-  x.slot = -1;
-  x.far = false;
-  if constexpr (WIN) {
-    if (it < n_far) {  // the chunks first: they are the longest items
-      const int4 w = __ldg(fl.item + it / heads);
-      x.k0 = x.s0 = w.x;
-      x.krows = win.sinks;
-      x.q0 = w.z;
-      x.q1 = min(w.y, w.z + kFarQueries);
-      x.nq = (x.q1 - x.q0 + TB - 1) / TB;
-      x.slot = w.w;
-      x.far = true;
-      return x;
-    }
-    it -= n_far;
-  }
-  const int4 w = __ldg(reinterpret_cast<const int4*>(pb.work) + it / heads);
   x.k0 = w.x;
   x.krows = w.y;
   x.s0 = w.z;
-  x.q0 = 0;
-  x.q1 = w.w;
-  if constexpr (WIN) {
-    const int p0 = w.x - w.z;
-    if (win.right >= 0) x.q0 = max(0, p0 - win.right);
-    if (win.left >= 0) {
-      const int far0 = TB + win.left + 1 + kFarStart;
-      x.q1 = min(w.w, p0 < win.sinks ? far0 : p0 + w.y + win.left);
-      if (p0 < win.sinks && w.w > far0) x.slot = w.z / kFarSlotTokens;
-    }
-  }
-  x.nq = (x.q1 - x.q0 + TB - 1) / TB;
+  x.slen = w.w;
+  x.nq = (w.w + TB - 1) / TB;
   return x;
 }
 
-template <bool WIN>
-__device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv, const CUtensorMap& tm_do,
-                                                      const CUtensorMap& tm_dq, const AttnWindow& win,
-                                                      const FarList& fl, const float* __restrict__ lse,
-                                                      const float* __restrict__ dsum,
-                                                      __nv_bfloat16* __restrict__ dqkv, int T, int d, int heads,
-                                                      const PackBuffers& pb, const float2* __restrict__ rope,
-                                                      int max_pos, unsigned* err) {
-  const int n_far = WIN && fl.count != nullptr ? *fl.count * heads : 0;
-  const int n_items = *pb.work_count * heads + n_far;
+__global__ void __launch_bounds__(THREADS, 1)
+    attention_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do,
+                            const __grid_constant__ CUtensorMap tm_dq, const float* __restrict__ lse,
+                            const float* __restrict__ dsum, __nv_bfloat16* __restrict__ dqkv, int T, int d, int heads,
+                            PackBuffers pb, const float2* __restrict__ rope, int max_pos, unsigned* err) {
+  const int n_items = *pb.work_count * heads;
   if ((int)blockIdx.x >= n_items) return;  // whole CTA, before any barrier or TMEM use
 
   extern __shared__ uint8_t smem_raw[];
@@ -238,7 +177,7 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
       tma_prefetch_desc(&tm_do);
       int g = 0, n = 0;
       for (int it = blockIdx.x; it < n_items && !sm->abort; it += gridDim.x, ++n) {
-        const BItem x = bitem<WIN>(pb, it, heads, win, fl, n_far);
+        const BItem x = bitem(pb, it, heads);
         if (!mbar_wait(&sm->kv_empty, (uint32_t)(n & 1) ^ 1u)) { latch_error(err, ERRBIT_TIMEOUT); sm->abort = 1; break; }
         mbar_arrive_expect_tx(&sm->kv_full, 2 * TILE);
         tma_load_2d(base + OFF_K, &tm_qkv, d + x.h * DH, x.k0, &sm->kv_full);
@@ -251,8 +190,8 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
             break;
           }
           mbar_arrive_expect_tx(&sm->q_full[st], 2 * TILE);
-          tma_load_2d(base + OFF_Q + st * TILE, &tm_qkv, x.h * DH, x.s0 + x.q0 + i * TB, &sm->q_full[st]);
-          tma_load_2d(base + OFF_DO + st * TILE, &tm_do, x.h * DH, x.s0 + x.q0 + i * TB, &sm->q_full[st]);
+          tma_load_2d(base + OFF_Q + st * TILE, &tm_qkv, x.h * DH, x.s0 + i * TB, &sm->q_full[st]);
+          tma_load_2d(base + OFF_DO + st * TILE, &tm_do, x.h * DH, x.s0 + i * TB, &sm->q_full[st]);
         }
       }
     }
@@ -298,7 +237,7 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
         return true;
       };
       for (int it = blockIdx.x; it < n_items && ok && !sm->abort; it += gridDim.x, ++n) {
-        const BItem x = bitem<WIN>(pb, it, heads, win, fl, n_far);
+        const BItem x = bitem(pb, it, heads);
         if (!mbar_wait(&sm->kv_full, (uint32_t)n & 1u)) { ok = false; break; }
         for (int i = 0; i < x.nq; ++i, ++g) {
           const int st = g & 1;
@@ -359,8 +298,8 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
         const int q = QPW * wg + 32 * k + lane;
         nl[k] = 0.f;
         nd[k] = 0.f;
-        if (q < min(TB, y.q1 - y.q0 - i * TB)) {
-          const size_t at = (size_t)y.h * T + y.s0 + y.q0 + i * TB + q;
+        if (q < min(TB, y.slen - i * TB)) {
+          const size_t at = (size_t)y.h * T + y.s0 + i * TB + q;
           nl[k] = ld_nc_early(lse + at);
           nd[k] = ld_nc_early(dsum + at);
         }
@@ -369,20 +308,12 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
     float nl_next[KS], nd_next[KS];
 #pragma unroll
     for (int k = 0; k < KS; ++k) nl_next[k] = nd_next[k] = 0.f;
-    if ((int)blockIdx.x < n_items) stat(bitem<WIN>(pb, blockIdx.x, heads, win, fl, n_far), 0, nl_next, nd_next);
+    if ((int)blockIdx.x < n_items) stat(bitem(pb, blockIdx.x, heads), 0, nl_next, nd_next);
     for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x, ++n) {
-      const BItem x = bitem<WIN>(pb, it, heads, win, fl, n_far);
+      const BItem x = bitem(pb, it, heads);
       const bool kval = r < x.krows;
       for (int i = 0; i < x.nq; ++i, ++g) {
-        const int qvalid = min(TB, x.q1 - x.q0 - i * TB);
-        // windowed: the queries (columns) [cl, ch) of the tile see this thread's key
-        int cl = 0, ch = qvalid;
-        if constexpr (WIN) {
-          const int key = x.k0 - x.s0 + r, first = x.q0 + i * TB;
-          if (win.right >= 0) cl = key - win.right - first;
-          if (win.left >= 0 && key >= win.sinks) ch = min(ch, key + win.left + 1 - first);
-          if (!kval) ch = 0;
-        }
+        const int qvalid = min(TB, x.slen - i * TB);
         __syncwarp();  // the warp is done reading the previous tile's slot
 #pragma unroll
         for (int k = 0; k < KS; ++k) {  // (the loads return lse and D; stored negated, lse in log2 units)
@@ -391,12 +322,12 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
         }
         __syncwarp();
         if (i + 1 < x.nq) stat(x, i + 1, nl_next, nd_next);
-        else if (it + (int)gridDim.x < n_items) stat(bitem<WIN>(pb, it + gridDim.x, heads, win, fl, n_far), 0, nl_next, nd_next);
+        else if (it + (int)gridDim.x < n_items) stat(bitem(pb, it + gridDim.x, heads), 0, nl_next, nd_next);
         if (!mbar_wait_warp(&sm->s_full, (uint32_t)g & 1u)) { ok = false; break; }
         tc_fence_after();
         // P^T and dS^T of this thread's key and QPW queries, as bf16 pairs, 16 queries at a time:
         // t = s c - lse (log2 units), p = 2^t, ds = p (dp - D), in f32x2 pairs
-        const bool full = WIN ? (bool)__all_sync(0xffffffffu, cl <= 0 && ch >= TB) : kval && qvalid == TB;
+        const bool full = kval && qvalid == TB;
         uint32_t pw[NSUB][8], dw[NSUB][8];
 #pragma unroll
         for (int sub = 0; sub < NSUB; ++sub) {
@@ -418,13 +349,8 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
               float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
               if (!full) {
                 const int q = cq + 2 * j;
-                if constexpr (WIN) {
-                  p0 = (q >= cl && q < ch) ? p0 : 0.f;
-                  p1 = (q + 1 >= cl && q + 1 < ch) ? p1 : 0.f;
-                } else {
-                  p0 = (kval && q < qvalid) ? p0 : 0.f;
-                  p1 = (kval && q + 1 < qvalid) ? p1 : 0.f;
-                }
+                p0 = (kval && q < qvalid) ? p0 : 0.f;
+                p1 = (kval && q + 1 < qvalid) ? p1 : 0.f;
               }
               const uint64_t pp = f2_pack(p0, p1);
               const uint64_t dd = f2_mul(pp, f2_add(f2_pack(dp[2 * j], dp[2 * j + 1]),
@@ -480,18 +406,6 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
           if (lane == 0) mbar_arrive(&sm->acc_free);
         }
         if (!kval) continue;
-        if constexpr (WIN) {
-          if (x.slot >= 0 && (x.far || r < win.sinks)) {  // a sink's partial sums, fp32
-            float* dst = fl.partial + (((size_t)x.slot * heads + x.h) * win.sinks + r) * (2 * DH) + (is_k ? 0 : DH) + c0;
-            float* dst2 = dst + (is_k ? 32 : 16);
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              *reinterpret_cast<float4*>(dst + j) = make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]);
-              *reinterpret_cast<float4*>(dst2 + j) = make_float4(b[j], b[j + 1], b[j + 2], b[j + 3]);
-            }
-            continue;
-          }
-        }
         if (is_k) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {  // pair (c0 + j, c0 + j + 32) turned back by its angle
@@ -544,7 +458,7 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
     bool ok = true;
     int g = 0;
     for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x) {
-      const BItem x = bitem<WIN>(pb, it, heads, win, fl, n_far);
+      const BItem x = bitem(pb, it, heads);
       for (int i = 0; i < x.nq; ++i, ++g) {
         if (!mbar_wait_warp(&sm->dq_full, (uint32_t)g & 1u)) { ok = false; break; }
         tc_fence_after();
@@ -568,7 +482,7 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          const int row = x.s0 + x.q0 + i * TB + wq * 32;
+          const int row = x.s0 + i * TB + wq * 32;
           tma_reduce_add_2d(&tm_dq, x.h * DH, row, stage);
           tma_reduce_add_2d(&tm_dq, x.h * DH + 32, row, stage + 4096);
           bulk_commit();
@@ -588,104 +502,6 @@ __device__ __forceinline__ void attention_bwd_tc_body(const CUtensorMap& tm_qkv,
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
-  }
-}
-
-__global__ void __launch_bounds__(THREADS, 1)
-    attention_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do,
-                            const __grid_constant__ CUtensorMap tm_dq, const float* __restrict__ lse,
-                            const float* __restrict__ dsum, __nv_bfloat16* __restrict__ dqkv, int T, int d, int heads,
-                            PackBuffers pb, const float2* __restrict__ rope, int max_pos, unsigned* err) {
-  attention_bwd_tc_body<false>(tm_qkv, tm_do, tm_dq, AttnWindow{-1, -1, 0}, FarList{}, lse, dsum, dqkv, T, d, heads, pb, rope,
-                               max_pos, err);
-}
-
-__global__ void __launch_bounds__(THREADS, 1)
-    attention_window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_qkv,
-                                   const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dq,
-                                   AttnWindow win, FarList fl, const float* __restrict__ lse,
-                                   const float* __restrict__ dsum, __nv_bfloat16* __restrict__ dqkv, int T, int d,
-                                   int heads, PackBuffers pb, const float2* __restrict__ rope, int max_pos,
-                                   unsigned* err) {
-  attention_bwd_tc_body<true>(tm_qkv, tm_do, tm_dq, win, fl, lse, dsum, dqkv, T, d, heads, pb, rope, max_pos, err);
-}
-
-// Far chunks a batch can have (each needs more than 1024 tokens of its sequence), and slots.
-int far_max_chunks(int T) { return T / kFarStart; }
-int far_max_slots(int T) { return T / kFarSlotTokens + 1; }
-
-// Lists the far chunks of the batch in sequence order; one CTA.
-__global__ void __launch_bounds__(1024) attention_far_list_kernel(const int32_t* __restrict__ seg_start,
-                                                                  const int32_t* __restrict__ seg_len, int B, int far0,
-                                                                  int max_chunks, int32_t* count, int4* item) {
-  __shared__ int warp_sum[32];
-  __shared__ int base;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  if (threadIdx.x == 0) base = 0;
-  __syncthreads();
-  for (int b0 = 0; b0 < B; b0 += 1024) {
-    const int b = b0 + threadIdx.x;
-    const int s0 = b < B ? seg_start[b] : 0, len = b < B ? seg_len[b] : 0;
-    const int n = len > far0 ? (len - far0 + kFarQueries - 1) / kFarQueries : 0;
-    int v = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) warp_sum[wid] = v;
-    __syncthreads();
-    if (wid == 0) {
-      int w = warp_sum[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += u;
-      }
-      warp_sum[lane] = w;
-    }
-    __syncthreads();
-    const int at = base + (wid > 0 ? warp_sum[wid - 1] : 0) + v - n;
-    for (int k = 0; k < n && at + k < max_chunks; ++k)
-      item[at + k] = make_int4(s0, len, far0 + k * kFarQueries, s0 / kFarSlotTokens + 1 + k);
-    __syncthreads();
-    if (threadIdx.x == 1023) base = at + n;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) *count = min(base, max_chunks);
-}
-
-// dK and dV of the sinks of sequences with far chunks: the slots' fp32 sums in slot order, dK
-// scaled and turned back through RoPE, as bf16.  A block per (sequence, head), a thread per pair
-// (j, j + 32) of a sink row (threads 0..31: dK, 32..63: dV).
-__global__ void __launch_bounds__(64) attention_far_sum_kernel(const int32_t* __restrict__ seg_start,
-                                                               const int32_t* __restrict__ seg_len, int far0, int sinks,
-                                                               const float* __restrict__ partial,
-                                                               __nv_bfloat16* __restrict__ dqkv, int d, int heads,
-                                                               const float2* __restrict__ rope, int max_pos) {
-  const int s0 = seg_start[blockIdx.x], len = seg_len[blockIdx.x], h = blockIdx.y;
-  if (len <= far0) return;
-  const int slots = 1 + (len - far0 + kFarQueries - 1) / kFarQueries;
-  const int j = threadIdx.x & 31;
-  const bool is_k = threadIdx.x < 32;
-  const float* src = partial + ((size_t)(s0 / kFarSlotTokens) * heads + h) * sinks * (2 * DH) + (is_k ? 0 : DH) + j;
-  for (int r = 0; r < sinks; ++r) {
-    float a = 0.f, b = 0.f;
-    for (int k = 0; k < slots; ++k) {
-      const float* at = src + ((size_t)k * heads * sinks + r) * (2 * DH);
-      a += at[0];
-      b += at[32];
-    }
-    if (is_k) {
-      const float u = a * 0.125f, w = b * 0.125f;
-      float2 cs = make_float2(1.f, 0.f);
-      if (rope != nullptr) cs = __ldg(rope + ((size_t)(j >> 1) * max_pos + min(r, max_pos - 1)) * 2 + (j & 1));
-      a = u * cs.x + w * cs.y;
-      b = w * cs.x - u * cs.y;
-    }
-    __nv_bfloat16* row = dqkv + (size_t)(s0 + r) * 3 * d + (is_k ? d : 2 * d) + h * DH + j;
-    row[0] = __float2bfloat16_rn(a);
-    row[32] = __float2bfloat16_rn(b);
   }
 }
 
@@ -766,6 +582,12 @@ __global__ void attention_bwd_dq_kernel(const float* __restrict__ dq_acc, __nv_b
 
 }  // namespace
 
+void launch_attention_bwd_dq(const float* dq_acc, __nv_bfloat16* dqkv, const int32_t* pos_id, const float2* rope,
+                             int max_pos, int T, int d, cudaStream_t st) {
+  const long long tq = (long long)T * (d / 16);
+  attention_bwd_dq_kernel<<<(unsigned)((tq + 255) / 256), 256, 0, st>>>(dq_acc, dqkv, pos_id, rope, max_pos, T, d);
+}
+
 cudaError_t launch_attention_bwd_tc(const CUtensorMap* tm_qkv, const CUtensorMap* tm_do, const CUtensorMap* tm_dq,
                                     const __nv_bfloat16* o,
                                     const __nv_bfloat16* dout, const float* lse, float* dsum, float* dq_acc,
@@ -787,57 +609,6 @@ cudaError_t launch_attention_bwd_tc(const CUtensorMap* tm_qkv, const CUtensorMap
   const unsigned grid = (unsigned)(items < num_sms ? items : num_sms);
   attention_bwd_tc_kernel<<<grid, THREADS, SMEM_BYTES, st>>>(*tm_qkv, *tm_do, *tm_dq, lse, dsum, dqkv, T, d, heads, pb,
                                                              rope, max_pos, err);
-  const long long tq = (long long)T * (d / 16);
-  attention_bwd_dq_kernel<<<(unsigned)((tq + 255) / 256), 256, 0, st>>>(dq_acc, dqkv, pb.pos_id, rope, max_pos, T, d);
-  return cudaGetLastError();
-}
-
-// Scratch of the far chunks: [count, padded to 16 bytes][chunks][partial sums].
-static bool window_has_far(const AttnWindow& w, int T) {
-  return w.sinks > 0 && w.left >= 0 && T > TB + w.left + 1 + kFarStart;
-}
-size_t attention_window_bwd_far_bytes(const AttnWindow& w, int T, int heads) {
-  if (!window_has_far(w, T)) return 0;
-  return 16 + 16 * (size_t)far_max_chunks(T) +
-         sizeof(float) * (size_t)far_max_slots(T) * heads * w.sinks * (2 * DH);
-}
-
-cudaError_t launch_attention_window_bwd_tc(const CUtensorMap* tm_qkv, const CUtensorMap* tm_do,
-                                           const CUtensorMap* tm_dq, const AttnWindow& win, const __nv_bfloat16* o,
-                                           const __nv_bfloat16* dout, const float* lse, float* dsum, float* dq_acc,
-                                           void* far, __nv_bfloat16* dqkv, int T, int B, int d, int heads,
-                                           int max_items, const PackBuffers& pb, const float2* rope, int max_pos,
-                                           int num_sms, unsigned* err, cudaStream_t st) {
-  if (T <= 0 || max_items <= 0) return cudaSuccess;
-  static bool configured = false;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(attention_window_bwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
-  const bool has_far = window_has_far(win, T);
-  const int far0 = TB + win.left + 1 + kFarStart;
-  FarList fl{};
-  if (has_far) {
-    int32_t* count = static_cast<int32_t*>(far);
-    int4* item = reinterpret_cast<int4*>(count + 4);
-    fl.count = count;
-    fl.item = item;
-    fl.partial = reinterpret_cast<float*>(item + far_max_chunks(T));
-    attention_far_list_kernel<<<1, 1024, 0, st>>>(pb.seg_start, pb.seg_klen, B, far0, far_max_chunks(T), count, item);
-  }
-  const long long th = (long long)T * heads;
-  attention_bwd_dsum_kernel<<<(unsigned)((8 * th + 255) / 256), 256, 0, st>>>(o, dout, dsum, T, d, heads);
-  cudaError_t e = cudaMemsetAsync(dq_acc, 0, sizeof(float) * (size_t)T * d, st);
-  if (e != cudaSuccess) return e;
-  const long long items = (long long)(max_items + (has_far ? far_max_chunks(T) : 0)) * heads;
-  const unsigned grid = (unsigned)(items < num_sms ? items : num_sms);
-  attention_window_bwd_tc_kernel<<<grid, THREADS, SMEM_BYTES, st>>>(*tm_qkv, *tm_do, *tm_dq, win, fl, lse, dsum, dqkv,
-                                                                    T, d, heads, pb, rope, max_pos, err);
-  if (has_far)
-    attention_far_sum_kernel<<<dim3(B, heads), 64, 0, st>>>(pb.seg_start, pb.seg_klen, far0, win.sinks, fl.partial,
-                                                            dqkv, d, heads, rope, max_pos);
   const long long tq = (long long)T * (d / 16);
   attention_bwd_dq_kernel<<<(unsigned)((tq + 255) / 256), 256, 0, st>>>(dq_acc, dqkv, pb.pos_id, rope, max_pos, T, d);
   return cudaGetLastError();

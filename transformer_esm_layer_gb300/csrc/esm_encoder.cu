@@ -183,14 +183,17 @@ struct esm_encoder {
     CUtensorMap m;
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {cols * elem};
-    cuuint32_t box[2] = {128u / elem, box_rows};
+    // (rows of 32 bytes are taken whole, wider ones 128 bytes at a time, swizzled alike)
+    const bool narrow = cols * elem == 32;
+    cuuint32_t box[2] = {(narrow ? 32u : 128u) / elem, box_rows};
     cuuint32_t es[2] = {1, 1};
     const CUtensorMapDataType dt = elem == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     CUresult r = fn(&m, dt, 2,
                     const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    narrow ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return nullptr;
     return &maps.emplace(k, m).first->second;
   }
@@ -651,7 +654,7 @@ TrainLayout train_layout(const esm_config& c, int Tm, const AttnWindow& win) {
   L.dob = take(2 * T * d);
   L.dqkv = take(2 * T * 3 * d);
   L.dqacc = take(4 * T * d);
-  L.dsum = take(4 * T * H);
+  L.dsum = take(is_full(win) ? 4 * T * H : 2 * kBwdTerms * T * H);  // windowed: the row terms
   L.far = take(attention_window_bwd_far_bytes(win, (int)T, (int)H));
   const size_t widest = std::max(3 * d, f);
   L.partial = take(4 * bwd_partial_floats((int)T, (int)widest));
@@ -866,14 +869,16 @@ esm_status backward_impl(esm_encoder* h, const esm_weights* w, const float* d_ou
       const CUtensorMap* tq = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 128, 2);
       const CUtensorMap* td = h->map(dob, (uint64_t)T, (uint64_t)d, 128, 2);
       const CUtensorMap* tdq = h->map(dqacc, (uint64_t)T, (uint64_t)d, 32, 4);
-      if (!tq || !td || !tdq) return ESM_ERR_CUDA;
+      const CUtensorMap* tt = is_full(win) ? nullptr : h->map(dsum, (uint64_t)T * H, kBwdTerms, 128, 2);
+      if (!tq || !td || !tdq || (!is_full(win) && !tt)) return ESM_ERR_CUDA;
       const __nv_bfloat16* ob = static_cast<const __nv_bfloat16*>(o);
       const cudaError_t e =
           is_full(win) ? launch_attention_bwd_tc(tq, td, tdq, ob, dob, lse, dsum, dqacc, dqkv, T, d, H, h->train_items,
                                                  pb, h->d_rope, c.max_positions, h->num_sms, h->d_err, st)
-                       : launch_attention_window_bwd_tc(tq, td, tdq, win, ob, dob, lse, dsum, dqacc, tb + R.far, dqkv,
-                                                        T, h->train_B, d, H, h->train_items, pb, h->d_rope,
-                                                        c.max_positions, h->num_sms, h->d_err, st);
+                       : launch_attention_window_bwd_tc(tq, td, tdq, tt, win, ob, dob, lse,
+                                                        reinterpret_cast<__nv_bfloat16*>(dsum), dqacc, tb + R.far, dqkv,
+                                                        T, h->train_B, c.max_positions, d, H, h->train_items, pb,
+                                                        h->d_rope, c.max_positions, h->num_sms, h->d_err, st);
       if (e != cudaSuccess) return ESM_ERR_CUDA;
     }
     PROF(h, P_OTHER, st, 2, launch_colsum(dqkv, true, T, 3 * d, g->b_qkv[l], partial, nullptr, st));
@@ -1566,7 +1571,7 @@ esm_status esm_op_attention(esm_encoder_t* h, const void* qkv, const int32_t* cu
 // Workspace of the windowed attention hooks: the batch's index (positions and segments only for
 // the fp32 kernel), then the backward's scratch.
 struct WindowWs {
-  size_t pos, seg, seg_start, seg_qlen, seg_klen, work, work_count, dsum, dq, far, total;
+  size_t pos, seg, seg_start, seg_qlen, seg_klen, work, work_count, terms, dq, far, total;
   int max_items;
 };
 static WindowWs window_ws(const esm_encoder* h, int Tm, int Bm, const AttnWindow& win, bool backward) {
@@ -1587,7 +1592,7 @@ static WindowWs window_ws(const esm_encoder* h, int Tm, int Bm, const AttnWindow
   L.seg_klen = take(4 * B);
   L.work = take(16 * (size_t)L.max_items);
   L.work_count = take(16);
-  L.dsum = take(backward ? 4 * T * h->cfg.heads : 0);
+  L.terms = take(backward ? 2 * kBwdTerms * T * h->cfg.heads : 0);
   L.dq = take(backward ? 4 * T * h->cfg.hidden : 0);
   L.far = take(backward ? attention_window_bwd_far_bytes(win, (int)T, h->cfg.heads) : 0);
   L.total = off;
@@ -1595,8 +1600,8 @@ static WindowWs window_ws(const esm_encoder* h, int Tm, int Bm, const AttnWindow
 }
 
 // Index of the batch in the workspace, for the windowed attention hooks.
-static esm_status window_index(esm_encoder* h, const int32_t* cu, int B, int T, int max_seqlen, const WindowWs& L,
-                               void* ws, PackBuffers* pb, cudaStream_t st) {
+static esm_status window_index(esm_encoder* h, const int32_t* cu, int B, int T, int max_seqlen, const AttnWindow& win,
+                               bool backward, const WindowWs& L, void* ws, PackBuffers* pb, cudaStream_t st) {
   uint8_t* b = static_cast<uint8_t*>(ws);
   auto at = [&](size_t off) { return reinterpret_cast<int32_t*>(b + off); };
   *pb = PackBuffers{at(L.pos),      at(L.seg),  at(L.seg_start), at(L.seg_qlen),
@@ -1607,7 +1612,10 @@ static esm_status window_index(esm_encoder* h, const int32_t* cu, int B, int T, 
       return ESM_ERR_CUDA;
     launch_pack_index(cu, B, T, max_seqlen, h->cfg.max_positions, *pb, h->d_err, st);
   } else {
-    launch_attn_plan(cu, B, T, max_seqlen, h->cfg.max_positions, kAttnQTileTc, L.max_items, *pb, h->d_err, st);
+    // (items that the grid takes in one round need no order)
+    const int sort_above = (backward ? 1 : 2) * h->num_sms / h->cfg.heads;
+    launch_attn_plan(cu, B, T, max_seqlen, h->cfg.max_positions, kAttnQTileTc, L.max_items, win, backward, sort_above,
+                     *pb, h->d_err, st);
   }
   return cuda_status(cudaGetLastError());
 }
@@ -1636,7 +1644,8 @@ esm_status esm_op_attention_window(esm_encoder_t* h, const void* qkv, const int3
   if (workspace == h->train_ws) h->train_buf = nullptr;  // as check_ws: the pending backward's index is overwritten
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   PackBuffers pb;
-  const esm_status s = window_index(h, cu_seqlens, num_seqs, total_tokens, max_seqlen, L, workspace, &pb, st);
+  const esm_status s = window_index(h, cu_seqlens, num_seqs, total_tokens, max_seqlen, win, false, L, workspace, &pb,
+                                    st);
   if (s != ESM_OK) return s;
   return run_attention(h, win, qkv, o, h->act(), total_tokens, L.max_items, pb, nullptr, nullptr, st, lse);
 }
@@ -1660,19 +1669,21 @@ esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, c
   if (workspace == h->train_ws) h->train_buf = nullptr;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   PackBuffers pb;
-  const esm_status s = window_index(h, cu_seqlens, num_seqs, total_tokens, max_seqlen, L, workspace, &pb, st);
+  const esm_status s = window_index(h, cu_seqlens, num_seqs, total_tokens, max_seqlen, win, true, L, workspace, &pb,
+                                    st);
   if (s != ESM_OK) return s;
   const int d = h->cfg.hidden, T = total_tokens;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const CUtensorMap* tq = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 128, 2);
   const CUtensorMap* td = h->map(d_o, (uint64_t)T, (uint64_t)d, 128, 2);
   const CUtensorMap* tdq = h->map(ws + L.dq, (uint64_t)T, (uint64_t)d, 32, 4);
-  if (!tq || !td || !tdq) return ESM_ERR_CUDA;
+  const CUtensorMap* tt = h->map(ws + L.terms, (uint64_t)T * h->cfg.heads, kBwdTerms, 128, 2);
+  if (!tq || !td || !tdq || !tt) return ESM_ERR_CUDA;
   return cuda_status(launch_attention_window_bwd_tc(
-      tq, td, tdq, win, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), lse,
-      reinterpret_cast<float*>(ws + L.dsum), reinterpret_cast<float*>(ws + L.dq), ws + L.far,
-      static_cast<__nv_bfloat16*>(dqkv), T, num_seqs, d, h->cfg.heads, L.max_items, pb, nullptr, h->cfg.max_positions,
-      h->num_sms, h->d_err, st));
+      tq, td, tdq, tt, win, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), lse,
+      reinterpret_cast<__nv_bfloat16*>(ws + L.terms), reinterpret_cast<float*>(ws + L.dq), ws + L.far,
+      static_cast<__nv_bfloat16*>(dqkv), T, num_seqs, max_seqlen, d, h->cfg.heads, L.max_items, pb, nullptr,
+      h->cfg.max_positions, h->num_sms, h->d_err, st));
 }
 
 // ------------------------------------------------------------------ distillation

@@ -43,10 +43,12 @@ void launch_pad_index(const int32_t* seq_lens, int B, int S, const PackBuffers& 
                       cudaStream_t st);
 // Work items (segment, first query row) in tiles of q_tile rows, longest segments first.
 void launch_attn_worklist(int B, int max_items, int q_tile, const PackBuffers& pb, cudaStream_t st);
-// Segment table (seg_start, seg_qlen, seg_klen) and work items straight from cu_seqlens, validated
-// like launch_pack_index, without positions; items in batch order.
+// Segment table (seg_start, seg_qlen, seg_klen) and work items of a windowed attention straight from
+// cu_seqlens, validated like launch_pack_index, without positions; with more than sort_above
+// items the longest under the window (forward: key tiles, backward: query tiles) come first.
 void launch_attn_plan(const int32_t* cu, int B, int T, int max_seqlen, int max_positions, int q_tile, int max_items,
-                      const PackBuffers& pb, unsigned* err, cudaStream_t st);
+                      const AttnWindow& win, bool backward, int sort_above, const PackBuffers& pb, unsigned* err,
+                      cudaStream_t st);
 void launch_embed(const int32_t* tok, int T, const void* emb, bool emb_f32, int vocab, int d, float scale,
                   float* x, unsigned* err, cudaStream_t st);
 void launch_rope_table(float2* tab, int max_pos, int half, float base, cudaStream_t st);
@@ -204,8 +206,8 @@ bool encode_attention_qkv_map(const void* qkv, int total_tokens, int hidden, CUt
 cudaError_t launch_attention_tc(const CUtensorMap* tm_qkv, void* o, Act out, int d, int heads, int max_items,
                                 const PackBuffers& pb, const float* q_scale, float* amax, unsigned* err,
                                 cudaStream_t st, float* lse = nullptr, int lse_stride = 0);
-// The same with a window (win.sinks <= kMaxSinks): tm_qkv16 is a map over the same qkv with a
-// 64 x 16 box, qkv the buffer itself (16-byte aligned).
+// attention_window_tc.cu: the same with a window (win.sinks <= kMaxSinks); tm_qkv16 is a map over the
+// same qkv with a 64 x 16 box, qkv the buffer itself (16-byte aligned).
 cudaError_t launch_attention_window_tc(const CUtensorMap* tm_qkv, const CUtensorMap* tm_qkv16, const AttnWindow& win,
                                        const void* qkv, void* o, Act out, int d, int heads, int max_items,
                                        const PackBuffers& pb, const float* q_scale, float* amax, unsigned* err,
@@ -225,15 +227,25 @@ cudaError_t launch_attention_bwd_tc(const CUtensorMap* tm_qkv, const CUtensorMap
                                     __nv_bfloat16* dqkv, int T, int d, int heads, int max_items, const PackBuffers& pb,
                                     const float2* rope, int max_pos, int num_sms, unsigned* err, cudaStream_t st);
 
-// The same with a window (win.sinks <= kMaxSinks); B sequences (pb.seg_*).  far: scratch of
-// attention_window_bwd_far_bytes bytes, 16-byte aligned (may be NULL when that is 0).
+// Its last step, for the windowed form too: dq = dq_acc / 8, turned back through RoPE (rope may be
+// NULL), into the q block of dqkv.
+void launch_attention_bwd_dq(const float* dq_acc, __nv_bfloat16* dqkv, const int32_t* pos_id, const float2* rope,
+                             int max_pos, int T, int d, cudaStream_t st);
+
+// ---------------------------------------------------------------- attention_window_bwd_tc.cu
+// launch_attention_bwd_tc with a window (win.sinks <= kMaxSinks); B sequences (pb.seg_*) of at
+// most max_len tokens.  Scratch: terms bf16 [heads, T, kBwdTerms] (tm_terms a map over it as
+// [heads * T, kBwdTerms] with a 128-row box), dq_acc as above, far: attention_window_bwd_far_bytes
+// bytes, 16-byte aligned (may be NULL when that is 0).
+constexpr int kBwdTerms = 16;
 size_t attention_window_bwd_far_bytes(const AttnWindow& w, int T, int heads);
 cudaError_t launch_attention_window_bwd_tc(const CUtensorMap* tm_qkv, const CUtensorMap* tm_do,
-                                           const CUtensorMap* tm_dq, const AttnWindow& win, const __nv_bfloat16* o,
-                                           const __nv_bfloat16* dout, const float* lse, float* dsum, float* dq_acc,
-                                           void* far, __nv_bfloat16* dqkv, int T, int B, int d, int heads,
-                                           int max_items, const PackBuffers& pb, const float2* rope, int max_pos,
-                                           int num_sms, unsigned* err, cudaStream_t st);
+                                           const CUtensorMap* tm_dq, const CUtensorMap* tm_terms, const AttnWindow& win,
+                                           const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse,
+                                           __nv_bfloat16* terms, float* dq_acc, void* far, __nv_bfloat16* dqkv, int T,
+                                           int B, int max_len, int d, int heads, int max_items, const PackBuffers& pb,
+                                           const float2* rope, int max_pos, int num_sms, unsigned* err,
+                                           cudaStream_t st);
 
 // ---------------------------------------------------------------- backward.cu
 // Scratch floats for the column reductions of rows x cols (LayerNorm: two sums per column).
