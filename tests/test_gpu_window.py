@@ -288,6 +288,74 @@ def test_backward_against_differences():
     assert abs((dqkv.double() * u).sum() - diff) <= (bound * u.abs()).sum() + slack
 
 
+def test_backward_of_scores_far_apart():
+    """Scores of up to about +-100 (lse of that size enters the exponent as a sum of three bf16)."""
+    heads, lengths, window = 4, [500, 130], (200, 10, 2)
+    enc = _enc(heads)
+    qkv, cu, g = _inputs(lengths, heads, 25)
+    d = 64 * heads
+    scale = torch.linspace(0.1, 8, len(qkv), device="cuda")[:, None]
+    for s in (scale, scale.flip(0)):
+        x = qkv.clone()
+        x[:, d:2 * d] = (x[:, d:2 * d].float() * s).to(torch.bfloat16)
+        o, lse = _forward(enc, x, cu, lengths, window, heads)
+        o = o.contiguous()
+        d_o = torch.randn(len(x), d, device="cuda", generator=g).to(torch.bfloat16)
+        dqkv = torch.empty_like(x)
+        enc.op_attention_window_backward(x, o, lse, d_o, cu, max(lengths), window, dqkv)
+        ref, bound = _backward_reference(x, o, lse, d_o, lengths, heads, window)
+        assert torch.all((dqkv.double() - ref).abs() <= bound)
+    assert enc.check_status() == 0
+
+
+@pytest.mark.parametrize("B", [1, 31, 32, 33, 300])
+def test_small_batches_with_and_without_a_work_list(B):
+    """Batches whose items are found from the offsets (up to 32 sequences and one item per block), and
+    their neighbours that go by the work list."""
+    heads, window = 4, (9, 3, 2)
+    lengths = [(7 * i) % 61 for i in range(B)]
+    lengths[-1] = 190
+    enc = _enc(heads)
+    qkv, cu, _ = _inputs(lengths, heads, 26)
+    o, lse = _forward(enc, qkv, cu, lengths, window, heads)
+    ro, bo, rl, bl = _reference(qkv, lengths, heads, window)
+    assert torch.all((o.double() - ro).abs() <= bo)
+    assert torch.all((lse.double() - rl).abs() <= bl)
+
+
+@pytest.mark.parametrize("B", [257, 1024, 1500])
+def test_many_sequences(B):
+    """More sequences than a block of the work list's kernels has threads, in both directions."""
+    heads, window = 4, (40, 20, 1)
+    lengths = [(11 * i) % 37 for i in range(B)]
+    lengths[B // 2] = 700
+    _, qkv, _, o, lse, d_o, dqkv = _backward_case(lengths, window, heads, 27)
+    ro, bo, _, _ = _reference(qkv, lengths, heads, window)
+    assert torch.all((o.double() - ro).abs() <= bo)
+    ref, bound = _backward_reference(qkv, o, lse, d_o, lengths, heads, window)
+    assert torch.all((dqkv.double() - ref).abs() <= bound)
+
+
+@pytest.mark.parametrize("heads", [4, 12, 20])
+def test_outputs_off_32_bytes(heads):
+    """o, dqkv 16-byte but not 32-byte aligned."""
+    lengths, window = [150, 70], (30, 30, 1)
+    enc = _enc(heads)
+    qkv, cu, g = _inputs(lengths, heads, 28)
+    T, d = len(qkv), 64 * heads
+    want, lse = _forward(enc, qkv, cu, lengths, window, heads)
+    o = torch.empty(T * d + 8, dtype=torch.bfloat16, device="cuda")[8:].view(T, d)
+    enc.op_attention_window(qkv, cu, 150, window, o)
+    assert torch.equal(o, want)
+    d_o = torch.randn(T, d, device="cuda", generator=g).to(torch.bfloat16)
+    a = torch.empty_like(qkv)
+    b = torch.empty(T * 3 * d + 8, dtype=torch.bfloat16, device="cuda")[8:].view(T, 3 * d)
+    for out in (a, b):
+        enc.op_attention_window_backward(qkv, o, lse, d_o, cu, 150, window, out)
+    assert torch.equal(a[:, d:], b[:, d:])
+    assert enc.check_status() == 0
+
+
 def test_backward_is_repeatable_but_for_dq():
     heads, lengths, window = 4, [3000, 500], (100, 100, 4)
     enc, qkv, cu, o, lse, d_o, dqkv = _backward_case(lengths, window, heads, 24)

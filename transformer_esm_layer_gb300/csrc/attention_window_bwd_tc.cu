@@ -55,6 +55,7 @@
 // window 128 + 128, one sink 229 us (276); 160 sequences of 100 tokens, one pair per item 147 us (205).
 // What the call has beside this kernel is memory traffic: the row terms, the accumulator's
 // zeros and its rounding to dq.
+#include "attn_plan.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -707,9 +708,10 @@ __global__ void __launch_bounds__(1024) attention_far_list_kernel(const int32_t*
 }
 
 // dK and dV of the sinks of sequences with far chunks: the slots' fp32 sums in slot order, dK
-// scaled and turned back through RoPE, as bf16.  A block per (sequence, head), a thread per pair
-// (j, j + 32) of a sink row (threads 0..31: dK, 32..63: dV).
-__global__ void __launch_bounds__(64) attention_far_sum_kernel(const int32_t* __restrict__ seg_start,
+// scaled and turned back through RoPE, as bf16.  A block per (sequence, head); kSumRows sink rows at
+// a time, each by a thread per pair (j, j + 32) (threads 0..31 of the row: dK, 32..63: dV).
+constexpr int kSumRows = 8;
+__global__ void __launch_bounds__(64 * kSumRows) attention_far_sum_kernel(const int32_t* __restrict__ seg_start,
                                                                const int32_t* __restrict__ seg_len, int far0, int sinks,
                                                                const float* __restrict__ partial,
                                                                __nv_bfloat16* __restrict__ dqkv, int d, int heads,
@@ -720,8 +722,9 @@ __global__ void __launch_bounds__(64) attention_far_sum_kernel(const int32_t* __
   const int j = threadIdx.x & 31;
   const bool is_k = threadIdx.x < 32;
   const float* src = partial + ((size_t)(s0 / kFarSlotTokens) * heads + h) * sinks * (2 * DH) + (is_k ? 0 : DH) + j;
-  for (int r = 0; r < sinks; ++r) {
+  for (int r = threadIdx.y; r < sinks; r += kSumRows) {
     float a = 0.f, b = 0.f;
+#pragma unroll 8
     for (int k = 0; k < slots; ++k) {
       const float* at = src + ((size_t)k * heads * sinks + r) * (2 * DH);
       a += at[0];
@@ -743,11 +746,18 @@ __global__ void __launch_bounds__(64) attention_far_sum_kernel(const int32_t* __
 // The row terms of the scores and of dP, per head and token 16 bf16: -8 lse and -D, D = sum_c dO_c O_c,
 // as sums of three (hi, mid, lo: 24 bits), columns 0..2 and 3..5; and 0 into the token's and
 // head's 64 values of the dQ accumulator.  Eight lanes per (token, head): lane p takes columns
-// 8p .. 8p + 7, so the eight read the head's 128 bytes together.
-__global__ void attention_bwd_terms_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
+// 8p .. 8p + 7, so the eight read the head's 128 bytes together.  With plan.cu the first block makes
+// the work list instead (a launch of its own took 4 us of a small call).
+constexpr int kTermThreads = 256;
+__global__ void __launch_bounds__(kTermThreads)
+    attention_bwd_terms_kernel(AttnPlan plan, PackBuffers pb, unsigned* err, const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                                            const float* __restrict__ lse, __nv_bfloat16* __restrict__ terms,
                                            float* __restrict__ dq_acc, int T, int d, int heads) {
-  const long long g = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (plan.cu != nullptr && blockIdx.x == 0) {
+    attn_plan<kTermThreads>(plan, pb, err);
+    return;
+  }
+  const long long g = (long long)(blockIdx.x - (plan.cu != nullptr ? 1 : 0)) * kTermThreads + threadIdx.x;
   const long long i = g >> 3;
   const int p = (int)(g & 7);
   const bool ok = i < (long long)T * heads;
@@ -809,7 +819,7 @@ cudaError_t launch_attention_window_bwd_tc(const CUtensorMap* tm_qkv, const CUte
                                            const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse,
                                            __nv_bfloat16* terms, float* dq_acc,
                                            void* far, __nv_bfloat16* dqkv, int T, int B, int max_len, int d, int heads,
-                                           int max_items, const PackBuffers& pb, const float2* rope, int max_pos,
+                                           int max_items, const PackBuffers& pb, const AttnPlan& plan, const float2* rope, int max_pos,
                                            int num_sms, unsigned* err, cudaStream_t st) {
   if (T <= 0 || max_items <= 0) return cudaSuccess;
   static bool configured = false;
@@ -823,6 +833,9 @@ cudaError_t launch_attention_window_bwd_tc(const CUtensorMap* tm_qkv, const CUte
     if (a.numRegs < kRegsLaunch) return cudaErrorInvalidKernelImage;
     configured = true;
   }
+  const long long th = (long long)T * heads;
+  const unsigned blocks = (unsigned)((8 * th + kTermThreads - 1) / kTermThreads) + (plan.cu != nullptr ? 1u : 0u);
+  attention_bwd_terms_kernel<<<blocks, kTermThreads, 0, st>>>(plan, pb, err, o, dout, lse, terms, dq_acc, T, d, heads);
   // (a sequence longer than max_len is malformed: it is reported and gets no chunks)
   const bool has_far = window_has_far(win, T, max_len);
   const int far0 = TB + win.left + 1 + kFarStart;
@@ -835,15 +848,13 @@ cudaError_t launch_attention_window_bwd_tc(const CUtensorMap* tm_qkv, const CUte
     fl.partial = reinterpret_cast<float*>(item + far_max_chunks(T));
     attention_far_list_kernel<<<1, 1024, 0, st>>>(pb.seg_start, pb.seg_klen, B, far0, far_max_chunks(T), count, item);
   }
-  const long long th = (long long)T * heads;
-  attention_bwd_terms_kernel<<<(unsigned)((8 * th + 255) / 256), 256, 0, st>>>(o, dout, lse, terms, dq_acc, T, d, heads);
   const long long items = (long long)(max_items + (has_far ? far_max_chunks(T) : 0)) * heads;
   const unsigned grid = (unsigned)(items < num_sms ? items : num_sms);
   const HeadDiv hd{(uint32_t)heads, (uint32_t)(((1ull << 32) + heads - 1) / heads)};
   attention_window_bwd_tc_kernel<<<grid, THREADS, SMEM_BYTES, st>>>(*tm_qkv, *tm_do, *tm_dq, *tm_terms, win, fl,
                                                                     dqkv, T, d, hd, pb, rope, max_pos, err);
   if (has_far)
-    attention_far_sum_kernel<<<dim3(B, heads), 64, 0, st>>>(pb.seg_start, pb.seg_klen, far0, win.sinks, fl.partial,
+    attention_far_sum_kernel<<<dim3(B, heads), dim3(64, kSumRows), 0, st>>>(pb.seg_start, pb.seg_klen, far0, win.sinks, fl.partial,
                                                             dqkv, d, heads, rope, max_pos);
   launch_attention_bwd_dq(dq_acc, dqkv, pb.pos_id, rope, max_pos, T, d, st);
   return cudaGetLastError();

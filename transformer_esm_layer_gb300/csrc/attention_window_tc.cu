@@ -67,6 +67,7 @@ struct WinSmem {
   uint64_t s_full, s_free, p_full, pv_done, mma_done, pv_fin;
   uint32_t tmem_base;
   volatile int abort;
+  int first[5];                        // the first item's list entry and head
 };
 // [Q0][Q1][K0][V0][K1][V1] then WinSmem
 constexpr int SMEM_BYTES = TILE_BYTES * (2 + 2 * STG) + 1024 + (int)sizeof(WinSmem);
@@ -133,6 +134,38 @@ __device__ __forceinline__ Raw load_item(const PackBuffers& pb, int it, const He
   hd.split((uint32_t)it, entry, h);
   return Raw{__ldg(reinterpret_cast<const int4*>(pb.work) + entry), (int)h};
 }
+// The same from the offsets themselves, by a whole warp, for batches of at most 32 sequences; reports
+// malformed offsets like the kernel that writes the list, and counts the items.
+__device__ __forceinline__ Raw find_item(const PackedBatch& b, int it, const HeadDiv& hd, int& n_items, unsigned* err) {
+  const int lane = threadIdx.x & 31;
+  int c0 = 0, L = 0;
+  if (lane < b.B) {
+    c0 = __ldg(b.cu + lane);
+    int c1 = __ldg(b.cu + lane + 1);
+    if ((lane == 0 && c0 != 0) || (lane == b.B - 1 && c1 != b.T) || c1 < c0 || c1 - c0 > b.max_seqlen ||
+        c1 - c0 > b.max_positions || c0 < 0 || c1 > b.T) {
+      if (threadIdx.x < 32) latch_error(err, ERRBIT_CU_SEQLENS);
+      c0 = min(max(c0, 0), b.T);
+      c1 = min(min(max(c1, c0), b.T), c0 + b.max_positions);
+    }
+    L = c1 - c0;
+  }
+  const int tiles = (L + QT - 1) / QT;
+  int v = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  n_items = __shfl_sync(0xffffffffu, v, 31) * (int)hd.heads;
+  uint32_t entry, h;
+  hd.split((uint32_t)it, entry, h);
+  const unsigned mine = __ballot_sync(0xffffffffu, (int)entry >= v - tiles && (int)entry < v);
+  const int src = mine ? __ffs(mine) - 1 : 0;
+  const int start = __shfl_sync(0xffffffffu, c0, src), len = __shfl_sync(0xffffffffu, L, src);
+  const int off = ((int)entry - __shfl_sync(0xffffffffu, v - tiles, src)) * QT;
+  return Raw{make_int4(start + off, min(QT, len - off), start, len), (int)h};
+}
 __device__ __forceinline__ Item make_item(const Raw& raw, const AttnWindow& win) {
   Item x;
   x.h = raw.h;
@@ -179,9 +212,17 @@ template <Act OUT, bool AMAX = false>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     attention_window_tc_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm16,
                                AttnWindow win, const __nv_bfloat16* __restrict__ qkv, void* __restrict__ o, int d,
-                               HeadDiv hd, PackBuffers pb, const float* q_scale, float* amax_out,
+                               HeadDiv hd, PackBuffers pb, PackedBatch batch, const float* q_scale, float* amax_out,
                                float* __restrict__ lse, int lse_stride, unsigned* err) {
-  const int n_items = *pb.work_count * (int)hd.heads;
+  // the CTA's first item: from the work list, or (then its only one) from the offsets
+  int n_items;
+  Raw first;
+  if (batch.cu != nullptr) {
+    first = find_item(batch, blockIdx.x, hd, n_items, err);
+  } else {
+    n_items = *pb.work_count * (int)hd.heads;
+    if ((int)blockIdx.x < n_items) first = load_item(pb, blockIdx.x, hd);
+  }
   if ((int)blockIdx.x >= n_items) return;  // whole CTA, before any barrier or TMEM use
 
   extern __shared__ uint8_t smem_raw[];
@@ -215,6 +256,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     mbar_init(&sm->mma_done, 1);
     mbar_init(&sm->pv_fin, 1);
     sm->abort = 0;
+    sm->first[0] = first.w.x;
+    sm->first[1] = first.w.y;
+    sm->first[2] = first.w.z;
+    sm->first[3] = first.w.w;
+    sm->first[4] = first.h;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) tma_prefetch_desc(&tm);
@@ -223,6 +269,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
+  auto first_item = [&]() { return Raw{make_int4(sm->first[0], sm->first[1], sm->first[2], sm->first[3]), sm->first[4]}; };
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWg0));
 
   if (warp == 0 || warp == 2) {
@@ -232,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     if (lane == 0) {
       const bool kq = warp == 0;
       int g = 0, n_q = 0;  // key tiles and Q tiles asked for
-      Raw nxt = load_item(pb, item_at(0), hd);
+      Raw nxt = first_item();
       for (int rnd = 0, it = item_at(0); it < n_items && !sm->abort; it = item_at(++rnd)) {
         const Item x = make_item(nxt, win);
         if (item_at(rnd + 1) < n_items) nxt = load_item(pb, item_at(rnd + 1), hd);  // prefetch
@@ -286,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       const uint64_t vdesc0 = make_sw128_desc(smem_u32(sV));
       bool ok = true;
       int g = 0, qi = 0;
-      Raw nxt = load_item(pb, item_at(0), hd);
+      Raw nxt = first_item();
       for (int rnd = 0, it = item_at(0); it < n_items && ok && !sm->abort; it = item_at(++rnd), ++qi) {
         const Item x = make_item(nxt, win);
         if (item_at(rnd + 1) < n_items) nxt = load_item(pb, item_at(rnd + 1), hd);  // prefetch
@@ -457,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         }
       }
     };
-    Raw nxt = load_item(pb, item_at(0), hd);
+    Raw nxt = first_item();
     for (int rnd = 0, it = item_at(0); it < n_items && ok; it = item_at(++rnd)) {
       const Item x = make_item(nxt, win);
       if (item_at(rnd + 1) < n_items) nxt = load_item(pb, item_at(rnd + 1), hd);  // prefetch
@@ -621,10 +668,14 @@ unsigned window_grid(long long items) {
 
 }  // namespace
 
+bool attention_window_direct(int B, int max_items, int heads) {
+  return B <= 32 && (long long)max_items * heads <= window_grid(1ll << 40);
+}
+
 cudaError_t launch_attention_window_tc(const CUtensorMap* tm_qkv, const CUtensorMap* tm_qkv16, const AttnWindow& win,
                                        const void* qkv, void* o, Act out, int d, int heads, int max_items,
-                                       const PackBuffers& pb, const float* q_scale, float* amax, unsigned* err,
-                                       cudaStream_t st, float* lse, int lse_stride) {
+                                       const PackBuffers& pb, const PackedBatch& batch, const float* q_scale,
+                                       float* amax, unsigned* err, cudaStream_t st, float* lse, int lse_stride) {
   if (max_items <= 0) return cudaSuccess;
   static bool configured[3] = {false, false, false};
   const unsigned grid = window_grid((long long)max_items * heads);
@@ -640,7 +691,7 @@ cudaError_t launch_attention_window_tc(const CUtensorMap* tm_qkv, const CUtensor
       configured[which] = true;
     }
     kernel<<<grid, THREADS, SMEM_BYTES, st>>>(*tm_qkv, *tm_qkv16, win, static_cast<const __nv_bfloat16*>(qkv), o, d, hd,
-                                              pb, q_scale, amax, lse, lse_stride, err);
+                                              pb, batch, q_scale, amax, lse, lse_stride, err);
     return cudaGetLastError();
   };
   if (out == Act::E4M3) return run(attention_window_tc_kernel<Act::E4M3>, 1);

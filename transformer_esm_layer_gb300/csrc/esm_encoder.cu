@@ -279,7 +279,7 @@ bool is_full(const AttnWindow& w) { return w.left < 0 && w.right < 0; }
 // segments): qkv [T, 3d] -> o [T, d] (act_out), with lse [heads, T] if given.
 esm_status run_attention(esm_encoder* h, const AttnWindow& win, const void* qkv, void* o, Act act_out, int T,
                          int max_items, const PackBuffers& pb, const float* q_scale, float* amax, cudaStream_t st,
-                         float* lse = nullptr) {
+                         float* lse = nullptr, const PackedBatch& batch = PackedBatch{}) {
   const int d = h->cfg.hidden, H = h->cfg.heads;
   if (h->cfg.precision == ESM_FP32) {
     launch_attention_f32(static_cast<const float*>(qkv), static_cast<float*>(o), d, H, T, pb, st, win);
@@ -291,8 +291,8 @@ esm_status run_attention(esm_encoder* h, const AttnWindow& win, const void* qkv,
     return cuda_status(launch_attention_tc(tq, o, act_out, d, H, max_items, pb, q_scale, amax, h->d_err, st, lse, T));
   const CUtensorMap* tq16 = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 16, 2);
   if (!tq16) return ESM_ERR_CUDA;
-  return cuda_status(launch_attention_window_tc(tq, tq16, win, qkv, o, act_out, d, H, max_items, pb, q_scale, amax,
-                                                h->d_err, st, lse, T));
+  return cuda_status(launch_attention_window_tc(tq, tq16, win, qkv, o, act_out, d, H, max_items, pb, batch, q_scale,
+                                                amax, h->d_err, st, lse, T));
 }
 
 bool weights_ok(const esm_encoder* h, const esm_weights* w) {
@@ -878,7 +878,7 @@ esm_status backward_impl(esm_encoder* h, const esm_weights* w, const float* d_ou
                        : launch_attention_window_bwd_tc(tq, td, tdq, tt, win, ob, dob, lse,
                                                         reinterpret_cast<__nv_bfloat16*>(dsum), dqacc, tb + R.far, dqkv,
                                                         T, h->train_B, c.max_positions, d, H, h->train_items, pb,
-                                                        h->d_rope, c.max_positions, h->num_sms, h->d_err, st);
+                                                        AttnPlan{}, h->d_rope, c.max_positions, h->num_sms, h->d_err, st);
       if (e != cudaSuccess) return ESM_ERR_CUDA;
     }
     PROF(h, P_OTHER, st, 2, launch_colsum(dqkv, true, T, 3 * d, g->b_qkv[l], partial, nullptr, st));
@@ -1599,25 +1599,18 @@ static WindowWs window_ws(const esm_encoder* h, int Tm, int Bm, const AttnWindow
   return L;
 }
 
-// Index of the batch in the workspace, for the windowed attention hooks.
-static esm_status window_index(esm_encoder* h, const int32_t* cu, int B, int T, int max_seqlen, const AttnWindow& win,
-                               bool backward, const WindowWs& L, void* ws, PackBuffers* pb, cudaStream_t st) {
+static PackBuffers window_buffers(const WindowWs& L, void* ws) {
   uint8_t* b = static_cast<uint8_t*>(ws);
   auto at = [&](size_t off) { return reinterpret_cast<int32_t*>(b + off); };
-  *pb = PackBuffers{at(L.pos),      at(L.seg),  at(L.seg_start), at(L.seg_qlen),
-                    at(L.seg_klen), at(L.work), at(L.work_count)};
-  if (h->cfg.precision == ESM_FP32) {
-    if (cudaMemsetAsync(pb->pos_id, 0, 4 * (size_t)T, st) != cudaSuccess ||
-        cudaMemsetAsync(pb->seg_id, 0, 4 * (size_t)T, st) != cudaSuccess)
-      return ESM_ERR_CUDA;
-    launch_pack_index(cu, B, T, max_seqlen, h->cfg.max_positions, *pb, h->d_err, st);
-  } else {
-    // (items that the grid takes in one round need no order)
-    const int sort_above = (backward ? 1 : 2) * h->num_sms / h->cfg.heads;
-    launch_attn_plan(cu, B, T, max_seqlen, h->cfg.max_positions, kAttnQTileTc, L.max_items, win, backward, sort_above,
-                     *pb, h->d_err, st);
-  }
-  return cuda_status(cudaGetLastError());
+  return PackBuffers{at(L.pos),      at(L.seg),  at(L.seg_start), at(L.seg_qlen),
+                     at(L.seg_klen), at(L.work), at(L.work_count)};
+}
+
+// (items that the grid takes in one round need no order)
+static AttnPlan window_plan(const esm_encoder* h, const int32_t* cu, int B, int T, int max_seqlen,
+                            const AttnWindow& win, bool backward, const WindowWs& L) {
+  return AttnPlan{cu,  B,        T, max_seqlen, h->cfg.max_positions, kAttnQTileTc, L.max_items,
+                  win, backward, (backward ? 1 : 2) * h->num_sms / h->cfg.heads};
 }
 
 esm_status esm_op_attention_window_workspace_size(const esm_encoder_t* h, int total_tokens, int num_seqs,
@@ -1643,11 +1636,20 @@ esm_status esm_op_attention_window(esm_encoder_t* h, const void* qkv, const int3
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return ESM_ERR_WORKSPACE;
   if (workspace == h->train_ws) h->train_buf = nullptr;  // as check_ws: the pending backward's index is overwritten
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  PackBuffers pb;
-  const esm_status s = window_index(h, cu_seqlens, num_seqs, total_tokens, max_seqlen, win, false, L, workspace, &pb,
-                                    st);
-  if (s != ESM_OK) return s;
-  return run_attention(h, win, qkv, o, h->act(), total_tokens, L.max_items, pb, nullptr, nullptr, st, lse);
+  const PackBuffers pb = window_buffers(L, workspace);
+  PackedBatch batch{};
+  if (h->cfg.precision == ESM_FP32) {
+    if (cudaMemsetAsync(pb.pos_id, 0, 4 * (size_t)total_tokens, st) != cudaSuccess ||
+        cudaMemsetAsync(pb.seg_id, 0, 4 * (size_t)total_tokens, st) != cudaSuccess)
+      return ESM_ERR_CUDA;
+    launch_pack_index(cu_seqlens, num_seqs, total_tokens, max_seqlen, h->cfg.max_positions, pb, h->d_err, st);
+  } else if (!is_full(win) && attention_window_direct(num_seqs, L.max_items, h->cfg.heads)) {
+    // a small batch: the attention kernel finds its items itself, which saves a launch
+    batch = PackedBatch{cu_seqlens, num_seqs, total_tokens, max_seqlen, h->cfg.max_positions};
+  } else {
+    launch_attn_plan(window_plan(h, cu_seqlens, num_seqs, total_tokens, max_seqlen, win, false, L), pb, h->d_err, st);
+  }
+  return run_attention(h, win, qkv, o, h->act(), total_tokens, L.max_items, pb, nullptr, nullptr, st, lse, batch);
 }
 
 esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, const void* o, const float* lse,
@@ -1668,10 +1670,6 @@ esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, c
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return ESM_ERR_WORKSPACE;
   if (workspace == h->train_ws) h->train_buf = nullptr;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  PackBuffers pb;
-  const esm_status s = window_index(h, cu_seqlens, num_seqs, total_tokens, max_seqlen, win, true, L, workspace, &pb,
-                                    st);
-  if (s != ESM_OK) return s;
   const int d = h->cfg.hidden, T = total_tokens;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const CUtensorMap* tq = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 128, 2);
@@ -1682,7 +1680,8 @@ esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, c
   return cuda_status(launch_attention_window_bwd_tc(
       tq, td, tdq, tt, win, static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(d_o), lse,
       reinterpret_cast<__nv_bfloat16*>(ws + L.terms), reinterpret_cast<float*>(ws + L.dq), ws + L.far,
-      static_cast<__nv_bfloat16*>(dqkv), T, num_seqs, max_seqlen, d, h->cfg.heads, L.max_items, pb, nullptr,
+      static_cast<__nv_bfloat16*>(dqkv), T, num_seqs, max_seqlen, d, h->cfg.heads, L.max_items,
+      window_buffers(L, workspace), window_plan(h, cu_seqlens, num_seqs, T, max_seqlen, win, true, L), nullptr,
       h->cfg.max_positions, h->num_sms, h->d_err, st));
 }
 

@@ -46,9 +46,14 @@ void launch_attn_worklist(int B, int max_items, int q_tile, const PackBuffers& p
 // Segment table (seg_start, seg_qlen, seg_klen) and work items of a windowed attention straight from
 // cu_seqlens, validated like launch_pack_index, without positions; with more than sort_above
 // items the longest under the window (forward: key tiles, backward: query tiles) come first.
-void launch_attn_plan(const int32_t* cu, int B, int T, int max_seqlen, int max_positions, int q_tile, int max_items,
-                      const AttnWindow& win, bool backward, int sort_above, const PackBuffers& pb, unsigned* err,
-                      cudaStream_t st);
+struct AttnPlan {
+  const int32_t* cu;
+  int B, T, max_seqlen, max_positions, q_tile, max_items;
+  AttnWindow win;
+  bool backward;
+  int sort_above;
+};
+void launch_attn_plan(const AttnPlan& plan, const PackBuffers& pb, unsigned* err, cudaStream_t st);
 void launch_embed(const int32_t* tok, int T, const void* emb, bool emb_f32, int vocab, int d, float scale,
                   float* x, unsigned* err, cudaStream_t st);
 void launch_rope_table(float2* tab, int max_pos, int half, float base, cudaStream_t st);
@@ -207,11 +212,18 @@ cudaError_t launch_attention_tc(const CUtensorMap* tm_qkv, void* o, Act out, int
                                 const PackBuffers& pb, const float* q_scale, float* amax, unsigned* err,
                                 cudaStream_t st, float* lse = nullptr, int lse_stride = 0);
 // attention_window_tc.cu: the same with a window (win.sinks <= kMaxSinks); tm_qkv16 is a map over the
-// same qkv with a 64 x 16 box, qkv the buffer itself (16-byte aligned).
+// same qkv with a 64 x 16 box, qkv the buffer itself (16-byte aligned).  A batch for which
+// attention_window_direct holds may be given by its offsets (batch.cu) in place of the work list.
+struct PackedBatch {
+  const int32_t* cu;
+  int B, T, max_seqlen, max_positions;
+};
+bool attention_window_direct(int B, int max_items, int heads);
 cudaError_t launch_attention_window_tc(const CUtensorMap* tm_qkv, const CUtensorMap* tm_qkv16, const AttnWindow& win,
                                        const void* qkv, void* o, Act out, int d, int heads, int max_items,
-                                       const PackBuffers& pb, const float* q_scale, float* amax, unsigned* err,
-                                       cudaStream_t st, float* lse = nullptr, int lse_stride = 0);
+                                       const PackBuffers& pb, const PackedBatch& batch, const float* q_scale,
+                                       float* amax, unsigned* err, cudaStream_t st, float* lse = nullptr,
+                                       int lse_stride = 0);
 void launch_attention_f32(const float* qkv, float* o, int d, int heads, int T, const PackBuffers& pb,
                           cudaStream_t st, const AttnWindow& win = kFullWindow);
 
@@ -236,7 +248,8 @@ void launch_attention_bwd_dq(const float* dq_acc, __nv_bfloat16* dqkv, const int
 // launch_attention_bwd_tc with a window (win.sinks <= kMaxSinks); B sequences (pb.seg_*) of at
 // most max_len tokens.  Scratch: terms bf16 [heads, T, kBwdTerms] (tm_terms a map over it as
 // [heads * T, kBwdTerms] with a 128-row box), dq_acc as above, far: attention_window_bwd_far_bytes
-// bytes, 16-byte aligned (may be NULL when that is 0).
+// bytes, 16-byte aligned (may be NULL when that is 0).  With plan.cu the call first makes pb's
+// segment table and work list from it (beside the row terms, in one launch).
 constexpr int kBwdTerms = 16;
 size_t attention_window_bwd_far_bytes(const AttnWindow& w, int T, int heads);
 cudaError_t launch_attention_window_bwd_tc(const CUtensorMap* tm_qkv, const CUtensorMap* tm_do,
@@ -244,7 +257,7 @@ cudaError_t launch_attention_window_bwd_tc(const CUtensorMap* tm_qkv, const CUte
                                            const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse,
                                            __nv_bfloat16* terms, float* dq_acc, void* far, __nv_bfloat16* dqkv, int T,
                                            int B, int max_len, int d, int heads, int max_items, const PackBuffers& pb,
-                                           const float2* rope, int max_pos, int num_sms, unsigned* err,
+                                           const AttnPlan& plan, const float2* rope, int max_pos, int num_sms, unsigned* err,
                                            cudaStream_t st);
 
 // ---------------------------------------------------------------- backward.cu

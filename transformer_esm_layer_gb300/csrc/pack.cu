@@ -6,6 +6,7 @@
 // the packed forward consumes (input_ids, cu_seqlens, max_seqlen).  The padded layout
 // with a key padding mask is the bshd / padding-mask configuration of the mlqm.cn
 // ESM-2 TransformerEngine walkthrough (attention-mask section).
+#include "attn_plan.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -134,134 +135,8 @@ __global__ void __launch_bounds__(WL_THREADS) attn_worklist_kernel(int B, int ma
   if (tid == 0) pb.work_count[0] = min(s_base, max_items);
 }
 
-// Sort key of a windowed item, longest first: its key tiles (forward) or query tiles (backward),
-// exact up to 64 and in steps of 8 above.
-constexpr int PLAN_CLASSES = 128;
-__device__ __forceinline__ int plan_class(int pos, int rows, int len, const AttnWindow& win, bool backward) {
-  const int before = backward ? win.right : win.left, after = backward ? win.left : win.right;
-  const int lo = before < 0 ? 0 : max(0, pos - before), hi = after < 0 ? len : min(len, pos + rows + after);
-  const int tiles = (max(0, hi - lo) + (!backward && lo > 0 ? (win.sinks + 15) / 16 * 16 : 0) + 127) / 128;
-  return PLAN_CLASSES - 1 - min(PLAN_CLASSES - 1, tiles <= 64 ? tiles : 64 + (tiles - 64) / 8);
-}
-
-// Single CTA: pack_index_kernel's validated segment table and the windowed attention's items in one
-// launch, for callers that need no positions.  A chunk of 1024 sequences at a time: their tiles
-// are scanned, then all threads take the chunk's items, each found by bisection.  With more than
-// sort_above items they are ordered longest first (a counting sort: one pass counts, one
-// writes), so that the CTAs' static shares come out even: 47 packed sequences under a window of
-// 128 + 128 hold items of one to four tiles, and in sequence order the busiest CTA had 1.17
-// times the mean's work, sorted 1.07; with a causal window 1.29 and 1.02.  Items of one length
-// stand in any order.
-__global__ void __launch_bounds__(WL_THREADS) attn_plan_kernel(const int32_t* __restrict__ cu, int B, int T,
-                                                               int max_seqlen, int max_positions, int q_tile,
-                                                               int max_items, AttnWindow win, bool backward,
-                                                               int sort_above, PackBuffers pb, unsigned* err) {
-  __shared__ int s_first[WL_THREADS + 1];  // items before the chunk's sequence i, within the chunk
-  __shared__ int s_start[WL_THREADS], s_len[WL_THREADS];
-  __shared__ int s_warp[WL_THREADS / 32];
-  __shared__ int s_class[PLAN_CLASSES];    // items of a class, then the next place of one
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  // the chunk at b0: segments (written once) and s_first; returns its items
-  auto scan_chunk = [&](int b0, bool write) -> int {
-    const int i = b0 + tid;
-    int tiles = 0;
-    if (i < B) {
-      int c0 = cu[i], c1 = cu[i + 1];
-      const bool bad = (i == 0 && c0 != 0) || (i == B - 1 && c1 != T) || c1 < c0 || c1 - c0 > max_seqlen ||
-                       c1 - c0 > max_positions || c0 < 0 || c1 > T;
-      if (bad) {
-        latch_error(err, ERRBIT_CU_SEQLENS);
-        c0 = min(max(c0, 0), T);
-        c1 = min(min(max(c1, c0), T), c0 + max_positions);
-      }
-      const int L = c1 - c0;
-      s_start[tid] = c0;
-      s_len[tid] = L;
-      if (write) {
-        pb.seg_start[i] = c0;
-        pb.seg_qlen[i] = pb.seg_klen[i] = L;
-      }
-      tiles = (L + q_tile - 1) / q_tile;
-    }
-    int v = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += n;
-    }
-    if (lane == 31) s_warp[wid] = v;
-    __syncthreads();
-    if (wid == 0) {
-      int w = s_warp[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += n;
-      }
-      s_warp[lane] = w;
-    }
-    __syncthreads();
-    v += wid > 0 ? s_warp[wid - 1] : 0;
-    s_first[tid] = v - tiles;
-    if (tid == WL_THREADS - 1) s_first[WL_THREADS] = v;
-    __syncthreads();
-    return s_first[WL_THREADS];
-  };
-  // item k of the chunk: its sequence's slot, and its first row there
-  auto item = [&](int k, int& off) -> int {
-    int lo = 0, hi = WL_THREADS;  // the last sequence with s_first <= k (it has tiles)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_first[mid] <= k) lo = mid;
-      else hi = mid;
-    }
-    off = (k - s_first[lo]) * q_tile;
-    return lo;
-  };
-  if (tid < PLAN_CLASSES) s_class[tid] = 0;
-  __syncthreads();
-  int total = 0;
-  for (int b0 = 0; b0 < B; b0 += WL_THREADS) {
-    const int n = scan_chunk(b0, true);
-    total += n;
-    if (max_items > sort_above)
-      for (int k = tid; k < n; k += WL_THREADS) {
-        int off;
-        const int q = item(k, off);
-        atomicAdd(&s_class[plan_class(off, min(q_tile, s_len[q] - off), s_len[q], win, backward)], 1);
-      }
-    __syncthreads();
-  }
-  const bool sorted = total > sort_above;
-  if (sorted && wid == 0) {  // first place of every class
-    int before = 0;
-    for (int c = lane; c < PLAN_CLASSES; c += 32) {
-      const int n = s_class[c];
-      int v = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      s_class[c] = before + v - n;
-      before += __shfl_sync(0xffffffffu, v, 31);
-    }
-  }
-  __syncthreads();
-  int base = 0;
-  for (int b0 = 0; b0 < B; b0 += WL_THREADS) {
-    const int n = B > WL_THREADS ? scan_chunk(b0, false) : total;  // (a single chunk is still there)
-    for (int k = tid; k < n; k += WL_THREADS) {
-      int off;
-      const int q = item(k, off), rows = min(q_tile, s_len[q] - off);
-      const int at = sorted ? atomicAdd(&s_class[plan_class(off, rows, s_len[q], win, backward)], 1) : base + k;
-      if (at < max_items)
-        reinterpret_cast<int4*>(pb.work)[at] = make_int4(s_start[q] + off, rows, s_start[q], s_len[q]);
-    }
-    base += n;
-    __syncthreads();
-  }
-  if (tid == 0) pb.work_count[0] = min(total, max_items);
+__global__ void __launch_bounds__(WL_THREADS) attn_plan_kernel(AttnPlan plan, PackBuffers pb, unsigned* err) {
+  attn_plan<WL_THREADS>(plan, pb, err);
 }
 
 // x[t, :] = scale * E[tok[t], :] into the fp32 residual stream; one warp per token,
@@ -348,11 +223,8 @@ void launch_attn_worklist(int B, int max_items, int q_tile, const PackBuffers& p
   attn_worklist_kernel<<<1, WL_THREADS, 0, st>>>(B, max_items, q_tile, pb);
 }
 
-void launch_attn_plan(const int32_t* cu, int B, int T, int max_seqlen, int max_positions, int q_tile, int max_items,
-                      const AttnWindow& win, bool backward, int sort_above, const PackBuffers& pb, unsigned* err,
-                      cudaStream_t st) {
-  attn_plan_kernel<<<1, WL_THREADS, 0, st>>>(cu, B, T, max_seqlen, max_positions, q_tile, max_items, win, backward,
-                                             sort_above, pb, err);
+void launch_attn_plan(const AttnPlan& plan, const PackBuffers& pb, unsigned* err, cudaStream_t st) {
+  attn_plan_kernel<<<1, WL_THREADS, 0, st>>>(plan, pb, err);
 }
 
 void launch_embed(const int32_t* tok, int T, const void* emb, bool emb_f32, int vocab, int d, float scale, float* x,
