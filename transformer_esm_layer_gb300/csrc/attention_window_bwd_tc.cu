@@ -31,9 +31,8 @@
 //                qkv and dO buffers), with their row terms: -8 lse and -D as sums of three bf16;
 //   warp 2       TMA: the items' K tiles (two buffers) and V tiles (one: V is done with an item's
 //                last dP^T);
-//   warp 1       one thread issues the MMAs: S^T and dP^T of pair g, then the three gradient
-//                products of pair g - 1;
-//   warp 3       no role (it completes warpgroup 0);
+//   warp 1       one thread issues S^T and dP^T of every pair, as soon as its operands are ready;
+//   warp 3       one thread issues the three gradient products of every pair;
 //   warps 4..11  two warpgroups, one per 64 queries of the tile; thread r owns key r: reads its
 //                S^T and dP^T row segment, forms P^T = 2^(S^T log2(e) / 8) and dS^T = P^T dP^T
 //                in registers (f32x2 pairs), hands S^T back, then writes P^T into tensor memory
@@ -85,7 +84,7 @@ constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DQ = 256, COL_DK = 320, COL_DV =
 struct BwdSmem {
   uint64_t k_full[2], k_empty[2], v_full, v_empty;
   uint64_t q_full[STG], q_empty[STG];
-  uint64_t s_full, s_free, p_full, p_free, ds_free, dq_full, dq_free, acc_full, acc_free, mma_done;
+  uint64_t s_full, s_free, p_full, p_free, ds_free, dq_full, dq_free, acc_full, acc_free, s_done, mma_done;
   uint32_t tmem_base;
   volatile int abort;
 };
@@ -277,6 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(&sm->dq_free, 4);
     mbar_init(&sm->acc_full, 1);
     mbar_init(&sm->acc_free, 4 * kComputeWgs);
+    mbar_init(&sm->s_done, 1);
     mbar_init(&sm->mma_done, 1);
     sm->abort = 0;
     fence_barrier_init();
@@ -356,55 +356,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer: S^T, dP^T
+    // (A thread that issues is held until the tensor core accepts its MMA: with one issuer, scores
+    // that were ready waited behind the 24 gradient MMAs before them.)
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16(TB, TB);                                   // S^T, dP^T
-      constexpr uint32_t idesc_kv = idesc_bf16(TB, DH) | kIdescBMn;                      // dV, dK
-      constexpr uint32_t idesc_q = idesc_bf16(TB, DH) | kIdescAMn | kIdescBMn;           // dQ
+      constexpr uint32_t idesc_s = idesc_bf16(TB, TB);
       const uint32_t sb = smem_u32(base);
-      const uint64_t ds_kmaj = make_sw128_desc(sb + OFF_DS);
-      const uint64_t ds_mn = make_sw128_mn_desc(sb + OFF_DS, TILE);  // queries 64.. one tile further
       const uint64_t v_kmaj = make_sw128_desc(sb + OFF_V);
       const uint64_t ones_s = make_sw32_desc(sb + OFF_ONE), ones_dp = make_sw32_desc(sb + OFF_ONE + TERM_BYTES);
       bool ok = true;
       int g = 0, n = 0;
-      // gradient products of pair gb, the item_n-th item's first and / or last one
-      auto back = [&](int gb, int item_n, bool first, bool last) -> bool {
-        if (!mbar_wait(&sm->p_full, (uint32_t)gb & 1u)) return false;
-        if (!mbar_wait(&sm->dq_free, (uint32_t)(gb & 1) ^ 1u)) return false;
-        if (first && !mbar_wait(&sm->acc_free, (uint32_t)(item_n & 1) ^ 1u)) return false;
-        tc_fence_after();
-        const int st = gb % STG, kb = item_n & 1;
-        const uint64_t q_mn = make_sw128_mn_desc(sb + OFF_Q + st * TILE, TILE);
-        const uint64_t do_mn = make_sw128_mn_desc(sb + OFF_DO + st * TILE, TILE);
-        const uint64_t k_mn = make_sw128_mn_desc(sb + OFF_K + kb * TILE, TILE);
-        // K = 128 queries in steps of 16
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_bf16_ts(tmem + COL_DV, tmem + COL_P + 8 * k, do_mn + 128u * (uint64_t)k, idesc_kv,
-                      (!first || k > 0) ? 1u : 0u);
-        mma_commit(&sm->p_free);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          // K-major dS^T: queries 64.. live in the second 16 KB block
-          const uint64_t koff = (uint64_t)(((k >> 2) * TILE) >> 4) + 2u * (uint64_t)(k & 3);
-          mma_bf16_ss(tmem + COL_DK, ds_kmaj + koff, q_mn + 128u * (uint64_t)k, idesc_kv, (!first || k > 0) ? 1u : 0u);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)  // K = 128 keys in steps of 16
-          mma_bf16_ss(tmem + COL_DQ, ds_mn + 128u * (uint64_t)k, k_mn + 128u * (uint64_t)k, idesc_q, k > 0 ? 1u : 0u);
-        mma_commit(&sm->ds_free);
-        mma_commit(&sm->dq_full);
-        mma_commit(&sm->q_empty[st]);
-        if (last) {
-          mma_commit(&sm->acc_full);
-          mma_commit(&sm->k_empty[kb]);
-        }
-        return true;
-      };
-      // the pair whose gradient products are still to be issued (always pair g - 1)
-      int last_n = 0;
-      bool last_first = false, last_last = false;
       for (int rnd = 0, it = item_at(0); it < n_items && ok && !sm->abort; it = item_at(++rnd), ++n) {
         const BItem x = make_item(load_item(pb, it, hd, fl, n_far), win, fl);
         const int kb = n & 1;
@@ -434,13 +395,70 @@ __global__ void __launch_bounds__(THREADS, 1)
           mma_bf16_ss(tmem + COL_DP, ones_dp, terms, idesc_s, 1u);
           mma_commit(&sm->s_full);
           if (i == x.nq - 1) mma_commit(&sm->v_empty);
-          if (g > 0 && !back(g - 1, last_n, last_first, last_last)) { ok = false; break; }
-          last_n = n;
-          last_first = i == 0;
-          last_last = i == x.nq - 1;
         }
       }
-      if (ok && g > 0) ok = back(g - 1, last_n, last_first, last_last);
+      if (!ok) {
+        latch_error(err, ERRBIT_TIMEOUT);
+        sm->abort = 1;
+      }
+      // every MMA of this thread has completed before tensor memory may be released
+      mma_commit(&sm->s_done);
+      mbar_wait(&sm->s_done, 0);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ MMA issuer: dV, dK, dQ
+    if (lane == 0) {
+      constexpr uint32_t idesc_kv = idesc_bf16(TB, DH) | kIdescBMn;             // dV, dK
+      constexpr uint32_t idesc_q = idesc_bf16(TB, DH) | kIdescAMn | kIdescBMn;  // dQ
+      const uint32_t sb = smem_u32(base);
+      const uint64_t ds_kmaj = make_sw128_desc(sb + OFF_DS);
+      const uint64_t ds_mn = make_sw128_mn_desc(sb + OFF_DS, TILE);  // queries 64.. one tile further
+      bool ok = true;
+      int g = 0, n = 0;
+      for (int rnd = 0, it = item_at(0); it < n_items && ok && !sm->abort; it = item_at(++rnd), ++n) {
+        const BItem x = make_item(load_item(pb, it, hd, fl, n_far), win, fl);
+        const int kb = n & 1;
+        const uint64_t k_mn = make_sw128_mn_desc(sb + OFF_K + kb * TILE, TILE);
+        for (int i = 0; i < x.nq; ++i, ++g) {
+          const int st = g % STG;
+          // the operands have landed (the pair's scores were made of them), P^T and dS^T are there,
+          // the previous dQ has been read, and so have the previous item's dK and dV
+          if (!mbar_wait(&sm->k_full[kb], (uint32_t)(n >> 1) & 1u) ||
+              !mbar_wait(&sm->q_full[st], (uint32_t)(g / STG) & 1u) || !mbar_wait(&sm->p_full, (uint32_t)g & 1u) ||
+              !mbar_wait(&sm->dq_free, (uint32_t)(g & 1) ^ 1u) ||
+              (i == 0 && !mbar_wait(&sm->acc_free, (uint32_t)(n & 1) ^ 1u))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t q_mn = make_sw128_mn_desc(sb + OFF_Q + st * TILE, TILE);
+          const uint64_t do_mn = make_sw128_mn_desc(sb + OFF_DO + st * TILE, TILE);
+          // K = 128 queries in steps of 16
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_ts(tmem + COL_DV, tmem + COL_P + 8 * k, do_mn + 128u * (uint64_t)k, idesc_kv,
+                        (i > 0 || k > 0) ? 1u : 0u);
+          mma_commit(&sm->p_free);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            // K-major dS^T: queries 64.. live in the second 16 KB block
+            const uint64_t koff = (uint64_t)(((k >> 2) * TILE) >> 4) + 2u * (uint64_t)(k & 3);
+            mma_bf16_ss(tmem + COL_DK, ds_kmaj + koff, q_mn + 128u * (uint64_t)k, idesc_kv, (i > 0 || k > 0) ? 1u : 0u);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // K = 128 keys in steps of 16
+            mma_bf16_ss(tmem + COL_DQ, ds_mn + 128u * (uint64_t)k, k_mn + 128u * (uint64_t)k, idesc_q,
+                        k > 0 ? 1u : 0u);
+          mma_commit(&sm->ds_free);
+          mma_commit(&sm->dq_full);
+          mma_commit(&sm->q_empty[st]);
+          if (i == x.nq - 1) {
+            mma_commit(&sm->acc_full);
+            mma_commit(&sm->k_empty[kb]);
+          }
+        }
+      }
       if (!ok) {
         latch_error(err, ERRBIT_TIMEOUT);
         sm->abort = 1;
