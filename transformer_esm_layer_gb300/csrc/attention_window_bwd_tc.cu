@@ -37,11 +37,11 @@
 //                S^T and dP^T row segment, forms P^T = 2^(S^T log2(e) / 8) and dS^T = P^T dP^T
 //                in registers (f32x2 pairs), hands S^T back, then writes P^T into tensor memory
 //                (once the previous pair's dV product has read it) and dS^T into shared
-//                memory (K-major, 128-byte swizzle), both as bf16; an item's dK and dV are taken out of TMEM after the
-//                next item's first pair has been handed over, dK scaled and turned back through RoPE;
+//                memory (K-major, 128-byte swizzle), both as bf16;
 //   warps 12..15 thread r owns query r of the tile: reads dQ_i from TMEM, stages it in shared
 //                memory and adds it into an fp32 accumulator in global memory with TMA
-//                reduce-add (several key tiles contribute to each query row).
+//                reduce-add (several key tiles contribute to each query row); after an item's last
+//                pair they also bring out its dK and dV.
 // Every mbarrier wait is bounded; on timeout the kernel latches an error bit and stops.
 //
 // What bounds it: the tensor core, by way of shared memory.  A pair is 34 MMAs of 75 to 100 cycles
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(&sm->dq_full, 1);
     mbar_init(&sm->dq_free, 4);
     mbar_init(&sm->acc_full, 1);
-    mbar_init(&sm->acc_free, 4 * kComputeWgs);
+    mbar_init(&sm->acc_free, 4);
     mbar_init(&sm->s_done, 1);
     mbar_init(&sm->mma_done, 1);
     sm->abort = 0;
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= kWarpCompute && warp < kWarpDq) {
-    // ------------------------------------------------------------ P^T / dS^T, dK / dV
+    // ------------------------------------------------------------ P^T / dS^T
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
     const int wg = (warp - kWarpCompute) >> 2;  // warpgroup: queries QPW wg .. QPW wg + QPW - 1 of each tile
     const int wq = warp & 3;
@@ -482,68 +482,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int unit0 = ((QPW * wg) & 63) >> 3;
     const uint32_t col_p = tmem + lane_off + COL_P + QPW / 2 * wg;
     bool ok = true;
-    int g = 0, n = 0;
-    // The item whose last gradient products may still run: its dK (warpgroup 0; scaled, RoPE undone)
-    // and dV (warpgroup 1) are taken out once the next item's first P^T and dS^T have been handed
-    // over, in 32-byte pieces straight from the threads that hold a key each.
-    const bool wide = (reinterpret_cast<uintptr_t>(dqkv) & 31) == 0;
-    auto take_out = [&](int item_n) -> bool {
-      const BItem x = make_item(load_item(pb, item_at(item_n), hd, fl, n_far), win, fl);
-      if (!mbar_wait_warp(&sm->acc_full, (uint32_t)item_n & 1u)) return false;
-      tc_fence_after();
-      const bool kval = r < x.krows;
-      const int key = x.k0 + r;
-      int p = key - x.s0;
-      p = p < 0 ? 0 : (p >= max_pos ? max_pos - 1 : p);
-      const bool part = x.slot >= 0 && (x.far || r < win.sinks);  // a sink's partial sums, fp32
-      __nv_bfloat16* out = dqkv + (size_t)key * 3 * d + (wg == 0 ? d : 2 * d) + x.h * DH;
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int c0 = wg == 0 ? 16 * v : 32 * v;  // dK: first pair j0; dV: first column
-        const int c1 = wg == 0 ? c0 + 32 : c0 + 16;
-        float a[16], b[16];
-        tmem_ld16x2(tmem + lane_off + (wg == 0 ? COL_DK : COL_DV) + c0, tmem + lane_off + (wg == 0 ? COL_DK : COL_DV) + c1, a, b);
-        if (v == 1) {  // this warp's last TMEM read of the item
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->acc_free);
-        }
-        if (kval && part) {
-          float* dst = fl.partial + (((size_t)x.slot * heads + x.h) * win.sinks + r) * (2 * DH) + (wg == 0 ? 0 : DH);
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            *reinterpret_cast<float4*>(dst + c0 + j) = make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]);
-            *reinterpret_cast<float4*>(dst + c1 + j) = make_float4(b[j], b[j + 1], b[j + 2], b[j + 3]);
-          }
-        }
-        if (wg == 0) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {  // pair (c0 + j, c0 + j + 32) turned back by its angle
-            const float u = a[j] * 0.125f, w = b[j] * 0.125f;
-            a[j] = u;
-            b[j] = w;
-            if (rope != nullptr) {
-              const int jj = c0 + j;
-              const float2 cs = __ldg(rope + ((size_t)(jj >> 1) * max_pos + p) * 2 + (jj & 1));
-              a[j] = u * cs.x + w * cs.y;
-              b[j] = w * cs.x - u * cs.y;
-            }
-          }
-        }
-        if (kval && !part) {
-          uint32_t w[2][8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            w[0][j] = pack_bf16x2(a[2 * j], a[2 * j + 1]);
-            w[1][j] = pack_bf16x2(b[2 * j], b[2 * j + 1]);
-          }
-          store32(out + c0, w[0], wide);
-          store32(out + c1, w[1], wide);
-        }
-      }
-      return true;
-    };
-    for (int rnd = 0, it = item_at(0); it < n_items && ok; it = item_at(++rnd), ++n) {
+    int g = 0;
+    for (int rnd = 0, it = item_at(0); it < n_items && ok; it = item_at(++rnd)) {
       const BItem x = make_item(load_item(pb, it, hd, fl, n_far), win, fl);
       const bool kval = r < x.krows;
       const int key = x.k0 - x.s0 + r;
@@ -612,16 +552,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_async_smem();  // generic-proxy writes of dS^T before the tensor core reads
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->p_full);
-        if (i == 0 && n > 0 && !take_out(n - 1)) { ok = false; break; }
       }
     }
-    if (ok) ok = take_out(n - 1);
     if (!ok) {
       latch_error(err, ERRBIT_TIMEOUT);
       sm->abort = 1;
     }
   } else if (warp >= kWarpDq) {
-    // ------------------------------------------------------------ dQ accumulation
+    // ------------------------------------------------------------ dQ accumulation, dK / dV
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDq));
     // Each warp adds its 32 rows of dQ_i (fp32) into the global accumulator with TMA reduce-add,
     // staged 32 columns at a time (128-byte swizzle); rows of queries past the sequence end hold
@@ -630,13 +568,73 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     uint8_t* stage = base + OFF_DQ + wq * DQ_WARP_BYTES;
     if (lane == 0) tma_prefetch_desc(&tm_dq);
+    const bool wide = (reinterpret_cast<uintptr_t>(dqkv) & 31) == 0;
     bool ok = true;
-    int g = 0;
-    for (int rnd = 0, it = item_at(0); it < n_items && ok; it = item_at(++rnd)) {
+    int g = 0, n = 0;
+    // An item's dK (scaled, RoPE undone) and dV, in 32-byte pieces straight from the threads that hold
+    // a key each: four parts of 32 values, v = 0, 1 dV columns 32 v .. + 31 and v = 2, 3 dK's pairs
+    // (j, j + 32), j in 16 (v - 2) .. + 15.
+    auto take_out = [&](const BItem& x) {
+      const int r = wq * 32 + lane, key = x.k0 + r;
+      const bool kval = r < x.krows, part = x.slot >= 0 && (x.far || r < win.sinks);  // a sink's partial sums, fp32
+      int p = key - x.s0;
+      p = p < 0 ? 0 : (p >= max_pos ? max_pos - 1 : p);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const bool is_k = v >= 2;
+        const int c0 = is_k ? 16 * (v - 2) : 32 * v, c1 = is_k ? c0 + 32 : c0 + 16;
+        float a[16], b[16];
+        tmem_ld16x2(tmem + lane_off + (is_k ? COL_DK : COL_DV) + c0, tmem + lane_off + (is_k ? COL_DK : COL_DV) + c1, a, b);
+        if (v == 3) {  // the last TMEM read of the item
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->acc_free);
+        }
+        if (!kval) continue;
+        if (part) {
+          float* dst = fl.partial + (((size_t)x.slot * heads + x.h) * win.sinks + r) * (2 * DH) + (is_k ? 0 : DH);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            *reinterpret_cast<float4*>(dst + c0 + j) = make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]);
+            *reinterpret_cast<float4*>(dst + c1 + j) = make_float4(b[j], b[j + 1], b[j + 2], b[j + 3]);
+          }
+          continue;
+        }
+        if (is_k) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {  // pair (c0 + j, c0 + j + 32) turned back by its angle
+            const float u = a[j] * 0.125f, w = b[j] * 0.125f;
+            a[j] = u;
+            b[j] = w;
+            if (rope != nullptr) {
+              const int jj = c0 + j;
+              const float2 cs = __ldg(rope + ((size_t)(jj >> 1) * max_pos + p) * 2 + (jj & 1));
+              a[j] = u * cs.x + w * cs.y;
+              b[j] = w * cs.x - u * cs.y;
+            }
+          }
+        }
+        __nv_bfloat16* out = dqkv + (size_t)key * 3 * d + (is_k ? d : 2 * d) + x.h * DH;
+        uint32_t w[2][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          w[0][j] = pack_bf16x2(a[2 * j], a[2 * j + 1]);
+          w[1][j] = pack_bf16x2(b[2 * j], b[2 * j + 1]);
+        }
+        store32(out + c0, w[0], wide);
+        store32(out + c1, w[1], wide);
+      }
+    };
+    for (int rnd = 0, it = item_at(0); it < n_items && ok; it = item_at(++rnd), ++n) {
       const BItem x = make_item(load_item(pb, it, hd, fl, n_far), win, fl);
       for (int i = 0; i < x.nq; ++i, ++g) {
         if (!mbar_wait_warp(&sm->dq_full, (uint32_t)g & 1u)) { ok = false; break; }
         tc_fence_after();
+        if (i == x.nq - 1) {  // the item's accumulators first: the next item's products wait for them
+          if (!mbar_wait_warp(&sm->acc_full, (uint32_t)n & 1u)) { ok = false; break; }
+          tc_fence_after();
+          take_out(x);
+        }
         uint32_t a[2][32];
         tmem_ld32_nowait(tmem + lane_off + COL_DQ, a[0]);
         tmem_ld32_nowait(tmem + lane_off + COL_DQ + 32, a[1]);
