@@ -434,12 +434,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_fence_after();
           const uint64_t q_mn = make_sw128_mn_desc(sb + OFF_Q + st * TILE, TILE);
           const uint64_t do_mn = make_sw128_mn_desc(sb + OFF_DO + st * TILE, TILE);
-          // K = 128 queries in steps of 16
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_bf16_ts(tmem + COL_DV, tmem + COL_P + 8 * k, do_mn + 128u * (uint64_t)k, idesc_kv,
-                        (i > 0 || k > 0) ? 1u : 0u);
-          mma_commit(&sm->p_free);
+          // dK and dQ first: what the next pair writes into dS^T's place takes longest.  K = 128
+          // queries (dQ: keys) in steps of 16
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             // K-major dS^T: queries 64.. live in the second 16 KB block
@@ -447,11 +443,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             mma_bf16_ss(tmem + COL_DK, ds_kmaj + koff, q_mn + 128u * (uint64_t)k, idesc_kv, (i > 0 || k > 0) ? 1u : 0u);
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // K = 128 keys in steps of 16
+          for (int k = 0; k < 8; ++k)
             mma_bf16_ss(tmem + COL_DQ, ds_mn + 128u * (uint64_t)k, k_mn + 128u * (uint64_t)k, idesc_q,
                         k > 0 ? 1u : 0u);
           mma_commit(&sm->ds_free);
           mma_commit(&sm->dq_full);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_ts(tmem + COL_DV, tmem + COL_P + 8 * k, do_mn + 128u * (uint64_t)k, idesc_kv,
+                        (i > 0 || k > 0) ? 1u : 0u);
+          mma_commit(&sm->p_free);
           mma_commit(&sm->q_empty[st]);
           if (i == x.nq - 1) {
             mma_commit(&sm->acc_full);
@@ -533,13 +534,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->s_free);
-        // P^T may be overwritten once the previous pair's dV product has read it, dS^T once its dK
-        // and dQ products have
-        if (!mbar_wait_warp(&sm->p_free, (uint32_t)(g & 1) ^ 1u)) { ok = false; break; }
-        tc_fence_after();
-        static_assert(NSUB == 4, "two 16-column stores");
-        tmem_st16(col_p, &pw[0][0]);
-        tmem_st16(col_p + 16, &pw[2][0]);
+        // dS^T may be overwritten once the previous pair's dK and dQ products have read it, P^T once its
+        // dV product has
         if (!mbar_wait_warp(&sm->ds_free, (uint32_t)(g & 1) ^ 1u)) { ok = false; break; }
 #pragma unroll
         for (int sub = 0; sub < NSUB; ++sub)
@@ -547,6 +543,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int h2 = 0; h2 < 2; ++h2)
             *reinterpret_cast<uint4*>(sDS + swz(r, unit0 + 2 * sub + h2)) =
                 make_uint4(dw[sub][4 * h2], dw[sub][4 * h2 + 1], dw[sub][4 * h2 + 2], dw[sub][4 * h2 + 3]);
+        if (!mbar_wait_warp(&sm->p_free, (uint32_t)(g & 1) ^ 1u)) { ok = false; break; }
+        tc_fence_after();
+        static_assert(NSUB == 4, "two 16-column stores");
+        tmem_st16(col_p, &pw[0][0]);
+        tmem_st16(col_p + 16, &pw[2][0]);
         tmem_st_wait();
         tc_fence_before();
         fence_async_smem();  // generic-proxy writes of dS^T before the tensor core reads
