@@ -170,6 +170,53 @@ def test_forward_fp32(window):
     assert torch.all((o.double() - ro).abs() <= 2.0 ** -6 * bo)
 
 
+@pytest.mark.parametrize("lengths", [[1] * 70, [7, 0, 3] * 20, [700], [31, 33, 1, 64, 65, 500], [32] * 9])
+@pytest.mark.parametrize("window", [(5, 0, 2), (100, 30, 40), (0, 0, 0), (-1, 0, 0), (3, -1, 128), (2000, 64, 1)])
+@pytest.mark.parametrize("heads,dh", [(4, 64), (3, 20), (8, 32), (2, 2)])
+def test_forward_fp32_batches(lengths, window, heads, dh):
+    """Blocks of several sequences, head sizes below 64; the bound of the test above."""
+    from transformer_esm_layer_gb300.binding import EsmEncoder
+    d, T = heads * dh, sum(lengths)
+    g = torch.Generator(device="cuda").manual_seed(T + heads)
+    qkv = 1.5 * torch.randn(T, 3 * d, device="cuda", generator=g)
+    cu = torch.from_numpy(synth.cu_seqlens_from_lengths(lengths)).cuda()
+    enc = EsmEncoder(1, d, heads, 2 * d, max_positions=4096, precision="fp32")
+    o, behind = _guarded((T, d), torch.float32)
+    o.fill_(float("nan"))
+    enc.op_attention_window(qkv, cu, max(lengths), window, o)
+    assert enc.check_status() == 0 and torch.all(behind == 7)
+    at = 0
+    for L in lengths:
+        q, k, v = qkv[at:at + L].double().view(L, 3, heads, dh).permute(1, 2, 0, 3)
+        p = (q @ k.transpose(1, 2) / dh ** 0.5).masked_fill(~visible(L, window, device="cuda"), -float("inf")).softmax(2)
+        ref, a = ((p @ x).transpose(0, 1).reshape(L, d) for x in (v, v.abs()))
+        assert torch.all((o[at:at + L].double() - ref).abs() <= 2.0 ** -14 * (a + ref.abs()) + 1e-30)
+        at += L
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_unseen_keys_and_values_have_no_influence_fp32(bad):
+    heads, lengths, window = 4, [200, 150, 400], (30, 20, 2)
+    qkv, cu, _ = _inputs(lengths, heads, 12, torch.float32)
+    enc = _enc(heads, "fp32")
+    want, _ = _forward(enc, qkv, cu, lengths, window, heads, lse=False)
+    spoiled = qkv.clone()
+    spoiled[[205, 450, 749], 64 * heads:] = bad
+    o, _ = _forward(enc, spoiled, cu, lengths, window, heads, lse=False)
+    sees = torch.zeros(len(qkv), dtype=torch.bool, device="cuda")
+    start = 0
+    for L in lengths:
+        ok = visible(L, window, device="cuda")
+        for r in (205, 450, 749):
+            if start <= r < start + L:
+                sees[start:start + L] |= ok[:, r - start]
+        start += L
+    ro, bo, _, _ = _reference(qkv, lengths, heads, window)
+    assert torch.all((o[~sees].double() - ro[~sees]).abs() <= 2.0 ** -6 * bo[~sees])
+    if bad != bad:
+        assert torch.isnan(o[sees]).all()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_unseen_keys_and_values_have_no_influence(bad):
     heads, lengths, window = 4, [200, 150, 400], (30, 20, 2)

@@ -282,7 +282,9 @@ esm_status run_attention(esm_encoder* h, const AttnWindow& win, const void* qkv,
                          float* lse = nullptr, const PackedBatch& batch = PackedBatch{}) {
   const int d = h->cfg.hidden, H = h->cfg.heads;
   if (h->cfg.precision == ESM_FP32) {
-    launch_attention_f32(static_cast<const float*>(qkv), static_cast<float*>(o), d, H, T, pb, st, win);
+    const float* x = static_cast<const float*>(qkv);
+    if (is_full(win)) launch_attention_f32(x, static_cast<float*>(o), d, H, T, pb, st);
+    else launch_attention_window_f32(x, static_cast<float*>(o), d, H, T, pb, win, st);
     return cuda_status(cudaGetLastError());
   }
   const CUtensorMap* tq = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 128, 2);
@@ -1643,7 +1645,12 @@ esm_status esm_op_attention_window(esm_encoder_t* h, const void* qkv, const int3
         cudaMemsetAsync(pb.seg_id, 0, 4 * (size_t)total_tokens, st) != cudaSuccess)
       return ESM_ERR_CUDA;
     launch_pack_index(cu_seqlens, num_seqs, total_tokens, max_seqlen, h->cfg.max_positions, pb, h->d_err, st);
-  } else if (!is_full(win) && attention_window_direct(num_seqs, L.max_items, h->cfg.heads)) {
+    // (a full window too: the encoder's full attention keeps its slower kernel and its sums' order)
+    launch_attention_window_f32(static_cast<const float*>(qkv), static_cast<float*>(o), h->cfg.hidden, h->cfg.heads,
+                                total_tokens, pb, win, st);
+    return cuda_status(cudaGetLastError());
+  }
+  if (!is_full(win) && attention_window_direct(num_seqs, L.max_items, h->cfg.heads)) {
     // a small batch: the attention kernel finds its items itself, which saves a launch
     batch = PackedBatch{cu_seqlens, num_seqs, total_tokens, max_seqlen, h->cfg.max_positions};
   } else {

@@ -225,7 +225,9 @@ cudaError_t launch_attention_window_tc(const CUtensorMap* tm_qkv, const CUtensor
                                        float* amax, unsigned* err, cudaStream_t st, float* lse = nullptr,
                                        int lse_stride = 0);
 void launch_attention_f32(const float* qkv, float* o, int d, int heads, int T, const PackBuffers& pb,
-                          cudaStream_t st, const AttnWindow& win = kFullWindow);
+                          cudaStream_t st);
+void launch_attention_window_f32(const float* qkv, float* o, int d, int heads, int T, const PackBuffers& pb,
+                                 const AttnWindow& win, cudaStream_t st);
 
 // tcgen05 attention backward (attention_bwd_tc.cu): dqkv (bf16 [T, 3d]) from the saved
 // qkv (RoPE applied), O, the forward's lse ([heads, T]) and dO (bf16 [T, d], tm_do a
