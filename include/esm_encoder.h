@@ -373,7 +373,8 @@ ESM_API esm_status esm_op_attention(esm_encoder_t* h, const void* qkv, const int
                             void* workspace, size_t workspace_bytes, esm_stream_t stream);
 
 /* esm_op_attention with a window, given in the call (the handle's own window plays no part).
- * qkv device [T, 3*hidden] in the activation dtype, o device [T, hidden], both 16-byte aligned.
+ * qkv device [T, 3*hidden] in the activation dtype, o device [T, hidden], both 16-byte aligned and
+ * apart from each other.
  * lse: device float32 [heads, T], head-major, or NULL: the natural-log softmax normaliser of
  * every row over the keys it sees, which the backward needs (bf16 activations only: an ESM_FP32
  * handle with lse is ESM_ERR_UNSUPPORTED).  Every row sees itself, so no row is empty.  Keys and
@@ -558,8 +559,8 @@ ESM_API esm_status esm_op_attention_backward(esm_encoder_t* h, const void* qkv, 
                                              size_t workspace_bytes, esm_stream_t stream);
 
 /* esm_op_attention_backward with a window (bf16, head_dim 64): dqkv = dL/d(q | k | v) from qkv, o
- * and lse of esm_op_attention_window with the same window, and d_o = dL/do.  qkv, d_o and o must
- * be finite.  The float32 sums over key tiles behind dq, and only those, are added in no fixed
+ * and lse of esm_op_attention_window with the same window, and d_o = dL/do.  qkv, d_o, o and lse
+ * must be finite, and dqkv apart from qkv and d_o.  The float32 sums over key tiles behind dq, and only those, are added in no fixed
  * order. */
 ESM_API esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, const void* o, const float* lse,
                                                     const void* d_o, const int32_t* cu_seqlens, int num_seqs,
@@ -599,7 +600,8 @@ ESM_API esm_status esm_op_distill_loss(esm_encoder_t* h, const void* logits, esm
  * forward's count, or the global batch's in data-parallel training; with n <= 0 every gradient is
  * 0) or 1 if loss_count is NULL.  lse: of esm_op_distill_loss for the same logits and temperature.
  * d_logits: of the logits' type, rows d_stride >= vocab elements apart; it may be the logits
- * themselves (then with the same stride), and must not overlap them otherwise.  Elements between
+ * themselves (then with the same stride).  Otherwise no value may be in both; rows of the two may
+ * alternate in one buffer if their strides are the same (ESM_ERR_INVALID_ARG where this is broken).  Elements between
  * the rows are left as they are. */
 ESM_API esm_status esm_op_distill_loss_backward(esm_encoder_t* h, const void* logits, esm_precision logits_type,
                                                 long long logits_stride, const int32_t* teacher_ids,

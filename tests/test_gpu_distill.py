@@ -305,6 +305,16 @@ def test_refusals(enc):
                  (z[:, ::2], ids, tl)):
         with pytest.raises(ValueError):
             enc.op_distill_loss(*args, 1.0, loss)
+    wide = torch.zeros(9, 100, device="cuda")
+    for zz, dd in ((wide[:8, :40], wide[:8, 39:79]), (wide[:8, 40:80], wide[:8, 1:41]), (wide[:8, :40], wide[1:, :40]),
+                   (wide.view(-1)[:480].view(8, 60)[:, :40], wide[:8, :40])):
+        with pytest.raises(EsmError) as e:
+            enc.op_distill_loss_backward(zz, ids, tl, 1.0, lse, dd)
+        assert e.value.status == 1
+    wide[:8, :40] = z                                     # side by side in one buffer
+    enc.op_distill_loss_backward(wide[:8, :40], ids, tl, 1.0, lse, wide[:8, 60:])
+    enc.op_distill_loss_backward(z, ids, tl, 1.0, lse, d)
+    assert torch.equal(wide[:8, 60:], d) and torch.equal(wide[:8, :40], z)
     for dd in (d.bfloat16(), d[:4], d.t().contiguous().t(), d.cpu()):
         with pytest.raises(ValueError):
             enc.op_distill_loss_backward(z, ids, tl, 1.0, lse, dd)

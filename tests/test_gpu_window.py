@@ -509,6 +509,17 @@ def test_refusals():
         args.update(bad)
         with pytest.raises(ValueError):
             enc.op_attention_window(qkv, cu, 300, (1, 1, 0), args["o"], lse=args["lse"])
+    buf = torch.zeros(300 * 4 * 256, dtype=torch.bfloat16, device="cuda")   # outputs over inputs
+    inside = buf[:300 * 768].view(300, 768)
+    with pytest.raises(EsmError) as e:
+        enc.op_attention_window(inside, cu, 300, (1, 1, 0), buf[300 * 767:300 * 767 + 300 * 256].view(300, 256))
+    assert e.value.status == 1
+    with pytest.raises(EsmError) as e:
+        enc.op_attention_window_backward(qkv, o, lse, o, cu, 300, (1, 1, 0), qkv)
+    assert e.value.status == 1
+    with pytest.raises(EsmError) as e:
+        enc.op_attention_window_backward(qkv, o, lse, buf[256 * 8:256 * 308].view(300, 256), cu, 300, (1, 1, 0), inside)
+    assert e.value.status == 1
     with pytest.raises(ValueError):
         enc.op_attention_window(qkv[:, :-1], cu, 300, (1, 1, 0), o)
     with pytest.raises(ValueError):

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads)
 // ---------------------------------------------------------------- warp and block forms
 // W warps per row (1 or kWarps), EN teacher entries per thread.  The forward loads the next
 // kRowUnits units of each thread before it works on the present ones, which keeps 64 bytes per
-// thread in flight through the exponentials (8192 x 32000 bf16: 5.9 TB/s; loads and work in
+// thread in flight through the exponentials (8192 x 32000 bf16: 5.7 TB/s; loads and work in
 // turn 4.7).
 // 16-byte unit of a row as floats.
 template <typename E>

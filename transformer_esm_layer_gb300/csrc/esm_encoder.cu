@@ -1615,6 +1615,11 @@ static AttnPlan window_plan(const esm_encoder* h, const int32_t* cu, int B, int 
                   win, backward, (backward ? 1 : 2) * h->num_sms / h->cfg.heads};
 }
 
+static bool disjoint(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x + na <= y || y + nb <= x;
+}
+
 esm_status esm_op_attention_window_workspace_size(const esm_encoder_t* h, int total_tokens, int num_seqs,
                                                   const esm_attn_window* window, int backward, size_t* bytes) {
   AttnWindow win;
@@ -1634,6 +1639,9 @@ esm_status esm_op_attention_window(esm_encoder_t* h, const void* qkv, const int3
   if (!qkv || !cu_seqlens || !o || num_seqs == 0 || max_seqlen <= 0 || max_seqlen > h->cfg.max_positions)
     return ESM_ERR_INVALID_ARG;
   if (!aligned(qkv, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(cu_seqlens, 4)) return ESM_ERR_INVALID_ARG;
+  // (blocks read q, k and v of rows that others write)
+  const size_t row = (size_t)h->cfg.hidden * h->act_bytes() * total_tokens;
+  if (!disjoint(qkv, 3 * row, o, row)) return ESM_ERR_INVALID_ARG;
   const WindowWs L = window_ws(h, total_tokens, num_seqs, win, false);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return ESM_ERR_WORKSPACE;
   if (workspace == h->train_ws) h->train_buf = nullptr;  // as check_ws: the pending backward's index is overwritten
@@ -1673,6 +1681,8 @@ esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, c
   if (!aligned(qkv, 16) || !aligned(o, 16) || !aligned(d_o, 16) || !aligned(dqkv, 16) || !aligned(lse, 4) ||
       !aligned(cu_seqlens, 4))
     return ESM_ERR_INVALID_ARG;
+  const size_t row = (size_t)h->cfg.hidden * 2 * total_tokens;
+  if (!disjoint(dqkv, 3 * row, qkv, 3 * row) || !disjoint(dqkv, 3 * row, d_o, row)) return ESM_ERR_INVALID_ARG;
   const WindowWs L = window_ws(h, total_tokens, num_seqs, win, true);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return ESM_ERR_WORKSPACE;
   if (workspace == h->train_ws) h->train_buf = nullptr;
@@ -1735,6 +1745,17 @@ esm_status esm_op_distill_loss_backward(esm_encoder_t* h, const void* logits, es
   if ((total_tokens > 0 && (!lse || !d_logits)) || !aligned(lse, 4) || !aligned(loss_count, 4) ||
       !aligned(d_logits, logits_type == ESM_FP32 ? 4 : 2))
     return ESM_ERR_INVALID_ARG;
+  if (total_tokens > 0 && d_logits != logits) {
+    // rows of the two may alternate in one buffer, but no value of one may be a value of the other
+    const size_t es = logits_type == ESM_FP32 ? 4 : 2, n = (size_t)total_tokens - 1;
+    const size_t na = (n * (size_t)logits_stride + vocab) * es, nb = (n * (size_t)d_stride + vocab) * es;
+    if (!disjoint(logits, na, d_logits, nb)) {
+      const long long pitch = logits_stride * (long long)es, width = vocab * (long long)es;
+      long long off = (long long)(reinterpret_cast<uintptr_t>(d_logits) - reinterpret_cast<uintptr_t>(logits)) % pitch;
+      if (off < 0) off += pitch;
+      if (d_stride != logits_stride || off < width || off > pitch - width) return ESM_ERR_INVALID_ARG;
+    }
+  }
   a.lse = const_cast<float*>(lse);
   a.loss_count = loss_count;
   a.d_logits = d_logits;
