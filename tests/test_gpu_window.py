@@ -411,6 +411,46 @@ def test_backward_is_repeatable_but_for_dq():
     assert torch.equal(again[:, 256:], dqkv[:, 256:])
 
 
+def test_backward_of_the_longest_sequences_at_sampled_rows():
+    """Five sequences of 65536 tokens at 40 heads: gradients past 2^31 elements, and sinks that 65536
+    queries see (their bound is that of _backward_reference, over one key's queries)."""
+    heads, L, B, window = 40, 65536, 5, (256, 100, 6)
+    enc = _enc(heads)
+    qkv, cu, g = _inputs([L] * B, heads, 29)
+    o = torch.empty(len(qkv), 64 * heads, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(heads, len(qkv), device="cuda")
+    enc.op_attention_window(qkv, cu, L, window, o, lse=lse)
+    d_o = torch.randn(len(qkv), 64 * heads, device="cuda", generator=g, dtype=torch.bfloat16)
+    dqkv = torch.empty_like(qkv)
+    enc.op_attention_window_backward(qkv, o, lse, d_o, cu, L, window, dqkv)
+    assert enc.check_status() == 0
+    x, grad = qkv.view(B, L, 3, heads, 64)[-1], dqkv.view(B, L, 3, heads, 64)[-1]
+    oo, do, ll = o.view(B, L, heads, 64)[-1], d_o.view(B, L, heads, 64)[-1], lse.view(heads, B, L)[:, -1]
+
+    def pairs(i, j):
+        """P, dS and the bound of dS for one query and its keys, or one key and its queries: [n, heads]."""
+        q, k, v, dd = x[i, 0].double(), x[j, 1].double(), x[j, 2].double(), do[i].double()
+        p = ((q * k).sum(-1) / 8 - ll.t()[i].double()).exp()
+        ds = p * ((dd * v).sum(-1) - (dd * oo[i].double()).sum(-1))
+        size = (dd.abs() * v.abs()).sum(-1) + (dd * oo[i].double()).abs().sum(-1)
+        return p, ds, (2.0 ** -8 + 2.0 ** -12) * ds.abs() + 2.0 ** -17 * p * size, q, k, dd
+
+    def check(got, w, e, other):
+        ref = (w[..., None] * other).sum(0)
+        assert torch.all((got.double() - ref).abs() <= (e[..., None] * other.abs()).sum(0) + 2.0 ** -8 * ref.abs() + 1e-30)
+
+    for r in (0, 5, 6, 300, 1383, 1384, 3431, 3432, 40000, 65407, 65408, 65535):
+        t = torch.tensor([r], device="cuda")
+        j = visible(L, window, device="cuda", rows=t)[0].nonzero().squeeze(1)
+        p, ds, e, _, k, _ = pairs(t, j)
+        check(grad[r, 0], ds / 8, e / 8, k)
+        lo = 0 if window[1] >= r else r - window[1]
+        hi = L if r < window[2] else min(L, r + window[0] + 1)
+        p, ds, e, q, _, dd = pairs(torch.arange(lo, hi, device="cuda"), t)
+        check(grad[r, 1], ds / 8, e / 8, q)
+        check(grad[r, 2], p, (2.0 ** -8 + 2.0 ** -12) * p, dd)
+
+
 # --------------------------------------------------------------------------- calls
 def test_other_stream_graph_replay_and_two_workspaces():
     heads, lengths, window = 4, [300, 77, 129], (40, 40, 2)
