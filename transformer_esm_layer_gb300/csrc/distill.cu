@@ -8,7 +8,8 @@
 //   lse  = log sum_v exp(z_v / t),
 //   dloss/dz_v = t (q_v - sum_{k: id_k = v} p_k).
 //
-// A row without a usable entry is not scored: loss, lse and gradient 0, its logits unread.
+// A row without a usable entry is not scored: loss, lse and gradient 0, whatever its logits (unread in
+// rows above 256 values).
 // Logits are read once per call (forward: running maximum and sum per thread, merged in a
 // fixed order; backward: q from the forward's lse, each value overwritten where it is read, so
 // the gradient may take the logits' place).  Exponentials, sums and the loss are fp32 whatever
