@@ -546,14 +546,15 @@ class EsmEncoder:
         _need(isinstance(logits, torch.Tensor) and logits.is_cuda, where, "logits must be a CUDA tensor")
         f32 = logits.dtype is torch.float32
         _need(f32 or logits.dtype is torch.bfloat16, where, "logits must be float32 or bfloat16")
-        _need(logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1), where,
+        shape, stride = logits.shape, logits.stride()
+        _need(len(shape) == 2 and (stride[1] == 1 or shape[1] == 1), where,
               "logits must be 2-D with contiguous rows")
-        T, V = logits.shape
+        T, V = shape
         _need(isinstance(teacher_ids, torch.Tensor) and teacher_ids.dim() == 2, where, "teacher_ids must be [T, K]")
-        shape, dev = (T, teacher_ids.shape[1]), logits.device
-        _check_tensor(teacher_ids, where, "teacher_ids", torch.int32, shape, dev)
-        _check_tensor(teacher_logits, where, "teacher_logits", torch.float32, shape, dev)
-        return PRECISIONS["fp32" if f32 else "bf16"], T, V, EsmEncoder._row_stride(logits), shape[1]
+        K, dev = teacher_ids.shape[1], logits.device
+        _check_tensor(teacher_ids, where, "teacher_ids", torch.int32, (T, K), dev)
+        _check_tensor(teacher_logits, where, "teacher_logits", torch.float32, (T, K), dev)
+        return PRECISIONS["fp32" if f32 else "bf16"], T, V, stride[0] if T > 1 else max(stride[0], V), K
 
     @staticmethod
     def _row_stride(t) -> int:
