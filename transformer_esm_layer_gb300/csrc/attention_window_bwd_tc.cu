@@ -35,25 +35,27 @@
 //   warp 3       one thread issues the three gradient products of every pair;
 //   warps 4..11  two warpgroups, one per 64 queries of the tile; thread r owns key r: reads its
 //                S^T and dP^T row segment, forms P^T = 2^(S^T log2(e) / 8) and dS^T = P^T dP^T
-//                in registers (f32x2 pairs), hands S^T back, then writes P^T into tensor memory
-//                (once the previous pair's dV product has read it) and dS^T into shared
-//                memory (K-major, 128-byte swizzle), both as bf16;
+//                in registers (f32x2 pairs), hands S^T back, then writes dS^T into shared memory
+//                (K-major, 128-byte swizzle; once the previous pair's dK and dQ products have read
+//                it) and P^T into tensor memory (once its dV product has), both rounded to bf16 as
+//                operands;
 //   warps 12..15 thread r owns query r of the tile: reads dQ_i from TMEM, stages it in shared
 //                memory and adds it into an fp32 accumulator in global memory with TMA
 //                reduce-add (several key tiles contribute to each query row); after an item's last
-//                pair they also bring out its dK and dV.
-// Every mbarrier wait is bounded; on timeout the kernel latches an error bit and stops.
+//                pair they also bring out its dK (turned back through RoPE) and dV.
+// Pairs run on across items.  Every mbarrier wait is bounded; on timeout the kernel latches an
+// error bit and stops.
 //
 // What bounds it: the tensor core, by way of shared memory.  A pair is 34 MMAs of 75 to 100 cycles
 // (M = 128 with N = 64 takes as long as N = 128: the operands' way out of shared memory), about
-// 3300 cycles; what remains of the 4400 that a pair takes in long runs is handing over.  So the
-// other readers of shared memory went where they could (row terms into the MMAs, P^T into tensor
-// memory) and nothing waits for memory: three Q / dO stages, the next item's K and V loaded ahead, its
-// first S^T and dP^T issued before the last item's gradient products, dK and dV taken out one pair
-// late.  Whole calls, against the full attention's form of the kernel: 16384 packed tokens, 20 heads,
-// window 128 + 128, one sink 229 us (276); 160 sequences of 100 tokens, one pair per item 147 us (205).
-// What the call has beside this kernel is memory traffic: the row terms, the accumulator's
-// zeros and its rounding to dq.
+// 3400 cycles of the 4100 that a pair takes in long runs.  So the other readers of shared memory went
+// where they could (row terms into the MMAs, P^T into tensor memory), and nothing waits for global
+// memory or for the other warps' ends of items: three Q / dO stages, the next item's K and V loaded
+// ahead, scores and gradient products from two threads.  Whole calls, against the full attention's
+// form of the kernel: 16384 packed tokens, 20 heads, window 128 + 128, one sink 195 us (276), of them
+// 148 here; 34374 tokens, left 512, four sinks 558 (791); 160 sequences of 100 tokens, one pair per
+// item 136 (205).  What the call has beside this kernel is memory traffic: the row terms, the
+// accumulator's zeros and its rounding to dq.
 #include "attn_plan.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -585,7 +587,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool is_k = v >= 2;
         const int c0 = is_k ? 16 * (v - 2) : 32 * v, c1 = is_k ? c0 + 32 : c0 + 16;
         float a[16], b[16];
-        tmem_ld16x2(tmem + lane_off + (is_k ? COL_DK : COL_DV) + c0, tmem + lane_off + (is_k ? COL_DK : COL_DV) + c1, a, b);
+        const uint32_t acc = tmem + lane_off + (is_k ? COL_DK : COL_DV);
+        tmem_ld16x2(acc + c0, acc + c1, a, b);
         if (v == 3) {  // the last TMEM read of the item
           tc_fence_before();
           __syncwarp();
@@ -767,9 +770,10 @@ __global__ void __launch_bounds__(64 * kSumRows) attention_far_sum_kernel(const 
 // the work list instead (a launch of its own took 4 us of a small call).
 constexpr int kTermThreads = 256;
 __global__ void __launch_bounds__(kTermThreads)
-    attention_bwd_terms_kernel(AttnPlan plan, PackBuffers pb, unsigned* err, const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
-                                           const float* __restrict__ lse, __nv_bfloat16* __restrict__ terms,
-                                           float* __restrict__ dq_acc, int T, int d, int heads) {
+    attention_bwd_terms_kernel(AttnPlan plan, PackBuffers pb, unsigned* err, const __nv_bfloat16* __restrict__ o,
+                               const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,
+                               __nv_bfloat16* __restrict__ terms, float* __restrict__ dq_acc, int T, int d,
+                               int heads) {
   if (plan.cu != nullptr && blockIdx.x == 0) {
     attn_plan<kTermThreads>(plan, pb, err);
     return;
@@ -836,8 +840,9 @@ cudaError_t launch_attention_window_bwd_tc(const CUtensorMap* tm_qkv, const CUte
                                            const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse,
                                            __nv_bfloat16* terms, float* dq_acc,
                                            void* far, __nv_bfloat16* dqkv, int T, int B, int max_len, int d, int heads,
-                                           int max_items, const PackBuffers& pb, const AttnPlan& plan, const float2* rope, int max_pos,
-                                           int num_sms, unsigned* err, cudaStream_t st) {
+                                           int max_items, const PackBuffers& pb, const AttnPlan& plan,
+                                           const float2* rope, int max_pos, int num_sms, unsigned* err,
+                                           cudaStream_t st) {
   if (T <= 0 || max_items <= 0) return cudaSuccess;
   static bool configured = false;
   if (!configured) {
@@ -871,8 +876,8 @@ cudaError_t launch_attention_window_bwd_tc(const CUtensorMap* tm_qkv, const CUte
   attention_window_bwd_tc_kernel<<<grid, THREADS, SMEM_BYTES, st>>>(*tm_qkv, *tm_do, *tm_dq, *tm_terms, win, fl,
                                                                     dqkv, T, d, hd, pb, rope, max_pos, err);
   if (has_far)
-    attention_far_sum_kernel<<<dim3(B, heads), dim3(64, kSumRows), 0, st>>>(pb.seg_start, pb.seg_klen, far0, win.sinks, fl.partial,
-                                                            dqkv, d, heads, rope, max_pos);
+    attention_far_sum_kernel<<<dim3(B, heads), dim3(64, kSumRows), 0, st>>>(
+        pb.seg_start, pb.seg_klen, far0, win.sinks, fl.partial, dqkv, d, heads, rope, max_pos);
   launch_attention_bwd_dq(dq_acc, dqkv, pb.pos_id, rope, max_pos, T, d, st);
   return cudaGetLastError();
 }
