@@ -54,7 +54,7 @@
 // ahead, scores and gradient products from two threads.  Whole calls, against the full attention's
 // form of the kernel: 16384 packed tokens, 20 heads, window 128 + 128, one sink 195 us (276), of them
 // 148 here; 34374 tokens, left 512, four sinks 558 (791); 160 sequences of 100 tokens, one pair per
-// item 136 (205).  What the call has beside this kernel is memory traffic: the row terms, the
+// item 136 (205, both as graph replays).  What the call has beside this kernel is memory traffic: the row terms, the
 // accumulator's zeros and its rounding to dq.
 #include "attn_plan.cuh"
 #include "common.cuh"
