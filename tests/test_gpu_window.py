@@ -515,6 +515,28 @@ def test_malformed_offsets_are_reported_and_stay_in_bounds():
     assert enc.check_status() == 0
 
 
+@pytest.mark.parametrize("window", [(20, 20, 3), (-1, 0, 0)])
+@pytest.mark.parametrize("cu", [[0, 1024, 0, 1024], [0, 1024, 0, 1024, 0, 1024, 0, 1024]])
+def test_overlapping_offsets_in_a_small_batch_stay_in_bounds(cu, window):
+    """More tiles than an honest batch of this size can have, found from the offsets."""
+    heads, T = 4, 1024
+    enc = _enc(heads)
+    qkv, _, _ = _inputs([T], heads, 35)
+    off = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o, behind = _guarded((T, 256), torch.bfloat16)
+    lse, lse_behind = _guarded((heads, T), torch.float32)
+    for _ in range(2):
+        enc.op_attention_window(qkv, off, T, window, o, lse=lse)
+        assert enc.check_status() == 3
+        assert torch.all(behind == 7) and torch.all(lse_behind == 7)
+    ok = torch.tensor([0, 400, T], dtype=torch.int32, device="cuda")
+    enc.op_attention_window(qkv, ok, T, window, o, lse=lse)
+    assert enc.check_status() == 0
+    ro, bo, rl, bl = _reference(qkv, [400, 624], heads, window)
+    assert torch.all((o.double() - ro).abs() <= bo)
+    assert torch.all((lse.double() - rl).abs() <= bl)
+
+
 def test_refusals():
     from transformer_esm_layer_gb300.binding import EsmError
     heads = 4

@@ -174,16 +174,6 @@ struct FarList {
   float* partial;  // [slot][heads][sinks][dK 64 | dV 64]
 };
 
-// it / heads by a multiplication with ceil(2^32 / heads): at most one too large.
-struct HeadDiv {
-  uint32_t heads, magic;
-  __device__ __forceinline__ void split(uint32_t it, uint32_t& entry, uint32_t& h) const {
-    entry = heads == 1 ? it : __umulhi(it, magic);
-    if (entry * heads > it) --entry;
-    h = it - entry * heads;
-  }
-};
-
 // Keys k0 .. k0 + krows - 1 (rows of the packed batch) of the sequence at row s0; its queries
 // q0 .. q1 - 1 (positions in the sequence) in nq tiles.  slot: where the sinks' fp32 partial
 // sums go (-1: nowhere, the gradients are written whole); far: a chunk item.

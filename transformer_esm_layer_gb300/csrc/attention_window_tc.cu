@@ -38,6 +38,7 @@
 // three CTAs per SM (68 us, the tensor pipe takes as long for 64 columns as for 128), skipping
 // or not masking 32-column chunks by branches (60 to 70 us: the compiler then schedules each
 // chunk by itself).
+#include "attn_plan.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -105,16 +106,6 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// it / heads by a multiplication with ceil(2^32 / heads): at most one too large.
-struct HeadDiv {
-  uint32_t heads, magic;
-  __device__ __forceinline__ void split(uint32_t it, uint32_t& entry, uint32_t& h) const {
-    entry = heads == 1 ? it : __umulhi(it, magic);
-    if (entry * heads > it) --entry;
-    h = it - entry * heads;
-  }
-};
-
 struct Item {
   int qrow0, qrows, krow0, klen, h;
   int qpos0;      // position of the first query in its sequence
@@ -124,49 +115,13 @@ struct Item {
   int nkb;        // key tiles
 };
 
-// Work item `it` = (work-list entry it / heads, head it % heads): one 16-byte load, and its unpacking.
-struct Raw {
-  int4 w;
-  int h;
-};
-__device__ __forceinline__ Raw load_item(const PackBuffers& pb, int it, const HeadDiv& hd) {
+// Work item `it` = (work-list entry it / heads, head it % heads), in one 16-byte load.
+__device__ __forceinline__ RawItem load_item(const PackBuffers& pb, int it, const HeadDiv& hd) {
   uint32_t entry, h;
   hd.split((uint32_t)it, entry, h);
-  return Raw{__ldg(reinterpret_cast<const int4*>(pb.work) + entry), (int)h};
+  return RawItem{__ldg(reinterpret_cast<const int4*>(pb.work) + entry), (int)h};
 }
-// The same from the offsets themselves, by a whole warp, for batches of at most 32 sequences; reports
-// malformed offsets like the kernel that writes the list, and counts the items.
-__device__ __forceinline__ Raw find_item(const PackedBatch& b, int it, const HeadDiv& hd, int& n_items, unsigned* err) {
-  const int lane = threadIdx.x & 31;
-  int c0 = 0, L = 0;
-  if (lane < b.B) {
-    c0 = __ldg(b.cu + lane);
-    int c1 = __ldg(b.cu + lane + 1);
-    if ((lane == 0 && c0 != 0) || (lane == b.B - 1 && c1 != b.T) || c1 < c0 || c1 - c0 > b.max_seqlen ||
-        c1 - c0 > b.max_positions || c0 < 0 || c1 > b.T) {
-      if (threadIdx.x < 32) latch_error(err, ERRBIT_CU_SEQLENS);
-      c0 = min(max(c0, 0), b.T);
-      c1 = min(min(max(c1, c0), b.T), c0 + b.max_positions);
-    }
-    L = c1 - c0;
-  }
-  const int tiles = (L + QT - 1) / QT;
-  int v = tiles;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  n_items = __shfl_sync(0xffffffffu, v, 31) * (int)hd.heads;
-  uint32_t entry, h;
-  hd.split((uint32_t)it, entry, h);
-  const unsigned mine = __ballot_sync(0xffffffffu, (int)entry >= v - tiles && (int)entry < v);
-  const int src = mine ? __ffs(mine) - 1 : 0;
-  const int start = __shfl_sync(0xffffffffu, c0, src), len = __shfl_sync(0xffffffffu, L, src);
-  const int off = ((int)entry - __shfl_sync(0xffffffffu, v - tiles, src)) * QT;
-  return Raw{make_int4(start + off, min(QT, len - off), start, len), (int)h};
-}
-__device__ __forceinline__ Item make_item(const Raw& raw, const AttnWindow& win) {
+__device__ __forceinline__ Item make_item(const RawItem& raw, const AttnWindow& win) {
   Item x;
   x.h = raw.h;
   x.qrow0 = raw.w.x;
@@ -216,9 +171,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
                                float* __restrict__ lse, int lse_stride, unsigned* err) {
   // the CTA's first item: from the work list, or (then its only one) from the offsets
   int n_items;
-  Raw first;
+  RawItem first;
   if (batch.cu != nullptr) {
-    first = find_item(batch, blockIdx.x, hd, n_items, err);
+    first = find_item<QT>(batch, blockIdx.x, hd, n_items, err);
   } else {
     n_items = *pb.work_count * (int)hd.heads;
     if ((int)blockIdx.x < n_items) first = load_item(pb, blockIdx.x, hd);
@@ -269,7 +224,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  auto first_item = [&]() { return Raw{make_int4(sm->first[0], sm->first[1], sm->first[2], sm->first[3]), sm->first[4]}; };
+  auto first_item = [&]() { return RawItem{make_int4(sm->first[0], sm->first[1], sm->first[2], sm->first[3]), sm->first[4]}; };
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWg0));
 
   if (warp == 0 || warp == 2) {
@@ -279,7 +234,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     if (lane == 0) {
       const bool kq = warp == 0;
       int g = 0, n_q = 0;  // key tiles and Q tiles asked for
-      Raw nxt = first_item();
+      RawItem nxt = first_item();
       for (int rnd = 0, it = item_at(0); it < n_items && !sm->abort; it = item_at(++rnd)) {
         const Item x = make_item(nxt, win);
         if (item_at(rnd + 1) < n_items) nxt = load_item(pb, item_at(rnd + 1), hd);  // prefetch
@@ -333,7 +288,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       const uint64_t vdesc0 = make_sw128_desc(smem_u32(sV));
       bool ok = true;
       int g = 0, qi = 0;
-      Raw nxt = first_item();
+      RawItem nxt = first_item();
       for (int rnd = 0, it = item_at(0); it < n_items && ok && !sm->abort; it = item_at(++rnd), ++qi) {
         const Item x = make_item(nxt, win);
         if (item_at(rnd + 1) < n_items) nxt = load_item(pb, item_at(rnd + 1), hd);  // prefetch
@@ -504,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         }
       }
     };
-    Raw nxt = first_item();
+    RawItem nxt = first_item();
     for (int rnd = 0, it = item_at(0); it < n_items && ok; it = item_at(++rnd)) {
       const Item x = make_item(nxt, win);
       if (item_at(rnd + 1) < n_items) nxt = load_item(pb, item_at(rnd + 1), hd);  // prefetch

@@ -5,6 +5,59 @@
 
 namespace esm {
 
+// it / heads by a multiplication with ceil(2^32 / heads): at most one too large.
+struct HeadDiv {
+  uint32_t heads, magic;
+  __device__ __forceinline__ void split(uint32_t it, uint32_t& entry, uint32_t& h) const {
+    entry = heads == 1 ? it : __umulhi(it, magic);
+    if (entry * heads > it) --entry;
+    h = it - entry * heads;
+  }
+};
+
+// A work item of the forward: its list entry (first query row, query rows, first key row, visible
+// keys) and head.
+struct RawItem {
+  int4 w;
+  int h;
+};
+// Item `it` from the offsets themselves, by a whole warp, for batches of at most 32 sequences whose
+// items one grid takes in one round; reports malformed offsets like the kernel that writes the
+// list, and counts the items.
+template <int QT>
+__device__ __forceinline__ RawItem find_item(const PackedBatch& b, int it, const HeadDiv& hd, int& n_items, unsigned* err) {
+  const int lane = threadIdx.x & 31;
+  int c0 = 0, L = 0;
+  if (lane < b.B) {
+    c0 = __ldg(b.cu + lane);
+    int c1 = __ldg(b.cu + lane + 1);
+    if ((lane == 0 && c0 != 0) || (lane == b.B - 1 && c1 != b.T) || c1 < c0 || c1 - c0 > b.max_seqlen ||
+        c1 - c0 > b.max_positions || c0 < 0 || c1 > b.T) {
+      if (threadIdx.x < 32) latch_error(err, ERRBIT_CU_SEQLENS);
+      c0 = min(max(c0, 0), b.T);
+      c1 = min(min(max(c1, c0), b.T), c0 + b.max_positions);
+    }
+    L = c1 - c0;
+  }
+  const int tiles = (L + QT - 1) / QT;
+  int v = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  // Malformed offsets (segments that overlap) can hold more items than the grid was made for: a second
+  // round would read a list that was never written.
+  n_items = min(__shfl_sync(0xffffffffu, v, 31) * (int)hd.heads, (int)gridDim.x);
+  uint32_t entry, h;
+  hd.split((uint32_t)it, entry, h);
+  const unsigned mine = __ballot_sync(0xffffffffu, (int)entry >= v - tiles && (int)entry < v);
+  const int src = mine ? __ffs(mine) - 1 : 0;
+  const int start = __shfl_sync(0xffffffffu, c0, src), len = __shfl_sync(0xffffffffu, L, src);
+  const int off = ((int)entry - __shfl_sync(0xffffffffu, v - tiles, src)) * QT;
+  return RawItem{make_int4(start + off, min(QT, len - off), start, len), (int)h};
+}
+
 // Sort key of a windowed item, longest first: its key tiles (forward) or query tiles (backward),
 // exact up to 64 and in steps of 8 above.
 constexpr int PLAN_CLASSES = 128;
