@@ -87,3 +87,41 @@ def test_items_from_offsets_cover_the_batch_once(host, lengths, heads):
         assert _in_batch(row, rows, key, keys, T)
         seen[h, row:row + rows] += 1
     assert np.all(seen == 1)
+
+
+def _plan(host, cu, T, window=(20, 20, 3), backward=False, sort_above=0, max_seqlen=65536):
+    """The listed items, and the room behind the list."""
+    cu, B = _offsets(cu), len(cu) - 1
+    room = _max_items(T, B)
+    work = np.full((room + 64, 4), UNWRITTEN, np.int32)
+    err = ctypes.c_uint(0)
+    n = host.host_attn_plan(_ptr(cu), B, T, max_seqlen, 65536, room, *window, int(backward), sort_above,
+                            _ptr(work[32:]), ctypes.byref(err))
+    assert np.all(work[:32] == UNWRITTEN) and np.all(work[32 + room:] == UNWRITTEN)
+    return work[32:32 + room], n, err.value
+
+
+@pytest.mark.parametrize("T,cu", MALFORMED + [(2048, [0, 2048] * 4), (2048, [0, 2048] * 200)])
+@pytest.mark.parametrize("sort_above", [0, 7, 15, 37, 10 ** 6])
+@pytest.mark.parametrize("window,backward", [((20, 20, 3), False), ((-1, 0, 0), False), ((-1, 0, 0), True)])
+def test_listed_items_of_malformed_offsets_were_written(host, T, cu, sort_above, window, backward):
+    """Also where the batch has room for fewer items than are sorted, and its offsets hold more."""
+    work, n, err = _plan(host, cu, T, window, backward, sort_above)
+    assert err
+    assert 0 <= n <= len(work)
+    for row, rows, key, keys in work[:n]:
+        assert _in_batch(row, rows, key, keys, T), (row, rows, key, keys)
+
+
+@pytest.mark.parametrize("lengths", [[180], [0, 1, 127, 128, 129, 300, 2, 0, 515], [7] * 300, [0] * 256 + [2000, 5]])
+@pytest.mark.parametrize("sort_above", [0, 3, 10 ** 6])
+def test_listed_items_cover_the_batch_once(host, lengths, sort_above):
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    T = int(cu[-1])
+    work, n, err = _plan(host, cu, T, window=(200, 0, 1), sort_above=sort_above)
+    assert not err and n == sum(-(-L // 128) for L in lengths)
+    seen = np.zeros(T, int)
+    for row, rows, key, keys in work[:n]:
+        assert _in_batch(row, rows, key, keys, T)
+        seen[row:row + rows] += 1
+    assert np.all(seen == 1)

@@ -537,6 +537,34 @@ def test_overlapping_offsets_in_a_small_batch_stay_in_bounds(cu, window):
     assert torch.all((lse.double() - rl).abs() <= bl)
 
 
+@pytest.mark.parametrize("window", [(20, 20, 3), (-1, 0, 0)])
+@pytest.mark.parametrize("cu", [[0, 2048] * 4, [0, 2048] * 40])
+def test_overlapping_offsets_in_a_work_list_stay_in_bounds(cu, window):
+    """More tiles than the list has room for; 40 pairs of offsets are past what the forward finds
+    without a list."""
+    heads, T = 4, 2048
+    enc = _enc(heads)
+    qkv, _, g = _inputs([T], heads, 36)
+    off = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o, behind = _guarded((T, 256), torch.bfloat16)
+    lse, lse_behind = _guarded((heads, T), torch.float32)
+    enc.op_attention_window(qkv, off, T, window, o, lse=lse)
+    assert enc.check_status() == 3
+    assert torch.all(behind == 7) and torch.all(lse_behind == 7)
+    d_o = torch.randn(T, 256, device="cuda", generator=g).to(torch.bfloat16)
+    dq, behind = _guarded((T, 768), torch.bfloat16)
+    enc.op_attention_window_backward(qkv, d_o, torch.zeros_like(lse), d_o, off, T, window, dq)
+    assert enc.check_status() == 3
+    assert torch.all(behind == 7)
+    ok = torch.tensor([0, 900, T], dtype=torch.int32, device="cuda")
+    enc.op_attention_window(qkv, ok, T, window, o, lse=lse)
+    o = o.contiguous()
+    enc.op_attention_window_backward(qkv, o, lse, d_o, ok, T, window, dq)
+    assert enc.check_status() == 0
+    ref, bound = _backward_reference(qkv, o, lse, d_o, [900, 1148], heads, window)
+    assert torch.all((dq.double() - ref).abs() <= bound)
+
+
 def test_refusals():
     from transformer_esm_layer_gb300.binding import EsmError
     heads = 4

@@ -75,7 +75,8 @@ __device__ __forceinline__ int plan_class(int pos, int rows, int len, const Attn
 // writes), so that the CTAs' static shares come out even: 47 packed sequences under a window of
 // 128 + 128 hold items of one to four tiles, and in sequence order the busiest CTA had 1.17
 // times the mean's work, sorted 1.07; with a causal window 1.29 and 1.02.  Items of one length
-// stand in any order.
+// stand in any order.  Malformed offsets can hold more items than the list has room for: the items
+// past max_items are left out, of the count and of both passes alike.
 template <int NT>
 __device__ __forceinline__ void attn_plan(const AttnPlan& pl, const PackBuffers& pb, unsigned* err) {
   __shared__ int s_first[NT + 1];  // items before the chunk's sequence i, within the chunk
@@ -144,7 +145,7 @@ __device__ __forceinline__ void attn_plan(const AttnPlan& pl, const PackBuffers&
   __syncthreads();
   int total = 0;
   for (int b0 = 0; b0 < pl.B; b0 += NT) {
-    const int n = scan_chunk(b0, true);
+    const int n = min(scan_chunk(b0, true), pl.max_items - total);
     total += n;
     if (pl.max_items > pl.sort_above)
       for (int k = tid; k < n; k += NT) {
@@ -172,18 +173,18 @@ __device__ __forceinline__ void attn_plan(const AttnPlan& pl, const PackBuffers&
   __syncthreads();
   int base = 0;
   for (int b0 = 0; b0 < pl.B; b0 += NT) {
-    const int n = pl.B > NT ? scan_chunk(b0, false) : total;  // (a single chunk is still there)
+    // (a single chunk is still there)
+    const int n = pl.B > NT ? min(scan_chunk(b0, false), pl.max_items - base) : total;
     for (int k = tid; k < n; k += NT) {
       int off;
       const int q = item(k, off), rows = min(pl.q_tile, s_len[q] - off);
       const int at = sorted ? atomicAdd(&s_class[plan_class(off, rows, s_len[q], pl.win, pl.backward)], 1) : base + k;
-      if (at < pl.max_items)
-        reinterpret_cast<int4*>(pb.work)[at] = make_int4(s_start[q] + off, rows, s_start[q], s_len[q]);
+      reinterpret_cast<int4*>(pb.work)[at] = make_int4(s_start[q] + off, rows, s_start[q], s_len[q]);
     }
     base += n;
     __syncthreads();
   }
-  if (tid == 0) pb.work_count[0] = min(total, pl.max_items);
+  if (tid == 0) pb.work_count[0] = total;
 }
 
 }  // namespace esm
