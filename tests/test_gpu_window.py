@@ -243,6 +243,29 @@ def test_unseen_keys_and_values_have_no_influence(bad):
         assert torch.isnan(o[sees]).all()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("window", [(-1, -1, 0), (70000, 70000, 3), (-1, 0, 0), (3, -1, 1), (600, 600, 0)])
+def test_other_sequences_have_no_influence_under_wide_windows(window, bad):
+    """A sequence's last key tile reaches into the next one; nothing of that may show."""
+    heads, lengths = 4, [200, 150, 400, 1, 90]
+    enc = _enc(heads)
+    qkv, cu, _ = _inputs(lengths, heads, 37)
+    ro, bo, rl, bl = _reference(qkv, lengths, heads, window)
+    d, other = 64 * heads, torch.ones(len(qkv), dtype=torch.bool, device="cuda")
+    other[200:350] = False
+    other[751:] = False
+    spoiled = qkv.clone()
+    spoiled[200:350, d:] = bad     # k and v of the second and the last sequence
+    spoiled[751:, d:] = bad
+    for lse in (False, True):
+        o, l = _forward(enc, spoiled, cu, lengths, window, heads, lse=lse)
+        assert torch.all((o[other].double() - ro[other]).abs() <= bo[other])
+        if lse:
+            assert torch.all((l[:, other].double() - rl[:, other]).abs() <= bl[:, other])
+        if bad != bad:
+            assert torch.isnan(o[~other]).all()
+
+
 def test_scores_far_apart():
     """Rows whose first key tile scores far below (and far above) the later ones."""
     heads, lengths, window = 4, [700], (400, 0, 1)

@@ -275,11 +275,23 @@ bool canonical_window(const esm_encoder* h, const esm_attn_window* w, AttnWindow
 }
 bool is_full(const AttnWindow& w) { return w.left < 0 && w.right < 0; }
 
+// Windowed attention of a batch by its work list or its offsets (batch.cu), bf16 activations.
+esm_status run_window_attention(esm_encoder* h, const AttnWindow& win, const void* qkv, void* o, Act act_out, int T,
+                                int max_items, const PackBuffers& pb, const PackedBatch& batch, const float* q_scale,
+                                float* amax, cudaStream_t st, float* lse) {
+  const uint64_t cols = (uint64_t)3 * h->cfg.hidden;
+  const CUtensorMap* tq = h->map(qkv, (uint64_t)T, cols, 128, 2);
+  const CUtensorMap* tq16 = h->map(qkv, (uint64_t)T, cols, 16, 2);
+  if (!tq || !tq16) return ESM_ERR_CUDA;
+  return cuda_status(launch_attention_window_tc(tq, tq16, win, qkv, o, act_out, h->cfg.hidden, h->cfg.heads, max_items, pb,
+                                                batch, q_scale, amax, h->d_err, st, lse, T));
+}
+
 // Attention of an indexed batch (work items in tiles of kAttnQTileTc rows; fp32: positions and
 // segments): qkv [T, 3d] -> o [T, d] (act_out), with lse [heads, T] if given.
 esm_status run_attention(esm_encoder* h, const AttnWindow& win, const void* qkv, void* o, Act act_out, int T,
                          int max_items, const PackBuffers& pb, const float* q_scale, float* amax, cudaStream_t st,
-                         float* lse = nullptr, const PackedBatch& batch = PackedBatch{}) {
+                         float* lse = nullptr) {
   const int d = h->cfg.hidden, H = h->cfg.heads;
   if (h->cfg.precision == ESM_FP32) {
     const float* x = static_cast<const float*>(qkv);
@@ -287,14 +299,11 @@ esm_status run_attention(esm_encoder* h, const AttnWindow& win, const void* qkv,
     else launch_attention_window_f32(x, static_cast<float*>(o), d, H, T, pb, win, st);
     return cuda_status(cudaGetLastError());
   }
+  if (!is_full(win))
+    return run_window_attention(h, win, qkv, o, act_out, T, max_items, pb, PackedBatch{}, q_scale, amax, st, lse);
   const CUtensorMap* tq = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 128, 2);
   if (!tq) return ESM_ERR_CUDA;
-  if (is_full(win))
-    return cuda_status(launch_attention_tc(tq, o, act_out, d, H, max_items, pb, q_scale, amax, h->d_err, st, lse, T));
-  const CUtensorMap* tq16 = h->map(qkv, (uint64_t)T, (uint64_t)3 * d, 16, 2);
-  if (!tq16) return ESM_ERR_CUDA;
-  return cuda_status(launch_attention_window_tc(tq, tq16, win, qkv, o, act_out, d, H, max_items, pb, batch, q_scale,
-                                                amax, h->d_err, st, lse, T));
+  return cuda_status(launch_attention_tc(tq, o, act_out, d, H, max_items, pb, q_scale, amax, h->d_err, st, lse, T));
 }
 
 bool weights_ok(const esm_encoder* h, const esm_weights* w) {
@@ -1658,13 +1667,15 @@ esm_status esm_op_attention_window(esm_encoder_t* h, const void* qkv, const int3
                                 total_tokens, pb, win, st);
     return cuda_status(cudaGetLastError());
   }
-  if (!is_full(win) && attention_window_direct(num_seqs, L.max_items, h->cfg.heads)) {
+  // (a full window too: the encoder's full attention lets infinite and NaN values behind a sequence's
+  // end through to it)
+  if (attention_window_direct(num_seqs, L.max_items, h->cfg.heads)) {
     // a small batch: the attention kernel finds its items itself, which saves a launch
     batch = PackedBatch{cu_seqlens, num_seqs, total_tokens, max_seqlen, h->cfg.max_positions};
   } else {
     launch_attn_plan(window_plan(h, cu_seqlens, num_seqs, total_tokens, max_seqlen, win, false, L), pb, h->d_err, st);
   }
-  return run_attention(h, win, qkv, o, h->act(), total_tokens, L.max_items, pb, nullptr, nullptr, st, lse, batch);
+  return run_window_attention(h, win, qkv, o, h->act(), total_tokens, L.max_items, pb, batch, nullptr, nullptr, st, lse);
 }
 
 esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, const void* o, const float* lse,
