@@ -266,6 +266,39 @@ def test_other_sequences_have_no_influence_under_wide_windows(window, bad):
             assert torch.isnan(o[~other]).all()
 
 
+@pytest.mark.parametrize("precision", ["bf16", "fp32"])
+def test_rows_whose_visible_scores_are_all_minus_infinity(precision):
+    """A softmax over nothing but -inf is NaN; -inf beside finite scores is a weight of 0, also in a
+    row that is summed again because of a NaN that it does not see."""
+    heads, window = 4, (2, 0, 1)
+    dt = torch.float32 if precision == "fp32" else torch.bfloat16
+    lengths, d = [150, 40], 64 * heads
+    qkv, cu, _ = _inputs(lengths, heads, 38, dt)
+    qkv[:, :d] = qkv[:, :d].abs() + 0.1      # q > 0: a key of -inf scores -inf
+    enc = _enc(heads, precision)
+    gone = torch.zeros(190, dtype=torch.bool, device="cuda")
+    x = qkv.clone()
+    for k in (0, 60, 61, 62, 100):           # the sink too
+        x[k, d:2 * d] = -float("inf")
+    gone[[0, 62]] = True                     # rows that see no other key: 0 itself; 0, 60, 61 and 62
+    x[120, 2 * d:] = float("nan")            # a value that most rows of its tile do not see
+    nan = gone.clone()
+    nan[120:123] = True
+    lse = None if precision == "fp32" else torch.empty(heads, 190, device="cuda")
+    o = torch.zeros(190, d, dtype=dt, device="cuda")
+    enc.op_attention_window(x, cu, 150, window, o, lse=lse)
+    assert enc.check_status() == 0
+    assert torch.isnan(o[nan]).all() and torch.isfinite(o[~nan]).all()
+    y = x.clone()
+    y[120, 2 * d:] = 0
+    ro, bo, rl, bl = [r.nan_to_num(nan=0.0, posinf=0.0, neginf=0.0) for r in _reference(y, lengths, heads, window)]
+    ok = ~nan
+    # _reference's bound of sum p |v| misses nothing here: the -inf scores have weight 0
+    assert torch.all((o[ok].double() - ro[ok]).abs() <= (2.0 ** -6 if precision == "fp32" else 1) * bo[ok])
+    if lse is not None:
+        assert torch.all(lse[:, gone] == -float("inf"))
+
+
 def test_scores_far_apart():
     """Rows whose first key tile scores far below (and far above) the later ones."""
     heads, lengths, window = 4, [700], (400, 0, 1)

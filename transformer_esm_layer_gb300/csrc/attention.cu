@@ -10,7 +10,8 @@
 //   o_t = sum_s softmax_s(q_t . k_s / sqrt(dh)) v_s,   s over the sequence of t,
 //
 // or, with a window (attention_window_f32_kernel), over the keys s <= t + right with s >= t - left or
-// s < sinks (positions in the sequence); a row that sees no key is zero.
+// s < sinks (positions in the sequence); a row that sees no key is zero, one whose visible scores are
+// all -inf is NaN.
 #include "common.cuh"
 #include "internal.h"
 
@@ -38,7 +39,8 @@ __device__ __forceinline__ void attention_f32_row(const float* __restrict__ qkv,
   const int pos = t - start;
   const int end = win.right < 0 ? klen : min(klen, pos + win.right + 1);
   const int lo = win.left < 0 ? 0 : max(0, pos - win.left), ns = min(win.sinks, min(lo, end));
-  for (int i = lane; i < ns + max(0, end - lo); i += 32) {
+  const int n = ns + max(0, end - lo);
+  for (int i = lane; i < n; i += 32) {
     const int j = i < ns ? i : lo + i - ns;
     const float* kr = qkv + (size_t)(start + j) * ld + d + h * dh;
     const float* vr = qkv + (size_t)(start + j) * ld + 2 * d + h * dh;
@@ -47,8 +49,8 @@ __device__ __forceinline__ void attention_f32_row(const float* __restrict__ qkv,
     for (int c = 0; c < 64; ++c)
       if (c < dh) s = fmaf(q[c], kr[c], s);
     s *= scale;
-    const float mn = fmaxf(m, s);
-    const float corr = expf(m - mn), p = expf(s - mn);
+    const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
+    const float corr = expf(m - base), p = expf(s - base);
     l = l * corr + p;
 #pragma unroll
     for (int c = 0; c < 64; ++c)
@@ -68,7 +70,7 @@ __device__ __forceinline__ void attention_f32_row(const float* __restrict__ qkv,
     float v = acc[c] * f;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (lane == 0) o[(size_t)t * d + h * dh + c] = l > 0.f || l != l ? v / l : 0.f;
+    if (lane == 0) o[(size_t)t * d + h * dh + c] = n > 0 ? v / l : 0.f;
   }
 }
 
@@ -91,8 +93,8 @@ __device__ __noinline__ void attention_f32_row_again(const float* qkv, float* o,
 // sinks of its first row's sequence, then the packed rows from the first to the last that any of its
 // rows sees in its band (a later sequence begins inside the block, and so within those rows).
 // Thread (ty, tx) holds rows 4 ty .. + 3 and columns 4 tx .. + 3 of the scores and of O.  A zero weight
-// times an infinite or NaN value is NaN: a row that ends up not finite is done again over its
-// visible keys alone.
+// times an infinite or NaN value is NaN: a row that ends up not finite, but for its own scores, is
+// done again over its visible keys alone.
 //
 // Bound by the FMA units and shared memory: 16 products per two 16-byte loads.  One sequence of 1024
 // tokens, 8 heads, window 1024 + 1024: 135 us a call (a warp per row: 3680).
@@ -232,18 +234,20 @@ __global__ void __launch_bounds__(128) attention_window_f32_kernel(const float* 
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 4 * ty + i;
+    const int row = 4 * ty + i, t = t0 + row;
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
-    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+    // (a sum of 0: the row sees no key, or only scores of -inf; a NaN: a score of NaN or +inf)
+    const bool sees = s_ns[row] > 0 || s_end[row] > s_lo[row], sums = l[i] > 0.f;
+    const float inv = sums ? 1.f / l[i] : sees ? __int_as_float(0x7fffffff) : 0.f;
     bool odd = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float v = l[i] == 0.f ? 0.f : acc[i][j] * inv;
-      odd |= !(fabsf(v) <= 3.402823466e38f);
+      const float v = sums ? acc[i][j] * inv : inv;
+      odd |= sums && !(fabsf(v) <= 3.402823466e38f);
       if (t < T && 4 * tx + j < dh) o[(size_t)t * d + h * dh + 4 * tx + j] = v;
     }
-    if (odd && t < T) atomicOr(&s_redo, 1u << (4 * ty + i));
+    if (odd && t < T) atomicOr(&s_redo, 1u << row);
   }
   __syncthreads();
   // (rare) the rows set aside, a warp each

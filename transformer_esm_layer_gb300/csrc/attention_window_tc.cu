@@ -4,7 +4,8 @@
 // Query i of a sequence sees key j of the same sequence if j <= i + right and (j >= i - left or
 // j < sinks), a side below zero being unlimited:
 //   o_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  s_ij = q_i . k_j / 8,
-//   lse_i = log sum_j exp(s_ij) over the keys that i sees; a row that sees none is zero.
+//   lse_i = log sum_j exp(s_ij) over the keys that i sees; a row that sees none is zero, one whose
+//   visible scores are all -inf is NaN.
 //
 // A query tile's keys are the list [sinks | lo .. hi), with lo .. hi the band that any of its 128
 // rows sees: first the sink rows, padded to a multiple of 16, then the band.  The key tiles are
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     // handed over, so that neither waits for the other.
     struct {
       Item x;
-      float m, inv;  // of this thread's row; inv = 0 where it sees no key
+      float m, inv;  // of this thread's row; inv = 0 where it sees no key, NaN where its scores make it so
       bool pending;
     } last;
     last.pending = false;
@@ -378,9 +379,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       const bool live = r < last.x.qrows;
       constexpr size_t kElem = (OUT == Act::BF16) ? 2 : 1;
       uint8_t* dst = static_cast<uint8_t*>(o) + ((size_t)(last.x.qrow0 + r) * d + (size_t)last.x.h * DH) * kElem;
-      // A row that sees no key is zero.  A zero weight times an infinite or NaN value is NaN, so
-      // values that a row does not see could reach it through the tile's product: a row whose sums
-      // are not finite is set aside and summed over its visible keys alone below.
+      // A row that sees no key is zero, one whose scores hold a NaN or +inf, or nothing but -inf, is
+      // NaN.  A zero weight times an infinite or NaN value is NaN, so values that a row does not see
+      // could reach it through the tile's product: any other row whose sums are not finite is set aside
+      // and summed over its visible keys alone below.
       uint64_t probe[4] = {0, 0, 0, 0};
       const uint64_t zero2 = f2_pack(0.f, 0.f);
 #pragma unroll
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       float p0, p1;
       f2_unpack(f2_add(f2_add(probe[0], probe[1]), f2_add(probe[2], probe[3])), p0, p1);
       const bool odd = p0 + p1 != 0.f;
-      const bool redo = odd && last.inv != 0.f && live;
+      const bool redo = odd && fabsf(last.inv) > 0.f && live;  // (false for NaN)
       if (odd || last.inv == 0.f) {
 #pragma unroll
         for (int i = 0; i < DH; ++i) u[i >> 5][i & 31] = 0u;
@@ -571,7 +573,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       // ---- the item's row statistics
       last.x = x;
       last.m = m_ref;
-      last.inv = l == 0.f ? 0.f : 1.f / l;
+      const bool sees = cs0 > 0 || ch0 > cl0;
+      last.inv = l == 0.f && !sees ? 0.f : l == 0.f ? __int_as_float(0x7fffffff) : 1.f / l;
       last.pending = true;
       // the natural-log softmax normaliser, ln 2 (m + log2 l) in the base-2 units used above
       if (lse != nullptr && r < x.qrows)
