@@ -375,6 +375,16 @@ def test_backward_lengths_and_distant_sinks(lengths, window):
     assert torch.all((dqkv.double() - ref).abs() <= bound)
 
 
+@pytest.mark.parametrize("window", [(64, 64, 5), (30, 0, 33), (16, 16, 127)])
+@pytest.mark.parametrize("lengths", [[1300, 17, 33, 1], [5, 1477, 61], [3, 31, 65, 97]])
+def test_backward_of_key_tiles_that_part_a_warp(lengths, window):
+    """Warps whose lanes hold sinks (fp32 partial sums), other keys, and rows behind the tile's last."""
+    heads = 4
+    _, qkv, _, o, lse, d_o, dqkv = _backward_case(lengths, window, heads, 39)
+    ref, bound = _backward_reference(qkv, o, lse, d_o, lengths, heads, window)
+    assert torch.all((dqkv.double() - ref).abs() <= bound)
+
+
 def test_backward_against_differences():
     """dL/dx along a random direction, L = sum(o64 * d_o), by central differences in float64:
     the directional derivative of the kernel's gradient within its summed bound."""

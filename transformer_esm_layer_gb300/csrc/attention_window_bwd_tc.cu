@@ -584,39 +584,39 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm->acc_free);
         }
-        if (!kval) continue;
-        if (part) {
+        if (kval && part) {
           float* dst = fl.partial + (((size_t)x.slot * heads + x.h) * win.sinks + r) * (2 * DH) + (is_k ? 0 : DH);
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             *reinterpret_cast<float4*>(dst + c0 + j) = make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]);
             *reinterpret_cast<float4*>(dst + c1 + j) = make_float4(b[j], b[j + 1], b[j + 2], b[j + 3]);
           }
-          continue;
-        }
-        if (is_k) {
+        } else if (kval) {
+          if (is_k) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {  // pair (c0 + j, c0 + j + 32) turned back by its angle
-            const float u = a[j] * 0.125f, w = b[j] * 0.125f;
-            a[j] = u;
-            b[j] = w;
-            if (rope != nullptr) {
-              const int jj = c0 + j;
-              const float2 cs = __ldg(rope + ((size_t)(jj >> 1) * max_pos + p) * 2 + (jj & 1));
-              a[j] = u * cs.x + w * cs.y;
-              b[j] = w * cs.x - u * cs.y;
+            for (int j = 0; j < 16; ++j) {  // pair (c0 + j, c0 + j + 32) turned back by its angle
+              const float u = a[j] * 0.125f, w = b[j] * 0.125f;
+              a[j] = u;
+              b[j] = w;
+              if (rope != nullptr) {
+                const int jj = c0 + j;
+                const float2 cs = __ldg(rope + ((size_t)(jj >> 1) * max_pos + p) * 2 + (jj & 1));
+                a[j] = u * cs.x + w * cs.y;
+                b[j] = w * cs.x - u * cs.y;
+              }
             }
           }
-        }
-        __nv_bfloat16* out = dqkv + (size_t)key * 3 * d + (is_k ? d : 2 * d) + x.h * DH;
-        uint32_t w[2][8];
+          __nv_bfloat16* out = dqkv + (size_t)key * 3 * d + (is_k ? d : 2 * d) + x.h * DH;
+          uint32_t w[2][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          w[0][j] = pack_bf16x2(a[2 * j], a[2 * j + 1]);
-          w[1][j] = pack_bf16x2(b[2 * j], b[2 * j + 1]);
+          for (int j = 0; j < 8; ++j) {
+            w[0][j] = pack_bf16x2(a[2 * j], a[2 * j + 1]);
+            w[1][j] = pack_bf16x2(b[2 * j], b[2 * j + 1]);
+          }
+          store32(out + c0, w[0], wide);
+          store32(out + c1, w[1], wide);
         }
-        store32(out + c0, w[0], wide);
-        store32(out + c1, w[1], wide);
+        __syncwarp();  // the lanes part above; the next read of tensor memory takes them together
       }
     };
     for (int rnd = 0, it = item_at(0); it < n_items && ok; it = item_at(++rnd), ++n) {

@@ -538,6 +538,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
         if (g > 0) {
           if (!mbar_wait_warp(&sm->pv_done, (uint32_t)(g - 1) & 1u)) { ok = false; break; }
           tc_fence_after();
+        } else {
+          __syncwarp();  // (the wait brings the lanes together for the stores below)
         }
         auto hand_over = [&]() {
           tmem_st_wait();
