@@ -113,6 +113,22 @@ def test_loss_and_gradient_match_float64(enc, T, V, K, pad, offset, dtype):
         assert enc.check_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,K", [(260, 64), (300, 20), (2100, 256)])
+def test_gradient_in_the_logits_place_reads_the_teachers_ids_first(enc, V, K, dtype):
+    """A warp per row: each lane's student logits at the teacher's ids are overwritten by other lanes."""
+    T = 900
+    _, logits, ids, tl = _case(T, V, K, dtype, 11)
+    _, lse, _, _ = _run(enc, logits, ids, tl, 1.5)
+    want = torch.empty_like(logits)
+    enc.op_distill_loss_backward(logits, ids, tl, 1.5, lse, want)
+    for _ in range(20):
+        z = logits.clone()
+        enc.op_distill_loss_backward(z, ids, tl, 1.5, lse, z)
+        assert torch.equal(z, want)
+    assert enc.check_status() == 0
+
+
 @pytest.mark.parametrize("V", [33, 900])
 def test_gradient_against_differences(enc, V):
     """Along a random direction, against central differences of the float64 loss."""

@@ -325,10 +325,17 @@ struct TeacherSum {
   }
 };
 
+// Any of the row's threads, and a barrier: what they read or wrote before is ordered with what they
+// write or read after it (a vote alone does not order memory).
 template <int W>
 __device__ __forceinline__ bool row_any(bool v) {
-  if constexpr (W == 1) return __any_sync(0xffffffffu, v);
-  else return __syncthreads_or(v);
+  if constexpr (W == 1) {
+    const bool any = __any_sync(0xffffffffu, v);
+    __syncwarp();
+    return any;
+  } else {
+    return __syncthreads_or(v);
+  }
 }
 template <int W>
 __device__ __forceinline__ void row_sync() {
