@@ -11,7 +11,18 @@ import os
 from typing import Dict, Optional, Sequence
 
 import numpy as np
-import torch
+
+
+class _Torch:
+    """Stands for torch until its first use, which imports it: the ctypes side needs none."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _Torch()
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libesm_encoder.so")
