@@ -187,6 +187,32 @@ def test_masked_vocabulary_and_extreme_values(enc, V, dtype):
     assert torch.all(d[:1, V // 2:] == 0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,V,K", [(12, 33, 4), (12, 200, 7), (12, 1000, 100), (700, 300, 40)])
+@pytest.mark.parametrize("t", [0.5, 1.0, 2.0])
+def test_teacher_logits_of_the_lowest_value(enc, T, V, K, dtype, t):
+    """The lowest float divided by a temperature below 1 is past the type: a row of nothing else is
+    uniform, beside other logits it has no weight.  The bounds of the top, with M over the others."""
+    low = torch.finfo(torch.float32).min
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    logits = (2 * torch.randn(T, V, device="cuda", generator=g)).to(dtype)
+    ids = torch.rand(T, V, device="cuda", generator=g).topk(K, dim=1).indices.to(torch.int32).contiguous()
+    tl = torch.randn(T, K, device="cuda", generator=g)
+    tl[::2] = low
+    tl[1::4, : K // 2] = low
+    ids[4, 1:] = -1
+    loss, lse, total, count = _run(enc, logits, ids, tl, t)
+    d = torch.empty_like(logits)
+    enc.op_distill_loss_backward(logits, ids, tl, t, lse, d)
+    assert enc.check_status() == 0 and int(count) == T
+    shown = torch.where((tl == low).all(1, keepdim=True), 0, tl.clamp(min=-1000))
+    scored, rloss, rlse, q, hot, M = _reference(logits, ids, shown, t)
+    M = logits.double().abs().amax(1) / t + torch.where(shown > -1000, shown, 0).double().abs().amax(1) / t + rlse.abs()
+    assert torch.all((loss.double() - rloss).abs() <= t * t * (1 + M) * (8 + M) * 2.0 ** -21)
+    bd = t * (q + hot) * (4 + M[:, None]) * 2.0 ** -21 + torch.finfo(dtype).eps / 2 * (t * (q - hot)).abs()
+    assert torch.all((d.double() - t * (q - hot)).abs() <= bd + 1e-38)
+
+
 def test_no_row_scored_and_no_rows(enc):
     for V in (33, 500):
         logits = torch.full((7, V), float("nan"), device="cuda")

@@ -101,8 +101,9 @@ __device__ __forceinline__ void write_partials(float loss, int count, float* par
 // deep, and a warp has four rows' chains in flight (16384 x 33 fp32, 8 entries: 5.0 us against
 // 10.7 us with a warp per row).
 //
-// Teacher softmax of the group's row, entries k = lane of the group, + G, ...: the maximum of l / t
-// (0 if there is no finite one), the sum of exp(l / t - m), whether any entry is usable.
+// Teacher softmax of the group's row, entries k = lane of the group, + G, ...: the maximum m of l (0 if
+// there is no finite one), the sum of exp((l - m) / t), whether any entry is usable.  The
+// difference is taken before the division: a lowest float divided by t < 1 would be -inf.
 struct Teacher {
   float m, sum;
   bool any;
@@ -114,14 +115,14 @@ __device__ __forceinline__ Teacher teacher_stats(const int32_t* ids, const float
   Teacher s{-INFINITY, 0.f, false};
   for (int k = gl; k < K; k += G) {
     if (usable_id(ids[k], tl[k], V, err) < 0) continue;
-    s.m = fmaxf(s.m, tl[k] * inv_t);
+    s.m = fmaxf(s.m, tl[k]);
     s.any = true;
   }
   s.m = anchor(group_max<G>(s.m));
   constexpr unsigned kGroup = G == 32 ? 0xffffffffu : (1u << G) - 1u;
   s.any = (__ballot_sync(0xffffffffu, s.any) >> (lane - gl) & kGroup) != 0u;
   for (int k = gl; k < K; k += G)
-    if (usable_id(ids[k], tl[k], V, nullptr) >= 0) s.sum += expf(tl[k] * inv_t - s.m);
+    if (usable_id(ids[k], tl[k], V, nullptr) >= 0) s.sum += expf((tl[k] - s.m) * inv_t);
   s.sum = group_sum<G>(s.sum);
   return s;
 }
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int k = gl; k < K; k += G) {
       const int v = usable_id(id[k], l[k], V, nullptr);
       if (v < 0) continue;
-      const float a = l[k] * inv_t - s.m, p = expf(a) * inv_sum;
+      const float a = (l[k] - s.m) * inv_t, p = expf(a) * inv_sum;
       // an entry whose probability underflows adds nothing, whatever the student makes of it
       if (p != 0.f) loss = fmaf(p, (a - log_sum) - (to_f(row[v]) * inv_t - lse), loss);
     }
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int k0 = 0; k0 < K; k0 += G) {
       const int k = k0 + gl;
       const int v = k < K ? usable_id(id[k], l[k], V, nullptr) : -1;
-      const float p = v >= 0 ? expf(l[k] * inv_t - s.m) * inv_sum : 0.f;
+      const float p = v >= 0 ? expf((l[k] - s.m) * inv_t) * inv_sum : 0.f;
       // (the key tells the rows of a warp apart, and unused entries)
       const unsigned same = __match_any_sync(0xffffffffu, v >= 0 ? (lane - gl) * kGroupVocab + v : -1 - lane);
       if (__any_sync(0xffffffffu, (same & (same - 1)) != 0u)) {
@@ -310,18 +311,17 @@ struct RunningSum {
   }
 };
 
-// The teacher's side of a row's loss over some of its entries, relative to their maximum m of
-// a = l / t: s = sum exp(a - m), x = sum exp(a - m) (a - m - z / t).  Then
-// loss / t^2 = x / s - log s + lse.
+// The teacher's side of a row's loss over some of its entries, relative to their maximum m: with
+// a = (l - m) / t, s = sum exp(a), x = sum exp(a) (a - z / t).  Then loss / t^2 = x / s - log s + lse.
 struct TeacherSum {
   float m = -INFINITY, s = 0.f, x = 0.f;
-  __device__ __forceinline__ void merge(float m2, float s2, float x2) {
-    const float mx = fmaxf(m, m2), a = anchor(mx);
-    const float f = m == -INFINITY ? 0.f : expf(m - a), g = m2 == -INFINITY ? 0.f : expf(m2 - a);
+  __device__ __forceinline__ void merge(float m2, float s2, float x2, float inv_t) {
+    const float mx = anchor(fmaxf(m, m2)), a = (m - mx) * inv_t, b = (m2 - mx) * inv_t;
+    const float f = m == -INFINITY ? 0.f : expf(a), g = m2 == -INFINITY ? 0.f : expf(b);
     // a part whose weight underflows adds nothing, whatever the student makes of its entries
-    x = (f != 0.f ? f * fmaf(s, m - a, x) : 0.f) + (g != 0.f ? g * fmaf(s2, m2 - a, x2) : 0.f);
+    x = (f != 0.f ? f * fmaf(s, a, x) : 0.f) + (g != 0.f ? g * fmaf(s2, b, x2) : 0.f);
     s = f * s + g * s2;
-    m = mx;
+    m = fmaxf(m, m2);
   }
 };
 
@@ -423,14 +423,14 @@ __global__ void __launch_bounds__(kThreads, EN > 2 ? 2 : kRowBlocks)
 #pragma unroll
     for (int e = 0; e < EN; ++e)
       if (id[e] >= 0) {
-        s.m = fmaxf(s.m, l[e] * inv_t);
+        s.m = fmaxf(s.m, l[e]);
         here = true;
       }
     if (__any_sync(0xffffffffu, here)) {
       s.m = group_max<32>(s.m);
 #pragma unroll
       for (int e = 0; e < EN; ++e) {
-        const float a = l[e] * inv_t - anchor(s.m), w = id[e] >= 0 ? expf(a) : 0.f;
+        const float a = (l[e] - anchor(s.m)) * inv_t, w = id[e] >= 0 ? expf(a) : 0.f;
         s.s += w;
         if (w != 0.f) s.x = fmaf(w, a - zk[e] * inv_t, s.x);
       }
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, EN > 2 ? 2 : kRowBlocks)
         r.merge(m2, s2, c);
         const float tm = __shfl_xor_sync(0xffffffffu, s.m, o), ts = __shfl_xor_sync(0xffffffffu, s.s, o);
         const float tx = __shfl_xor_sync(0xffffffffu, s.x, o);
-        s.merge(tm, ts, tx);
+        s.merge(tm, ts, tx, inv_t);
       }
     }
     if (lane == 0) {
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kThreads)
     auto grad = [&](float z) { return scored ? amp * ex2_approx(fmaf(z, inv_t, -lse) * kLog2e) : 0.f; };
     if (scored && warp == 0) {
       const Teacher s = teacher_stats<32>(id, l, K, V, inv_t, nullptr);
-      for (int k = lane; k < K; k += 32) s_p[k] = s_id[k] >= 0 ? expf(l[k] * inv_t - s.m) / s.sum : 0.f;
+      for (int k = lane; k < K; k += 32) s_p[k] = s_id[k] >= 0 ? expf((l[k] - s.m) * inv_t) / s.sum : 0.f;
     }
     const int head = row_head(out, V);
     const bool together = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
