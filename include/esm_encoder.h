@@ -581,7 +581,7 @@ ESM_API esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void
  * logits: device, float32 (logits_type ESM_FP32) or bfloat16 (ESM_BF16; other types:
  *   ESM_ERR_UNSUPPORTED) [T, vocab], rows logits_stride >= vocab elements apart; any vocab >= 1
  * teacher_ids, teacher_logits: device int32 and float32 [T, K], 1 <= K <= ESM_DISTILL_MAX_K
- * temperature: > 0, it and its inverse finite
+ * temperature: > 0, its square a normal float32 (about 1.1e-19 to 1.8e19)
  * token_loss: device float32 [T]; lse: device float32 [T] or NULL (the backward needs it);
  * loss_sum, count: device float32 and int32 scalars, each may be NULL: the sum of token_loss, in a
  *   fixed order, and the number of scored rows.  The workspace (the size query's bytes, 256-byte

@@ -213,6 +213,27 @@ def test_teacher_logits_of_the_lowest_value(enc, T, V, K, dtype, t):
     assert torch.all((d.double() - t * (q - hot)).abs() <= bd + 1e-38)
 
 
+@pytest.mark.parametrize("V", [33, 900])
+def test_extreme_temperatures(enc, V):
+    """t^2 and log2(e) / t stay normal floats within the range; beyond it the call is refused."""
+    from transformer_esm_layer_gb300.binding import EsmError
+    _, logits, ids, tl = _case(20, V, 9, torch.float32, 12)
+    for t in (1.2e-19, 1e-6, 5e18):  # (t^2 log V overflows from 7e18 on)
+        loss, lse, total, count = _run(enc, logits, ids, tl, t)
+        scored, rloss, rlse, q, hot, M = _reference(logits, ids, tl, t)
+        assert torch.all((loss.double() - rloss).abs() <= t * t * (1 + M) * (8 + M) * 2.0 ** -21)
+        assert torch.all((lse.double() - rlse).abs() <= (4 + M) * 2.0 ** -21)
+        assert torch.isfinite(loss).all() and torch.isfinite(lse).all()
+    d = torch.empty_like(logits)
+    for t in (1e-19, 1e-30, 1.2e-38, 4e-39, 1.9e19, 1e30, 3e38):
+        for call in (lambda: enc.op_distill_loss(logits, ids, tl, t, loss),
+                     lambda: enc.op_distill_loss_backward(logits, ids, tl, t, lse, d)):
+            with pytest.raises(EsmError) as e:
+                call()
+            assert e.value.status == 1
+    assert enc.check_status() == 0
+
+
 def test_no_row_scored_and_no_rows(enc):
     for V in (33, 500):
         logits = torch.full((7, V), float("nan"), device="cuda")

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cstring>
 #include <unordered_map>
 #include <vector>
@@ -1142,7 +1143,9 @@ static bool distill_args(esm_encoder* h, const void* logits, esm_precision type,
                          const int32_t* teacher_ids, const float* teacher_logits, int K, int T, int V,
                          float temperature, DistillArgs* a) {
   if (T < 0 || V <= 0 || K <= 0 || K > kDistillMaxK || stride < V) return false;
-  if (!(temperature > 0.f) || !(1.f / temperature > 0.f) || !(1.f / temperature <= 3.0e38f)) return false;
+  // (the loss takes the square of the temperature, the exponents log2(e) over it: both normal floats then)
+  const float sq = temperature * temperature;
+  if (!(temperature > 0.f) || !(sq >= FLT_MIN) || !(sq <= FLT_MAX)) return false;
   const size_t es = type == ESM_FP32 ? 4 : 2;
   if (T > 0 && (!logits || !teacher_ids || !teacher_logits || !aligned(logits, es) || !aligned(teacher_ids, 4) ||
                 !aligned(teacher_logits, 4)))
