@@ -64,3 +64,19 @@ def test_one_row_may_report_any_stride():
     assert binding.EsmEncoder._row_stride(one) == 7
     assert binding.EsmEncoder._row_stride(torch.zeros(1, 7).as_strided((1, 7), (1, 1))) == 7
     assert binding.EsmEncoder._row_stride(torch.zeros(3, 9)[:, :4]) == 9
+
+
+def test_integers_that_the_library_cannot_take_are_refused():
+    """ctypes would keep the low 32 bits: a side of 2^32 became one of 0."""
+    for window in ((2 ** 32, 0, 0), (0, 2 ** 31, 0), (1, 1, 2 ** 63), (-2 ** 31 - 1, 0, 0)):
+        with pytest.raises(ValueError, match="32"):
+            binding._window_struct(window)
+    for window in ((1.5, 0, 0), (1, "2", 0), (1, 1, float("nan"))):
+        with pytest.raises(ValueError):
+            binding._window_struct(window)
+    w = binding._window_struct((torch.tensor(7), 2 ** 31 - 1, 4.0))
+    assert (w.left, w.right, w.sinks) == (7, 2 ** 31 - 1, 4)
+    assert binding._c_int("f", "max_seqlen", 5) == 5
+    for n in (2 ** 32 + 64, 64.7):
+        with pytest.raises(ValueError, match="max_seqlen"):
+            binding._c_int("f", "max_seqlen", n)

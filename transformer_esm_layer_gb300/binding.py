@@ -245,9 +245,18 @@ def _check_workspace(t, where: str, device):
         _refuse(where, f"workspace must be a contiguous tensor on {device}")
 
 
+def _c_int(where: str, name: str, value) -> int:
+    """A whole number that fits the library's int (ctypes keeps the low 32 bits of any other)."""
+    n = int(value)
+    if n != value or not -2 ** 31 <= n < 2 ** 31:
+        _refuse(where, f"{name} must be a 32-bit whole number, not {value}")
+    return n
+
+
 def _window_struct(window) -> EsmAttnWindow:
     left, right, sinks = window
-    return EsmAttnWindow(int(left), int(right), int(sinks))
+    return EsmAttnWindow(_c_int("window", "left", left), _c_int("window", "right", right),
+                         _c_int("window", "sinks", sinks))
 
 
 class DeviceWeights:
@@ -514,8 +523,8 @@ class EsmEncoder:
                 workspace = self.op_attention_window_workspace(T, B, window, device=dev)
         _check_workspace(workspace, where, dev)
         self._raise(self.lib.esm_op_attention_window(self.handle, qkv.data_ptr(), cu_seqlens.data_ptr(), B, T,
-                                                     int(max_seqlen), ctypes.byref(_window_struct(window)),
-                                                     o.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                                                     _c_int(where, "max_seqlen", max_seqlen),
+                                                     ctypes.byref(_window_struct(window)), o.data_ptr(), _ptr(lse), workspace.data_ptr(),
                                                      workspace.nbytes, st), "esm_op_attention_window")
         return o
 
@@ -537,7 +546,7 @@ class EsmEncoder:
         _check_workspace(workspace, where, dev)
         self._raise(self.lib.esm_op_attention_window_backward(self.handle, qkv.data_ptr(), o.data_ptr(),
                                                               lse.data_ptr(), d_o.data_ptr(), cu_seqlens.data_ptr(),
-                                                              B, T, int(max_seqlen),
+                                                              B, T, _c_int(where, "max_seqlen", max_seqlen),
                                                               ctypes.byref(_window_struct(window)), dqkv.data_ptr(),
                                                               workspace.data_ptr(), workspace.nbytes, st),
                     "esm_op_attention_window_backward")
