@@ -579,7 +579,8 @@ ESM_API esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void
  * esm_encoder_check).  An id may stand in a row more than once.  A row without a usable entry is
  * not scored: its loss, its lse and its gradient are 0, whatever its logits are.
  * logits: device, float32 (logits_type ESM_FP32) or bfloat16 (ESM_BF16; other types:
- *   ESM_ERR_UNSUPPORTED) [T, vocab], rows logits_stride >= vocab elements apart; any vocab >= 1
+ *   ESM_ERR_UNSUPPORTED) [T, vocab], rows logits_stride >= vocab elements apart; T and vocab of up to
+ *   ESM_DISTILL_MAX each, vocab >= 1
  * teacher_ids, teacher_logits: device int32 and float32 [T, K], 1 <= K <= ESM_DISTILL_MAX_K
  * temperature: > 0, its square a normal float32 (about 1.1e-19 to 1.8e19)
  * token_loss: device float32 [T]; lse: device float32 [T] or NULL (the backward needs it);
@@ -588,6 +589,7 @@ ESM_API esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void
  *   aligned) may be NULL when both are NULL.
  * T == 0 sets loss_sum and count to 0.  Sums are float32 whatever the logits' type. */
 #define ESM_DISTILL_MAX_K 256
+#define ESM_DISTILL_MAX (1 << 30)
 ESM_API esm_status esm_op_distill_loss_workspace_size(const esm_encoder_t* h, int total_tokens, int vocab,
                                                       size_t* bytes);
 ESM_API esm_status esm_op_distill_loss(esm_encoder_t* h, const void* logits, esm_precision logits_type,

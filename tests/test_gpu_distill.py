@@ -234,6 +234,21 @@ def test_extreme_temperatures(enc, V):
     assert enc.check_status() == 0
 
 
+def test_sizes_that_32_bits_cannot_step_through_are_refused(enc):
+    from transformer_esm_layer_gb300.binding import EsmError
+    for T, V in ((2 ** 30, 33), (5, 2 ** 30)):
+        assert enc.op_distill_loss_workspace(T, V).numel() > 0
+    for T, V in ((2 ** 30 + 1, 33), (2 ** 31 - 1, 1), (5, 2 ** 30 + 1), (-1, 33), (5, 0)):
+        with pytest.raises(EsmError) as e:
+            enc.op_distill_loss_workspace(T, V)
+        assert e.value.status == 1
+    one = torch.zeros(1, 1, device="cuda")
+    ids = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    for T in (2 ** 30 + 1, 2 ** 32 + 1):  # (of the second the library would see one row)
+        with pytest.raises(ValueError, match="30 rows"):
+            enc.op_distill_loss(one.expand(T, 1), ids, one, 1.0, one[0])
+
+
 def test_no_row_scored_and_no_rows(enc):
     for V in (33, 500):
         logits = torch.full((7, V), float("nan"), device="cuda")

@@ -50,6 +50,7 @@ EXPORTS = ("esm_encoder_create", "esm_encoder_destroy", "esm_encoder_workspace_s
            "esm_encoder_set_attention_window", "esm_op_attention_window_workspace_size", "esm_op_attention_window",
            "esm_op_attention_window_backward", "esm_op_distill_loss_workspace_size", "esm_op_distill_loss",
            "esm_op_distill_loss_backward", "esm_encoder_lm_head_distill_backward")
+DISTILL_MAX = 1 << 30  # ESM_DISTILL_MAX
 PROFILE_CLASSES = ("gemm_qkv", "attention", "gemm_oproj", "gemm_fc1", "gemm_fc2", "layernorm", "other",
                    "gemm_backward")
 
@@ -524,8 +525,9 @@ class EsmEncoder:
         _check_workspace(workspace, where, dev)
         self._raise(self.lib.esm_op_attention_window(self.handle, qkv.data_ptr(), cu_seqlens.data_ptr(), B, T,
                                                      _c_int(where, "max_seqlen", max_seqlen),
-                                                     ctypes.byref(_window_struct(window)), o.data_ptr(), _ptr(lse), workspace.data_ptr(),
-                                                     workspace.nbytes, st), "esm_op_attention_window")
+                                                     ctypes.byref(_window_struct(window)), o.data_ptr(), _ptr(lse),
+                                                     workspace.data_ptr(), workspace.nbytes, st),
+                    "esm_op_attention_window")
         return o
 
     def op_attention_window_backward(self, qkv, o, lse, d_o, cu_seqlens, max_seqlen: int, window, dqkv,
@@ -570,6 +572,7 @@ class EsmEncoder:
         _need(len(shape) == 2 and (stride[1] == 1 or shape[1] == 1), where,
               "logits must be 2-D with contiguous rows")
         T, V = shape
+        _need(max(T, V) <= DISTILL_MAX, where, "logits must have at most 2^30 rows and columns")
         _need(isinstance(teacher_ids, torch.Tensor) and teacher_ids.dim() == 2, where, "teacher_ids must be [T, K]")
         K, dev = teacher_ids.shape[1], logits.device
         _check_tensor(teacher_ids, where, "teacher_ids", torch.int32, (T, K), dev)

@@ -1138,11 +1138,14 @@ esm_status esm_encoder_lm_head_backward_workspace_size(const esm_encoder_t* h, i
   return ESM_OK;
 }
 
+// Rows and values of a row that the distillation kernels count in 32 bits, with room for a step.
+static bool distill_sizes(int T, int V) { return T >= 0 && T <= ESM_DISTILL_MAX && V > 0 && V <= ESM_DISTILL_MAX; }
+
 // Arguments of the distillation loss that both directions share; false if one is invalid.
 static bool distill_args(esm_encoder* h, const void* logits, esm_precision type, long long stride,
                          const int32_t* teacher_ids, const float* teacher_logits, int K, int T, int V,
                          float temperature, DistillArgs* a) {
-  if (T < 0 || V <= 0 || K <= 0 || K > kDistillMaxK || stride < V) return false;
+  if (!distill_sizes(T, V) || K <= 0 || K > kDistillMaxK || stride < V) return false;
   // (the loss takes the square of the temperature, the exponents log2(e) over it: both normal floats then)
   const float sq = temperature * temperature;
   if (!(temperature > 0.f) || !(sq >= FLT_MIN) || !(sq <= FLT_MAX)) return false;
@@ -1718,7 +1721,7 @@ esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, c
 
 // ------------------------------------------------------------------ distillation
 esm_status esm_op_distill_loss_workspace_size(const esm_encoder_t* h, int total_tokens, int vocab, size_t* bytes) {
-  if (!h || !bytes || total_tokens < 0 || vocab <= 0) return ESM_ERR_INVALID_ARG;
+  if (!h || !bytes || !distill_sizes(total_tokens, vocab)) return ESM_ERR_INVALID_ARG;
   *bytes = distill_workspace_bytes(total_tokens, vocab, h->num_sms);
   return ESM_OK;
 }
