@@ -248,6 +248,8 @@ def _check_workspace(t, where: str, device):
 
 def _c_int(where: str, name: str, value) -> int:
     """A whole number that fits the library's int (ctypes keeps the low 32 bits of any other)."""
+    if type(value) is int and -2 ** 31 <= value < 2 ** 31:
+        return value
     n = int(value)
     if n != value or not -2 ** 31 <= n < 2 ** 31:
         _refuse(where, f"{name} must be a 32-bit whole number, not {value}")
@@ -572,7 +574,8 @@ class EsmEncoder:
         _need(len(shape) == 2 and (stride[1] == 1 or shape[1] == 1), where,
               "logits must be 2-D with contiguous rows")
         T, V = shape
-        _need(max(T, V) <= DISTILL_MAX, where, "logits must have at most 2^30 rows and columns")
+        if T > DISTILL_MAX or V > DISTILL_MAX:
+            _refuse(where, "logits must have at most 2^30 rows and columns")
         _need(isinstance(teacher_ids, torch.Tensor) and teacher_ids.dim() == 2, where, "teacher_ids must be [T, K]")
         K, dev = teacher_ids.shape[1], logits.device
         _check_tensor(teacher_ids, where, "teacher_ids", torch.int32, (T, K), dev)

@@ -364,7 +364,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
     // handed over, so that neither waits for the other.
     struct {
       Item x;
-      float m, inv;  // of this thread's row; inv = 0 where it sees no key, NaN where its scores make it so
+      // of this thread's row; inv = 0 where it sees no key (a padding query), inf where its scores are
+      // all -inf (0 inf = NaN), NaN where one is NaN or +inf
+      float m, inv;
       bool pending;
     } last;
     last.pending = false;
@@ -379,10 +381,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       const bool live = r < last.x.qrows;
       constexpr size_t kElem = (OUT == Act::BF16) ? 2 : 1;
       uint8_t* dst = static_cast<uint8_t*>(o) + ((size_t)(last.x.qrow0 + r) * d + (size_t)last.x.h * DH) * kElem;
-      // A row that sees no key is zero, one whose scores hold a NaN or +inf, or nothing but -inf, is
-      // NaN.  A zero weight times an infinite or NaN value is NaN, so values that a row does not see
-      // could reach it through the tile's product: any other row whose sums are not finite is set aside
-      // and summed over its visible keys alone below.
+      // A row that sees no key is zero.  A zero weight times an infinite or NaN value is NaN, so
+      // values that a row does not see could reach it through the tile's product: a row whose sums
+      // are not finite, but for its own scores, is set aside and summed over its visible keys alone below.
       uint64_t probe[4] = {0, 0, 0, 0};
       const uint64_t zero2 = f2_pack(0.f, 0.f);
 #pragma unroll
@@ -575,8 +576,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM)
       // ---- the item's row statistics
       last.x = x;
       last.m = m_ref;
-      const bool sees = cs0 > 0 || ch0 > cl0;
-      last.inv = l == 0.f && !sees ? 0.f : l == 0.f ? __int_as_float(0x7fffffff) : 1.f / l;
+      last.inv = l == 0.f && q >= x.klen ? 0.f : 1.f / l;  // (a query before klen sees itself)
       last.pending = true;
       // the natural-log softmax normaliser, ln 2 (m + log2 l) in the base-2 units used above
       if (lse != nullptr && r < x.qrows)
