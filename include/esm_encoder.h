@@ -377,8 +377,9 @@ ESM_API esm_status esm_op_attention(esm_encoder_t* h, const void* qkv, const int
  * apart from each other.
  * lse: device float32 [heads, T], head-major, or NULL: the natural-log softmax normaliser of
  * every row over the keys it sees, which the backward needs (bf16 activations only: an ESM_FP32
- * handle with lse is ESM_ERR_UNSUPPORTED).  Every row sees itself, so no row is empty.  Keys and
- * values that a row does not see have no influence on it, infinite and NaN ones included.
+ * handle with lse is ESM_ERR_UNSUPPORTED).  Every row sees itself, so no row is empty; one whose
+ * visible scores are all -inf is NaN, with lse -inf.  Keys and values that a row does not see have
+ * no influence on it, infinite and NaN ones included, under an unlimited window too.
  * Workspace: esm_op_attention_window_workspace_size bytes (backward: 1 for the backward below),
  * 256-byte aligned, of this call alone while it runs.  cu_seqlens and max_seqlen as for
  * esm_encoder_forward; total_tokens == 0 is a no-op. */
@@ -560,8 +561,8 @@ ESM_API esm_status esm_op_attention_backward(esm_encoder_t* h, const void* qkv, 
 
 /* esm_op_attention_backward with a window (bf16, head_dim 64): dqkv = dL/d(q | k | v) from qkv, o
  * and lse of esm_op_attention_window with the same window, and d_o = dL/do.  qkv, d_o, o and lse
- * must be finite, and dqkv apart from qkv and d_o.  The float32 sums over key tiles behind dq, and only those, are added in no fixed
- * order. */
+ * must be finite, and dqkv apart from qkv and d_o.  The float32 sums over key tiles behind dq, and
+ * only those, are added in no fixed order. */
 ESM_API esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, const void* o, const float* lse,
                                                     const void* d_o, const int32_t* cu_seqlens, int num_seqs,
                                                     int total_tokens, int max_seqlen, const esm_attn_window* window,

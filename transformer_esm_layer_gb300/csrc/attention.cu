@@ -96,8 +96,9 @@ __device__ __noinline__ void attention_f32_row_again(const float* qkv, float* o,
 // times an infinite or NaN value is NaN: a row that ends up not finite, but for its own scores, is
 // done again over its visible keys alone.
 //
-// Bound by the FMA units and shared memory: 16 products per two 16-byte loads.  One sequence of 1024
-// tokens, 8 heads, window 1024 + 1024: 135 us a call (a warp per row: 3680).
+// 16 products per two 16-byte loads of shared memory, four barriers per tile and no loads ahead of it:
+// one sequence of 1024 tokens, 8 heads, window 1024 + 1024, takes 143 us a call after an L2 flush, five
+// times its products at the FMA rate (the full attention's warp per row: 3700).
 constexpr int FQ = 32, FK = 64, FD = 64;
 __global__ void __launch_bounds__(128) attention_window_f32_kernel(const float* __restrict__ qkv, float* __restrict__ o,
                                                                    int d, int heads, int T, PackBuffers pb,

@@ -51,11 +51,12 @@
 // 3400 cycles of the 4100 that a pair takes in long runs.  So the other readers of shared memory went
 // where they could (row terms into the MMAs, P^T into tensor memory), and nothing waits for global
 // memory or for the other warps' ends of items: three Q / dO stages, the next item's K and V loaded
-// ahead, scores and gradient products from two threads.  Whole calls, against the full attention's
-// form of the kernel: 16384 packed tokens, 20 heads, window 128 + 128, one sink 195 us (276), of them
-// 148 here; 34374 tokens, left 512, four sinks 558 (791); 160 sequences of 100 tokens, one pair per
-// item 136 (205, both as graph replays).  What the call has beside this kernel is memory traffic: the row terms, the
-// accumulator's zeros and its rounding to dq.
+// ahead, scores and gradient products from two threads.  Whole calls with fresh inputs, and in
+// parentheses those of the first version, the full attention's form of the kernel with masks: 16384
+// packed tokens, 20 heads, window 128 + 128, one sink 195 us (276), three quarters of it here; 34374
+// tokens, left 512, four sinks 560 (791).  160 sequences of 100 tokens, one pair per item, 147 us a call
+// after an L2 flush, where the full attention's backward takes 222.  What the call has beside this
+// kernel is memory traffic: the row terms, the accumulator's zeros and its rounding to dq.
 #include "attn_plan.cuh"
 #include "common.cuh"
 #include "internal.h"

@@ -32,13 +32,13 @@
 // (scores from tensor memory, maximum, exponentials, P back, P V), on GB300 about 2800 cycles of
 // which the arithmetic is half, and two CTAs per SM interleave two of them; no pipe is above half
 // of its rate.  An item's O is brought out after the next item's first P has been handed over, from
-// registers in 32-byte pieces, which hides the last P V and leaves Q's buffers to the loads: 16384
-// packed tokens, 20 heads, window 128 + 128, one sink: 58 us (floor: 25 us of memory traffic);
-// with O brought out at the item's end through shared memory, 64 us.  Masks cost a fifth of that
-// call.  Measured and slower: two threads per row (72 us, twice the waits), 64-key tiles with
-// three CTAs per SM (68 us, the tensor pipe takes as long for 64 columns as for 128), skipping
-// or not masking 32-column chunks by branches (60 to 70 us: the compiler then schedules each
-// chunk by itself).
+// registers in 32-byte pieces, which hides the last P V and leaves Q's buffers to the loads.  Whole
+// calls on 16384 packed tokens, 20 heads, window 128 + 128, one sink: 66 us (floor: 25 us of memory
+// traffic); with O brought out at the item's end, 69 us; without masks a fifth less.  Measured and
+// slower, on the same call: two threads per row (87 us, twice the waits), 64-key tiles with three
+// CTAs per SM (77 us, the tensor pipe takes as long for 64 columns as for 128), skipping or not
+// masking 32-column chunks by branches (69 to 79 us: the compiler then schedules each chunk by
+// itself), and what a row sees kept for the epilogue through the tile loop (68 us).
 #include "attn_plan.cuh"
 #include "common.cuh"
 #include "internal.h"

@@ -8,8 +8,8 @@
 //   lse  = log sum_v exp(z_v / t),
 //   dloss/dz_v = t (q_v - sum_{k: id_k = v} p_k).
 //
-// A row without a usable entry is not scored: loss, lse and gradient 0, whatever its logits (unread in
-// rows above 256 values).
+// A row without a usable entry is not scored: loss, lse and gradient 0, whatever its logits (the loss
+// leaves them unread in rows above 256 values).
 // Logits are read once per call (forward: running maximum and sum per thread, merged in a
 // fixed order; backward: q from the forward's lse, each value overwritten where it is read, so
 // the gradient may take the logits' place).  Exponentials, sums and the loss are fp32 whatever
@@ -98,8 +98,8 @@ __device__ __forceinline__ void write_partials(float loss, int count, float* par
 // ---------------------------------------------------------------- group form
 // G lanes per row, N values of it per lane.  All loads of a row but the student's logits at the
 // teacher's ids are issued together; with 8 lanes per row the reductions are three shuffles
-// deep, and a warp has four rows' chains in flight (16384 x 33 fp32, 8 entries: 5.0 us against
-// 10.7 us with a warp per row).
+// deep, and a warp has four rows' chains in flight (16384 x 33 fp32, 8 entries: loss 8.9 us and
+// gradient 8.9 us a call against 15.0 and 17.0 with a warp per row, measured as at rows_form).
 //
 // Teacher softmax of the group's row, entries k = lane of the group, + G, ...: the maximum m of l (0 if
 // there is no finite one), the sum of exp((l - m) / t), whether any entry is usable.  The
@@ -560,8 +560,8 @@ __global__ void __launch_bounds__(kThreads)
     if (scored) {
       // Many entries: each leaves its number where its value goes, and one that finds another's
       // shares its id.  Ids of a row are nearly always distinct, and then this replaces comparing
-      // each with all (65536 x 1000 bf16, 100 entries: 212 us against 388; with 16 entries the
-      // comparisons are faster, 67 us against 73).
+      // each with all (65536 x 1000 bf16, 100 entries: 222 us against 388; with 16 entries the
+      // comparisons are faster, 71 us against 78; measured as at rows_form).
       bool shared = K <= kFewEntries;
       if (!shared) {
 #pragma unroll
@@ -633,9 +633,10 @@ __global__ void __launch_bounds__(256) distill_sum_kernel(const float* __restric
 // The form of a call, as the threads of a row: 8, 16 or 32 lanes with the row in registers; a warp
 // (with 2 or 8 teacher entries per lane) or a block that streams it.  A warp per row keeps eight
 // times the rows in flight: it is taken when there are more rows than resident blocks, unless
-// they are long (2000 rows of 8 KB: forward 14.4 us against 19.5 with a block per row, backward
-// 12.4 against 17.5; 65536 x 1000 bf16: 51 against 320 and 66 against 300; 300 rows of 16 KB,
-// the other way: 15.5 against 13.4 and 14.4 against 9.2; from 64 KB on they are alike).
+// they are long.  Warp and block per row, loss (without its sums) and gradient in us, each call by
+// events after an L2 flush, with 16 to 32 entries: 2000 rows of 8 KB 13.0 / 15.0 and 17.1 / 19.1;
+// 65536 x 1000 bf16 56 / 70 and 257 / 322; 2000 rows of 32 KB 25.2 / 33.4 and 23.2 / 31.5, of 64 KB
+// 41.6 / 55.9 and 35.5 / 51.9; 300 rows of 16 KB 12.9 / 15.0 and 8.9 / 10.9.
 enum class Form { kGroup8x4, kGroup8x8, kGroup16x8, kGroup32x8, kWarpRow2, kWarpRow8, kBlockRow };
 constexpr int kWarpRowBytes = 32768;
 Form rows_form(int T, int V, int K, int elem, int num_sms) {
