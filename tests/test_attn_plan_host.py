@@ -26,7 +26,7 @@ def host(tmp_path_factory):
         text = re.sub(r"^#(include|pragma once).*$", "", f.read(), flags=re.M)
     (tmp / "attn_plan.inc").write_text(text)
     so = str(tmp / "plan.so")
-    subprocess.run([gxx, "-std=c++20", "-O1", "-shared", "-fPIC", "-pthread", "-w",
+    subprocess.run([gxx, "-std=c++20", "-O1", "-fwrapv", "-shared", "-fPIC", "-pthread", "-w",
                     f'-DATTN_PLAN_SOURCE="{tmp}/attn_plan.inc"', os.path.join(ROOT, "tests", "host_plan.cpp"), "-o", so],
                    check=True)
     return ctypes.CDLL(so)
