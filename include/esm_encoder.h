@@ -612,6 +612,114 @@ ESM_API esm_status esm_op_distill_loss_backward(esm_encoder_t* h, const void* lo
                                                 float temperature, const float* lse, const int* loss_count,
                                                 void* d_logits, long long d_stride, esm_stream_t stream);
 
+/* ---- the residual stream of a training step: dropout, embedding, norms around a block ----
+ * No counterpart on the pages, which only name the embedding: what a training step does between its
+ * products and its attention.  rows, vocab and token counts of up to ESM_STREAM_MAX each.  float32
+ * arithmetic and sums whatever the types; every sum runs in a fixed order.
+ * Tensors named in one call lie apart from each other except where it says that two may be the same
+ * (ESM_ERR_INVALID_ARG where this is broken). */
+#define ESM_STREAM_MAX (1 << 30)
+
+/* Dropout by a counter-based generator.  The mask is a function of (rng[0], rng[1] + offset, row,
+ * column): the backward draws it again, and nothing is stored.  rng is read when the kernels run, so
+ * a captured graph draws new masks when the program writes another base between replays; offset tells
+ * the dropouts of one step apart.
+ * Element (r, c) of [rows, cols] has 16 bits u: of Philox4x32-10 with key rng[0] (lower word first)
+ * and counter (b, o), b = r * ceil(cols / 8) + c / 8 and o = rng[1] + offset modulo 2^64 (each lower
+ * word first), the output word (c % 8) / 2, its lower half for even c and its upper half for odd.
+ * With n = p * 65536 rounded to a whole number (halves up), the element is kept if u >= n and then multiplied by
+ * 65536 / (65536 - n); others become 0 whatever they hold (n = 65536: all of them).
+ * A NULL esm_dropout*, or n = 0, is no dropout. */
+typedef struct {
+  const int64_t* rng; /* device int64 [2], 8-byte aligned: seed, base */
+  int64_t offset;
+  double p;           /* 0 <= p <= 1 */
+} esm_dropout;
+
+/* y = dropout(x), or residual + dropout(x).  x: device [rows, cols] of x_type, y (and residual, or
+ * NULL) of y_type, each ESM_FP32 or ESM_BF16 (others: ESM_ERR_UNSUPPORTED), rows x_stride, residual_stride
+ * and y_stride >= cols elements apart (cols of up to ESM_STREAM_MAX).  y may be x (same type and stride) or
+ * the residual (same stride); rows of y and another tensor may alternate in one buffer if
+ * their strides and types are the same.  Elements between the rows are left as they are.  The gradient with
+ * respect to x is the same call on dy (without a residual). */
+ESM_API esm_status esm_op_dropout(esm_encoder_t* h, const void* x, esm_precision x_type, long long x_stride,
+                                  const void* residual, long long residual_stride, void* y, esm_precision y_type,
+                                  long long y_stride, int rows, int cols, const esm_dropout* dropout,
+                                  esm_stream_t stream);
+
+/* out[t] = dropout(scale * row_scale[t] * table[ids[t]]): the embedding with the factors that go with it
+ * (row_scale: 0 for masked tokens and 1 / (1 - their share) for the others of a sequence, say).
+ * ids device int32 [tokens], each in [0, vocab) or -1: no token, a row of zeros; any other id is
+ * treated as -1 and latches ESM_ERR_TOKEN_RANGE (see esm_encoder_check).  table: device [vocab, cols] of
+ * table_type; row_scale: device float32 [tokens] or NULL (all 1); out: device, out_type, rows
+ * out_stride >= cols elements apart, elements between them left as they are.  Types: ESM_FP32 or ESM_BF16
+ * (others: ESM_ERR_UNSUPPORTED).  cols of up to ESM_EMBED_MAX_COLS. */
+#define ESM_EMBED_MAX_COLS (1 << 20)
+ESM_API esm_status esm_op_embed(esm_encoder_t* h, const int32_t* ids, int tokens, const void* table,
+                                esm_precision table_type, int vocab, int cols, float scale, const float* row_scale,
+                                const esm_dropout* dropout, void* out, esm_precision out_type, long long out_stride,
+                                esm_stream_t stream);
+
+/* Its gradient: d_table[v] = sum over the tokens with ids[t] = v of scale * row_scale[t] *
+ * dropout(d_out[t]), added to what d_table holds if accumulate != 0 (a tied table's other part).
+ * d_table: device float32 [vocab, cols], every row written; d_out: device, d_type (ESM_FP32 or ESM_BF16),
+ * rows d_stride >= cols elements apart; the rest as in the forward.  Every element's sum runs over its
+ * tokens in an order that the ids alone determine.  Workspace: the size query's bytes, 256-byte aligned, of this call
+ * alone while it runs. */
+ESM_API esm_status esm_op_embed_backward_workspace_size(const esm_encoder_t* h, int tokens, int vocab, int cols,
+                                                        size_t* bytes);
+ESM_API esm_status esm_op_embed_backward(esm_encoder_t* h, const int32_t* ids, int tokens, const void* d_out,
+                                         esm_precision d_type, long long d_stride, float scale, const float* row_scale,
+                                         const esm_dropout* dropout, float* d_table, int vocab, int cols, int accumulate,
+                                         void* workspace, size_t workspace_bytes, esm_stream_t stream);
+
+/* The residual stream between two blocks: for every row,
+ *   u = dropout(post(y)),   x_out = residual_scale * x + gate * u,   h = pre(x_out),
+ * post the norm after the block that made y, pre the norm before the next block; each
+ * (z - mean(z)) / sqrt(var(z) + eps) * gamma + beta (ESM_NORM_LAYER, the biased variance) or
+ * z / sqrt(mean(z^2) + eps) * gamma + beta (ESM_NORM_RMS), eps of the handle's config.
+ * post_gamma NULL: post(y) = y; pre_gamma NULL: no h (h_out is NULL then); a beta of NULL (as it must be
+ * without its gamma) is 0; gate NULL is 1.
+ * y, h_out: device [rows, cols] in the activation dtype; gammas, betas and gate: device [cols] of that
+ * type too, or, with gate_rows != 0, a gate [rows, cols] of its own for every row; x, x_out: device float32
+ * [rows, cols].  x_out may be x and h_out may be y.  stats: device float32 [rows, 4] or NULL, 16-byte
+ * aligned: mean and 1 / sqrt(.. + eps) of post, then of pre, which the backward needs (0 where there is no norm;
+ * an RMS norm's mean is 0).  1 <= cols <= ESM_BLOCK_NORM_MAX_COLS (more: ESM_ERR_UNSUPPORTED). */
+#define ESM_BLOCK_NORM_MAX_COLS 8192
+typedef enum { ESM_NORM_LAYER = 0, ESM_NORM_RMS = 1 } esm_norm_kind;
+typedef struct {
+  esm_norm_kind kind;
+  float residual_scale;
+  const void* post_gamma;
+  const void* post_beta;
+  const void* pre_gamma;
+  const void* pre_beta;
+} esm_block_norm;
+ESM_API esm_status esm_op_block_norm(esm_encoder_t* h, const esm_block_norm* norm, const void* gate, int gate_rows,
+                                     const esm_dropout* dropout, const float* x, const void* y, float* x_out,
+                                     void* h_out, float* stats, int rows, int cols, esm_stream_t stream);
+
+/* Its gradient.  From x_out, y and stats of the forward with the same norm, gate and dropout, d_x_out = dL/d(x_out)
+ * (device float32 [rows, cols]; NULL: 0) and d_h = dL/dh (the activation dtype; NULL exactly
+ * when there is no pre): dx (float32 [rows, cols]; may be d_x_out), dy (activation dtype; may be d_h or y)
+ * and the parameters' gradients, each of which may be NULL: float32 [cols], summed over the rows; with
+ * gate_rows the gate's is [rows, cols] in the activation dtype.  A gradient of a parameter that is NULL must be NULL.
+ * x_out and stats are not read for pre if there is none (x_out may be NULL then).  rows == 0 sets the
+ * parameters' gradients to 0.  Workspace as above. */
+typedef struct {
+  float* post_gamma;
+  float* post_beta;
+  float* pre_gamma;
+  float* pre_beta;
+  void* gate;
+} esm_block_norm_grads;
+ESM_API esm_status esm_op_block_norm_backward_workspace_size(const esm_encoder_t* h, int rows, int cols, size_t* bytes);
+ESM_API esm_status esm_op_block_norm_backward(esm_encoder_t* h, const esm_block_norm* norm, const void* gate,
+                                              int gate_rows, const esm_dropout* dropout, const float* x_out,
+                                              const void* y, const float* stats, const float* d_x_out, const void* d_h,
+                                              float* dx, void* dy, const esm_block_norm_grads* grads, int rows,
+                                              int cols, void* workspace, size_t workspace_bytes, esm_stream_t stream);
+
 /* ---- measurement hooks ----
  * Kernel classes of the forward: 0 QKV GEMM (+bias, RoPE), 1 attention, 2 output-projection
  * GEMM (+bias, residual), 3 fc1 GEMM (+bias, GELU), 4 fc2 GEMM (+bias, residual),

@@ -49,7 +49,10 @@ EXPORTS = ("esm_encoder_create", "esm_encoder_destroy", "esm_encoder_workspace_s
            "esm_op_quantize_nvfp4", "esm_op_gemm_nvfp4", "esm_encoder_get_fp4_scales", "esm_status_string",
            "esm_encoder_set_attention_window", "esm_op_attention_window_workspace_size", "esm_op_attention_window",
            "esm_op_attention_window_backward", "esm_op_distill_loss_workspace_size", "esm_op_distill_loss",
-           "esm_op_distill_loss_backward", "esm_encoder_lm_head_distill_backward")
+           "esm_op_distill_loss_backward", "esm_encoder_lm_head_distill_backward", "esm_op_dropout", "esm_op_embed",
+           "esm_op_embed_backward_workspace_size", "esm_op_embed_backward", "esm_op_block_norm",
+           "esm_op_block_norm_backward_workspace_size", "esm_op_block_norm_backward")
+STREAM_MAX = 1 << 30  # ESM_STREAM_MAX
 DISTILL_MAX = 1 << 30  # ESM_DISTILL_MAX
 PROFILE_CLASSES = ("gemm_qkv", "attention", "gemm_oproj", "gemm_fc1", "gemm_fc2", "layernorm", "other",
                    "gemm_backward")
@@ -104,6 +107,24 @@ class EsmLmHead(ctypes.Structure):
 
 class EsmLmHeadGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in LM_HEAD_NAMES]
+
+
+class EsmDropout(ctypes.Structure):
+    _fields_ = [("rng", ctypes.c_void_p), ("offset", ctypes.c_int64), ("p", ctypes.c_double)]
+
+
+_PD = ctypes.POINTER(EsmDropout)
+NORM_KINDS = {"layer": 0, "rms": 1}
+BLOCK_NORM_PARAMS = ("post_gamma", "post_beta", "pre_gamma", "pre_beta")
+
+
+class EsmBlockNorm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("residual_scale", ctypes.c_float)] + \
+        [(n, ctypes.c_void_p) for n in BLOCK_NORM_PARAMS]
+
+
+class EsmBlockNormGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in BLOCK_NORM_PARAMS + ("gate",)]
 
 
 _lib = None
@@ -174,6 +195,14 @@ def load_library() -> ctypes.CDLL:
         "esm_op_distill_loss_workspace_size": (i32, [vp, i32, i32, ctypes.POINTER(sz)]),
         "esm_op_distill_loss": (i32, [vp, vp, i32, i64, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp, sz, vp]),
         "esm_op_distill_loss_backward": (i32, [vp, vp, i32, i64, vp, vp, i32, i32, i32, f32, vp, vp, vp, i64, vp]),
+        "esm_op_dropout": (i32, [vp, vp, i32, i64, vp, i64, vp, i32, i64, i32, i32, _PD, vp]),
+        "esm_op_embed": (i32, [vp, vp, i32, vp, i32, i32, i32, f32, vp, _PD, vp, i32, i64, vp]),
+        "esm_op_embed_backward_workspace_size": (i32, [vp, i32, i32, i32, ctypes.POINTER(sz)]),
+        "esm_op_embed_backward": (i32, [vp, vp, i32, vp, i32, i64, f32, vp, _PD, vp, i32, i32, i32, vp, sz, vp]),
+        "esm_op_block_norm": (i32, [vp, ctypes.POINTER(EsmBlockNorm), vp, i32, _PD, vp, vp, vp, vp, vp, i32, i32, vp]),
+        "esm_op_block_norm_backward_workspace_size": (i32, [vp, i32, i32, ctypes.POINTER(sz)]),
+        "esm_op_block_norm_backward": (i32, [vp, ctypes.POINTER(EsmBlockNorm), vp, i32, _PD, vp, vp, vp, vp, vp, vp,
+                                             vp, ctypes.POINTER(EsmBlockNormGrads), i32, i32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -325,6 +354,67 @@ class DeviceLmHead:
         to = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(device=device, dtype=dt)
         self.t = {k: to(w[k]) for k in ("dense_w", "dense_b", "ln_g", "ln_b", "emb", "bias")}
         self.struct = EsmLmHead(*[self.t[k].data_ptr() for k in ("dense_w", "dense_b", "ln_g", "ln_b", "emb", "bias")])
+
+
+class _Frozen:
+    """Objects whose C struct is made once: a later change of an attribute would not reach it."""
+
+    __slots__ = ()
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{type(self).__name__} cannot be changed: make another")
+
+    def _set(self, **values):
+        for name, value in values.items():
+            object.__setattr__(self, name, value)
+
+
+class Dropout(_Frozen):
+    """A dropout of probability p whose mask is drawn from (seed, base + offset) and never stored.
+
+    ``rng``: int64 CUDA tensor (seed, base), read when a kernel runs: a training program adds to the
+    base every step (in place, on the device), and captured graphs see it.  ``offset`` tells the
+    dropouts of one step apart.  Give the same object to a forward call and its backward."""
+
+    __slots__ = ("p", "rng", "offset", "device", "struct")
+
+    def __init__(self, p: float, rng, offset: int = 0):
+        where = "Dropout"
+        _need(isinstance(rng, torch.Tensor) and rng.is_cuda, where, "rng must be a CUDA tensor")
+        _check_tensor(rng, where, "rng", torch.int64, (2,), rng.device)
+        p, offset = float(p), int(offset)
+        _need(0.0 <= p <= 1.0, where, f"p must be in [0, 1], not {p}")
+        _need(-2 ** 63 <= offset < 2 ** 63, where, "offset must be a 64-bit whole number")
+        self._set(p=p, rng=rng, offset=offset, device=rng.device, struct=EsmDropout(rng.data_ptr(), offset, p))
+
+
+class BlockNorm(_Frozen):
+    """The norms on both sides of a block and the scale of the residual they are added to (the
+    arguments of EsmEncoder.op_block_norm that a model keeps): kind "layer" or "rms"; gammas and betas
+    [cols] of the handle's parameter dtype, a gamma of None for no norm, a beta of None for none."""
+
+    __slots__ = ("kind", "residual_scale", "cols", "dtype", "device", "struct") + BLOCK_NORM_PARAMS
+
+    def __init__(self, kind: str = "layer", post_gamma=None, post_beta=None, pre_gamma=None, pre_beta=None,
+                 residual_scale: float = 1.0):
+        where = "BlockNorm"
+        _need(kind in NORM_KINDS, where, f"kind must be one of {sorted(NORM_KINDS)}")
+        given = dict(post_gamma=post_gamma, post_beta=post_beta, pre_gamma=pre_gamma, pre_beta=pre_beta)
+        for norm in ("post", "pre"):
+            _need(given[norm + "_gamma"] is not None or given[norm + "_beta"] is None, where,
+                  f"{norm}_beta needs {norm}_gamma")
+        first = next((t for t in given.values() if t is not None), None)
+        cols = dtype = device = None
+        if first is not None:
+            _need(isinstance(first, torch.Tensor) and first.dim() == 1, where, "parameters must be 1-D tensors")
+            _need(first.dtype in (torch.float32, torch.bfloat16), where, "parameters must be float32 or bfloat16")
+            cols, dtype, device = first.shape[0], first.dtype, first.device
+            for name, t in given.items():
+                if t is not None:
+                    _check_tensor(t, where, name, dtype, (cols,), device)
+        scale = float(residual_scale)
+        self._set(kind=kind, residual_scale=scale, cols=cols, dtype=dtype, device=device,
+                  struct=EsmBlockNorm(NORM_KINDS[kind], scale, *[_ptr(given[n]) for n in BLOCK_NORM_PARAMS]), **given)
 
 
 class EsmEncoder:
@@ -636,6 +726,192 @@ class EsmEncoder:
                                                           _launch_stream(where, stream, dev)),
                     "esm_op_distill_loss_backward")
         return d_logits
+
+    # ------------------------------------------------------------------ the residual stream
+    @staticmethod
+    def _check_rows(t, where: str, name: str, device):
+        """A 2-D float32 or bfloat16 tensor with contiguous rows; returns its esm_precision and row stride."""
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device):
+            _refuse(where, f"{name} must be a CUDA tensor on {device}")
+        kind = 0 if t.dtype is torch.float32 else 1 if t.dtype is torch.bfloat16 else -1
+        if kind < 0:
+            _refuse(where, f"{name} must be float32 or bfloat16")
+        if t.dim() != 2:
+            _refuse(where, f"{name} must be 2-D")
+        (rows, cols), (stride, step) = t.shape, t.stride()
+        if not (step == 1 or cols == 1):
+            _refuse(where, f"{name} must have contiguous rows")
+        if rows > STREAM_MAX or cols > STREAM_MAX:
+            _refuse(where, f"{name} must have at most 2^30 rows and columns")
+        return kind, stride if rows > 1 else max(stride, cols)
+
+    @staticmethod
+    def _dropout_struct(dropout, where: str, device):
+        if dropout is None:
+            return None
+        if not (isinstance(dropout, Dropout) and dropout.device == device):
+            _refuse(where, f"dropout must be a Dropout with its rng on {device}")
+        return dropout.struct
+
+    def op_dropout(self, x, y, dropout: Optional[Dropout], residual=None, stream=None):
+        """esm_op_dropout: y = dropout(x), or residual + dropout(x); float32 or bf16 [rows, cols], rows
+        may be strided.  y may be x or the residual.  The gradient: the same call on dy."""
+        where = "op_dropout"
+        _need(isinstance(x, torch.Tensor) and x.is_cuda, where, "x must be a CUDA tensor")
+        dev = x.device
+        kx, sx = self._check_rows(x, where, "x", dev)
+        ky, sy = self._check_rows(y, where, "y", dev)
+        _need(y.shape == x.shape, where, "y must have the shape of x")
+        sr = 0
+        if residual is not None:
+            kr, sr = self._check_rows(residual, where, "residual", dev)
+            _need(kr == ky and residual.shape == x.shape, where, "residual must have the type and shape of y")
+        d = self._dropout_struct(dropout, where, dev)
+        self._raise(self.lib.esm_op_dropout(self.handle, x.data_ptr(), kx, sx, _ptr(residual), sr, y.data_ptr(), ky, sy,
+                                            x.shape[0], x.shape[1], d, _launch_stream(where, stream, dev)),
+                    "esm_op_dropout")
+        return y
+
+    @staticmethod
+    def _check_ids(where: str, ids, row_scale):
+        _need(isinstance(ids, torch.Tensor) and ids.is_cuda and ids.dim() == 1, where, "ids must be a 1-D CUDA tensor")
+        T, dev = ids.shape[0], ids.device
+        _check_tensor(ids, where, "ids", torch.int32, (T,), dev)
+        _need(T <= STREAM_MAX, where, "ids must hold at most 2^30 tokens")
+        if row_scale is not None:
+            _check_tensor(row_scale, where, "row_scale", torch.float32, (T,), dev)
+        return T, dev
+
+    def op_embed(self, ids, table, out, scale: float = 1.0, row_scale=None, dropout: Optional[Dropout] = None,
+                 stream=None):
+        """esm_op_embed: out[t] = dropout(scale * row_scale[t] * table[ids[t]]), a row of zeros for id -1.
+        ids int32 [T], table [vocab, cols] and out [T, cols] float32 or bf16 (out's rows may be strided),
+        row_scale float32 [T]."""
+        where = "op_embed"
+        T, dev = self._check_ids(where, ids, row_scale)
+        kt, _ = self._check_rows(table, where, "table", dev)
+        ko, so = self._check_rows(out, where, "out", dev)
+        V, cols = table.shape
+        _need(table.is_contiguous(), where, "table must be contiguous")
+        _need(out.shape == (T, cols), where, f"out must be {[T, cols]}")
+        d = self._dropout_struct(dropout, where, dev)
+        self._raise(self.lib.esm_op_embed(self.handle, ids.data_ptr(), T, table.data_ptr(), kt, V, cols, float(scale),
+                                          _ptr(row_scale), d, out.data_ptr(), ko, so,
+                                          _launch_stream(where, stream, dev)), "esm_op_embed")
+        return out
+
+    def op_embed_backward_workspace(self, T: int, vocab: int, cols: int, device="cuda"):
+        where, n = "op_embed_backward_workspace", ctypes.c_size_t()
+        T, vocab, cols = _c_int(where, "T", T), _c_int(where, "vocab", vocab), _c_int(where, "cols", cols)
+        self._raise(self.lib.esm_op_embed_backward_workspace_size(self.handle, T, vocab, cols, ctypes.byref(n)),
+                    "esm_op_embed_backward_workspace_size")
+        return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+
+    def op_embed_backward(self, ids, d_out, d_table, scale: float = 1.0, row_scale=None,
+                          dropout: Optional[Dropout] = None, accumulate: bool = False, workspace=None, stream=None):
+        """esm_op_embed_backward: d_table (float32 [vocab, cols]) = or, with accumulate, += the sum over each
+        id's tokens of scale * row_scale[t] * dropout(d_out[t]); d_out float32 or bf16 [T, cols]."""
+        where = "op_embed_backward"
+        T, dev = self._check_ids(where, ids, row_scale)
+        kd, sd = self._check_rows(d_out, where, "d_out", dev)
+        _need(isinstance(d_table, torch.Tensor) and d_table.dim() == 2, where, "d_table must be a 2-D tensor")
+        V, cols = d_table.shape
+        _need(V <= STREAM_MAX and cols <= STREAM_MAX, where, "d_table must have at most 2^30 rows and columns")
+        _check_tensor(d_table, where, "d_table", torch.float32, (V, cols), dev)
+        _need(d_out.shape == (T, cols), where, f"d_out must be {[T, cols]}")
+        d = self._dropout_struct(dropout, where, dev)
+        st = _launch_stream(where, stream, dev)
+        if workspace is None:
+            with _allocating(stream):
+                workspace = self.op_embed_backward_workspace(T, V, cols, dev)
+        _check_workspace(workspace, where, dev)
+        self._raise(self.lib.esm_op_embed_backward(self.handle, ids.data_ptr(), T, d_out.data_ptr(), kd, sd,
+                                                   float(scale), _ptr(row_scale), d, d_table.data_ptr(), V, cols,
+                                                   int(bool(accumulate)), workspace.data_ptr(), workspace.nbytes, st),
+                    "esm_op_embed_backward")
+        return d_table
+
+    def _check_block_norm(self, where: str, norm, y, gate):
+        """The block's output, norms and gate; returns rows, cols, the device and whether the gate has rows."""
+        _need(isinstance(norm, BlockNorm), where, "norm must be a BlockNorm")
+        _need(isinstance(y, torch.Tensor) and y.is_cuda and y.dim() == 2, where, "y must be a 2-D CUDA tensor")
+        rows, cols = y.shape
+        dev, act = y.device, self.out_dtype
+        _check_tensor(y, where, "y", act, (rows, cols), dev)
+        _need(rows <= STREAM_MAX and cols <= STREAM_MAX, where, "y must have at most 2^30 rows and columns")
+        if norm.cols is not None and not (norm.cols == cols and norm.dtype is act and norm.device == dev):
+            _refuse(where, f"norm's parameters must be {act} [{cols}] on {dev}")
+        gate_rows = 0
+        if gate is not None:
+            gate_rows = int(isinstance(gate, torch.Tensor) and gate.dim() == 2)
+            _check_tensor(gate, where, "gate", act, (rows, cols) if gate_rows else (cols,), dev)
+        return rows, cols, dev, gate_rows
+
+    def op_block_norm(self, norm: BlockNorm, x, y, x_out, h=None, gate=None, dropout: Optional[Dropout] = None,
+                      stats=None, stream=None):
+        """esm_op_block_norm: x_out = residual_scale * x + gate * dropout(post(y)), h = pre(x_out), with
+        norm's post and pre.  x, x_out float32 [rows, cols] (x_out may be x); y, h of the activation dtype (h may
+        be y; None without a pre); gate [cols] or [rows, cols]; stats float32 [rows, 4] for the backward."""
+        where = "op_block_norm"
+        rows, cols, dev, gate_rows = self._check_block_norm(where, norm, y, gate)
+        _check_tensor(x, where, "x", torch.float32, (rows, cols), dev)
+        _check_tensor(x_out, where, "x_out", torch.float32, (rows, cols), dev)
+        _need((h is not None) == (norm.pre_gamma is not None), where, "h goes with a norm before the next block")
+        if h is not None:
+            _check_tensor(h, where, "h", self.out_dtype, (rows, cols), dev)
+        if stats is not None:
+            _check_tensor(stats, where, "stats", torch.float32, (rows, 4), dev)
+        d = self._dropout_struct(dropout, where, dev)
+        self._raise(self.lib.esm_op_block_norm(self.handle, norm.struct, _ptr(gate), gate_rows, d, x.data_ptr(),
+                                               y.data_ptr(), x_out.data_ptr(), _ptr(h), _ptr(stats), rows, cols,
+                                               _launch_stream(where, stream, dev)), "esm_op_block_norm")
+        return x_out, h
+
+    def op_block_norm_backward_workspace(self, rows: int, cols: int, device="cuda"):
+        where, n = "op_block_norm_backward_workspace", ctypes.c_size_t()
+        rows, cols = _c_int(where, "rows", rows), _c_int(where, "cols", cols)
+        self._raise(self.lib.esm_op_block_norm_backward_workspace_size(self.handle, rows, cols, ctypes.byref(n)),
+                    "esm_op_block_norm_backward_workspace_size")
+        return torch.empty(int(n.value), dtype=torch.uint8, device=device)
+
+    def op_block_norm_backward(self, norm: BlockNorm, x_out, y, stats, d_x_out, d_h, dx, dy, grads: Dict, gate=None,
+                               dropout: Optional[Dropout] = None, workspace=None, stream=None):
+        """esm_op_block_norm_backward: dx (float32; may be d_x_out), dy (the activation dtype; may be d_h or
+        y) and the gradients named in grads ("post_gamma", "post_beta", "pre_gamma", "pre_beta", "gate":
+        float32 [cols]; the gradient of a gate [rows, cols] like the gate) from x_out, y and stats of the forward,
+        d_x_out float32 (None: 0) and d_h (None exactly without a pre)."""
+        where = "op_block_norm_backward"
+        rows, cols, dev, gate_rows = self._check_block_norm(where, norm, y, gate)
+        act, full = self.out_dtype, (rows, cols)
+        pre = norm.pre_gamma is not None
+        _need((d_h is not None) == pre, where, "d_h goes with a norm before the next block")
+        for name, t, dt in (("x_out", x_out, torch.float32), ("d_x_out", d_x_out, torch.float32), ("d_h", d_h, act),
+                            ("dx", dx, torch.float32), ("dy", dy, act)):
+            if t is not None or name in ("dx", "dy") or (pre and name == "x_out"):
+                _check_tensor(t, where, name, dt, full, dev)
+        if pre or norm.post_gamma is not None:
+            _check_tensor(stats, where, "stats", torch.float32, (rows, 4), dev)
+        g = EsmBlockNormGrads()
+        for name, t in grads.items():
+            has = gate if name == "gate" else getattr(norm, name) if name in BLOCK_NORM_PARAMS else None
+            _need(has is not None, where, f"there is no {name!r} to take a gradient of")
+            if name == "gate" and gate_rows:
+                _check_tensor(t, where, "grads['gate']", act, full, dev)
+            else:
+                _check_tensor(t, where, f"grads[{name!r}]", torch.float32, (cols,), dev)
+            setattr(g, name, t.data_ptr())
+        d = self._dropout_struct(dropout, where, dev)
+        st = _launch_stream(where, stream, dev)
+        if workspace is None:
+            with _allocating(stream):
+                workspace = self.op_block_norm_backward_workspace(rows, cols, dev)
+        _check_workspace(workspace, where, dev)
+        self._raise(self.lib.esm_op_block_norm_backward(self.handle, norm.struct, _ptr(gate), gate_rows, d, _ptr(x_out),
+                                                        y.data_ptr(), _ptr(stats), _ptr(d_x_out), _ptr(d_h),
+                                                        dx.data_ptr(), dy.data_ptr(), g, rows, cols,
+                                                        workspace.data_ptr(), workspace.nbytes, st),
+                    "esm_op_block_norm_backward")
+        return dx, dy, grads
 
     def set_layer_precision(self, per_layer):
         """esm_encoder_set_layer_precision: one of "fp32", "bf16", "fp8", "fp4" per layer."""

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cstring>
 #include <unordered_map>
 #include <vector>
@@ -1778,6 +1779,270 @@ esm_status esm_op_distill_loss_backward(esm_encoder_t* h, const void* logits, es
   a.d_logits = d_logits;
   a.d_stride = d_stride;
   return cuda_status(launch_distill_loss_backward(a, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ the residual stream
+// A tensor of rows as a call names it: rows `stride` elements of `es` bytes apart.
+struct Rows {
+  const void* p;
+  long long stride;
+  int rows, cols, es;
+  size_t bytes() const { return rows > 0 ? ((size_t)(rows - 1) * stride + cols) * es : 0; }
+};
+
+// No element of one is an element of the other: apart in memory, or rows that alternate.
+static bool rows_apart(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return true;
+  if (disjoint(a.p, a.bytes(), b.p, b.bytes())) return true;
+  if (a.stride != b.stride || a.es != b.es || a.cols != b.cols) return false;
+  const long long pitch = a.stride * a.es, width = (long long)a.cols * a.es;
+  long long off = (long long)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % pitch;
+  if (off < 0) off += pitch;
+  return off >= width && off <= pitch - width;
+}
+static bool same_or_apart(const Rows& a, const Rows& b) {
+  return (a.p == b.p && a.stride == b.stride && a.es == b.es) || rows_apart(a, b);
+}
+static bool apart(const Rows& a, const void* p, size_t n) { return !p || disjoint(a.p, a.bytes(), p, n); }
+
+static bool stream_size(int n) { return n >= 0 && n <= ESM_STREAM_MAX; }
+static bool stream_type(esm_precision t) { return t == ESM_FP32 || t == ESM_BF16; }
+static int type_bytes(esm_precision t) { return t == ESM_FP32 ? 4 : 2; }
+
+// The mask of a dropout that may be NULL; false if it is malformed.
+static bool drop_mask(const esm_dropout* d, DropMask* m) {
+  *m = DropMask{nullptr, 0, 0, 1.f};
+  if (!d) return true;
+  if (!(d->p >= 0.0 && d->p <= 1.0) || !d->rng || !aligned(d->rng, 8)) return false;
+  const unsigned n = (unsigned)(d->p * 65536.0 + 0.5);
+  if (n == 0) return true;
+  m->rng = reinterpret_cast<const unsigned long long*>(d->rng);
+  m->offset = (unsigned long long)d->offset;
+  m->threshold = n;
+  m->scale = n >= 65536 ? 0.f : (float)(65536.0 / (65536 - n));
+  return true;
+}
+
+esm_status esm_op_dropout(esm_encoder_t* h, const void* x, esm_precision x_type, long long x_stride,
+                          const void* residual, long long residual_stride, void* y, esm_precision y_type,
+                          long long y_stride, int rows, int cols, const esm_dropout* dropout, esm_stream_t stream) {
+  DropoutArgs a{};
+  if (!h || !stream_size(rows) || !stream_size(cols) || !drop_mask(dropout, &a.mask)) return ESM_ERR_INVALID_ARG;
+  if (!stream_type(x_type) || !stream_type(y_type)) return ESM_ERR_UNSUPPORTED;
+  if (x_stride < cols || y_stride < cols || (residual && residual_stride < cols)) return ESM_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return ESM_OK;
+  const int ex = type_bytes(x_type), ey = type_bytes(y_type);
+  if (!x || !y || !aligned(x, ex) || !aligned(y, ey) || !aligned(residual, ey)) return ESM_ERR_INVALID_ARG;
+  const Rows rx{x, x_stride, rows, cols, ex}, ry{y, y_stride, rows, cols, ey}, rr{residual, residual_stride, rows, cols, ey};
+  if (!same_or_apart(ry, rx) || !same_or_apart(ry, rr) || !apart(ry, a.mask.rng, 16)) return ESM_ERR_INVALID_ARG;
+  a.x = x;
+  a.residual = residual;
+  a.y = y;
+  a.x_bf16 = x_type == ESM_BF16;
+  a.y_bf16 = y_type == ESM_BF16;
+  a.x_stride = x_stride;
+  a.res_stride = residual_stride;
+  a.y_stride = y_stride;
+  a.rows = rows;
+  a.cols = cols;
+  return cuda_status(launch_dropout(a, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static bool embed_sizes(int tokens, int vocab, int cols) {
+  return stream_size(tokens) && vocab > 0 && vocab <= ESM_STREAM_MAX && cols > 0 && cols <= ESM_EMBED_MAX_COLS;
+}
+
+// What the lookup and its gradient share; `rows` is out or d_out.
+static bool embed_args(esm_encoder* h, const int32_t* ids, int tokens, int vocab, int cols, float scale,
+                       const float* row_scale, const esm_dropout* dropout, const void* rows, esm_precision type,
+                       long long stride, EmbedArgs* a) {
+  *a = EmbedArgs{};
+  if (!embed_sizes(tokens, vocab, cols) || stride < cols || !drop_mask(dropout, &a->mask)) return false;
+  if (tokens > 0 && (!ids || !rows)) return false;
+  if (!aligned(ids, 4) || !aligned(row_scale, 4) || !aligned(rows, type_bytes(type))) return false;
+  a->ids = ids;
+  a->row_scale = row_scale;
+  a->out = const_cast<void*>(rows);
+  a->out_bf16 = type == ESM_BF16;
+  a->out_stride = stride;
+  a->tokens = tokens;
+  a->vocab = vocab;
+  a->cols = cols;
+  a->scale = scale;
+  a->err = h->d_err;
+  return true;
+}
+
+esm_status esm_op_embed(esm_encoder_t* h, const int32_t* ids, int tokens, const void* table, esm_precision table_type,
+                        int vocab, int cols, float scale, const float* row_scale, const esm_dropout* dropout, void* out,
+                        esm_precision out_type, long long out_stride, esm_stream_t stream) {
+  EmbedArgs a;
+  if (!h) return ESM_ERR_INVALID_ARG;
+  if (!stream_type(table_type) || !stream_type(out_type)) return ESM_ERR_UNSUPPORTED;
+  if (!embed_args(h, ids, tokens, vocab, cols, scale, row_scale, dropout, out, out_type, out_stride, &a))
+    return ESM_ERR_INVALID_ARG;
+  if (tokens == 0) return ESM_OK;
+  const int et = type_bytes(table_type);
+  if (!table || !aligned(table, et)) return ESM_ERR_INVALID_ARG;
+  const Rows ro{out, out_stride, tokens, cols, type_bytes(out_type)};
+  if (!apart(ro, table, (size_t)vocab * cols * et) || !apart(ro, ids, 4 * (size_t)tokens) ||
+      !apart(ro, row_scale, 4 * (size_t)tokens) || !apart(ro, a.mask.rng, 16))
+    return ESM_ERR_INVALID_ARG;
+  a.table = table;
+  a.table_bf16 = table_type == ESM_BF16;
+  return cuda_status(launch_embed_scaled(a, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+esm_status esm_op_embed_backward_workspace_size(const esm_encoder_t* h, int tokens, int vocab, int cols, size_t* bytes) {
+  if (!h || !bytes || !embed_sizes(tokens, vocab, cols)) return ESM_ERR_INVALID_ARG;
+  *bytes = embed_grad_workspace_bytes(tokens, vocab, cols, h->num_sms);
+  return ESM_OK;
+}
+
+esm_status esm_op_embed_backward(esm_encoder_t* h, const int32_t* ids, int tokens, const void* d_out,
+                                 esm_precision d_type, long long d_stride, float scale, const float* row_scale,
+                                 const esm_dropout* dropout, float* d_table, int vocab, int cols, int accumulate,
+                                 void* workspace, size_t workspace_bytes, esm_stream_t stream) {
+  EmbedArgs a;
+  if (!h) return ESM_ERR_INVALID_ARG;
+  if (!stream_type(d_type)) return ESM_ERR_UNSUPPORTED;
+  if (!embed_args(h, ids, tokens, vocab, cols, scale, row_scale, dropout, d_out, d_type, d_stride, &a) || !d_table ||
+      !aligned(d_table, 4))
+    return ESM_ERR_INVALID_ARG;
+  const size_t need = embed_grad_workspace_bytes(tokens, vocab, cols, h->num_sms);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ESM_ERR_WORKSPACE;
+  const Rows rd{d_out, d_stride, tokens, cols, type_bytes(d_type)}, rt{d_table, cols, vocab, cols, 4};
+  if (!rows_apart(rt, rd) || !apart(rt, tokens ? ids : nullptr, 4 * (size_t)tokens) ||
+      !apart(rt, tokens ? row_scale : nullptr, 4 * (size_t)tokens) || !apart(rt, a.mask.rng, 16) ||
+      !apart(rt, workspace, need))
+    return ESM_ERR_INVALID_ARG;
+  if (workspace == h->train_ws) h->train_buf = nullptr;  // as check_ws: the pending backward's index is overwritten
+  a.d_table = d_table;
+  a.accumulate = accumulate != 0;
+  return cuda_status(launch_embed_grad(a, workspace, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// What both directions of the block norm share.
+static esm_status block_norm_args(esm_encoder* h, const esm_block_norm* n, const void* gate, int gate_rows,
+                                  const esm_dropout* dropout, const void* y, int rows, int cols, BlockNormArgs* a) {
+  *a = BlockNormArgs{};
+  if (!h || !n || !stream_size(rows) || cols <= 0 || !drop_mask(dropout, &a->mask)) return ESM_ERR_INVALID_ARG;
+  if (cols > ESM_BLOCK_NORM_MAX_COLS) return ESM_ERR_UNSUPPORTED;
+  if (n->kind != ESM_NORM_LAYER && n->kind != ESM_NORM_RMS) return ESM_ERR_INVALID_ARG;
+  if ((n->post_beta && !n->post_gamma) || (n->pre_beta && !n->pre_gamma)) return ESM_ERR_INVALID_ARG;
+  const size_t es = h->act_bytes();
+  if (rows > 0 && !y) return ESM_ERR_INVALID_ARG;
+  for (const void* p : {n->post_gamma, n->post_beta, n->pre_gamma, n->pre_beta, gate, y})
+    if (!aligned(p, es)) return ESM_ERR_INVALID_ARG;
+  a->rms = n->kind == ESM_NORM_RMS;
+  a->gate_rows = gate && gate_rows;
+  a->eps = h->cfg.ln_eps;
+  a->residual_scale = n->residual_scale;
+  a->post_gamma = n->post_gamma;
+  a->post_beta = n->post_beta;
+  a->pre_gamma = n->pre_gamma;
+  a->pre_beta = n->pre_beta;
+  a->gate = gate;
+  a->rows = rows;
+  a->cols = cols;
+  a->y = y;
+  return ESM_OK;
+}
+
+// A tensor that a block norm writes lies apart from the parameters and the generator's state.
+static bool apart_from_params(const BlockNormArgs& a, const Rows& r, size_t es) {
+  for (const void* p : {a.post_gamma, a.post_beta, a.pre_gamma, a.pre_beta})
+    if (!apart(r, p, a.cols * es)) return false;
+  return apart(r, a.gate, (a.gate_rows ? (size_t)a.rows : 1) * a.cols * es) && apart(r, a.mask.rng, 16);
+}
+
+esm_status esm_op_block_norm(esm_encoder_t* h, const esm_block_norm* norm, const void* gate, int gate_rows,
+                             const esm_dropout* dropout, const float* x, const void* y, float* x_out, void* h_out,
+                             float* stats, int rows, int cols, esm_stream_t stream) {
+  BlockNormArgs a;
+  const esm_status s = block_norm_args(h, norm, gate, gate_rows, dropout, y, rows, cols, &a);
+  if (s != ESM_OK) return s;
+  if (rows == 0) return ESM_OK;
+  const int es = (int)h->act_bytes();
+  if (!x || !x_out || (norm->pre_gamma != nullptr) != (h_out != nullptr)) return ESM_ERR_INVALID_ARG;
+  if (!aligned(x, 4) || !aligned(x_out, 4) || !aligned(h_out, es) || !aligned(stats, 16)) return ESM_ERR_INVALID_ARG;
+  const Rows rx{x, cols, rows, cols, 4}, ry{y, cols, rows, cols, es}, ro{x_out, cols, rows, cols, 4},
+      rh{h_out, cols, rows, cols, es}, rs{stats, 4, rows, 4, 4};
+  if (!same_or_apart(ro, rx) || !rows_apart(ro, ry) || !rows_apart(ro, rh) || !rows_apart(rh, rx) ||
+      !same_or_apart(rh, ry) || !rows_apart(rs, rx) || !rows_apart(rs, ry) || !rows_apart(rs, ro) || !rows_apart(rs, rh))
+    return ESM_ERR_INVALID_ARG;
+  if (!apart_from_params(a, ro, es) || (h_out && !apart_from_params(a, rh, es)) || (stats && !apart_from_params(a, rs, es)))
+    return ESM_ERR_INVALID_ARG;
+  a.x = x;
+  a.x_out = x_out;
+  a.h = h_out;
+  a.stats = stats;
+  return cuda_status(launch_block_norm(a, es == 2, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+esm_status esm_op_block_norm_backward_workspace_size(const esm_encoder_t* h, int rows, int cols, size_t* bytes) {
+  if (!h || !bytes || !stream_size(rows) || cols <= 0) return ESM_ERR_INVALID_ARG;
+  if (cols > ESM_BLOCK_NORM_MAX_COLS) return ESM_ERR_UNSUPPORTED;
+  *bytes = align256(block_norm_bwd_workspace_bytes(rows, cols, h->num_sms));
+  return ESM_OK;
+}
+
+esm_status esm_op_block_norm_backward(esm_encoder_t* h, const esm_block_norm* norm, const void* gate, int gate_rows,
+                                      const esm_dropout* dropout, const float* x_out, const void* y, const float* stats,
+                                      const float* d_x_out, const void* d_h, float* dx, void* dy,
+                                      const esm_block_norm_grads* grads, int rows, int cols, void* workspace,
+                                      size_t workspace_bytes, esm_stream_t stream) {
+  BlockNormArgs a;
+  const esm_status s = block_norm_args(h, norm, gate, gate_rows, dropout, y, rows, cols, &a);
+  if (s != ESM_OK) return s;
+  const int es = (int)h->act_bytes();
+  const bool pre = norm->pre_gamma != nullptr, post = norm->post_gamma != nullptr;
+  if (!grads || (grads->post_gamma && !post) || (grads->post_beta && !norm->post_beta) || (grads->pre_gamma && !pre) ||
+      (grads->pre_beta && !norm->pre_beta) || (grads->gate && !gate))
+    return ESM_ERR_INVALID_ARG;
+  if (rows > 0 && ((pre || post) && !stats)) return ESM_ERR_INVALID_ARG;
+  if (rows > 0 && (!dx || !dy || (pre && !x_out) || pre != (d_h != nullptr))) return ESM_ERR_INVALID_ARG;
+  const int eg = a.gate_rows ? es : 4;
+  if (!aligned(x_out, 4) || !aligned(stats, 16) || !aligned(d_x_out, 4) || !aligned(d_h, es) || !aligned(dx, 4) ||
+      !aligned(dy, es) || !aligned(grads->post_gamma, 4) || !aligned(grads->post_beta, 4) ||
+      !aligned(grads->pre_gamma, 4) || !aligned(grads->pre_beta, 4) || !aligned(grads->gate, eg))
+    return ESM_ERR_INVALID_ARG;
+  const size_t need = align256(block_norm_bwd_workspace_bytes(rows, cols, h->num_sms));
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ESM_ERR_WORKSPACE;
+  // what is written: each apart from what is read (dx may be d_x_out, dy may be d_h or y) and from the others
+  const Rows in[] = {{d_x_out, cols, rows, cols, 4}, {y, cols, rows, cols, es}, {d_h, cols, rows, cols, es},
+                     {x_out, cols, rows, cols, 4},   {stats, 4, rows, 4, 4}};
+  const Rows out[] = {{dx, cols, rows, cols, 4},
+                      {dy, cols, rows, cols, es},
+                      {grads->gate, cols, a.gate_rows ? rows : 1, cols, eg},
+                      {grads->post_gamma, cols, 1, cols, 4},
+                      {grads->post_beta, cols, 1, cols, 4},
+                      {grads->pre_gamma, cols, 1, cols, 4},
+                      {grads->pre_beta, cols, 1, cols, 4},
+                      {workspace, (long long)need, 1, (int)std::min(need, (size_t)INT_MAX), 1}};
+  for (int i = 0; i < 8; ++i) {
+    if (!out[i].p) continue;
+    for (int j = 0; j < 5; ++j) {
+      const bool may_be = (i == 0 && j == 0) || (i == 1 && (j == 1 || j == 2));
+      if (may_be ? !same_or_apart(out[i], in[j]) : !rows_apart(out[i], in[j])) return ESM_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < i; ++j)
+      if (!rows_apart(out[i], out[j])) return ESM_ERR_INVALID_ARG;
+    if (!apart_from_params(a, out[i], es)) return ESM_ERR_INVALID_ARG;
+  }
+  if (workspace == h->train_ws) h->train_buf = nullptr;
+  a.x_out = const_cast<float*>(x_out);
+  a.stats = const_cast<float*>(stats);
+  a.d_x_out = d_x_out;
+  a.d_h = d_h;
+  a.dx = dx;
+  a.dy = dy;
+  a.d_post_gamma = grads->post_gamma;
+  a.d_post_beta = grads->post_beta;
+  a.d_pre_gamma = grads->pre_gamma;
+  a.d_pre_beta = grads->pre_beta;
+  a.d_gate = grads->gate;
+  return cuda_status(launch_block_norm_bwd(a, es == 2, workspace, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------------------------ training

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/esm_encoder.h"
+#include "dropout.cuh"
 
 namespace esm {
 
@@ -325,6 +326,65 @@ size_t distill_workspace_bytes(int T, int V, int num_sms);
 cudaError_t launch_distill_loss(const DistillArgs& a, float* loss_sum, int* count, void* workspace, int num_sms,
                                 cudaStream_t st);
 cudaError_t launch_distill_loss_backward(const DistillArgs& a, int num_sms, cudaStream_t st);
+
+// ---------------------------------------------------------------- dropout.cu, embedding.cu, block_norm.cu
+// True if rows `stride` elements of `es` bytes apart all start on 16-byte boundaries (NULL: true).
+inline bool rows_on_16(const void* p, long long stride, int es) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * es)) & 15) == 0 || p == nullptr;
+}
+struct DropoutArgs {
+  const void* x;
+  const void* residual;  // of y's type, or NULL
+  void* y;
+  bool x_bf16, y_bf16;
+  long long x_stride, res_stride, y_stride;
+  int rows, cols;
+  DropMask mask;
+};
+cudaError_t launch_dropout(const DropoutArgs& a, int num_sms, cudaStream_t st);
+
+// Lookup: table (vocab x cols) -> out; gradient: out (= dL/d(out)) -> d_table.
+struct EmbedArgs {
+  const int32_t* ids;      // [tokens], -1: none
+  const float* row_scale;  // [tokens] or NULL
+  const void* table;
+  void* out;               // rows out_stride apart
+  float* d_table;
+  bool table_bf16, out_bf16, accumulate;
+  long long out_stride;
+  int tokens, vocab, cols;
+  float scale;
+  DropMask mask;
+  unsigned* err;
+};
+cudaError_t launch_embed_scaled(const EmbedArgs& a, int num_sms, cudaStream_t st);
+size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols, int num_sms);
+cudaError_t launch_embed_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaStream_t st);
+
+// Norm after a block, dropout, gate, residual and norm before the next (cols <= ESM_BLOCK_NORM_MAX_COLS).
+// y, h, the norms' parameters and the gate are bf16 or fp32, the residual stream is fp32.
+struct BlockNormArgs {
+  bool rms, gate_rows;
+  float eps, residual_scale;
+  const void *post_gamma, *post_beta, *pre_gamma, *pre_beta;  // [cols]; a gamma of NULL: no norm
+  const void* gate;                                           // [cols], [rows, cols] (gate_rows) or NULL
+  DropMask mask;
+  int rows, cols;
+  const void* y;
+  const float* x;
+  float* x_out;   // (the backward only reads it)
+  void* h;
+  float* stats;   // [rows, 4]: mean and 1 / deviation of post, of pre
+  const float* d_x_out;
+  const void* d_h;
+  float* dx;
+  void* dy;
+  float *d_post_gamma, *d_post_beta, *d_pre_gamma, *d_pre_beta;  // each may be NULL
+  void* d_gate;   // fp32 [cols], or [rows, cols] of y's type
+};
+cudaError_t launch_block_norm(const BlockNormArgs& a, bool bf16, int num_sms, cudaStream_t st);
+size_t block_norm_bwd_workspace_bytes(int rows, int cols, int num_sms);
+cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, bool bf16, void* workspace, int num_sms, cudaStream_t st);
 
 // ---------------------------------------------------------------- fp8.cu
 // Quantise a bf16 tensor to e4m3 with *scale; record max|w| into *amax.
