@@ -1895,7 +1895,7 @@ esm_status esm_op_embed(esm_encoder_t* h, const int32_t* ids, int tokens, const 
 
 esm_status esm_op_embed_backward_workspace_size(const esm_encoder_t* h, int tokens, int vocab, int cols, size_t* bytes) {
   if (!h || !bytes || !embed_sizes(tokens, vocab, cols)) return ESM_ERR_INVALID_ARG;
-  *bytes = embed_grad_workspace_bytes(tokens, vocab, cols, h->num_sms);
+  *bytes = embed_grad_workspace_bytes(tokens, vocab, cols);
   return ESM_OK;
 }
 
@@ -1909,7 +1909,7 @@ esm_status esm_op_embed_backward(esm_encoder_t* h, const int32_t* ids, int token
   if (!embed_args(h, ids, tokens, vocab, cols, scale, row_scale, dropout, d_out, d_type, d_stride, &a) || !d_table ||
       !aligned(d_table, 4))
     return ESM_ERR_INVALID_ARG;
-  const size_t need = embed_grad_workspace_bytes(tokens, vocab, cols, h->num_sms);
+  const size_t need = embed_grad_workspace_bytes(tokens, vocab, cols);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ESM_ERR_WORKSPACE;
   const Rows rd{d_out, d_stride, tokens, cols, type_bytes(d_type)}, rt{d_table, cols, vocab, cols, 4};
   if (!rows_apart(rt, rd) || !apart(rt, tokens ? ids : nullptr, 4 * (size_t)tokens) ||
