@@ -54,16 +54,17 @@ __device__ __forceinline__ uint4 philox(const PhiloxState& s, unsigned long long
   return make_uint4(c0, c1, c2, c3);
 }
 
-// Bit j: element j of block b is kept (all of them without a dropout).
+// Bit j: element j of block b is kept (all of them without a dropout).  With n >= 1, bits u are kept if
+// u > n - 1: the upper half of a word w is if w > (n - 1) * 65536 + 65535, the lower one if 65536 w is.
 __device__ __forceinline__ uint32_t keep8(const DropMask& m, const PhiloxState& s, unsigned long long b) {
   if (m.rng == nullptr) return 0xffu;
   const uint4 w = philox(s, b);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w}, limit = (m.threshold << 16) - 1u;
   uint32_t bits = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    bits |= ((u[j] & 0xffffu) >= m.threshold ? 1u : 0u) << (2 * j);
-    bits |= ((u[j] >> 16) >= m.threshold ? 1u : 0u) << (2 * j + 1);
+    if ((u[j] << 16) > limit) bits |= 1u << (2 * j);
+    if (u[j] > limit) bits |= 2u << (2 * j);
   }
   return bits;
 }
@@ -143,6 +144,68 @@ __device__ __forceinline__ void span_store(T* row, int left, int lane, const flo
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     if (span_col<VEC>(lane, k) < left) st1(row + span_col<VEC>(lane, k), v[k]);
+}
+
+// Eight values of a lane as they stand in memory: four registers for bfloat16, which kernels keep or stage.
+template <typename T, bool VEC>
+struct Span8 {
+  float v[8];
+  __device__ __forceinline__ void load(const T* row, int left, int lane) { span_load<VEC>(row, left, lane, v); }
+  __device__ __forceinline__ void fill(float x) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = x;
+  }
+  __device__ __forceinline__ void get(float (&out)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) out[k] = v[k];
+  }
+};
+template <>
+struct Span8<__nv_bfloat16, true> {
+  uint32_t v[4];
+  // (the row's length is a multiple of 8 here)
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int left, int lane) {
+    const uint4 a = 8 * lane < left ? __ldg(reinterpret_cast<const uint4*>(row + 8 * lane)) : make_uint4(0, 0, 0, 0);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+  __device__ __forceinline__ void fill(float x) { v[0] = v[1] = v[2] = v[3] = pack_bf16x2(x, x); }
+  __device__ __forceinline__ void get(float (&out)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = bf16x2_to_f2(v[i]);
+      out[2 * i] = f.x;
+      out[2 * i + 1] = f.y;
+    }
+  }
+};
+
+// ---- a thread's own eight values of rows to come, copied ahead into shared memory ----
+// Chunk c of 16 bytes of thread t stands at (c * threads + t) * 16 of its stage, so a warp's accesses are
+// conflict-free; a thread reads only what it copied itself, so waiting for its own copies is enough.
+template <typename T>
+constexpr int kChunks = sizeof(T) / 2;  // 16-byte chunks of eight values
+
+template <typename T>
+__device__ __forceinline__ void stage_copy(uint8_t* stage, int chunk, const T* row, int left, int lane) {
+#pragma unroll
+  for (int i = 0; i < kChunks<T>; ++i) {
+    constexpr int per = 16 / sizeof(T);
+    const bool in = 8 * lane + per * i < left;
+    cp_async_16(stage + ((size_t)(chunk + i) * blockDim.x + threadIdx.x) * 16, row + (in ? 8 * lane + per * i : 0),
+                in ? 16u : 0u);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void stage_read(const uint8_t* stage, int chunk, float (&v)[8]) {
+  const uint8_t* at = stage + ((size_t)chunk * blockDim.x + threadIdx.x) * 16;
+  if constexpr (sizeof(T) == 2) {
+    ld8(reinterpret_cast<const __nv_bfloat16*>(at), v);
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(at);
+    const float4 b = *reinterpret_cast<const float4*>(at + (size_t)blockDim.x * 16);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
 }
 
 #endif  // __CUDACC__
