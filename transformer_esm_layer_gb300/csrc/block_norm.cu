@@ -8,6 +8,7 @@
 // stream and its gradient are float32).  So every value is read and written once, a row's statistics and
 // sums never leave the SM, and the rows to come are copied into shared memory while this one is worked on.
 #include <algorithm>
+#include <type_traits>
 
 #include "dropout.cuh"
 #include "internal.h"
@@ -15,149 +16,225 @@
 namespace esm {
 namespace {
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// Mean and 1 / sqrt(var + eps) of a row of `cols` values held by W warps, 256 columns each.  A warp's own
-// mean and squared deviations are taken in two passes over its registers; those of several warps are
-// joined with their counts (Chan, Golub, LeVeque 1979): no digits are lost to a large mean, and there
-// is one barrier.  slot: [W] of shared memory; sync: the barrier of the row's threads.
-template <bool VEC, typename Sync>
-__device__ __forceinline__ float2 row_moments(const float (&z)[8], bool rms, float eps, int cols, int left, int W, int w,
-                                              int lane, float2* slot, Sync sync) {
-  float mean = 0.f, q = 0.f;
-  if (!rms) {
-    const float s = ((z[0] + z[1]) + (z[2] + z[3])) + ((z[4] + z[5]) + (z[6] + z[7]));
-    mean = warp_sum(s) / (float)min(left, 256);
-  }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float d = span_col<VEC>(lane, k) < left ? z[k] - mean : 0.f;
-    q = fmaf(d, d, q);
-  }
-  q = warp_sum(q);
-  if (W > 1) {
-    if (lane == 0) slot[w] = make_float2(mean, q);
-    sync();
-    const float last = (float)(cols - 256 * (W - 1));
-    float m = 0.f;
-    q = 0.f;
-    if (!rms) {
-      for (int i = 0; i < W - 1; ++i) m += slot[i].x;
-      m = (m * 256.f + slot[W - 1].x * last) / (float)cols;
-    }
-    for (int i = 0; i < W; ++i) {
-      const float2 o = slot[i];
-      const float d = o.x - m;
-      q += fmaf((i < W - 1 ? 256.f : last) * d, d, o.y);
-    }
-    mean = m;
-  }
-  return make_float2(mean, rsqrtf(q / (float)cols + eps));
-}
-
 // ---- forward ----
-// One warp per 256 columns, W = ceil(cols / 256) warps per row and block; a block takes every gridDim.x-th
-// row.  Some rows of x and y are on their way while one is worked on (VEC; rows that do not start
-// on 16 bytes are read where they are used).
-template <int MAXT>
-constexpr int kFwdStages = MAXT <= 256 ? 4 : 3;  // (8192 float32 columns: 64 KB each)
+// A block takes R rows, W = ceil(cols / 256) warps to each, eight columns of every row to a lane.  Rows come as
+// blocks of the grid, not in a loop: with 40 to 80 registers the SM holds 30 to 45 warps whose loads, sums and
+// stores interleave by themselves.  R = 2 where there are rows enough: the parameters are read and unpacked
+// once for both, the generator's round keys are shared, and one barrier serves both rows' sums.
+#ifndef KFWDROWS
+#define KFWDROWS 2
+#endif
+#ifndef KFWDMIN
+#define KFWDMIN 0
+#endif
+struct RowShape {
+  float inv_cols, last, inv_last;  // of the columns of a row's last warp
+};
 
-template <typename T, bool VEC, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 1) block_norm_kernel(const BlockNormArgs a) {
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 slots[2][2][32];
-  const int W = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// A warp's own mean and squared deviations are taken in two passes over its registers, and those of
+// several warps joined by their counts (Chan, Golub, LeVeque 1979), so no digits are lost to a large mean
+// and the row's warps meet once.  Counts are 256 but for the last warp's; means are taken relative to the
+// first warp's, so that one pass over the slots is enough:  sum of n d^2 about the joint mean is
+// sum of n d^2 - cols shift^2.
+template <int W>
+__device__ __forceinline__ float2 join_moments(const float2* slot, int warps, const RowShape& s) {
+  const float2 first = slot[0];
+  float d1 = 0.f, d2 = 0.f, q = first.y;
+  auto add = [&](int i) {
+    const float2 o = slot[i];
+    const float d = o.x - first.x;
+    d1 += d;
+    d2 = fmaf(d, d, d2);
+    q += o.y;
+  };
+  if constexpr (W > 0) {
+#pragma unroll
+    for (int i = 1; i < W - 1; ++i) add(i);
+  } else {
+#pragma unroll 4
+    for (int i = 1; i < warps - 1; ++i) add(i);
+  }
+  const float2 o = slot[warps - 1];
+  const float d = o.x - first.x, nd = s.last * d;
+  d1 = fmaf(256.f, d1, nd);
+  d2 = fmaf(256.f, d2, nd * d);
+  const float shift = d1 * s.inv_cols;
+  return make_float2(first.x + shift, q + o.y + fmaf(-shift, d1, d2));
+}
+
+// Mean and 1 / sqrt(var + eps) of R rows of which this lane holds z (0 past the row's end).
+template <int R, int W, bool VEC>
+__device__ __forceinline__ void row_moments(const Pairs (&z)[R], const BlockNormArgs& a, const RowShape& s, int left,
+                                            int warps, int w, int lane, float2 (*slot)[W > 0 ? W : 32], float2 (&out)[R]) {
+  float mean[R], q[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) mean[r] = a.rms ? 0.f : sum(z[r]);
+  if (!a.rms) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) mean[r] += __shfl_xor_sync(0xffffffffu, mean[r], o);
+#pragma unroll
+    for (int r = 0; r < R; ++r) mean[r] *= w == warps - 1 ? s.inv_last : 1.f / 256.f;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    Pairs d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = f2_add(z[r][i], f2_both(-mean[r]));
+    if (left < 256) span_trim<VEC>(left, lane, d);
+    uint64_t t = f2_mul(d[0], d[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) t = f2_fma(d[i], d[i], t);
+    q[r] = f2_sum(t);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int r = 0; r < R; ++r) q[r] += __shfl_xor_sync(0xffffffffu, q[r], o);
+  if (warps > 1) {
+    if (lane == 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) slot[r][w] = make_float2(mean[r], q[r]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float2 j = make_float2(mean[r], q[r]);
+    if (warps > 1) j = join_moments<W>(slot[r], warps, s);
+    out[r] = make_float2(j.x, rsqrtf(fmaf(j.y, s.inv_cols, a.eps)));
+  }
+}
+
+// W = 0: the number of warps is blockDim.x / 32.  VEC: every row on 16 bytes and cols % 8 == 0.
+template <typename T, bool VEC, int W, int R>
+__global__ void __launch_bounds__(W > 0 ? 32 * W : 1024, W > 0 && KFWDMIN ? KFWDMIN : 1)
+    block_norm_kernel(const BlockNormArgs a, const RowShape shape) {
+  __shared__ float2 slots[2][R][W > 0 ? W : 32];
+  const int warps = W > 0 ? W : blockDim.x >> 5, w = W == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = w * 256, left = a.cols - c0;
-  const bool post_on = a.post_gamma != nullptr, pre_on = a.pre_gamma != nullptr;
-  const size_t stage_bytes = (size_t)(2 + kChunks<T>) * blockDim.x * 16;
-  const T* yc = static_cast<const T*>(a.y) + c0;
-  const float* xc = a.x + c0;
-  auto copy_ahead = [&](long long row, int stage) {
-    if (row < a.rows) {
-      stage_copy(ring + stage * stage_bytes, 0, xc + (size_t)row * a.cols, left, lane);
-      stage_copy(ring + stage * stage_bytes, 2, yc + (size_t)row * a.cols, left, lane);
-    }
-    cp_async_commit();
+  const bool active = 8 * lane < left;  // (VEC)
+  // (a lane past the row's end works on the row's first columns and writes nothing)
+  const int c = VEC ? (active ? c0 + 8 * lane : 0) : c0;
+  auto fetch = [&](auto* p, auto& raw) {
+    if constexpr (VEC) raw.load(p + c, 8);
+    else span_load<false>(p + c0, left, lane, raw);
   };
-  if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < kFwdStages<MAXT> - 1; ++i) copy_ahead(blockIdx.x + (long long)i * gridDim.x, i);
-  }
-  const PhiloxState ps = philox_state(a.mask);
-  const int per_row = (a.cols + 7) / 8;
-  // bfloat16 parameters stay in registers, float32 ones are read again for every row (from the L1)
-  constexpr bool kKeep = sizeof(T) == 2 && VEC;
-  Span8<T, VEC> post_gamma, post_beta, pre_gamma, pre_beta, gate;
-  auto fetch = [&](Span8<T, VEC>& to, const void* p, float without) {
-    to.fill(without);
-    if (p) to.load(static_cast<const T*>(p) + c0, left, lane);
+  auto read = [](const auto& raw, Pairs& v) {
+    if constexpr (VEC) raw.get(v);
+    else v[0] = raw[0], v[1] = raw[1], v[2] = raw[2], v[3] = raw[3];
   };
-  if (kKeep) {
-    fetch(post_gamma, a.post_gamma, 1.f);
-    fetch(post_beta, a.post_beta, 0.f);
-    fetch(pre_gamma, a.pre_gamma, 1.f);
-    fetch(pre_beta, a.pre_beta, 0.f);
-    if (!a.gate_rows) fetch(gate, a.gate, 1.f);
-  }
-  int stage = 0, flip = 0;
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const size_t base = (size_t)row * a.cols + c0;
-    float x[8], u[8], p[8];
-    if (a.gate_rows) gate.load(static_cast<const T*>(a.gate) + base, left, lane);
+  auto store = [&](auto* p, const Pairs& v) {
     if constexpr (VEC) {
-      copy_ahead(row + (long long)(kFwdStages<MAXT> - 1) * gridDim.x, stage == 0 ? kFwdStages<MAXT> - 1 : stage - 1);
-      cp_async_wait<kFwdStages<MAXT> - 1>();
-      stage_read<float>(ring + stage * stage_bytes, 0, x);
-      stage_read<T>(ring + stage * stage_bytes, 2, u);
-      stage = stage == kFwdStages<MAXT> - 1 ? 0 : stage + 1;
+      if (active) st8(p + c, v);
     } else {
-      span_load<VEC>(xc + (size_t)row * a.cols, left, lane, x);
-      span_load<VEC>(yc + (size_t)row * a.cols, left, lane, u);
+      span_store<false>(p + c0, left, lane, v);
     }
-    float2 post = make_float2(0.f, 0.f), pre = make_float2(0.f, 0.f);
-    const uint32_t keep = span_keep<VEC>(a.mask, ps, (unsigned long long)row * per_row + c0 / 8, lane);
-    if (post_on) {
-      post = row_moments<VEC>(u, a.rms, a.eps, a.cols, left, W, w, lane, slots[flip][0], [] { __syncthreads(); });
-      float b[8];
-      if (!kKeep) {
-        fetch(post_gamma, a.post_gamma, 1.f);
-        fetch(post_beta, a.post_beta, 0.f);
-      }
-      post_gamma.get(p);
-      post_beta.get(b);
+  };
+  using RawT = std::conditional_t<VEC, Raw8<T>, Pairs>;
+  using RawF = std::conditional_t<VEC, Raw8<float>, Pairs>;
+  // (an odd last row is worked on twice by a block of two, and written once)
+  long long row[R];
+  size_t base[R];
+  RawT y[R], gate[R];
+  RawF x[R];
+  bool own[R];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = fmaf((u[k] - post.x) * post.y, p[k], b[k]);
+  for (int r = 0; r < R; ++r) {
+    const long long n = (long long)blockIdx.x * R + r;
+    own[r] = n < a.rows;
+    row[r] = own[r] ? n : a.rows - 1;
+    base[r] = (size_t)row[r] * (uint32_t)a.cols;
+    fetch(static_cast<const T*>(a.y) + base[r], y[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) fetch(a.x + base[r], x[r]);
+  if (a.gate_rows) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) fetch(static_cast<const T*>(a.gate) + base[r], gate[r]);
+  }
+  uint4 words[R];
+  const PhiloxState ps = philox_state(a.mask);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t block = VEC ? (uint32_t)c / 8 : (uint32_t)c0 / 8 + lane;
+    words[r] = drop_words(a.mask, ps, (unsigned long long)row[r] * ((uint32_t)(a.cols + 7) / 8) + block);
+    words[r] = span_words<VEC>(a.mask, words[r], lane);
+  }
+  Pairs u[R], p;
+  float2 post[R], pre[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    read(y[r], u[r]);
+    if (left < 256) span_trim<VEC>(left, lane, u[r]);
+    post[r] = pre[r] = make_float2(0.f, 0.f);
+  }
+  auto vector = [&](const void* from) {
+    RawT raw;
+    fetch(static_cast<const T*>(from), raw);
+    read(raw, p);
+  };
+  auto normalise = [&](const float2 (&m)[R], const void* gamma, const void* beta) {
+    vector(gamma);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[r][i] = f2_mul(f2_mul(f2_add(u[r][i], f2_both(-m[r].x)), f2_both(m[r].y)), p[i]);
+    if (beta) {
+      vector(beta);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[r][i] = f2_add(u[r][i], p[i]);
     }
-    if (!kKeep && !a.gate_rows) fetch(gate, a.gate, 1.f);
-    gate.get(p);
+  };
+  if (a.post_gamma) {
+    row_moments<R, W, VEC>(u, a, shape, left, warps, w, lane, slots[0], post);
+    normalise(post, a.post_gamma, a.post_beta);
+  }
+  if (a.mask.rng) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float v = keep >> k & 1u ? u[k] * a.mask.scale : 0.f;
-      x[k] = fmaf(a.residual_scale, x[k], p[k] * v);
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[r][i] = f2_mul(u[r][i], f2_both(a.mask.scale));
+      keep(words[r], ps, u[r]);
     }
-    span_store<VEC>(a.x_out + base, left, lane, x);
-    if (pre_on) {
-      float b[8];
+  }
+  if (a.gate) {
+    if (!a.gate_rows) vector(a.gate);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = span_col<VEC>(lane, k) < left ? x[k] : 0.f;
-      pre = row_moments<VEC>(x, a.rms, a.eps, a.cols, left, W, w, lane, slots[flip][1], [] { __syncthreads(); });
-      if (!kKeep) {
-        fetch(pre_gamma, a.pre_gamma, 1.f);
-        fetch(pre_beta, a.pre_beta, 0.f);
-      }
-      pre_gamma.get(p);
-      pre_beta.get(b);
+    for (int r = 0; r < R; ++r) {
+      if (a.gate_rows) read(gate[r], p);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = fmaf((x[k] - pre.x) * pre.y, p[k], b[k]);
-      span_store<VEC>(static_cast<T*>(a.h) + base, left, lane, x);
+      for (int i = 0; i < 4; ++i) u[r][i] = f2_mul(u[r][i], p[i]);
     }
-    if (a.stats && threadIdx.x == 0)
-      reinterpret_cast<float4*>(a.stats)[row] = make_float4(post.x, post.y, pre.x, pre.y);
-    flip ^= 1;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    read(x[r], p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[r][i] = f2_fma(f2_both(a.residual_scale), p[i], u[r][i]);
+  }
+  // (x_out may be x: a lane writes only places that it alone reads, and has read, a last row's twice)
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (own[r]) store(a.x_out + base[r], u[r]);
+  if (a.pre_gamma) {
+    if (left < 256) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) span_trim<VEC>(left, lane, u[r]);
+    }
+    row_moments<R, W, VEC>(u, a, shape, left, warps, w, lane, slots[1], pre);
+    normalise(pre, a.pre_gamma, a.pre_beta);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (own[r]) store(static_cast<T*>(a.h) + base[r], u[r]);
+  }
+  if (a.stats && threadIdx.x == 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (own[r]) reinterpret_cast<float4*>(a.stats)[row[r]] = make_float4(post[r].x, post[r].y, pre[r].x, pre[r].y);
   }
 }
 
@@ -196,147 +273,377 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
 }
 
 constexpr int kSums = 4;         // column sums: d_h xh, d_h, P, Q
-constexpr int kBwdWarps = 20;    // warps of a block
+#ifndef KBWDWARPS
+#define KBWDWARPS 16
+#endif
+constexpr int kBwdWarps = KBWDWARPS;    // warps of a block
 
-// A block of `groups` groups of W warps, a row per group and step; a lane owns 8 G columns of every row
-// that its group takes, so the column sums stay with it (G = 1: in registers, else in shared memory) and
-// leave once per block, into partial[block][kSums][cols].
-template <typename T, bool VEC, int G, int STAGES>
-__global__ void __launch_bounds__(G == 1 ? 32 * kBwdWarps : 512, 1)
+#ifndef KSTAGES
+#define KSTAGES 3
+#endif
+constexpr int kStages = KSTAGES;
+constexpr int kMaxGroups = 15;  // named barriers
+
+// Rows on 16 bytes, cols % 8 == 0 and <= 4096.  A block of `groups` groups of W = ceil(cols / 256) warps stays on
+// its SM and takes a row per group and step; a lane owns eight columns of every row that its group takes, so
+// the four column sums stay in its registers and leave once per block, into partial[block][kSums][cols].  The
+// rows to come arrive by bulk copies, kStages of them per group, which leaves the threads and the L1 out of
+// it; gamma_pre and gate gamma_post stand in shared memory as float32.
+template <typename T>
+__global__ void __launch_bounds__(32 * kBwdWarps, 1)
     block_norm_bwd_kernel(const BlockNormArgs a, int W, int groups, float* __restrict__ partial) {
-  extern __shared__ __align__(16) uint8_t smem[];  // the stages of copies ahead; [kSums][cols] sums
+  extern __shared__ __align__(16) uint8_t smem[];  // vectors, then the rows on their way; at the end the sums
   __shared__ float red[2][kBwdWarps][8];           // the two latest rows' sums of every warp
+  __shared__ uint64_t full[kMaxGroups * kStages];
+  __shared__ PhiloxKeys keys;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / W, w = warp - group * W;
+  const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr, partly = a.cols - w * 256 < 256;
+  const int c = w * 256 + 8 * lane;  // the lane's first column
+  const bool active = c < a.cols;
+  const long long first = (long long)blockIdx.x * groups + group, step = (long long)gridDim.x * groups;
+  const PhiloxState ps = philox_state(a.mask);
+  philox_keys(ps, &keys);
+  // a stage: rows of d_x_out, x_out (float32), y, d_h and the gate (T)
+  const uint32_t f_bytes = (uint32_t)a.cols * 4, t_bytes = (uint32_t)a.cols * sizeof(T);
+  const uint32_t stage_bytes = 2 * f_bytes + (a.gate_rows ? 3 : 2) * t_bytes;
+  uint8_t* ring = smem + 2048 * W + group * kStages * stage_bytes;
+  uint64_t* bars = full + group * kStages;
+  if (threadIdx.x < groups * kStages) mbar_init(full + threadIdx.x, 1);
+  fence_barrier_init();
+  auto arrive = [&](long long row, int stage) {  // (one thread of the group)
+    if (row >= a.rows) return;
+    const size_t at = (size_t)row * a.cols;
+    uint8_t* to = ring + stage * stage_bytes;
+    mbar_arrive_expect_tx(bars + stage, (a.d_x_out ? f_bytes : 0) + t_bytes + (pre ? f_bytes + t_bytes : 0) +
+                                            (a.gate_rows ? t_bytes : 0));
+    if (a.d_x_out) bulk_load(to, a.d_x_out + at, f_bytes, bars + stage);
+    if (pre) bulk_load(to + f_bytes, a.x_out + at, f_bytes, bars + stage);
+    to += 2 * f_bytes;
+    bulk_load(to, static_cast<const T*>(a.y) + at, t_bytes, bars + stage);
+    if (pre) bulk_load(to + t_bytes, static_cast<const T*>(a.d_h) + at, t_bytes, bars + stage);
+    if (a.gate_rows) bulk_load(to + 2 * t_bytes, static_cast<const T*>(a.gate) + at, t_bytes, bars + stage);
+  };
+  __syncthreads();
+  if (w == 0 && lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) arrive(first + i * step, i);
+  }
+  float* vf = reinterpret_cast<float*>(smem);
+  for (int i = threadIdx.x; i < 256 * W; i += blockDim.x) {
+    const int at = ((i >> 8) * 2 + (i >> 2 & 1)) * 128 + (i >> 3 & 31) * 4 + (i & 3);
+    auto value = [&](const void* p, float without) { return p ? ld1(static_cast<const T*>(p) + i) : without; };
+    vf[at] = i < a.cols ? value(a.pre_gamma, 0.f) : 0.f;
+    vf[256 * W + at] = i < a.cols ? value(a.gate_rows ? nullptr : a.gate, 1.f) * value(a.post_gamma, 1.f) : 0.f;
+  }
+  const ulonglong2* vectors = reinterpret_cast<const ulonglong2*>(smem) + w * 64 + lane;
+  auto vector = [&](int v, Pairs& out) {
+    const ulonglong2 lo = vectors[v * 64 * W], hi = vectors[v * 64 * W + 32];
+    out[0] = lo.x; out[1] = lo.y; out[2] = hi.x; out[3] = hi.y;
+  };
+  auto statistics = [&](long long row) {
+    return (pre || post) && row < a.rows ? __ldg(reinterpret_cast<const float4*>(a.stats) + row)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  Pairs acc[kSums];
+#pragma unroll
+  for (int i = 0; i < kSums; ++i) fill(acc[i], 0.f);
+  float4 next = statistics(first);
+  const float inv_n = 1.f / (float)a.cols;
+  const uint32_t per_row = (uint32_t)a.cols / 8;
+  unsigned long long block = (unsigned long long)first * per_row + (uint32_t)c / 8;
+  size_t at = (size_t)first * a.cols + c;
+  bool alive = true;
+  int flip = 0, stage = 0;
+  uint32_t parity = 0;
+  __syncthreads();
+  for (long long row = first; row < a.rows; row += step) {
+    const float4 st = next;
+    next = statistics(row + step);
+    if (alive && !mbar_wait_warp(bars + stage, parity)) {
+      alive = false;  // (the copy never came: nothing of this call is right, and nothing more is waited for)
+      latch_error(a.err, ERRBIT_TIMEOUT);
+    }
+    const uint8_t* from = ring + stage * stage_bytes;
+    auto row_f = [&](int i, Pairs& v) { ld8(reinterpret_cast<const float*>(from + i * f_bytes) + c, v); };
+    auto row_t = [&](int i, Pairs& v) { ld8(reinterpret_cast<const T*>(from + 2 * f_bytes + i * t_bytes) + c, v); };
+    Pairs xh, e, yh, kf, p;
+    float s[8];
+    // 0 or the dropout's scale, per element
+    fill(kf, a.mask.scale);
+    if (a.mask.rng) keep(drop_words(a.mask, ps, &keys, block), ps, kf);
+    if (a.d_x_out) row_f(0, e);
+    else fill(e, 0.f);
+    row_t(0, yh);
+    if (partly && !active) {
+      fill(e, 0.f);
+      fill(yh, 0.f);
+      fill(kf, 0.f);
+    }
+    uint64_t s2[8] = {};
+    if (pre) {
+      Pairs dh;
+      row_f(1, xh);
+      row_t(1, dh);
+      if (partly && !active) {
+        fill(xh, st.z);
+        fill(dh, 0.f);
+      }
+      vector(0, p);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        xh[k] = f2_mul(f2_add(xh[k], f2_both(-st.z)), f2_both(st.w));
+        acc[0][k] = f2_fma(dh[k], xh[k], acc[0][k]);
+        acc[1][k] = f2_add(dh[k], acc[1][k]);
+        const uint64_t gg = f2_mul(dh[k], p[k]);
+        s2[0] = f2_add(s2[0], gg);
+        s2[1] = f2_fma(gg, xh[k], s2[1]);
+        e[k] = f2_fma(f2_both(st.w), gg, e[k]);
+      }
+    } else {
+      fill(xh, 0.f);
+    }
+    if (post) {
+      Pairs cg;
+      vector(1, cg);
+      if (a.gate_rows) {
+        row_t(2, p);
+        if (partly && !active) fill(p, 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cg[k] = f2_mul(cg[k], p[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t ck = f2_mul(cg[k], kf[k]);
+        yh[k] = f2_mul(f2_add(yh[k], f2_both(-st.x)), f2_both(st.y));
+        const uint64_t ce = f2_mul(ck, e[k]), cyh = f2_mul(ck, yh[k]);
+        s2[2] = f2_add(s2[2], ce);
+        s2[3] = f2_add(s2[3], ck);
+        s2[4] = f2_fma(ck, xh[k], s2[4]);
+        s2[5] = f2_fma(ce, yh[k], s2[5]);
+        s2[6] = f2_add(s2[6], cyh);
+        s2[7] = f2_fma(cyh, xh[k], s2[7]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = f2_sum(s2[i]);
+    float total = warp_sum8(s, lane);
+    if (W > 1) {
+      if (lane % 4 == 0) red[flip][warp][lane / 4] = total;
+      named_bar_sync(1 + group, 32 * W);
+      total = 0.f;
+      for (int i = lane & 3; i < W; i += 4) total += red[flip][group * W + i][lane / 4];
+      total += __shfl_xor_sync(0xffffffffu, total, 2);
+      total += __shfl_xor_sync(0xffffffffu, total, 1);
+      flip ^= 1;
+    } else {
+      __syncwarp();
+    }
+    // the whole group is done with the row before: its stage takes the row after those on their way
+    if (w == 0 && lane == 0 && row != first) arrive(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = __shfl_sync(0xffffffffu, total, 4 * i);
+    const float A = a.rms ? 0.f : st.w * s[0] * inv_n, B = st.w * s[1] * inv_n;
+    const float m0 = a.rms ? 0.f : (s[2] - A * s[3] - B * s[4]) * inv_n, m1 = (s[5] - A * s[6] - B * s[7]) * inv_n;
+    Pairs q, out;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      e[k] = f2_fma(f2_both(-B), xh[k], f2_add(e[k], f2_both(-A)));  // now G
+      out[k] = f2_mul(f2_both(a.residual_scale), e[k]);
+      q[k] = f2_mul(e[k], kf[k]);
+    }
+    if (active) st8(a.dx + at, out);
+    vector(1, p);
+    if (!post) {
+      // (y as it came: a dropped one adds nothing, whatever it holds)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        yh[k] = f2_pack(f2_lo(kf[k]) != 0.f ? f2_lo(yh[k]) : 0.f, f2_hi(kf[k]) != 0.f ? f2_hi(yh[k]) : 0.f);
+    }
+    if (a.gate_rows) {
+      Pairs n, gate, beta;
+      row_t(2, gate);
+      if (partly && !active) fill(gate, 0.f);
+      fill(beta, 0.f);
+      if (a.post_beta && active) ld8(static_cast<const T*>(a.post_beta) + c, beta);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        n[k] = f2_mul(q[k], f2_fma(yh[k], p[k], beta[k]));
+        q[k] = f2_mul(q[k], gate[k]);
+      }
+      if (a.d_gate && active) st8(static_cast<T*>(a.d_gate) + at, n);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      acc[2][k] = f2_fma(q[k], yh[k], acc[2][k]);
+      acc[3][k] = f2_add(q[k], acc[3][k]);
+      out[k] = f2_mul(p[k], q[k]);
+      if (post) out[k] = f2_mul(f2_both(st.y), f2_fma(f2_both(-m1), yh[k], f2_add(out[k], f2_both(-m0))));
+    }
+    if (active) st8(static_cast<T*>(a.dy) + at, out);
+    at += step * a.cols;
+    block += step * per_row;
+    if (++stage == kStages) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+  // the rows' place is taken by the sums, which the groups add in order
+  __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
+  for (int turn = 0; turn < groups; ++turn) {
+    if (turn == group && active) {
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) {
+        float* to = sums + (size_t)i * a.cols + c;
+        Pairs v;
+        if (turn) {
+          ld8(to, v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = f2_add(v[k], acc[i][k]);
+          st8(to, v);
+        } else {
+          st8(to, acc[i]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < kSums * a.cols; i += blockDim.x)
+    partial[(size_t)blockIdx.x * kSums * a.cols + i] = sums[i];
+}
+
+// Any alignment, and rows of up to 8192 columns: the same sums, rows read where they are used and parameters
+// from the L1; a lane owns 8 G columns, G = 2 with its column sums in shared memory.
+template <typename T, bool VEC, int G>
+__global__ void __launch_bounds__(512, 1)
+    block_norm_bwd_any_kernel(const BlockNormArgs a, int W, int groups, float* __restrict__ partial) {
+  extern __shared__ float sums[];          // [kSums][cols]
+  __shared__ float red[2][kBwdWarps][8];  // the two latest rows' sums of every warp
+  __shared__ PhiloxKeys keys;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = warp / W, w = warp - group * W;
   const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr;
   const long long first = (long long)blockIdx.x * groups + group, step = (long long)gridDim.x * groups;
-  // chunks of a stage: d_x_out, y, x_out, d_h, the gate's row
-  constexpr int cy = 2, cx = cy + kChunks<T>, ch = cx + 2, cg = ch + kChunks<T>;
-  const size_t stage_bytes = (size_t)(cg + (a.gate_rows ? kChunks<T> : 0)) * blockDim.x * 16;
-  auto copy_ahead = [&](long long row, int stage) {
-    if (row < a.rows) {
-      uint8_t* at = smem + stage * stage_bytes;
-      const size_t base = (size_t)row * a.cols + w * 256;
-      const int left = a.cols - w * 256;
-      if (a.d_x_out) stage_copy(at, 0, a.d_x_out + base, left, lane);
-      stage_copy(at, cy, static_cast<const T*>(a.y) + base, left, lane);
-      if (pre) {
-        stage_copy(at, cx, static_cast<const float*>(a.x_out) + base, left, lane);
-        stage_copy(at, ch, static_cast<const T*>(a.d_h) + base, left, lane);
-      }
-      if (a.gate_rows) stage_copy(at, cg, static_cast<const T*>(a.gate) + base, left, lane);
-    }
-    cp_async_commit();
-  };
-  if constexpr (STAGES > 0) {
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) copy_ahead(first + i * step, i);
-  }
   const PhiloxState ps = philox_state(a.mask);
-  const float inv_n = 1.f / (float)a.cols;
-  const int per_row = (a.cols + 7) / 8;
-  float acc[G == 1 ? kSums : 1][8];
-  if constexpr (G == 1) {
+  philox_keys(ps, &keys);
+  const int own_left = a.cols - w * 256;
+  auto load = [&](const void* p, size_t at, int left, Pairs& out) { span_load<VEC>(static_cast<const T*>(p) + at, left, lane, out); };
+  Pairs acc[G == 1 ? kSums : 1];
 #pragma unroll
-    for (int i = 0; i < kSums; ++i)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
-  } else {
+  for (int i = 0; i < (G == 1 ? kSums : 1); ++i) fill(acc[i], 0.f);
+  if constexpr (G > 1) {
     for (int i = threadIdx.x; i < kSums * a.cols; i += blockDim.x) sums[i] = 0.f;
-    __syncthreads();
   }
-  int flip = 0, stage = 0;
+  __syncthreads();
+  const float inv_n = 1.f / (float)a.cols;
+  const uint32_t per_row = (uint32_t)(a.cols + 7) / 8;
+  const uint64_t scale = f2_both(a.mask.scale), alpha = f2_both(a.residual_scale);
+  int flip = 0;
+  auto statistics = [&](long long row) {
+    return (pre || post) && row < a.rows ? __ldg(reinterpret_cast<const float4*>(a.stats) + row)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  float4 next = statistics(first);
   for (long long row = first; row < a.rows; row += step) {
-    const float4 st = pre || post ? __ldg(reinterpret_cast<const float4*>(a.stats) + row) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float my = st.x, ry = st.y, mx = st.z, rx = st.w;
-    const uint8_t* at = smem + stage * stage_bytes;
-    if constexpr (STAGES > 0) {
-      copy_ahead(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
-      cp_async_wait<STAGES - 1>();
-      stage = stage == STAGES - 1 ? 0 : stage + 1;
-    }
-    float xh[G][8], e[G][8], yh[G][8], c[G][8];
-    uint32_t keep[G];
-    float s[8] = {};
-    auto add = [&](int g, int i, int k, float v) {
+    const float4 st = next;
+    next = statistics(row + step);
+    const uint64_t minus_x = f2_both(-st.z), rx = f2_both(st.w), minus_y = f2_both(-st.x), ry = f2_both(st.y);
+    Pairs xh[G], e[G], yh[G];
+    uint4 words[G];
+    uint64_t s2[8] = {};
+    auto add = [&](int g, int i, const Pairs& v) {  // (products are added as they are made)
       if constexpr (G == 1) {
-        acc[i][k] += v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k] = f2_add(acc[i][k], v[k]);
       } else {
-        const int col = (g * W + w) * 256 + span_col<VEC>(lane, k);
-        if (col < a.cols) sums[(size_t)i * a.cols + col] += v;
+        const int c0 = (g * W + w) * 256;
+        float* to = sums + (size_t)i * a.cols + c0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int p = span_col<VEC>(lane, 2 * k), q = span_col<VEC>(lane, 2 * k + 1);
+          if (c0 + p < a.cols) to[p] += f2_lo(v[k]);
+          if (c0 + q < a.cols) to[q] += f2_hi(v[k]);
+        }
       }
+    };
+    auto add_product = [&](int g, int i, const Pairs& v, const Pairs& by) {
+      if constexpr (G == 1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k] = f2_fma(v[k], by[k], acc[i][k]);
+      } else {
+        Pairs p;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = f2_mul(v[k], by[k]);
+        add(g, i, p);
+      }
+    };
+    // c before the mask (made again after the exchange: registers are short)
+    auto factors = [&](int g, size_t base, Pairs& c) {
+      Pairs p;
+      const int c0 = (g * W + w) * 256, left = a.cols - c0;
+      load(a.post_gamma, c0, left, c);
+      if (a.gate) {
+        load(a.gate, a.gate_rows ? base : c0, left, p);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = f2_mul(c[k], p[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[k] = f2_mul(c[k], scale);
     };
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int c0 = (g * W + w) * 256, left = a.cols - c0;
       const size_t base = (size_t)row * a.cols + c0;
-      float dh[8], p[8];
-      if constexpr (STAGES > 0) {
-        stage_read<float>(at, 0, e[g]);
-        stage_read<T>(at, cy, yh[g]);
-        stage_read<float>(at, cx, xh[g]);
-        stage_read<T>(at, ch, dh);
-      } else {
-        if (a.d_x_out) span_load<VEC>(a.d_x_out + base, left, lane, e[g]);
-        span_load<VEC>(static_cast<const T*>(a.y) + base, left, lane, yh[g]);
-        if (pre) {
-          span_load<VEC>(static_cast<const float*>(a.x_out) + base, left, lane, xh[g]);
-          span_load<VEC>(static_cast<const T*>(a.d_h) + base, left, lane, dh);
-        }
-      }
-      if (!a.d_x_out) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) e[g][k] = 0.f;
-      }
-      keep[g] = span_keep<VEC>(a.mask, ps, (unsigned long long)row * per_row + c0 / 8, lane);
+      Pairs dh, p;
+      fill(e[g], 0.f);
+      if (a.d_x_out) span_load<VEC>(a.d_x_out + base, left, lane, e[g]);
+      load(a.y, base, left, yh[g]);
       if (pre) {
-        Span8<T, VEC> gamma;
-        gamma.load(static_cast<const T*>(a.pre_gamma) + c0, left, lane);
-        gamma.get(p);
+        span_load<VEC>(static_cast<const float*>(a.x_out) + base, left, lane, xh[g]);
+        load(a.d_h, base, left, dh);
+      }
+      words[g] = span_words<VEC>(
+          a.mask, drop_words(a.mask, ps, &keys, (unsigned long long)row * per_row + c0 / 8 + lane), lane);
+      if (pre) {
+        load(a.pre_gamma, c0, left, p);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          xh[g][k] = span_col<VEC>(lane, k) < left ? (xh[g][k] - mx) * rx : 0.f;
-          const float gg = dh[k] * p[k];
-          add(g, 0, k, dh[k] * xh[g][k]);
-          add(g, 1, k, dh[k]);
-          s[0] += gg;
-          s[1] = fmaf(gg, xh[g][k], s[1]);
-          e[g][k] = fmaf(rx, gg, e[g][k]);
+        for (int k = 0; k < 4; ++k) xh[g][k] = f2_mul(f2_add(xh[g][k], minus_x), rx);
+        span_trim<VEC>(left, lane, xh[g]);
+        add_product(g, 0, dh, xh[g]);
+        add(g, 1, dh);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t gg = f2_mul(dh[k], p[k]);
+          s2[0] = f2_add(s2[0], gg);
+          s2[1] = f2_fma(gg, xh[g][k], s2[1]);
+          e[g][k] = f2_fma(rx, gg, e[g][k]);
         }
       } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) xh[g][k] = 0.f;
+        fill(xh[g], 0.f);
       }
       if (post) {
-        Span8<T, VEC> gamma;
-        gamma.load(static_cast<const T*>(a.post_gamma) + c0, left, lane);
-        gamma.get(c[g]);
-        if (a.gate) {
-          if (STAGES > 0 && a.gate_rows) {
-            stage_read<T>(at, cg, p);
-          } else {
-            gamma.load(static_cast<const T*>(a.gate) + (a.gate_rows ? base : c0), left, lane);
-            gamma.get(p);
-          }
+        Pairs c;
+        factors(g, base, c);
+        keep(words[g], ps, c);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) c[g][k] *= p[k];
-        }
+        for (int k = 0; k < 4; ++k) yh[g][k] = f2_mul(f2_add(yh[g][k], minus_y), ry);
+        span_trim<VEC>(left, lane, yh[g]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          yh[g][k] = span_col<VEC>(lane, k) < left ? (yh[g][k] - my) * ry : 0.f;
-          c[g][k] = keep[g] >> k & 1u ? c[g][k] * a.mask.scale : 0.f;
-          const float ce = c[g][k] * e[g][k], cyh = c[g][k] * yh[g][k];
-          s[2] += ce;
-          s[3] += c[g][k];
-          s[4] = fmaf(c[g][k], xh[g][k], s[4]);
-          s[5] = fmaf(ce, yh[g][k], s[5]);
-          s[6] += cyh;
-          s[7] = fmaf(cyh, xh[g][k], s[7]);
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t ce = f2_mul(c[k], e[g][k]), cyh = f2_mul(c[k], yh[g][k]);
+          s2[2] = f2_add(s2[2], ce);
+          s2[3] = f2_add(s2[3], c[k]);
+          s2[4] = f2_fma(c[k], xh[g][k], s2[4]);
+          s2[5] = f2_fma(ce, yh[g][k], s2[5]);
+          s2[6] = f2_add(s2[6], cyh);
+          s2[7] = f2_fma(cyh, xh[g][k], s2[7]);
         }
       }
     }
+    float s[8];
     if (pre || post) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = f2_sum(s2[i]);
       float total = warp_sum8(s, lane);
       if (W > 1) {
         if (lane % 4 == 0) red[flip][warp][lane / 4] = total;
@@ -350,76 +657,72 @@ __global__ void __launch_bounds__(G == 1 ? 32 * kBwdWarps : 512, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = __shfl_sync(0xffffffffu, total, 4 * i);
     }
-    const float A = pre && !a.rms ? rx * s[0] * inv_n : 0.f, B = pre ? rx * s[1] * inv_n : 0.f;
-    const float m0 = a.rms ? 0.f : (s[2] - A * s[3] - B * s[4]) * inv_n, m1 = (s[5] - A * s[6] - B * s[7]) * inv_n;
+    const float A = pre && !a.rms ? st.w * s[0] * inv_n : 0.f, B = pre ? st.w * s[1] * inv_n : 0.f;
+    const float m0 = post && !a.rms ? (s[2] - A * s[3] - B * s[4]) * inv_n : 0.f;
+    const float m1 = post ? (s[5] - A * s[6] - B * s[7]) * inv_n : 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int c0 = (g * W + w) * 256, left = a.cols - c0;
       const size_t base = (size_t)row * a.cols + c0;
-      float out[8];
+      Pairs out, q;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        e[g][k] = fmaf(-B, xh[g][k], e[g][k] - A);  // now G
-        out[k] = a.residual_scale * e[g][k];
+      for (int k = 0; k < 4; ++k) {
+        e[g][k] = f2_fma(f2_both(-B), xh[g][k], f2_add(e[g][k], f2_both(-A)));  // now G
+        out[k] = f2_mul(alpha, e[g][k]);
+        q[k] = f2_mul(scale, e[g][k]);
       }
       span_store<VEC>(a.dx + base, left, lane, out);
+      keep(words[g], ps, q);
       if (a.gate_rows) {
-        float gate[8], n[8];
-        if constexpr (STAGES > 0) stage_read<T>(at, cg, gate);
-        else span_load<VEC>(static_cast<const T*>(a.gate) + base, left, lane, gate);
+        Pairs gate, n;
+        load(a.gate, base, left, gate);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) n[k] = yh[g][k];
+        for (int k = 0; k < 4; ++k) n[k] = yh[g][k];
         if (post) {
-          float p[8];
-          Span8<T, VEC> v;
-          v.load(static_cast<const T*>(a.post_gamma) + c0, left, lane);
-          v.get(p);
+          Pairs p, b;
+          load(a.post_gamma, c0, left, p);
+          fill(b, 0.f);
+          if (a.post_beta) load(a.post_beta, c0, left, b);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) n[k] *= p[k];
-          if (a.post_beta) {
-            v.load(static_cast<const T*>(a.post_beta) + c0, left, lane);
-            v.get(p);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) n[k] += p[k];
-          }
+          for (int k = 0; k < 4; ++k) n[k] = f2_fma(n[k], p[k], b[k]);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const bool kept = keep[g] >> k & 1u;
-          const float q = kept ? e[g][k] * a.mask.scale : 0.f;
-          n[k] = kept ? q * n[k] : 0.f;
-          out[k] = q * gate[k];
+        for (int k = 0; k < 4; ++k) {
+          n[k] = f2_mul(n[k], q[k]);
+          q[k] = f2_mul(q[k], gate[k]);
         }
+        keep(words[g], ps, n);
         if (a.d_gate) span_store<VEC>(static_cast<T*>(a.d_gate) + base, left, lane, n);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) out[k] = keep[g] >> k & 1u ? e[g][k] * a.mask.scale : 0.f;
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      if (!post) {
         // (a dropped value adds nothing, whatever y holds there)
-        add(g, 2, k, keep[g] >> k & 1u ? out[k] * yh[g][k] : 0.f);
-        add(g, 3, k, out[k]);
+        keep(words[g], ps, yh[g]);
       }
+      add_product(g, 2, q, yh[g]);
+      add(g, 3, q);
       if (post) {
+        Pairs c;
+        factors(g, base, c);
+        keep(words[g], ps, c);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) out[k] = ry * (fmaf(c[g][k], e[g][k], -m0) - yh[g][k] * m1);
-      } else if (a.gate && !a.gate_rows) {
-        float p[8];
-        Span8<T, VEC> v;
-        v.load(static_cast<const T*>(a.gate) + c0, left, lane);
-        v.get(p);
+        for (int k = 0; k < 4; ++k)
+          out[k] = f2_mul(ry, f2_fma(f2_both(-m1), yh[g][k], f2_fma(c[k], e[g][k], f2_both(-m0))));
+      } else {
+        if (a.gate && !a.gate_rows) {
+          load(a.gate, c0, left, out);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) out[k] *= p[k];
+          for (int k = 0; k < 4; ++k) out[k] = f2_mul(out[k], q[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) out[k] = q[k];
+        }
       }
       span_store<VEC>(static_cast<T*>(a.dy) + base, left, lane, out);
     }
   }
   if constexpr (G == 1) {
-    // the stages' place is taken by the sums, which the groups add in order
-    if constexpr (STAGES > 0) cp_async_wait<0>();
-    __syncthreads();
-    const int c0 = w * 256, left = a.cols - c0;
+    // the groups add their sums in order
+    const int c0 = w * 256;
     for (int turn = 0; turn < groups; ++turn) {
       if (turn == group) {
 #pragma unroll
@@ -427,9 +730,10 @@ __global__ void __launch_bounds__(G == 1 ? 32 * kBwdWarps : 512, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int col = span_col<VEC>(lane, k);
-            if (col < left) {
+            if (col < own_left) {
+              const float v = k & 1 ? f2_hi(acc[i][k / 2]) : f2_lo(acc[i][k / 2]);
               float* to = sums + (size_t)i * a.cols + c0 + col;
-              *to = turn ? *to + acc[i][k] : acc[i][k];
+              *to = turn ? *to + v : v;
             }
           }
       }
@@ -492,59 +796,83 @@ BwdShape bwd_shape(int rows, int cols, int num_sms) {
   const int spans = (cols + 255) / 256;
   s.G = spans > 16 ? 2 : 1;
   s.W = (spans + s.G - 1) / s.G;
-  s.groups = s.G == 2 ? 1 : std::min(15, kBwdWarps / s.W);
+  s.groups = s.G == 2 ? 1 : std::min(kMaxGroups, kBwdWarps / s.W);
   s.blocks = std::max(1, std::min(num_sms, (rows + s.groups - 1) / s.groups));
   return s;
 }
 
-constexpr size_t kSmemMax = 227 * 1024 - 2048;  // (the rest: static shared memory)
+constexpr size_t kSmemMax = 227 * 1024 - 4096;  // (the rest: static shared memory)
 
-template <typename T, bool VEC, int G, int STAGES>
-cudaError_t launch_bwd_as(const BlockNormArgs& a, const BwdShape& s, size_t stage, float* partial, cudaStream_t st) {
-  const size_t smem = std::max(sizeof(float) * kSums * a.cols, stage * STAGES);
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(block_norm_bwd_kernel<T, VEC, G, STAGES>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  block_norm_bwd_kernel<T, VEC, G, STAGES><<<s.blocks, 32 * s.W * s.groups, smem, st>>>(a, s.W, s.groups, partial);
+// Lets a kernel have `smem` bytes of dynamic shared memory.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel k, size_t smem) {
+  return smem <= 40 * 1024 ? cudaSuccess : cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+template <typename T, bool VEC, int G>
+cudaError_t launch_bwd_any(const BlockNormArgs& a, const BwdShape& s, float* partial, cudaStream_t st) {
+  const size_t smem = sizeof(float) * kSums * a.cols;
+  const cudaError_t e = allow_smem(block_norm_bwd_any_kernel<T, VEC, G>, smem);
+  if (e != cudaSuccess) return e;
+  block_norm_bwd_any_kernel<T, VEC, G><<<s.blocks, 32 * s.W * s.groups, smem, st>>>(a, s.W, s.groups, partial);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num_sms, cudaStream_t st) {
-  const BwdShape s = bwd_shape(a.rows, a.cols, num_sms);
-  const size_t stage = (size_t)(4 + (a.gate_rows ? 3 : 2) * kChunks<T>) * 16 * 32 * s.W * s.groups;
+  BwdShape s = bwd_shape(a.rows, a.cols, num_sms);
+  const size_t row = (size_t)a.cols * (8 + (a.gate_rows ? 3 : 2) * sizeof(T)) * kStages;
+  const size_t fits = (kSmemMax - 2048 * s.W - 1024) / row;  // groups whose rows fit shared memory
   cudaError_t e;
-  if (s.G == 2) e = vec ? launch_bwd_as<T, true, 2, 0>(a, s, 0, partial, st) : launch_bwd_as<T, false, 2, 0>(a, s, 0, partial, st);
-  else if (!vec) e = launch_bwd_as<T, false, 1, 0>(a, s, 0, partial, st);
-  else if (3 * stage <= kSmemMax) e = launch_bwd_as<T, true, 1, 3>(a, s, stage, partial, st);
-  else e = launch_bwd_as<T, true, 1, 2>(a, s, stage, partial, st);
+  if (s.G == 2) {
+    e = vec ? launch_bwd_any<T, true, 2>(a, s, partial, st) : launch_bwd_any<T, false, 2>(a, s, partial, st);
+  } else if (!vec || a.cols % 8 || fits == 0) {
+    s.groups = std::min(s.groups, 16 / s.W);
+    e = vec ? launch_bwd_any<T, true, 1>(a, s, partial, st) : launch_bwd_any<T, false, 1>(a, s, partial, st);
+  } else {
+    s.groups = (int)std::min((size_t)s.groups, fits);
+    // (1 KB more: lanes past a row's end read on behind it)
+    const size_t smem = std::max(sizeof(float) * kSums * a.cols, 2048 * s.W + row * s.groups + 1024);
+    e = allow_smem(block_norm_bwd_kernel<T>, smem);
+    if (e != cudaSuccess) return e;
+    block_norm_bwd_kernel<T><<<s.blocks, 32 * s.W * s.groups, smem, st>>>(a, s.W, s.groups, partial);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   block_norm_sums_kernel<T><<<dim3((a.cols + 31) / 32, 2), 512, 0, st>>>(a, partial, s.blocks);
   return cudaGetLastError();
 }
 
-template <typename T, bool VEC, int MAXT>
-cudaError_t launch_fwd_as(const BlockNormArgs& a, int num_sms, cudaStream_t st) {
-  const int threads = (a.cols + 255) / 256 * 32;
-  const size_t smem = VEC ? (size_t)kFwdStages<MAXT> * (2 + kChunks<T>) * threads * 16 : 0;
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(block_norm_kernel<T, VEC, MAXT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  // as many blocks as the SMs hold at once (64 registers per thread)
-  const int per_sm = std::max(1, (int)std::min({(size_t)32, (size_t)1024 / threads, kSmemMax / (smem + 2048)}));
-  const unsigned grid = (unsigned)std::min((long long)a.rows, (long long)num_sms * per_sm);
-  block_norm_kernel<T, VEC, MAXT><<<grid, threads, smem, st>>>(a);
-  return cudaGetLastError();
+template <typename T, int W>
+void launch_fwd_as(const BlockNormArgs& a, const RowShape& s, int warps, int num_sms, cudaStream_t st) {
+  constexpr int R = KFWDROWS;
+  if (a.rows > R * num_sms) block_norm_kernel<T, true, W, R><<<(unsigned)((a.rows + R - 1) / R), 32 * warps, 0, st>>>(a, s);
+  else block_norm_kernel<T, true, W, 1><<<(unsigned)a.rows, 32 * warps, 0, st>>>(a, s);
 }
+
 template <typename T>
 cudaError_t launch_fwd(const BlockNormArgs& a, bool vec, int num_sms, cudaStream_t st) {
-  if (a.cols <= 2048)
-    return vec ? launch_fwd_as<T, true, 256>(a, num_sms, st) : launch_fwd_as<T, false, 256>(a, num_sms, st);
-  return vec ? launch_fwd_as<T, true, 1024>(a, num_sms, st) : launch_fwd_as<T, false, 1024>(a, num_sms, st);
+  const int W = (a.cols + 255) / 256;
+  RowShape s;
+  s.inv_cols = 1.f / (float)a.cols;
+  s.last = (float)(a.cols - 256 * (W - 1));
+  s.inv_last = 1.f / s.last;
+  if (!vec || a.cols % 8) {
+    block_norm_kernel<T, false, 0, 1><<<(unsigned)a.rows, 32 * W, 0, st>>>(a, s);
+    return cudaGetLastError();
+  }
+  switch (W) {
+    case 1: launch_fwd_as<T, 1>(a, s, W, num_sms, st); break;
+    case 2: launch_fwd_as<T, 2>(a, s, W, num_sms, st); break;
+    case 3: launch_fwd_as<T, 3>(a, s, W, num_sms, st); break;
+    case 4: launch_fwd_as<T, 4>(a, s, W, num_sms, st); break;
+    case 5: launch_fwd_as<T, 5>(a, s, W, num_sms, st); break;
+    case 6: launch_fwd_as<T, 6>(a, s, W, num_sms, st); break;
+    case 7: launch_fwd_as<T, 7>(a, s, W, num_sms, st); break;
+    case 8: launch_fwd_as<T, 8>(a, s, W, num_sms, st); break;
+    default: launch_fwd_as<T, 0>(a, s, W, num_sms, st); break;
+  }
+  return cudaGetLastError();
 }
 
 // 16-byte accesses to every row and parameter

@@ -188,6 +188,15 @@ __device__ __forceinline__ void bulk_wait_read() {
 // Wait until all committed bulk groups of this thread have completed.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// Bulk copy of `bytes` contiguous bytes global -> shared (both addresses and the size multiples of 16),
+// completing them on the mbarrier.
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(smem_dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // Per-thread 16-byte asynchronous copy global -> shared through the load/store unit (not
 // the TMA engine); src_bytes 0 writes zeros without reading.  Groups complete in order.
 __device__ __forceinline__ void cp_async_16(void* smem_dst, const void* gsrc, uint32_t src_bytes) {

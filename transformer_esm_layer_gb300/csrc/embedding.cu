@@ -24,60 +24,107 @@ __device__ __forceinline__ float token_scale(const EmbedArgs& a, int t) {
   return a.row_scale ? a.scale * __ldg(a.row_scale + t) : a.scale;
 }
 
-// One warp per 256 columns of a token.
-template <typename TE, typename TO, bool VEC>
-__global__ void __launch_bounds__(256) embed_scaled_kernel(const EmbedArgs a) {
+// Blocks of eight columns in the order of the tokens: a thread takes four of them, 256 apart, and has all its ids
+// and then all its rows on the way before it draws the first bits.  Rows on 16 bytes.
+#ifndef KBLOCKS
+#define KBLOCKS 4
+#endif
+#ifndef KMIN
+#define KMIN 4
+#endif
+constexpr int kBlocks = KBLOCKS;
+
+template <typename TE, typename TO>
+__global__ void __launch_bounds__(256, KMIN) embed_scaled_kernel(const EmbedArgs a, const FastDiv per_row, long long total) {
+  const PhiloxState ps = philox_state(a.mask);
+  const long long first = (long long)blockIdx.x * (256 * kBlocks) + threadIdx.x;
+  int t[kBlocks], col[kBlocks], id[kBlocks];
+  float f[kBlocks];
+#pragma unroll
+  for (int j = 0; j < kBlocks; ++j) {
+    const long long b = first + j * 256;
+    t[j] = total <= INT32_MAX ? (int)div_by((uint32_t)min(b, total), per_row) : (int)(b / per_row.d);
+    col[j] = (int)(b - (long long)t[j] * per_row.d) * 8;
+    id[j] = b < total ? checked_id(a, t[j], col[j] == 0) : -1;
+    f[j] = b < total ? token_scale(a, t[j]) * a.mask.scale : 0.f;
+  }
+  Raw8<TE> x[kBlocks];
+#pragma unroll
+  for (int j = 0; j < kBlocks; ++j)
+    if (id[j] >= 0) x[j].load(static_cast<const TE*>(a.table) + (long long)id[j] * a.cols + col[j], a.cols - col[j]);
+#pragma unroll
+  for (int j = 0; j < kBlocks; ++j) {
+    const uint4 w = drop_words(a.mask, ps, (unsigned long long)(first + j * 256));
+    Pairs v;
+    x[j].get(v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], f2_both(f[j]));
+    if (id[j] < 0) fill(v, 0.f);
+    keep(w, ps, v);
+    if (first + j * 256 < total)
+      span_store<true>(static_cast<TO*>(a.out) + (long long)t[j] * a.out_stride + col[j], a.cols - col[j], 0, v);
+  }
+}
+
+// Rows off 16-byte boundaries: one warp per 256 columns of a token.
+template <typename TE, typename TO>
+__global__ void __launch_bounds__(256) embed_rows_kernel(const EmbedArgs a, const FastDiv spans, long long total) {
   const PhiloxState ps = philox_state(a.mask);
   const int lane = threadIdx.x & 31;
-  const long long spans = (a.cols + 255) / 256, per_row = (a.cols + 7) / 8, total = spans * a.tokens;
-  for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (long long)gridDim.x * 8) {
-    const int t = (int)(i / spans);
-    const long long c0 = (i - t * spans) * 256;
-    const int left = (int)min((long long)256, a.cols - c0);
-    const int id = checked_id(a, t, lane == 0 && c0 == 0);
-    float v[8];
-    if (id >= 0) {
-      span_load<VEC>(static_cast<const TE*>(a.table) + (long long)id * a.cols + c0, left, lane, v);
-      const float f = token_scale(a, t);
-      const uint32_t keep = span_keep<VEC>(a.mask, ps, (unsigned long long)(t * per_row + c0 / 8), lane);
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5), per_row = (a.cols + 7) / 8;
+  if (i >= total) return;
+  const int t = total <= INT32_MAX ? (int)div_by((uint32_t)i, spans) : (int)(i / spans.d);
+  const int c0 = (int)(i - (long long)t * spans.d) * 256, left = a.cols - c0, id = checked_id(a, t, lane == 0 && c0 == 0);
+  Pairs v;
+  fill(v, 0.f);
+  if (id >= 0) {
+    span_load<false>(static_cast<const TE*>(a.table) + (long long)id * a.cols + c0, left, lane, v);
+    const uint4 own = drop_words(a.mask, ps, (unsigned long long)(t * per_row + c0 / 8 + lane));
+    const uint64_t f = f2_both(token_scale(a, t) * a.mask.scale);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = keep >> k & 1u ? v[k] * f * a.mask.scale : 0.f;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = 0.f;
-    }
-    span_store<VEC>(static_cast<TO*>(a.out) + t * a.out_stride + c0, left, lane, v);
+    for (int k = 0; k < 4; ++k) v[k] = f2_mul(v[k], f);
+    keep(span_words<false>(a.mask, own, lane), ps, v);
   }
+  span_store<false>(static_cast<TO*>(a.out) + t * a.out_stride + c0, left, lane, v);
+}
+
+// acc += keep(token t, block of the lane) * f * g
+template <bool VEC>
+__device__ __forceinline__ void add_token(const EmbedArgs& a, const PhiloxState& ps, const PhiloxKeys* keys, int t, int c0,
+                                          int lane, float f, Pairs& g, Pairs& acc) {
+  const unsigned long long b = (unsigned long long)t * ((a.cols + 7) / 8) + c0 / 8 + lane;
+  keep(span_words<VEC>(a.mask, drop_words(a.mask, ps, keys, b), lane), ps, g);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = f2_fma(g[i], f2_both(f), acc[i]);
 }
 
 // One warp per id and 256 columns: it looks through all tokens, 32 at a time.
 template <typename TO, bool VEC>
-__global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedArgs a) {
+__global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedArgs a, const FastDiv spans, long long total) {
+  __shared__ PhiloxKeys keys;
   const PhiloxState ps = philox_state(a.mask);
+  philox_keys(ps, &keys);
+  __syncthreads();
   const int lane = threadIdx.x & 31;
-  const long long spans = (a.cols + 255) / 256, per_row = (a.cols + 7) / 8, total = spans * a.vocab;
-  for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (long long)gridDim.x * 8) {
-    const int v = (int)(i / spans);
-    const long long c0 = (i - v * spans) * 256;
-    const int left = (int)min((long long)256, a.cols - c0);
-    float* dst = a.d_table + (long long)v * a.cols + c0;
-    float acc[8] = {};
-    if (a.accumulate) span_load<VEC>(dst, left, lane, acc);
-    for (int t0 = 0; t0 < a.tokens; t0 += 32) {
-      const int t = t0 + lane;
-      const int id = t < a.tokens ? checked_id(a, t, i == 0) : -1;
-      for (uint32_t hit = __ballot_sync(0xffffffffu, id == v); hit; hit &= hit - 1) {
-        const int m = t0 + __ffs(hit) - 1;
-        float g[8];
-        span_load<VEC>(static_cast<const TO*>(a.out) + m * a.out_stride + c0, left, lane, g);
-        const float f = token_scale(a, m);
-        const uint32_t keep = span_keep<VEC>(a.mask, ps, (unsigned long long)(m * per_row + c0 / 8), lane);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += keep >> k & 1u ? g[k] * f * a.mask.scale : 0.f;
-      }
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= total) return;
+  const int v = total <= INT32_MAX ? (int)div_by((uint32_t)i, spans) : (int)(i / spans.d);
+  const int c0 = (int)(i - (long long)v * spans.d) * 256, left = a.cols - c0;
+  float* dst = a.d_table + (long long)v * a.cols + c0;
+  Pairs acc;
+  fill(acc, 0.f);
+  if (a.accumulate) span_load<VEC>(dst, left, lane, acc);
+  for (int t0 = 0; t0 < a.tokens; t0 += 32) {
+    const int t = t0 + lane;
+    const int id = t < a.tokens ? checked_id(a, t, i == 0) : -1;
+    for (uint32_t hit = __ballot_sync(0xffffffffu, id == v); hit; hit &= hit - 1) {
+      const int m = t0 + __ffs(hit) - 1;
+      Pairs g;
+      span_load<VEC>(static_cast<const TO*>(a.out) + m * a.out_stride + c0, left, lane, g);
+      add_token<VEC>(a, ps, &keys, m, c0, lane, token_scale(a, m) * a.mask.scale, g, acc);
     }
-    span_store<VEC>(dst, left, lane, acc);
   }
+  span_store<VEC>(dst, left, lane, acc);
 }
 
 // ---- the gradient of larger batches: tokens sorted by id, then summed in pieces of 32 ----
@@ -114,11 +161,12 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
     for (size_t i = 4 * n4 + first; i < n; i += step) a.d_table[i] = 0.f;
     return;
   }
-  __shared__ int hist[kSortWarps * kBins];  // counts, then next positions
-  __shared__ int block_count[kBins];
+  constexpr int kRow = kBins + 1;  // (lanes read a column without bank conflicts)
+  __shared__ int hist[kSortWarps * kRow];  // each warp's counts, then the next place of each digit within the block
+  __shared__ int block_count[kBins], start[kBins];
   __shared__ int warp_total[kSortWarps];
   const int rank = (int)cluster_ctarank(), bins = 1 << s.digit_bits;
-  int* mine = hist + warp * kBins;
+  int* mine = hist + warp * kRow;
   int n = a.tokens;
   for (int pass = 0; pass < s.passes; ++pass) {
     const uint2* src = (s.passes - pass) & 1 ? s.other : s.list;
@@ -142,15 +190,17 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
       __syncwarp();
     }
     __syncthreads();
-    // counts of the warps before, and the block's
-    if (tid < bins) {
-      int sum = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int c = hist[w * kBins + tid];
-        hist[w * kBins + tid] = sum;
-        sum += c;
+    // counts of the warps before, and the block's: a warp per digit, a lane per warp's count
+    for (int d = warp; d < bins; d += kSortWarps) {
+      const int own = hist[lane * kRow + d];
+      int incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
       }
-      block_count[tid] = sum;
+      hist[lane * kRow + d] = incl - own;
+      if (lane == 31) block_count[d] = incl;
     }
     __syncwarp();
     cluster_sync();
@@ -178,17 +228,14 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
       if (w < warp) lower += c;
       all += c;
     }
-    if (tid < bins) {
-      const int start = lower + incl - total + before;
-      for (int w = 0; w < kSortWarps; ++w) hist[w * kBins + tid] += start;
-    }
+    if (tid < bins) start[tid] = lower + incl - total + before;
     __syncthreads();
     for (long long i0 = begin; i0 < end; i0 += 32) {
       const uint2 v = item((int)i0 + lane);
       const int d = v.x == 0xffffffffu ? kBins : (int)(v.x >> shift) & (bins - 1);
       const uint32_t peers = __match_any_sync(0xffffffffu, d);
       const int ahead = __popc(peers & ((1u << lane) - 1));
-      if (d < kBins) dst[mine[d] + ahead] = v;
+      if (d < kBins) dst[start[d] + mine[d] + ahead] = v;
       __syncwarp();
       if (d < kBins && ahead == 0) mine[d] += __popc(peers);
       __syncwarp();
@@ -204,64 +251,82 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
 // Sums of 32 consecutive places of the sorted list and 256 columns by one warp.  An id whose tokens all lie
 // within the piece is written at once; of an id that goes on over the piece's border the piece keeps its part:
 // part[piece][0] for one that began before, part[piece][1] for one that begins here and goes on.
-constexpr int kPiece = 32;
+#ifndef KPIECE
+#define KPIECE 32
+#endif
+#ifndef KAHEAD
+#define KAHEAD 4
+#endif
+#ifndef KMINB
+#define KMINB 3
+#endif
+constexpr int kPiece = KPIECE;
 
 template <typename TO, bool VEC>
-__global__ void __launch_bounds__(256) embed_grad_pieces_kernel(const EmbedArgs a, const uint2* __restrict__ list,
-                                                                const int* __restrict__ valid, float* __restrict__ part) {
-  constexpr int kAhead = 4;  // rows in flight
+__global__ void __launch_bounds__(256, KMINB)
+    embed_grad_pieces_kernel(const EmbedArgs a, const uint2* __restrict__ list, const int* __restrict__ valid,
+                             float* __restrict__ part, const FastDiv spans, long long total) {
+  constexpr int kAhead = KAHEAD;  // rows in flight
+  __shared__ PhiloxKeys keys;
   const PhiloxState ps = philox_state(a.mask);
+  philox_keys(ps, &keys);
+  __syncthreads();
   const int lane = threadIdx.x & 31, n = *valid;
-  const int spans = (a.cols + 255) / 256;
-  const long long per_row = (a.cols + 7) / 8, total = (long long)spans * ((n + kPiece - 1) / kPiece);
-  for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (long long)gridDim.x * 8) {
-    const int piece = (int)(i / spans), c0 = (int)(i - (long long)piece * spans) * 256, left = min(256, a.cols - c0);
-    const int p0 = piece * kPiece, count = min(kPiece, n - p0);
-    const uint2 own = lane < count ? list[p0 + lane] : make_uint2(0xffffffffu, 0);
-    const float own_scale = lane < count ? token_scale(a, (int)own.y) * a.mask.scale : 0.f;
-    const int before = p0 > 0 ? (int)list[p0 - 1].x : -1, after = p0 + kPiece < n ? (int)list[p0 + kPiece].x : -1;
-    int id = (int)__shfl_sync(0xffffffffu, own.x, 0);
-    float acc[8] = {};
-    auto leave = [&](bool last) {
-      const bool from_before = id == before, goes_on = last && id == after;
-      if (from_before || goes_on) {
-        span_store<VEC>(part + ((size_t)piece * 2 + (from_before ? 0 : 1)) * a.cols + c0, left, lane, acc);
-        return;
-      }
-      float* dst = a.d_table + (size_t)id * a.cols + c0;
-      if (a.accumulate) {
-        float old[8];
-        span_load<VEC>(dst, left, lane, old);
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= total) return;
+  const int piece = total <= INT32_MAX ? (int)div_by((uint32_t)i, spans) : (int)(i / spans.d);
+  const int c0 = (int)(i - (long long)piece * spans.d) * 256, left = a.cols - c0;
+  const int p0 = piece * kPiece, count = min(kPiece, n - p0);
+  if (count <= 0) return;
+  const uint2 own = lane < count ? list[p0 + lane] : make_uint2(0xffffffffu, 0);
+  const float own_scale = lane < count ? token_scale(a, (int)own.y) * a.mask.scale : 0.f;
+  const int before = p0 > 0 ? (int)list[p0 - 1].x : -1, after = p0 + kPiece < n ? (int)list[p0 + kPiece].x : -1;
+  int id = (int)__shfl_sync(0xffffffffu, own.x, 0);
+  Pairs acc;
+  fill(acc, 0.f);
+  auto leave = [&](bool last) {
+    const bool from_before = id == before, goes_on = last && id == after;
+    if (from_before || goes_on) {
+      span_store<VEC>(part + ((size_t)piece * 2 + (from_before ? 0 : 1)) * a.cols + c0, left, lane, acc);
+      return;
+    }
+    float* dst = a.d_table + (size_t)id * a.cols + c0;
+    if (a.accumulate) {
+      Pairs old;
+      span_load<VEC>(dst, left, lane, old);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += old[k];
-      }
-      span_store<VEC>(dst, left, lane, acc);
-    };
-    for (int j0 = 0; j0 < count; j0 += kAhead) {
-      float g[kAhead][8];
+      for (int k = 0; k < 4; ++k) acc[k] = f2_add(acc[k], old[k]);
+    }
+    span_store<VEC>(dst, left, lane, acc);
+  };
+  for (int j0 = 0; j0 < count; j0 += kAhead) {
+    Raw8<TO> g[kAhead];
+    Pairs scalar[VEC ? 1 : kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int t = (int)__shfl_sync(0xffffffffu, own.y, j0 + j);
-        if (j0 + j < count) span_load<VEC>(static_cast<const TO*>(a.out) + (size_t)t * a.out_stride + c0, left, lane, g[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int t = (int)__shfl_sync(0xffffffffu, own.y, j0 + j), v = (int)__shfl_sync(0xffffffffu, own.x, j0 + j);
-        const float f = __shfl_sync(0xffffffffu, own_scale, j0 + j);
-        if (j0 + j >= count) break;
-        if (v != id) {
-          leave(false);
-          id = v;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-        }
-        const uint32_t keep = span_keep<VEC>(a.mask, ps, (unsigned long long)(t * per_row + c0 / 8), lane);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += keep >> k & 1u ? g[j][k] * f : 0.f;
+    for (int j = 0; j < kAhead; ++j) {
+      const int t = (int)__shfl_sync(0xffffffffu, own.y, j0 + j);
+      const TO* row = static_cast<const TO*>(a.out) + (size_t)t * a.out_stride + c0;
+      if constexpr (VEC) {
+        if (j0 + j < count) g[j].load(row + 8 * lane, left - 8 * lane);
+      } else {
+        if (j0 + j < count) span_load<false>(row, left, lane, scalar[j]);
       }
     }
-    leave(true);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int t = (int)__shfl_sync(0xffffffffu, own.y, j0 + j), v = (int)__shfl_sync(0xffffffffu, own.x, j0 + j);
+      const float f = __shfl_sync(0xffffffffu, own_scale, j0 + j);
+      if (j0 + j >= count) break;
+      if (v != id) {
+        leave(false);
+        id = v;
+        fill(acc, 0.f);
+      }
+      if constexpr (VEC) g[j].get(scalar[0]);
+      add_token<VEC>(a, ps, &keys, t, c0, lane, f, scalar[VEC ? 0 : j], acc);
+    }
   }
+  leave(true);
 }
 
 // Ids that cross borders: one block per piece in which such an id begins and 256 columns; its warps add
@@ -270,11 +335,11 @@ template <bool VEC>
 __global__ void __launch_bounds__(256) embed_grad_join_kernel(const EmbedArgs a, const uint2* __restrict__ list,
                                                               const int* __restrict__ valid,
                                                               const float* __restrict__ part) {
-  __shared__ float sums[8][256];
+  __shared__ uint64_t sums[8][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = *valid;
   const int spans = (a.cols + 255) / 256, pieces = (n + kPiece - 1) / kPiece;
   for (long long i = blockIdx.x; i < (long long)spans * pieces; i += gridDim.x) {
-    const int piece = (int)(i / spans), c0 = (int)(i - (long long)piece * spans) * 256, left = min(256, a.cols - c0);
+    const int piece = (int)(i / spans), c0 = (int)(i - (long long)piece * spans) * 256, left = a.cols - c0;
     const int p0 = piece * kPiece;
     if (p0 + kPiece >= n) continue;
     const uint32_t id = list[p0 + kPiece - 1].x;
@@ -287,24 +352,26 @@ __global__ void __launch_bounds__(256) embed_grad_join_kernel(const EmbedArgs a,
       more += same;
       if (same < 32) break;
     }
-    float acc[8] = {}, v[8];
+    Pairs acc, v;
+    fill(acc, 0.f);
     for (int k = warp; k <= more; k += 8) {
       span_load<VEC>(part + ((size_t)(piece + k) * 2 + (k ? 0 : 1)) * a.cols + c0, left, lane, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += v[e];
+      for (int e = 0; e < 4; ++e) acc[e] = f2_add(acc[e], v[e]);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[warp][32 * e + lane] = acc[e];
+    for (int e = 0; e < 4; ++e) sums[warp][32 * e + lane] = acc[e];
     __syncthreads();
     if (warp == 0) {
       float* dst = a.d_table + (size_t)id * a.cols + c0;
+      fill(v, 0.f);
       if (a.accumulate) span_load<VEC>(dst, left, lane, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float s = 0.f;
+      for (int e = 0; e < 4; ++e) {
+        uint64_t s = sums[0][32 * e + lane];
 #pragma unroll
-        for (int w = 0; w < 8; ++w) s += sums[w][32 * e + lane];
-        v[e] = a.accumulate ? v[e] + s : s;
+        for (int w = 1; w < 8; ++w) s = f2_add(s, sums[w][32 * e + lane]);
+        v[e] = f2_add(v[e], s);
       }
       span_store<VEC>(dst, left, lane, v);
     }
@@ -312,17 +379,18 @@ __global__ void __launch_bounds__(256) embed_grad_join_kernel(const EmbedArgs a,
   }
 }
 
-unsigned warps_grid(long long warps, int num_sms) {
-  return (unsigned)std::min((warps + 7) / 8, (long long)num_sms * 64);
-}
-
 template <typename TE, typename TO>
-void launch_lookup(const EmbedArgs& a, int num_sms, cudaStream_t st) {
-  const unsigned grid = warps_grid((a.cols + 255) / 256 * (long long)a.tokens, num_sms);
-  if (rows_on_16(a.table, a.cols, sizeof(TE)) && rows_on_16(a.out, a.out_stride, sizeof(TO)))
-    embed_scaled_kernel<TE, TO, true><<<grid, 256, 0, st>>>(a);
-  else
-    embed_scaled_kernel<TE, TO, false><<<grid, 256, 0, st>>>(a);
+cudaError_t launch_lookup(const EmbedArgs& a, cudaStream_t st) {
+  if (rows_on_16(a.table, a.cols, sizeof(TE)) && rows_on_16(a.out, a.out_stride, sizeof(TO))) {
+    const int per_row = (a.cols + 7) / 8;
+    const long long total = (long long)a.tokens * per_row, grid = (total + 256 * kBlocks - 1) / (256 * kBlocks);
+    embed_scaled_kernel<TE, TO><<<(unsigned)grid, 256, 0, st>>>(a, fast_div(per_row), total);
+  } else {
+    const int spans = (a.cols + 255) / 256;
+    const long long total = (long long)a.tokens * spans;
+    embed_rows_kernel<TE, TO><<<(unsigned)((total + 7) / 8), 256, 0, st>>>(a, fast_div(spans), total);
+  }
+  return cudaGetLastError();
 }
 
 // Few tokens: a search through all of them for every id is one launch.
@@ -347,7 +415,7 @@ template <typename TO, bool VEC>
 cudaError_t launch_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaStream_t st) {
   const long long spans = (a.cols + 255) / 256;
   if (direct(a.tokens, a.vocab)) {
-    embed_grad_kernel<TO, VEC><<<warps_grid(spans * a.vocab, num_sms), 256, 0, st>>>(a);
+    embed_grad_kernel<TO, VEC><<<(unsigned)((spans * a.vocab + 7) / 8), 256, 0, st>>>(a, fast_div((uint32_t)spans), spans * a.vocab);
     return cudaGetLastError();
   }
   const GradWorkspace w = grad_workspace(a.tokens, a.cols);
@@ -369,7 +437,7 @@ cudaError_t launch_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaSt
   }
   embed_sort_kernel<<<kSortBlocks + clear, kSortThreads, 0, st>>>(a, s);
   const long long pieces = (a.tokens + kPiece - 1) / kPiece;
-  embed_grad_pieces_kernel<TO, VEC><<<warps_grid(spans * pieces, num_sms), 256, 0, st>>>(a, s.list, s.valid, part);
+  embed_grad_pieces_kernel<TO, VEC><<<(unsigned)((spans * pieces + 7) / 8), 256, 0, st>>>(a, s.list, s.valid, part, fast_div((uint32_t)spans), spans * pieces);
   const unsigned join = (unsigned)std::min(spans * pieces, (long long)num_sms * 32);
   embed_grad_join_kernel<VEC><<<join, 256, 0, st>>>(a, s.list, s.valid, part);
   return cudaGetLastError();
@@ -377,17 +445,11 @@ cudaError_t launch_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaSt
 
 }  // namespace
 
-cudaError_t launch_embed_scaled(const EmbedArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_embed_scaled(const EmbedArgs& a, cudaStream_t st) {
   if (a.tokens <= 0) return cudaSuccess;
   using bf16 = __nv_bfloat16;
-  if (a.table_bf16) {
-    if (a.out_bf16) launch_lookup<bf16, bf16>(a, num_sms, st);
-    else launch_lookup<bf16, float>(a, num_sms, st);
-  } else {
-    if (a.out_bf16) launch_lookup<float, bf16>(a, num_sms, st);
-    else launch_lookup<float, float>(a, num_sms, st);
-  }
-  return cudaGetLastError();
+  if (a.table_bf16) return a.out_bf16 ? launch_lookup<bf16, bf16>(a, st) : launch_lookup<bf16, float>(a, st);
+  return a.out_bf16 ? launch_lookup<float, bf16>(a, st) : launch_lookup<float, float>(a, st);
 }
 
 size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols) {

@@ -1845,7 +1845,7 @@ esm_status esm_op_dropout(esm_encoder_t* h, const void* x, esm_precision x_type,
   a.y_stride = y_stride;
   a.rows = rows;
   a.cols = cols;
-  return cuda_status(launch_dropout(a, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_dropout(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 static bool embed_sizes(int tokens, int vocab, int cols) {
@@ -1890,7 +1890,7 @@ esm_status esm_op_embed(esm_encoder_t* h, const int32_t* ids, int tokens, const 
     return ESM_ERR_INVALID_ARG;
   a.table = table;
   a.table_bf16 = table_type == ESM_BF16;
-  return cuda_status(launch_embed_scaled(a, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_embed_scaled(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 esm_status esm_op_embed_backward_workspace_size(const esm_encoder_t* h, int tokens, int vocab, int cols, size_t* bytes) {
@@ -2042,6 +2042,7 @@ esm_status esm_op_block_norm_backward(esm_encoder_t* h, const esm_block_norm* no
   a.d_pre_gamma = grads->pre_gamma;
   a.d_pre_beta = grads->pre_beta;
   a.d_gate = grads->gate;
+  a.err = h->d_err;
   return cuda_status(launch_block_norm_bwd(a, es == 2, workspace, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 

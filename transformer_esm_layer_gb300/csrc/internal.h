@@ -341,7 +341,7 @@ struct DropoutArgs {
   int rows, cols;
   DropMask mask;
 };
-cudaError_t launch_dropout(const DropoutArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_dropout(const DropoutArgs& a, cudaStream_t st);
 
 // Lookup: table (vocab x cols) -> out; gradient: out (= dL/d(out)) -> d_table.
 struct EmbedArgs {
@@ -357,7 +357,7 @@ struct EmbedArgs {
   DropMask mask;
   unsigned* err;
 };
-cudaError_t launch_embed_scaled(const EmbedArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_embed_scaled(const EmbedArgs& a, cudaStream_t st);
 size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols);
 cudaError_t launch_embed_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaStream_t st);
 
@@ -381,6 +381,7 @@ struct BlockNormArgs {
   void* dy;
   float *d_post_gamma, *d_post_beta, *d_pre_gamma, *d_pre_beta;  // each may be NULL
   void* d_gate;   // fp32 [cols], or [rows, cols] of y's type
+  unsigned* err;
 };
 cudaError_t launch_block_norm(const BlockNormArgs& a, bool bf16, int num_sms, cudaStream_t st);
 size_t block_norm_bwd_workspace_bytes(int rows, int cols, int num_sms);
