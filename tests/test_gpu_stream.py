@@ -359,7 +359,8 @@ def test_embed_tables_past_32_bits(enc):
 # ------------------------------------------------------------------ block norm
 EPS = 1e-5
 NORM_SHAPES = [(1, 1), (1, 8), (3, 7), (5, 33), (173, 1280), (64, 256), (37, 1283), (9, 2560), (4, 4096), (3, 4104),
-               (3, 5120), (2, 8192), (2, 8191), (1500, 64), (700, 260)]
+               (3, 5120), (2, 8192), (2, 8191), (1500, 64), (700, 260), (701, 1280), (305, 8), (311, 2056), (7, 2304),
+               (333, 4088), (309, 904)]
 # kind, post, pre, betas, gate, residual scale, dropout
 NORMS = [("layer", True, True, True, "vector", 1.0, 0.1), ("layer", True, True, False, "rows", 0.7, None),
          ("rms", True, True, False, "vector", 1.0, 0.3), ("rms", True, True, True, "none", -0.5, None),

@@ -17,26 +17,21 @@ namespace esm {
 namespace {
 
 // ---- forward ----
-// A block takes R rows, W = ceil(cols / 256) warps to each, eight columns of every row to a lane.  Rows come as
-// blocks of the grid, not in a loop: with 40 to 80 registers the SM holds 30 to 45 warps whose loads, sums and
-// stores interleave by themselves.  R = 2 where there are rows enough: the parameters are read and unpacked
-// once for both, the generator's round keys are shared, and one barrier serves both rows' sums.
-#ifndef KFWDROWS
-#define KFWDROWS 2
-#endif
-#ifndef KFWDMIN
-#define KFWDMIN 0
-#endif
+// A block takes R rows, W warps to each; a warp holds G spans of 256 columns, eight of each to a lane.  Rows
+// come as blocks of the grid, not in a loop: the SM holds 25 to 40 warps whose loads, sums and stores interleave
+// by themselves (blocks that stay, with rows copied ahead by the threads, took 60 us where this takes 49.5).
+// Up to 2048 columns G = 1, and R = 2 where there are rows enough: the parameters are read and unpacked once
+// for both, the generator's round keys are shared, and one barrier serves both rows' sums.
 struct RowShape {
   float inv_cols, last, inv_last;  // of the columns of a row's last warp
 };
 
 // A warp's own mean and squared deviations are taken in two passes over its registers, and those of
 // several warps joined by their counts (Chan, Golub, LeVeque 1979), so no digits are lost to a large mean
-// and the row's warps meet once.  Counts are 256 but for the last warp's; means are taken relative to the
+// and the row's warps meet once.  Counts are 256 G but for the last warp's; means are taken relative to the
 // first warp's, so that one pass over the slots is enough:  sum of n d^2 about the joint mean is
 // sum of n d^2 - cols shift^2.
-template <int W>
+template <int W, int G>
 __device__ __forceinline__ float2 join_moments(const float2* slot, int warps, const RowShape& s) {
   const float2 first = slot[0];
   float d1 = 0.f, d2 = 0.f, q = first.y;
@@ -56,36 +51,46 @@ __device__ __forceinline__ float2 join_moments(const float2* slot, int warps, co
   }
   const float2 o = slot[warps - 1];
   const float d = o.x - first.x, nd = s.last * d;
-  d1 = fmaf(256.f, d1, nd);
-  d2 = fmaf(256.f, d2, nd * d);
+  d1 = fmaf(256.f * G, d1, nd);
+  d2 = fmaf(256.f * G, d2, nd * d);
   const float shift = d1 * s.inv_cols;
   return make_float2(first.x + shift, q + o.y + fmaf(-shift, d1, d2));
 }
 
-// Mean and 1 / sqrt(var + eps) of R rows of which this lane holds z (0 past the row's end).
-template <int R, int W, bool VEC>
-__device__ __forceinline__ void row_moments(const Pairs (&z)[R], const BlockNormArgs& a, const RowShape& s, int left,
+// Mean and 1 / sqrt(var + eps) of R rows of which this lane holds z (0 past the row's end); left: columns from the
+// warp's first on.
+template <int R, int G, int W, bool VEC>
+__device__ __forceinline__ void row_moments(const Pairs (&z)[R][G], const BlockNormArgs& a, const RowShape& s, int left,
                                             int warps, int w, int lane, float2 (*slot)[W > 0 ? W : 32], float2 (&out)[R]) {
   float mean[R], q[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) mean[r] = a.rms ? 0.f : sum(z[r]);
+  for (int r = 0; r < R; ++r) mean[r] = 0.f;
   if (!a.rms) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = sum(z[r][0]);
+#pragma unroll
+      for (int g = 1; g < G; ++g) mean[r] += sum(z[r][g]);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
       for (int r = 0; r < R; ++r) mean[r] += __shfl_xor_sync(0xffffffffu, mean[r], o);
 #pragma unroll
-    for (int r = 0; r < R; ++r) mean[r] *= w == warps - 1 ? s.inv_last : 1.f / 256.f;
+    for (int r = 0; r < R; ++r) mean[r] *= w == warps - 1 ? s.inv_last : 1.f / (256.f * G);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    Pairs d;
+    uint64_t t = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = f2_add(z[r][i], f2_both(-mean[r]));
-    if (left < 256) span_trim<VEC>(left, lane, d);
-    uint64_t t = f2_mul(d[0], d[0]);
+    for (int g = 0; g < G; ++g) {
+      Pairs d;
 #pragma unroll
-    for (int i = 1; i < 4; ++i) t = f2_fma(d[i], d[i], t);
+      for (int i = 0; i < 4; ++i) d[i] = f2_add(z[r][g][i], f2_both(-mean[r]));
+      if (left < 256 * (g + 1)) span_trim<VEC>(left - 256 * g, lane, d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t = g + i ? f2_fma(d[i], d[i], t) : f2_mul(d[0], d[0]);
+    }
     q[r] = f2_sum(t);
   }
 #pragma unroll
@@ -102,43 +107,57 @@ __device__ __forceinline__ void row_moments(const Pairs (&z)[R], const BlockNorm
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     float2 j = make_float2(mean[r], q[r]);
-    if (warps > 1) j = join_moments<W>(slot[r], warps, s);
+    if (warps > 1) j = join_moments<W, G>(slot[r], warps, s);
     out[r] = make_float2(j.x, rsqrtf(fmaf(j.y, s.inv_cols, a.eps)));
   }
 }
 
 // W = 0: the number of warps is blockDim.x / 32.  VEC: every row on 16 bytes and cols % 8 == 0.
-template <typename T, bool VEC, int W, int R>
-__global__ void __launch_bounds__(W > 0 ? 32 * W : 1024, W > 0 && KFWDMIN ? KFWDMIN : 1)
+template <typename T, bool VEC, int W, int R, int G, int MAX_THREADS, int MIN_BLOCKS>
+__global__ void __launch_bounds__(MAX_THREADS, MIN_BLOCKS)
     block_norm_kernel(const BlockNormArgs a, const RowShape shape) {
   __shared__ float2 slots[2][R][W > 0 ? W : 32];
   const int warps = W > 0 ? W : blockDim.x >> 5, w = W == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = w * 256, left = a.cols - c0;
-  const bool active = 8 * lane < left;  // (VEC)
-  // (a lane past the row's end works on the row's first columns and writes nothing)
-  const int c = VEC ? (active ? c0 + 8 * lane : 0) : c0;
-  auto fetch = [&](auto* p, auto& raw) {
-    if constexpr (VEC) raw.load(p + c, 8);
-    else span_load<false>(p + c0, left, lane, raw);
+  const int left = a.cols - w * G * 256;  // columns from the warp's first on
+  using RawT = std::conditional_t<VEC, Raw8<T>, Pairs>;
+  using RawF = std::conditional_t<VEC, Raw8<float>, Pairs>;
+  // VEC: the lane's first column of each span, or, past the row's end, the row's first, and then it writes nothing
+  bool active[G];
+  int c[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int c0 = (w * G + g) * 256;
+    active[g] = 8 * lane < left - 256 * g;
+    c[g] = VEC ? (active[g] ? c0 + 8 * lane : 0) : c0;
+  }
+  auto fetch = [&](auto* p, int g, auto& raw) {
+    if constexpr (VEC) raw.load(p + c[g], 8);
+    else span_load<false>(p + c[g], a.cols - c[g], lane, raw);
   };
   auto read = [](const auto& raw, Pairs& v) {
     if constexpr (VEC) raw.get(v);
     else v[0] = raw[0], v[1] = raw[1], v[2] = raw[2], v[3] = raw[3];
   };
-  auto store = [&](auto* p, const Pairs& v) {
+  auto store = [&](auto* p, int g, const Pairs& v) {
     if constexpr (VEC) {
-      if (active) st8(p + c, v);
+      if (active[g]) st8(p + c[g], v);
     } else {
-      span_store<false>(p + c0, left, lane, v);
+      span_store<false>(p + c[g], a.cols - c[g], lane, v);
     }
   };
-  using RawT = std::conditional_t<VEC, Raw8<T>, Pairs>;
-  using RawF = std::conditional_t<VEC, Raw8<float>, Pairs>;
+  auto trim = [&](Pairs (&v)[R][G]) {
+    if (left < 256 * G) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int g = 0; g < G; ++g) span_trim<VEC>(left - 256 * g, lane, v[r][g]);
+    }
+  };
   // (an odd last row is worked on twice by a block of two, and written once)
   long long row[R];
   size_t base[R];
-  RawT y[R], gate[R];
-  RawF x[R];
+  RawT y[R][G], gate[R][G];
+  RawF x[R][G];
   bool own[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -146,90 +165,106 @@ __global__ void __launch_bounds__(W > 0 ? 32 * W : 1024, W > 0 && KFWDMIN ? KFWD
     own[r] = n < a.rows;
     row[r] = own[r] ? n : a.rows - 1;
     base[r] = (size_t)row[r] * (uint32_t)a.cols;
-    fetch(static_cast<const T*>(a.y) + base[r], y[r]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) fetch(static_cast<const T*>(a.y) + base[r], g, y[r][g]);
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r) fetch(a.x + base[r], x[r]);
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int g = 0; g < G; ++g) fetch(a.x + base[r], g, x[r][g]);
   if (a.gate_rows) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) fetch(static_cast<const T*>(a.gate) + base[r], gate[r]);
-  }
-  uint4 words[R];
-  const PhiloxState ps = philox_state(a.mask);
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const uint32_t block = VEC ? (uint32_t)c / 8 : (uint32_t)c0 / 8 + lane;
-    words[r] = drop_words(a.mask, ps, (unsigned long long)row[r] * ((uint32_t)(a.cols + 7) / 8) + block);
-    words[r] = span_words<VEC>(a.mask, words[r], lane);
-  }
-  Pairs u[R], p;
-  float2 post[R], pre[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    read(y[r], u[r]);
-    if (left < 256) span_trim<VEC>(left, lane, u[r]);
-    post[r] = pre[r] = make_float2(0.f, 0.f);
-  }
-  auto vector = [&](const void* from) {
-    RawT raw;
-    fetch(static_cast<const T*>(from), raw);
-    read(raw, p);
-  };
-  auto normalise = [&](const float2 (&m)[R], const void* gamma, const void* beta) {
-    vector(gamma);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[r][i] = f2_mul(f2_mul(f2_add(u[r][i], f2_both(-m[r].x)), f2_both(m[r].y)), p[i]);
-    if (beta) {
-      vector(beta);
+      for (int g = 0; g < G; ++g) fetch(static_cast<const T*>(a.gate) + base[r], g, gate[r][g]);
+  }
+  uint4 words[R][G];
+  const PhiloxState ps = philox_state(a.mask);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t block = (uint32_t)c[g] / 8 + (VEC ? 0 : lane);
+      words[r][g] = drop_words(a.mask, ps, (unsigned long long)row[r] * ((uint32_t)(a.cols + 7) / 8) + block);
+      words[r][g] = span_words<VEC>(a.mask, words[r][g], lane);
+    }
+  Pairs u[R][G], p;
+  float2 post[R], pre[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) read(y[r][g], u[r][g]);
+    post[r] = pre[r] = make_float2(0.f, 0.f);
+  }
+  trim(u);
+  auto vector = [&](const void* from, int g) {
+    RawT raw;
+    fetch(static_cast<const T*>(from), g, raw);
+    read(raw, p);
+  };
+  auto normalise = [&](const float2 (&m)[R], const void* gamma, const void* beta) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      vector(gamma, g);
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[r][i] = f2_add(u[r][i], p[i]);
+        for (int i = 0; i < 4; ++i)
+          u[r][g][i] = f2_mul(f2_mul(f2_add(u[r][g][i], f2_both(-m[r].x)), f2_both(m[r].y)), p[i]);
+      if (beta) {
+        vector(beta, g);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[r][g][i] = f2_add(u[r][g][i], p[i]);
+      }
     }
   };
   if (a.post_gamma) {
-    row_moments<R, W, VEC>(u, a, shape, left, warps, w, lane, slots[0], post);
+    row_moments<R, G, W, VEC>(u, a, shape, left, warps, w, lane, slots[0], post);
     normalise(post, a.post_gamma, a.post_beta);
   }
   if (a.mask.rng) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[r][i] = f2_mul(u[r][i], f2_both(a.mask.scale));
-      keep(words[r], ps, u[r]);
-    }
+      for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[r][g][i] = f2_mul(u[r][g][i], f2_both(a.mask.scale));
+        keep(words[r][g], ps, u[r][g]);
+      }
   }
   if (a.gate) {
-    if (!a.gate_rows) vector(a.gate);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (a.gate_rows) read(gate[r], p);
+    for (int g = 0; g < G; ++g) {
+      if (!a.gate_rows) vector(a.gate, g);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[r][i] = f2_mul(u[r][i], p[i]);
+      for (int r = 0; r < R; ++r) {
+        if (a.gate_rows) read(gate[r][g], p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[r][g][i] = f2_mul(u[r][g][i], p[i]);
+      }
     }
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    read(x[r], p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[r][i] = f2_fma(f2_both(a.residual_scale), p[i], u[r][i]);
   }
   // (x_out may be x: a lane writes only places that it alone reads, and has read, a last row's twice)
 #pragma unroll
   for (int r = 0; r < R; ++r)
-    if (own[r]) store(a.x_out + base[r], u[r]);
-  if (a.pre_gamma) {
-    if (left < 256) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) span_trim<VEC>(left, lane, u[r]);
+    for (int g = 0; g < G; ++g) {
+      read(x[r][g], p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[r][g][i] = f2_fma(f2_both(a.residual_scale), p[i], u[r][g][i]);
+      if (own[r]) store(a.x_out + base[r], g, u[r][g]);
     }
-    row_moments<R, W, VEC>(u, a, shape, left, warps, w, lane, slots[1], pre);
+  if (a.pre_gamma) {
+    trim(u);
+    row_moments<R, G, W, VEC>(u, a, shape, left, warps, w, lane, slots[1], pre);
     normalise(pre, a.pre_gamma, a.pre_beta);
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (own[r]) store(static_cast<T*>(a.h) + base[r], u[r]);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (own[r]) store(static_cast<T*>(a.h) + base[r], g, u[r][g]);
   }
   if (a.stats && threadIdx.x == 0) {
 #pragma unroll
@@ -273,26 +308,21 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
 }
 
 constexpr int kSums = 4;         // column sums: d_h xh, d_h, P, Q
-#ifndef KBWDWARPS
-#define KBWDWARPS 16
-#endif
-constexpr int kBwdWarps = KBWDWARPS;    // warps of a block
+constexpr int kBwdWarps = 20;    // warps of a block
 
-#ifndef KSTAGES
-#define KSTAGES 3
-#endif
-constexpr int kStages = KSTAGES;
+constexpr int kStages = 2;
 constexpr int kMaxGroups = 15;  // named barriers
 
 // Rows on 16 bytes, cols % 8 == 0 and <= 4096.  A block of `groups` groups of W = ceil(cols / 256) warps stays on
 // its SM and takes a row per group and step; a lane owns eight columns of every row that its group takes, so
-// the four column sums stay in its registers and leave once per block, into partial[block][kSums][cols].  The
-// rows to come arrive by bulk copies, kStages of them per group, which leaves the threads and the L1 out of
-// it; gamma_pre and gate gamma_post stand in shared memory as float32.
+// the four column sums stay with it (in shared memory: 32 registers fewer let 20 warps run, not 16) and leave
+// once per block, into partial[block][kSums][cols].  The rows to come arrive by bulk copies, kStages of them per
+// group, which leaves the threads and the L1 out of it; gamma_pre and gate gamma_post stand in shared memory
+// as float32.
 template <typename T>
 __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     block_norm_bwd_kernel(const BlockNormArgs a, int W, int groups, float* __restrict__ partial) {
-  extern __shared__ __align__(16) uint8_t smem[];  // vectors, then the rows on their way; at the end the sums
+  extern __shared__ __align__(16) uint8_t smem[];  // vectors, column sums, the rows on their way
   __shared__ float red[2][kBwdWarps][8];           // the two latest rows' sums of every warp
   __shared__ uint64_t full[kMaxGroups * kStages];
   __shared__ PhiloxKeys keys;
@@ -300,22 +330,26 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr, partly = a.cols - w * 256 < 256;
   const int c = w * 256 + 8 * lane;  // the lane's first column
   const bool active = c < a.cols;
-  const long long first = (long long)blockIdx.x * groups + group, step = (long long)gridDim.x * groups;
+  const int first = blockIdx.x * groups + group, step = gridDim.x * groups;  // (rows + 4 steps fit 32 bits)
   const PhiloxState ps = philox_state(a.mask);
   philox_keys(ps, &keys);
-  // a stage: rows of d_x_out, x_out (float32), y, d_h and the gate (T)
+  // a stage: the statistics, rows of d_x_out and x_out (float32), of y, d_h and the gate (T)
   const uint32_t f_bytes = (uint32_t)a.cols * 4, t_bytes = (uint32_t)a.cols * sizeof(T);
-  const uint32_t stage_bytes = 2 * f_bytes + (a.gate_rows ? 3 : 2) * t_bytes;
-  uint8_t* ring = smem + 2048 * W + group * kStages * stage_bytes;
+  const uint32_t stage_bytes = 16 + 2 * f_bytes + (a.gate_rows ? 3 : 2) * t_bytes;
+  // sum i of the lane's columns: its own 16 bytes at 2 i and 2 i + 1 blocks' widths
+  float4* own_sums = reinterpret_cast<float4*>(smem + 2048 * W) + threadIdx.x;
+  uint8_t* ring = smem + 2048 * W + (size_t)blockDim.x * (32 * kSums) + group * kStages * stage_bytes;
   uint64_t* bars = full + group * kStages;
   if (threadIdx.x < groups * kStages) mbar_init(full + threadIdx.x, 1);
   fence_barrier_init();
-  auto arrive = [&](long long row, int stage) {  // (one thread of the group)
+  auto arrive = [&](int row, int stage) {  // (one thread of the group)
     if (row >= a.rows) return;
     const size_t at = (size_t)row * a.cols;
     uint8_t* to = ring + stage * stage_bytes;
-    mbar_arrive_expect_tx(bars + stage, (a.d_x_out ? f_bytes : 0) + t_bytes + (pre ? f_bytes + t_bytes : 0) +
+    mbar_arrive_expect_tx(bars + stage, (pre || post ? 16 : 0) + (a.d_x_out ? f_bytes : 0) + t_bytes + (pre ? f_bytes + t_bytes : 0) +
                                             (a.gate_rows ? t_bytes : 0));
+    if (pre || post) bulk_load(to, a.stats + 4 * (size_t)row, 16, bars + stage);
+    to += 16;
     if (a.d_x_out) bulk_load(to, a.d_x_out + at, f_bytes, bars + stage);
     if (pre) bulk_load(to + f_bytes, a.x_out + at, f_bytes, bars + stage);
     to += 2 * f_bytes;
@@ -327,6 +361,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   if (w == 0 && lane == 0) {
 #pragma unroll
     for (int i = 0; i < kStages; ++i) arrive(first + i * step, i);
+  }
+  if (!a.d_x_out) {  // zeros stand in its place
+    for (int s = 0; s < kStages; ++s)
+      for (int i = w * 32 + lane; i < a.cols; i += 32 * W) reinterpret_cast<float*>(ring + 16 + s * stage_bytes)[i] = 0.f;
   }
   float* vf = reinterpret_cast<float*>(smem);
   for (int i = threadIdx.x; i < 256 * W; i += blockDim.x) {
@@ -340,46 +378,46 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     const ulonglong2 lo = vectors[v * 64 * W], hi = vectors[v * 64 * W + 32];
     out[0] = lo.x; out[1] = lo.y; out[2] = hi.x; out[3] = hi.y;
   };
-  auto statistics = [&](long long row) {
-    return (pre || post) && row < a.rows ? __ldg(reinterpret_cast<const float4*>(a.stats) + row)
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  Pairs acc[kSums];
 #pragma unroll
-  for (int i = 0; i < kSums; ++i) fill(acc[i], 0.f);
-  float4 next = statistics(first);
+  for (int i = 0; i < 2 * kSums; ++i) own_sums[i * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto sum_at = [&](int i, Pairs& v) {
+    const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(own_sums + 2 * i * blockDim.x),
+                     hi = *reinterpret_cast<const ulonglong2*>(own_sums + (2 * i + 1) * blockDim.x);
+    v[0] = lo.x; v[1] = lo.y; v[2] = hi.x; v[3] = hi.y;
+  };
+  auto put_sum = [&](int i, const Pairs& v) {
+    *reinterpret_cast<ulonglong2*>(own_sums + 2 * i * blockDim.x) = make_ulonglong2(v[0], v[1]);
+    *reinterpret_cast<ulonglong2*>(own_sums + (2 * i + 1) * blockDim.x) = make_ulonglong2(v[2], v[3]);
+  };
   const float inv_n = 1.f / (float)a.cols;
   const uint32_t per_row = (uint32_t)a.cols / 8;
-  unsigned long long block = (unsigned long long)first * per_row + (uint32_t)c / 8;
-  size_t at = (size_t)first * a.cols + c;
   bool alive = true;
   int flip = 0, stage = 0;
+  const uint8_t* from = ring;
   uint32_t parity = 0;
   __syncthreads();
-  for (long long row = first; row < a.rows; row += step) {
-    const float4 st = next;
-    next = statistics(row + step);
+  for (int row = first; row < a.rows; row += step) {
     if (alive && !mbar_wait_warp(bars + stage, parity)) {
       alive = false;  // (the copy never came: nothing of this call is right, and nothing more is waited for)
       latch_error(a.err, ERRBIT_TIMEOUT);
     }
-    const uint8_t* from = ring + stage * stage_bytes;
-    auto row_f = [&](int i, Pairs& v) { ld8(reinterpret_cast<const float*>(from + i * f_bytes) + c, v); };
-    auto row_t = [&](int i, Pairs& v) { ld8(reinterpret_cast<const T*>(from + 2 * f_bytes + i * t_bytes) + c, v); };
+    const float4 st = pre || post ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint8_t* values = from + 16;
+    auto row_f = [&](int i, Pairs& v) { ld8(reinterpret_cast<const float*>(values + i * f_bytes) + c, v); };
+    auto row_t = [&](int i, Pairs& v) { ld8(reinterpret_cast<const T*>(values + 2 * f_bytes + i * t_bytes) + c, v); };
     Pairs xh, e, yh, kf, p;
     float s[8];
     // 0 or the dropout's scale, per element
     fill(kf, a.mask.scale);
-    if (a.mask.rng) keep(drop_words(a.mask, ps, &keys, block), ps, kf);
-    if (a.d_x_out) row_f(0, e);
-    else fill(e, 0.f);
+    keep(drop_words(a.mask, ps, &keys, (unsigned long long)(uint32_t)row * per_row + (uint32_t)c / 8), ps, kf);
+    row_f(0, e);
     row_t(0, yh);
     if (partly && !active) {
       fill(e, 0.f);
       fill(yh, 0.f);
       fill(kf, 0.f);
     }
-    uint64_t s2[8] = {};
+    uint64_t s2[8];
     if (pre) {
       Pairs dh;
       row_f(1, xh);
@@ -388,26 +426,33 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
         fill(xh, st.z);
         fill(dh, 0.f);
       }
+      Pairs sx, sd;
+      sum_at(0, sx);
+      sum_at(1, sd);
       vector(0, p);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         xh[k] = f2_mul(f2_add(xh[k], f2_both(-st.z)), f2_both(st.w));
-        acc[0][k] = f2_fma(dh[k], xh[k], acc[0][k]);
-        acc[1][k] = f2_add(dh[k], acc[1][k]);
+        sx[k] = f2_fma(dh[k], xh[k], sx[k]);
+        sd[k] = f2_add(dh[k], sd[k]);
         const uint64_t gg = f2_mul(dh[k], p[k]);
-        s2[0] = f2_add(s2[0], gg);
-        s2[1] = f2_fma(gg, xh[k], s2[1]);
+        s2[0] = k ? f2_add(s2[0], gg) : gg;
+        s2[1] = k ? f2_fma(gg, xh[k], s2[1]) : f2_mul(gg, xh[k]);
         e[k] = f2_fma(f2_both(st.w), gg, e[k]);
       }
+      put_sum(0, sx);
+      put_sum(1, sd);
     } else {
       fill(xh, 0.f);
+      s2[0] = s2[1] = 0;
     }
+    Raw8<T> gate;
+    if (a.gate_rows) gate.load(reinterpret_cast<const T*>(values + 2 * f_bytes + 2 * t_bytes) + (active ? c : 0), 8);
     if (post) {
       Pairs cg;
       vector(1, cg);
       if (a.gate_rows) {
-        row_t(2, p);
-        if (partly && !active) fill(p, 0.f);
+        gate.get(p);
 #pragma unroll
         for (int k = 0; k < 4; ++k) cg[k] = f2_mul(cg[k], p[k]);
       }
@@ -416,13 +461,15 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
         const uint64_t ck = f2_mul(cg[k], kf[k]);
         yh[k] = f2_mul(f2_add(yh[k], f2_both(-st.x)), f2_both(st.y));
         const uint64_t ce = f2_mul(ck, e[k]), cyh = f2_mul(ck, yh[k]);
-        s2[2] = f2_add(s2[2], ce);
-        s2[3] = f2_add(s2[3], ck);
-        s2[4] = f2_fma(ck, xh[k], s2[4]);
-        s2[5] = f2_fma(ce, yh[k], s2[5]);
-        s2[6] = f2_add(s2[6], cyh);
-        s2[7] = f2_fma(cyh, xh[k], s2[7]);
+        s2[2] = k ? f2_add(s2[2], ce) : ce;
+        s2[3] = k ? f2_add(s2[3], ck) : ck;
+        s2[4] = k ? f2_fma(ck, xh[k], s2[4]) : f2_mul(ck, xh[k]);
+        s2[5] = k ? f2_fma(ce, yh[k], s2[5]) : f2_mul(ce, yh[k]);
+        s2[6] = k ? f2_add(s2[6], cyh) : cyh;
+        s2[7] = k ? f2_fma(cyh, xh[k], s2[7]) : f2_mul(cyh, xh[k]);
       }
+    } else {
+      s2[2] = s2[3] = s2[4] = s2[5] = s2[6] = s2[7] = 0;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = f2_sum(s2[i]);
@@ -431,20 +478,23 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       if (lane % 4 == 0) red[flip][warp][lane / 4] = total;
       named_bar_sync(1 + group, 32 * W);
       total = 0.f;
-      for (int i = lane & 3; i < W; i += 4) total += red[flip][group * W + i][lane / 4];
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        if (i + (lane & 3) < W) total += red[flip][group * W + i + (lane & 3)][lane / 4];
       total += __shfl_xor_sync(0xffffffffu, total, 2);
       total += __shfl_xor_sync(0xffffffffu, total, 1);
       flip ^= 1;
     } else {
       __syncwarp();
     }
-    // the whole group is done with the row before: its stage takes the row after those on their way
-    if (w == 0 && lane == 0 && row != first) arrive(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+    // the whole group has this row in its registers: the stage takes the next one
+    if (w == 0 && lane == 0) arrive(row + kStages * step, stage);
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = __shfl_sync(0xffffffffu, total, 4 * i);
     const float A = a.rms ? 0.f : st.w * s[0] * inv_n, B = st.w * s[1] * inv_n;
     const float m0 = a.rms ? 0.f : (s[2] - A * s[3] - B * s[4]) * inv_n, m1 = (s[5] - A * s[6] - B * s[7]) * inv_n;
     Pairs q, out;
+    const size_t at = (size_t)row * (uint32_t)a.cols + c;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       e[k] = f2_fma(f2_both(-B), xh[k], f2_add(e[k], f2_both(-A)));  // now G
@@ -460,56 +510,47 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
         yh[k] = f2_pack(f2_lo(kf[k]) != 0.f ? f2_lo(yh[k]) : 0.f, f2_hi(kf[k]) != 0.f ? f2_hi(yh[k]) : 0.f);
     }
     if (a.gate_rows) {
-      Pairs n, gate, beta;
-      row_t(2, gate);
-      if (partly && !active) fill(gate, 0.f);
+      Pairs n, own_gate, beta;
+      gate.get(own_gate);
       fill(beta, 0.f);
       if (a.post_beta && active) ld8(static_cast<const T*>(a.post_beta) + c, beta);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         n[k] = f2_mul(q[k], f2_fma(yh[k], p[k], beta[k]));
-        q[k] = f2_mul(q[k], gate[k]);
+        q[k] = f2_mul(q[k], own_gate[k]);
       }
       if (a.d_gate && active) st8(static_cast<T*>(a.d_gate) + at, n);
     }
+    Pairs sp, sq;
+    sum_at(2, sp);
+    sum_at(3, sq);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      acc[2][k] = f2_fma(q[k], yh[k], acc[2][k]);
-      acc[3][k] = f2_add(q[k], acc[3][k]);
+      sp[k] = f2_fma(q[k], yh[k], sp[k]);
+      sq[k] = f2_add(q[k], sq[k]);
       out[k] = f2_mul(p[k], q[k]);
       if (post) out[k] = f2_mul(f2_both(st.y), f2_fma(f2_both(-m1), yh[k], f2_add(out[k], f2_both(-m0))));
     }
+    put_sum(2, sp);
+    put_sum(3, sq);
     if (active) st8(static_cast<T*>(a.dy) + at, out);
-    at += step * a.cols;
-    block += step * per_row;
+    from += stage_bytes;
     if (++stage == kStages) {
       stage = 0;
+      from = ring;
       parity ^= 1;
     }
   }
-  // the rows' place is taken by the sums, which the groups add in order
+  // the groups' sums are added in order
   __syncthreads();
-  float* sums = reinterpret_cast<float*>(smem);
-  for (int turn = 0; turn < groups; ++turn) {
-    if (turn == group && active) {
-#pragma unroll
-      for (int i = 0; i < kSums; ++i) {
-        float* to = sums + (size_t)i * a.cols + c;
-        Pairs v;
-        if (turn) {
-          ld8(to, v);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = f2_add(v[k], acc[i][k]);
-          st8(to, v);
-        } else {
-          st8(to, acc[i]);
-        }
-      }
-    }
-    __syncthreads();
+  const float* all = reinterpret_cast<const float*>(smem + 2048 * W);
+  for (int i = threadIdx.x; i < kSums * a.cols; i += blockDim.x) {
+    const int s = i / a.cols, col = i - s * a.cols;
+    float v = 0.f;
+    for (int g = 0; g < groups; ++g)
+      v += all[((size_t)(2 * s + (col >> 2 & 1)) * blockDim.x + (g * W + (col >> 8)) * 32 + (col >> 3 & 31)) * 4 + (col & 3)];
+    partial[(size_t)blockIdx.x * kSums * a.cols + i] = v;
   }
-  for (int i = threadIdx.x; i < kSums * a.cols; i += blockDim.x)
-    partial[(size_t)blockIdx.x * kSums * a.cols + i] = sums[i];
 }
 
 // Any alignment, and rows of up to 8192 columns: the same sums, rows read where they are used and parameters
@@ -801,7 +842,7 @@ BwdShape bwd_shape(int rows, int cols, int num_sms) {
   return s;
 }
 
-constexpr size_t kSmemMax = 227 * 1024 - 4096;  // (the rest: static shared memory)
+constexpr size_t kSmemMax = 227 * 1024 - 2048;  // (the rest: static shared memory)
 
 // Lets a kernel have `smem` bytes of dynamic shared memory.
 template <typename Kernel>
@@ -821,8 +862,9 @@ cudaError_t launch_bwd_any(const BlockNormArgs& a, const BwdShape& s, float* par
 template <typename T>
 cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num_sms, cudaStream_t st) {
   BwdShape s = bwd_shape(a.rows, a.cols, num_sms);
-  const size_t row = (size_t)a.cols * (8 + (a.gate_rows ? 3 : 2) * sizeof(T)) * kStages;
-  const size_t fits = (kSmemMax - 2048 * s.W - 1024) / row;  // groups whose rows fit shared memory
+  // a group's rows and sums, behind the vectors (1 KB more: lanes past a row's end read on behind it)
+  const size_t group = ((size_t)a.cols * (8 + (a.gate_rows ? 3 : 2) * sizeof(T)) + 16) * kStages + (size_t)1024 * kSums * s.W;
+  const size_t fixed = 2048 * s.W + 1024, fits = (kSmemMax - fixed) / group;
   cudaError_t e;
   if (s.G == 2) {
     e = vec ? launch_bwd_any<T, true, 2>(a, s, partial, st) : launch_bwd_any<T, false, 2>(a, s, partial, st);
@@ -831,8 +873,7 @@ cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num
     e = vec ? launch_bwd_any<T, true, 1>(a, s, partial, st) : launch_bwd_any<T, false, 1>(a, s, partial, st);
   } else {
     s.groups = (int)std::min((size_t)s.groups, fits);
-    // (1 KB more: lanes past a row's end read on behind it)
-    const size_t smem = std::max(sizeof(float) * kSums * a.cols, 2048 * s.W + row * s.groups + 1024);
+    const size_t smem = fixed + group * s.groups;
     e = allow_smem(block_norm_bwd_kernel<T>, smem);
     if (e != cudaSuccess) return e;
     block_norm_bwd_kernel<T><<<s.blocks, 32 * s.W * s.groups, smem, st>>>(a, s.W, s.groups, partial);
@@ -843,34 +884,45 @@ cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num
   return cudaGetLastError();
 }
 
+// W warps to a row of up to 4096 columns.  Registers for 800 threads an SM with bfloat16 blocks (80 each; 16384 x
+// 1280: 49.5 us, with 64 registers 52, with 104 56) and for 640 with float32 ones (68.6 us, with 80 registers 82).
 template <typename T, int W>
-void launch_fwd_as(const BlockNormArgs& a, const RowShape& s, int warps, int num_sms, cudaStream_t st) {
-  constexpr int R = KFWDROWS;
-  if (a.rows > R * num_sms) block_norm_kernel<T, true, W, R><<<(unsigned)((a.rows + R - 1) / R), 32 * warps, 0, st>>>(a, s);
-  else block_norm_kernel<T, true, W, 1><<<(unsigned)a.rows, 32 * warps, 0, st>>>(a, s);
+void launch_fwd_as(const BlockNormArgs& a, const RowShape& s, int spans, int num_sms, cudaStream_t st) {
+  constexpr int kThreads = 32 * W, kBlocks = std::min(24, (sizeof(T) == 2 ? 800 : 640) / kThreads);
+  if (spans > 8)
+    block_norm_kernel<T, true, W, 1, 2, kThreads, kBlocks><<<(unsigned)a.rows, kThreads, 0, st>>>(a, s);
+  else if (a.rows > 2 * num_sms)
+    block_norm_kernel<T, true, W, 2, 1, kThreads, kBlocks><<<(unsigned)((a.rows + 1) / 2), kThreads, 0, st>>>(a, s);
+  else
+    block_norm_kernel<T, true, W, 1, 1, kThreads, 1><<<(unsigned)a.rows, kThreads, 0, st>>>(a, s);
 }
 
 template <typename T>
 cudaError_t launch_fwd(const BlockNormArgs& a, bool vec, int num_sms, cudaStream_t st) {
-  const int W = (a.cols + 255) / 256;
+  const int spans = (a.cols + 255) / 256;
+  const bool by_width = vec && a.cols % 8 == 0 && spans <= 16;
+  const int G = by_width && spans > 8 ? 2 : 1, W = (spans + G - 1) / G;
   RowShape s;
   s.inv_cols = 1.f / (float)a.cols;
-  s.last = (float)(a.cols - 256 * (W - 1));
+  s.last = (float)(a.cols - 256 * G * (W - 1));
   s.inv_last = 1.f / s.last;
-  if (!vec || a.cols % 8) {
-    block_norm_kernel<T, false, 0, 1><<<(unsigned)a.rows, 32 * W, 0, st>>>(a, s);
+  if (!by_width) {
+    const unsigned rows = (unsigned)a.rows;
+    const int threads = 32 * spans;
+    if (vec && a.cols % 8 == 0) block_norm_kernel<T, true, 0, 1, 1, 1024, 1><<<rows, threads, 0, st>>>(a, s);
+    else if (spans <= 8) block_norm_kernel<T, false, 0, 1, 1, 256, 4><<<rows, threads, 0, st>>>(a, s);
+    else block_norm_kernel<T, false, 0, 1, 1, 1024, 1><<<rows, threads, 0, st>>>(a, s);
     return cudaGetLastError();
   }
   switch (W) {
-    case 1: launch_fwd_as<T, 1>(a, s, W, num_sms, st); break;
-    case 2: launch_fwd_as<T, 2>(a, s, W, num_sms, st); break;
-    case 3: launch_fwd_as<T, 3>(a, s, W, num_sms, st); break;
-    case 4: launch_fwd_as<T, 4>(a, s, W, num_sms, st); break;
-    case 5: launch_fwd_as<T, 5>(a, s, W, num_sms, st); break;
-    case 6: launch_fwd_as<T, 6>(a, s, W, num_sms, st); break;
-    case 7: launch_fwd_as<T, 7>(a, s, W, num_sms, st); break;
-    case 8: launch_fwd_as<T, 8>(a, s, W, num_sms, st); break;
-    default: launch_fwd_as<T, 0>(a, s, W, num_sms, st); break;
+    case 1: launch_fwd_as<T, 1>(a, s, spans, num_sms, st); break;
+    case 2: launch_fwd_as<T, 2>(a, s, spans, num_sms, st); break;
+    case 3: launch_fwd_as<T, 3>(a, s, spans, num_sms, st); break;
+    case 4: launch_fwd_as<T, 4>(a, s, spans, num_sms, st); break;
+    case 5: launch_fwd_as<T, 5>(a, s, spans, num_sms, st); break;
+    case 6: launch_fwd_as<T, 6>(a, s, spans, num_sms, st); break;
+    case 7: launch_fwd_as<T, 7>(a, s, spans, num_sms, st); break;
+    default: launch_fwd_as<T, 8>(a, s, spans, num_sms, st); break;
   }
   return cudaGetLastError();
 }

@@ -5,6 +5,7 @@
 //
 // Bound by memory: the rows met and the output; for the gradient d_out and the table's rows.
 #include <algorithm>
+#include <type_traits>
 
 #include "dropout.cuh"
 #include "internal.h"
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(256, KMINB)
   const float own_scale = lane < count ? token_scale(a, (int)own.y) * a.mask.scale : 0.f;
   const int before = p0 > 0 ? (int)list[p0 - 1].x : -1, after = p0 + kPiece < n ? (int)list[p0 + kPiece].x : -1;
   int id = (int)__shfl_sync(0xffffffffu, own.x, 0);
+  const bool active = 8 * lane < left;
   Pairs acc;
   fill(acc, 0.f);
   auto leave = [&](bool last) {
@@ -299,18 +301,16 @@ __global__ void __launch_bounds__(256, KMINB)
     }
     span_store<VEC>(dst, left, lane, acc);
   };
+  using Row = std::conditional_t<VEC, Raw8<TO>, Pairs>;
   for (int j0 = 0; j0 < count; j0 += kAhead) {
-    Raw8<TO> g[kAhead];
-    Pairs scalar[VEC ? 1 : kAhead];
+    Row g[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int t = (int)__shfl_sync(0xffffffffu, own.y, j0 + j);
+      // (past the end: the last row once more, which is not added)
+      const int t = (int)__shfl_sync(0xffffffffu, own.y, min(j0 + j, count - 1));
       const TO* row = static_cast<const TO*>(a.out) + (size_t)t * a.out_stride + c0;
-      if constexpr (VEC) {
-        if (j0 + j < count) g[j].load(row + 8 * lane, left - 8 * lane);
-      } else {
-        if (j0 + j < count) span_load<false>(row, left, lane, scalar[j]);
-      }
+      if constexpr (VEC) g[j].load(row + (active ? 8 * lane : 0), 8);
+      else span_load<false>(row, left, lane, g[j]);
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -322,8 +322,14 @@ __global__ void __launch_bounds__(256, KMINB)
         id = v;
         fill(acc, 0.f);
       }
-      if constexpr (VEC) g[j].get(scalar[0]);
-      add_token<VEC>(a, ps, &keys, t, c0, lane, f, scalar[VEC ? 0 : j], acc);
+      Pairs p;
+      if constexpr (VEC) {
+        g[j].get(p);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = g[j][k];
+      }
+      add_token<VEC>(a, ps, &keys, t, c0, lane, f, p, acc);
     }
   }
   leave(true);
