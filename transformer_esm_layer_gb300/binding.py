@@ -730,20 +730,21 @@ class EsmEncoder:
     # ------------------------------------------------------------------ the residual stream
     @staticmethod
     def _check_rows(t, where: str, name: str, device):
-        """A 2-D float32 or bfloat16 tensor with contiguous rows; returns its esm_precision and row stride."""
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device):
-            _refuse(where, f"{name} must be a CUDA tensor on {device}")
-        kind = 0 if t.dtype is torch.float32 else 1 if t.dtype is torch.bfloat16 else -1
-        if kind < 0:
-            _refuse(where, f"{name} must be float32 or bfloat16")
-        if t.dim() != 2:
-            _refuse(where, f"{name} must be 2-D")
-        (rows, cols), (stride, step) = t.shape, t.stride()
-        if not (step == 1 or cols == 1):
-            _refuse(where, f"{name} must have contiguous rows")
-        if rows > STREAM_MAX or cols > STREAM_MAX:
-            _refuse(where, f"{name} must have at most 2^30 rows and columns")
-        return kind, stride if rows > 1 else max(stride, cols)
+        """A 2-D float32 or bfloat16 CUDA tensor with contiguous rows; returns its esm_precision, shape and
+        row stride (attributes are read once: an operator of a few microseconds has several tensors)."""
+        if isinstance(t, torch.Tensor) and t.device == device and t.is_cuda:
+            dtype, shape, strides = t.dtype, t.shape, t.stride()
+            kind = 0 if dtype is torch.float32 else 1 if dtype is torch.bfloat16 else -1
+            if kind >= 0 and len(shape) == 2:
+                rows, cols = shape
+                if (strides[1] == 1 or cols == 1) and rows <= STREAM_MAX and cols <= STREAM_MAX:
+                    return kind, shape, strides[0] if rows > 1 else max(strides[0], cols)
+        _need(isinstance(t, torch.Tensor) and t.is_cuda, where, f"{name} must be a CUDA tensor")
+        _need(t.device == device, where, f"{name} must be on {device}")
+        _need(t.dtype in (torch.float32, torch.bfloat16), where, f"{name} must be float32 or bfloat16")
+        _need(t.dim() == 2, where, f"{name} must be 2-D")
+        _need(t.stride(1) == 1 or t.shape[1] == 1, where, f"{name} must have contiguous rows")
+        _refuse(where, f"{name} must have at most 2^30 rows and columns")
 
     @staticmethod
     def _dropout_struct(dropout, where: str, device):
@@ -759,16 +760,17 @@ class EsmEncoder:
         where = "op_dropout"
         _need(isinstance(x, torch.Tensor) and x.is_cuda, where, "x must be a CUDA tensor")
         dev = x.device
-        kx, sx = self._check_rows(x, where, "x", dev)
-        ky, sy = self._check_rows(y, where, "y", dev)
-        _need(y.shape == x.shape, where, "y must have the shape of x")
+        kx, shape, sx = self._check_rows(x, where, "x", dev)
+        ky, y_shape, sy = self._check_rows(y, where, "y", dev)
+        if y_shape != shape:
+            _refuse(where, "y must have the shape of x")
         sr = 0
         if residual is not None:
-            kr, sr = self._check_rows(residual, where, "residual", dev)
-            _need(kr == ky and residual.shape == x.shape, where, "residual must have the type and shape of y")
+            kr, r_shape, sr = self._check_rows(residual, where, "residual", dev)
+            _need(kr == ky and r_shape == shape, where, "residual must have the type and shape of y")
         d = self._dropout_struct(dropout, where, dev)
         self._raise(self.lib.esm_op_dropout(self.handle, x.data_ptr(), kx, sx, _ptr(residual), sr, y.data_ptr(), ky, sy,
-                                            x.shape[0], x.shape[1], d, _launch_stream(where, stream, dev)),
+                                            shape[0], shape[1], d, _launch_stream(where, stream, dev)),
                     "esm_op_dropout")
         return y
 
@@ -789,11 +791,12 @@ class EsmEncoder:
         row_scale float32 [T]."""
         where = "op_embed"
         T, dev = self._check_ids(where, ids, row_scale)
-        kt, _ = self._check_rows(table, where, "table", dev)
-        ko, so = self._check_rows(out, where, "out", dev)
-        V, cols = table.shape
-        _need(table.is_contiguous(), where, "table must be contiguous")
-        _need(out.shape == (T, cols), where, f"out must be {[T, cols]}")
+        kt, (V, cols), _ = self._check_rows(table, where, "table", dev)
+        ko, shape, so = self._check_rows(out, where, "out", dev)
+        if not table.is_contiguous():
+            _refuse(where, "table must be contiguous")
+        if shape != (T, cols):
+            _refuse(where, f"out must be {[T, cols]}")
         d = self._dropout_struct(dropout, where, dev)
         self._raise(self.lib.esm_op_embed(self.handle, ids.data_ptr(), T, table.data_ptr(), kt, V, cols, float(scale),
                                           _ptr(row_scale), d, out.data_ptr(), ko, so,
@@ -813,12 +816,12 @@ class EsmEncoder:
         id's tokens of scale * row_scale[t] * dropout(d_out[t]); d_out float32 or bf16 [T, cols]."""
         where = "op_embed_backward"
         T, dev = self._check_ids(where, ids, row_scale)
-        kd, sd = self._check_rows(d_out, where, "d_out", dev)
-        _need(isinstance(d_table, torch.Tensor) and d_table.dim() == 2, where, "d_table must be a 2-D tensor")
-        V, cols = d_table.shape
-        _need(V <= STREAM_MAX and cols <= STREAM_MAX, where, "d_table must have at most 2^30 rows and columns")
-        _check_tensor(d_table, where, "d_table", torch.float32, (V, cols), dev)
-        _need(d_out.shape == (T, cols), where, f"d_out must be {[T, cols]}")
+        kd, shape, sd = self._check_rows(d_out, where, "d_out", dev)
+        kt, (V, cols), _ = self._check_rows(d_table, where, "d_table", dev)
+        if kt or not d_table.is_contiguous():
+            _refuse(where, "d_table must be contiguous float32")
+        if shape != (T, cols):
+            _refuse(where, f"d_out must be {[T, cols]}")
         d = self._dropout_struct(dropout, where, dev)
         st = _launch_stream(where, stream, dev)
         if workspace is None:

@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     if (a.gate_rows) bulk_load(to + 2 * t_bytes, static_cast<const T*>(a.gate) + at, t_bytes, bars + stage);
   };
   __syncthreads();
+  grid_dependency_launch();
   if (w == 0 && lane == 0) {
 #pragma unroll
     for (int i = 0; i < kStages; ++i) arrive(first + i * step, i);
@@ -560,6 +561,7 @@ __global__ void __launch_bounds__(512, 1)
     block_norm_bwd_any_kernel(const BlockNormArgs a, int W, int groups, float* __restrict__ partial) {
   extern __shared__ float sums[];          // [kSums][cols]
   __shared__ float red[2][kBwdWarps][8];  // the two latest rows' sums of every warp
+  grid_dependency_launch();
   __shared__ PhiloxKeys keys;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = warp / W, w = warp - group * W;
@@ -788,12 +790,13 @@ __global__ void __launch_bounds__(512, 1)
 }
 
 // The parameters' gradients from the blocks' column sums, in a fixed order: warp w of a block adds blocks
-// w, w + 16, ... of 32 columns, then the warps' sums are added in order.  blockIdx.y: the sums of pre, of post.
+// w, w + 16, ... of 32 columns, then the warps' sums are added in order.  Even blocks: the sums of pre, odd: of post.
 template <typename T>
 __global__ void __launch_bounds__(512) block_norm_sums_kernel(const BlockNormArgs a, const float* __restrict__ partial,
                                                               int blocks) {
   __shared__ float part[2][16][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, post = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, post = blockIdx.x & 1, c = (blockIdx.x >> 1) * 32 + lane;
+  grid_dependency_wait();
   float s0 = 0.f, s1 = 0.f;
   if (c < a.cols) {
 #pragma unroll 4
@@ -880,8 +883,7 @@ cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  block_norm_sums_kernel<T><<<dim3((a.cols + 31) / 32, 2), 512, 0, st>>>(a, partial, s.blocks);
-  return cudaGetLastError();
+  return launch_after(block_norm_sums_kernel<T>, 2 * ((a.cols + 31) / 32), 512, st, a, (const float*)partial, s.blocks);
 }
 
 // W warps to a row of up to 4096 columns.  Registers for 800 threads an SM with bfloat16 blocks (80 each; 16384 x

@@ -14,16 +14,10 @@ namespace {
 // Blocks of eight elements in the order of the rows: a thread takes four of them, 256 apart, and has all its
 // loads on the way before it draws the first bits; the four calls of the generator share its round keys.
 // DENSE: rows follow each other without a gap, so a block's place is its number.
-#ifndef KBLOCKS
-#define KBLOCKS 4
-#endif
-#ifndef KMIN
-#define KMIN 4
-#endif
-constexpr int kBlocks = KBLOCKS;
+constexpr int kBlocks = 4;
 
 template <typename TX, typename TY, bool DENSE>
-__global__ void __launch_bounds__(256, KMIN) dropout_kernel(const DropoutArgs a, const FastDiv per_row, long long total) {
+__global__ void __launch_bounds__(256, 4) dropout_kernel(const DropoutArgs a, const FastDiv per_row, long long total) {
   const PhiloxState ps = philox_state(a.mask);
   const TX* xs = static_cast<const TX*>(a.x);
   const TY* rs = static_cast<const TY*>(a.residual);

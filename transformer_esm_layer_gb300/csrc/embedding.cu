@@ -27,16 +27,10 @@ __device__ __forceinline__ float token_scale(const EmbedArgs& a, int t) {
 
 // Blocks of eight columns in the order of the tokens: a thread takes four of them, 256 apart, and has all its ids
 // and then all its rows on the way before it draws the first bits.  Rows on 16 bytes.
-#ifndef KBLOCKS
-#define KBLOCKS 4
-#endif
-#ifndef KMIN
-#define KMIN 4
-#endif
-constexpr int kBlocks = KBLOCKS;
+constexpr int kBlocks = 1;
 
 template <typename TE, typename TO>
-__global__ void __launch_bounds__(256, KMIN) embed_scaled_kernel(const EmbedArgs a, const FastDiv per_row, long long total) {
+__global__ void __launch_bounds__(256, 8) embed_scaled_kernel(const EmbedArgs a, const FastDiv per_row, long long total) {
   const PhiloxState ps = philox_state(a.mask);
   const long long first = (long long)blockIdx.x * (256 * kBlocks) + threadIdx.x;
   int t[kBlocks], col[kBlocks], id[kBlocks];
@@ -153,6 +147,7 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
 __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThreads)
     embed_sort_kernel(const EmbedArgs a, const SortArgs s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dependency_launch();
   if (blockIdx.x >= kSortBlocks) {
     // (d_table is zeroed in 16-byte steps where it allows them)
     const size_t n = (size_t)a.vocab * a.cols, step = (size_t)(gridDim.x - kSortBlocks) * kSortThreads;
@@ -252,29 +247,21 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
 // Sums of 32 consecutive places of the sorted list and 256 columns by one warp.  An id whose tokens all lie
 // within the piece is written at once; of an id that goes on over the piece's border the piece keeps its part:
 // part[piece][0] for one that began before, part[piece][1] for one that begins here and goes on.
-#ifndef KPIECE
-#define KPIECE 32
-#endif
-#ifndef KAHEAD
-#define KAHEAD 4
-#endif
-#ifndef KMINB
-#define KMINB 3
-#endif
-constexpr int kPiece = KPIECE;
+constexpr int kPiece = 32;
 
 template <typename TO, bool VEC>
-__global__ void __launch_bounds__(256, KMINB)
+__global__ void __launch_bounds__(32, 24)
     embed_grad_pieces_kernel(const EmbedArgs a, const uint2* __restrict__ list, const int* __restrict__ valid,
                              float* __restrict__ part, const FastDiv spans, long long total) {
-  constexpr int kAhead = KAHEAD;  // rows in flight
+  constexpr int kAhead = 4;  // rows in flight
   __shared__ PhiloxKeys keys;
   const PhiloxState ps = philox_state(a.mask);
   philox_keys(ps, &keys);
   __syncthreads();
-  const int lane = threadIdx.x & 31, n = *valid;
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= total) return;
+  grid_dependency_wait();
+  grid_dependency_launch();
+  const int lane = threadIdx.x, n = *valid;
+  const long long i = blockIdx.x;
   const int piece = total <= INT32_MAX ? (int)div_by((uint32_t)i, spans) : (int)(i / spans.d);
   const int c0 = (int)(i - (long long)piece * spans.d) * 256, left = a.cols - c0;
   const int p0 = piece * kPiece, count = min(kPiece, n - p0);
@@ -342,6 +329,7 @@ __global__ void __launch_bounds__(256) embed_grad_join_kernel(const EmbedArgs a,
                                                               const int* __restrict__ valid,
                                                               const float* __restrict__ part) {
   __shared__ uint64_t sums[8][128];
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = *valid;
   const int spans = (a.cols + 255) / 256, pieces = (n + kPiece - 1) / kPiece;
   for (long long i = blockIdx.x; i < (long long)spans * pieces; i += gridDim.x) {
@@ -443,10 +431,13 @@ cudaError_t launch_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaSt
   }
   embed_sort_kernel<<<kSortBlocks + clear, kSortThreads, 0, st>>>(a, s);
   const long long pieces = (a.tokens + kPiece - 1) / kPiece;
-  embed_grad_pieces_kernel<TO, VEC><<<(unsigned)((spans * pieces + 7) / 8), 256, 0, st>>>(a, s.list, s.valid, part, fast_div((uint32_t)spans), spans * pieces);
+  // (each launch may start while the one before it still runs, and waits for it where it needs its results)
+  cudaError_t e = launch_after(embed_grad_pieces_kernel<TO, VEC>, (unsigned)(spans * pieces), 32, st, a, (const uint2*)s.list, (const int*)s.valid, part,
+                               fast_div((uint32_t)spans), spans * pieces);
+  if (e != cudaSuccess) return e;
   const unsigned join = (unsigned)std::min(spans * pieces, (long long)num_sms * 32);
-  embed_grad_join_kernel<VEC><<<join, 256, 0, st>>>(a, s.list, s.valid, part);
-  return cudaGetLastError();
+  return launch_after(embed_grad_join_kernel<VEC>, join, 256, st, a, (const uint2*)s.list, (const int*)s.valid,
+                      (const float*)part);
 }
 
 }  // namespace
