@@ -24,7 +24,8 @@
  *   u = GELU(LN2(x) W1^T + b1); x += u W2^T + b2.   Output: LNf(x) (or x).
  * Readings where the pages are silent: LayerNorm eps from the config (1e-5), biased
  * variance; exact erf GELU; RoPE base from the config (10000), rotate-half pairs
- * (j, j + head_dim/2), positions restart at 0 at every sequence start; no dropout.
+ * (j, j + head_dim/2), positions restart at 0 at every sequence start; no dropout (training:
+ * none unless esm_encoder_set_dropout asks for it).
  *
  * Conventions for every call:
  *   * All device buffers belong to the caller; the library only borrows them for the
@@ -448,170 +449,6 @@ ESM_API esm_status esm_op_gemm_nvfp4(esm_encoder_t* h, esm_epilogue epi, const u
                                      const uint8_t* b_scales, const float* b_scale, const void* bias,
                                      const int32_t* pos_id, void* out, int M, int N, int K, esm_stream_t stream);
 
-/* ---- FP8 delayed-scaling state (ESM_FP8_E4M3 handles) ----
- * Layout, float32: for each layer l and each of the 8 quantised tensors k in the order
- * {x_qkv, w_qkv, x_o, w_o, x_1, w_1, x_2, w_2}: scale[l][k] (num_layers*8 floats), then
- * amax_history[l][k][amax_history_len] (newest first).  n is the number of floats in
- * host_buf and must equal num_layers*8*(1 + amax_history_len).  Initial state: every
- * scale 1, every history entry 0.  get synchronises the device. */
-ESM_API esm_status esm_encoder_get_fp8_state(const esm_encoder_t* h, float* host_buf, size_t n);
-ESM_API esm_status esm_encoder_set_fp8_state(esm_encoder_t* h, const float* host_buf, size_t n);
-
-/* ---- training: a forward that keeps its activations, and the backward pass ----
- * The hotelren.com guide trains the packed model over cu_seqlens (section 3.2, the packed
- * training loop; section 6, the training step with loss.backward()); the mlqm.cn walkthrough
- * describes the same layer stack under training.  The pages do not write the backward
- * out: it is the exact gradient of the forward above (chain rule through the final
- * LayerNorm, every layer in reverse, and the embedding), with bf16 GEMM and attention
- * operands and fp32 accumulation, reductions over tokens in a fixed order.
- * ESM_BF16 handles with hidden <= 4096 only (others: ESM_ERR_UNSUPPORTED).
- *
- * Gradient buffers: device float32, same shapes as the weights ([out, in] for linear
- * maps); the per-layer members point to HOST arrays of num_layers DEVICE pointers.
- * Every buffer is overwritten (not accumulated into); 16-byte aligned. */
-typedef struct {
-  float* emb;                 /* [vocab, hidden]                                 */
-  float* const* ln1_g;
-  float* const* ln1_b;
-  float* const* w_qkv;        /* [3*hidden, hidden]                              */
-  float* const* b_qkv;
-  float* const* w_o;          /* [hidden, hidden]                                */
-  float* const* b_o;
-  float* const* ln2_g;
-  float* const* ln2_b;
-  float* const* w_1;          /* [ffn, hidden]                                   */
-  float* const* b_1;
-  float* const* w_2;          /* [hidden, ffn]                                   */
-  float* const* b_2;
-  float* lnf_g;               /* [hidden] (ignored if final_ln == 0)             */
-  float* lnf_b;
-} esm_grads;
-
-/* Bytes of the training buffer for up to max_tokens tokens: per layer the layer input and
- * mid-layer residual (float32 [T, hidden]), the LayerNorm outputs, q|k|v after RoPE, the
- * attention output (bf16), the attention log-sum-exp (float32 [heads, T]), fc1's
- * pre-activation and GELU output (bf16 [T, ffn]); then the backward's scratch.  About
- * 46 KB per token per layer for ESM-2 650M. */
-ESM_API esm_status esm_encoder_train_buffer_size(const esm_encoder_t* h, int max_tokens, size_t* bytes);
-
-/* The packed forward of esm_encoder_forward (same arguments, same hidden_out in bf16) that
- * also keeps its activations in train_buf (device, 256-byte aligned, at least
- * esm_encoder_train_buffer_size bytes).  total_tokens > 0.  The workspace and train_buf
- * belong to the handle's next esm_encoder_backward: leave both untouched until then (another
- * call of this handle with the same workspace withdraws that backward, which then returns
- * ESM_ERR_INVALID_ARG).
- * Errors as esm_encoder_forward; ESM_ERR_WORKSPACE for a short train_buf. */
-ESM_API esm_status esm_encoder_forward_train(esm_encoder_t* h, const esm_weights* w, const int32_t* token_ids,
-                                             const int32_t* cu_seqlens, int num_seqs, int total_tokens,
-                                             int max_seqlen, void* hidden_out, void* train_buf, size_t train_bytes,
-                                             void* workspace, size_t workspace_bytes, esm_stream_t stream);
-
-/* Gradients of a loss L with respect to every parameter, given d_hidden_out = dL/d(hidden_out)
- * (device float32 [T, hidden], T of the last esm_encoder_forward_train on this handle).
- * train_buf and workspace must be the ones that forward used (ESM_ERR_INVALID_ARG
- * otherwise); weights as in that forward.  grads->emb receives emb_scale times the sum of
- * the embedded rows' gradients per token id. */
-ESM_API esm_status esm_encoder_backward(esm_encoder_t* h, const esm_weights* w, const float* d_hidden_out,
-                                        const esm_grads* grads, void* train_buf, size_t train_bytes,
-                                        void* workspace, size_t workspace_bytes, esm_stream_t stream);
-
-/* Backward hooks (the kernels the backward uses, exposed for parity); bf16 operands,
- * handles of precision ESM_BF16 or ESM_FP8_E4M3.
- * esm_op_gemm_dgrad: out[M, K] = dY[M, N] W with dY device bf16 [M, N] and W device bf16
- *   [N, K] (a weight, [out, in]); out device float32, or bf16 with out_bf16 != 0.
- *   N % 64 == 0, K % 256 == 0, 16-byte aligned pointers.
- * esm_op_gemm_wgrad: dW[N, K] = dY^T X summed over the M rows of dY (bf16 [M, N]) and X
- *   (bf16 [M, K]); dW device float32.  N % 256 == 0, K % 256 == 0, any M.  The workspace
- *   (esm_op_gemm_wgrad_workspace_size bytes, 256-byte aligned; NULL allowed, then the
- *   token reduction is not split) holds split partial products, added in a fixed order. */
-ESM_API esm_status esm_op_gemm_dgrad(esm_encoder_t* h, const void* dY, const void* W, void* out, int out_bf16, int M,
-                                     int N, int K, esm_stream_t stream);
-ESM_API esm_status esm_op_gemm_wgrad_workspace_size(const esm_encoder_t* h, int N, int K, size_t* bytes);
-ESM_API esm_status esm_op_gemm_wgrad(esm_encoder_t* h, const void* dY, const void* X, float* dW, int M, int N, int K,
-                                     void* workspace, size_t workspace_bytes, esm_stream_t stream);
-
-/* LayerNorm backward over rows of x (device float32 [rows, cols], cols % 4 == 0, cols <= 4096): with
- * dy = dL/dy (float32 [rows, cols]) and gamma in the parameter dtype,
- *   dx = dres + dL/dx (dres may be NULL or equal to dx), dgamma = sum_rows dy xhat,
- *   dbeta = sum_rows dy (float32 [cols]).  Workspace: the size query's bytes. */
-ESM_API esm_status esm_op_layernorm_backward_workspace_size(const esm_encoder_t* h, int rows, int cols,
-                                                            size_t* bytes);
-ESM_API esm_status esm_op_layernorm_backward(esm_encoder_t* h, const float* x, const void* gamma, const float* dy,
-                                             const float* dres, float* dx, float* dgamma, float* dbeta, int rows,
-                                             int cols, void* workspace, size_t workspace_bytes,
-                                             esm_stream_t stream);
-
-/* esm_op_attention (bf16, head_dim 64) that also writes lse (device float32 [heads, T],
- * head-major): the natural-log softmax normaliser log sum_s exp(q_t . k_s / 8) of every query
- * row.
- * esm_op_attention_backward: from the same qkv (bf16 [T, 3*hidden], q | k | v as the
- * attention read them), its output o (bf16 [T, hidden]), lse and d_o = dL/do (bf16
- * [T, hidden]), writes dqkv = dL/d(q | k | v) (bf16 [T, 3*hidden]).  Workspace:
- * esm_op_attention_backward_workspace_size bytes (the forward's work list plus float32
- * scratch [heads, T] and [T, hidden]). */
-ESM_API esm_status esm_op_attention_train(esm_encoder_t* h, const void* qkv, const int32_t* cu_seqlens, int num_seqs,
-                                          int total_tokens, int max_seqlen, void* o, float* lse, void* workspace,
-                                          size_t workspace_bytes, esm_stream_t stream);
-ESM_API esm_status esm_op_attention_backward_workspace_size(const esm_encoder_t* h, int total_tokens, int num_seqs,
-                                                            size_t* bytes);
-ESM_API esm_status esm_op_attention_backward(esm_encoder_t* h, const void* qkv, const void* o, const float* lse,
-                                             const void* d_o, const int32_t* cu_seqlens, int num_seqs,
-                                             int total_tokens, int max_seqlen, void* dqkv, void* workspace,
-                                             size_t workspace_bytes, esm_stream_t stream);
-
-/* esm_op_attention_backward with a window (bf16, head_dim 64): dqkv = dL/d(q | k | v) from qkv, o
- * and lse of esm_op_attention_window with the same window, and d_o = dL/do.  qkv, d_o, o and lse
- * must be finite, and dqkv apart from qkv and d_o.  The float32 sums over key tiles behind dq, and
- * only those, are added in no fixed order. */
-ESM_API esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, const void* o, const float* lse,
-                                                    const void* d_o, const int32_t* cu_seqlens, int num_seqs,
-                                                    int total_tokens, int max_seqlen, const esm_attn_window* window,
-                                                    void* dqkv, void* workspace, size_t workspace_bytes,
-                                                    esm_stream_t stream);
-
-/* ---- distillation from a teacher's top logits ----
- * No counterpart on the pages.  For every token, K entries of a teacher's output are given: ids
- * and logits (its K largest, say).  With temperature t, q = softmax(logits / t) over the
- * vocabulary and p = softmax(teacher_logits / t) over the row's usable entries,
- *   token_loss = t^2 sum_k p_k (log p_k - log q_{id_k}),   lse = log sum_v exp(logits_v / t),
- *   d token_loss / d logits_v = t (q_v - sum_{k: id_k = v} p_k).
- * An entry is usable if its id is in [0, vocab) and its logit is not -inf; id -1 marks an unused
- * entry, any other id outside [0, vocab) is unused and latches ESM_ERR_TOKEN_RANGE (see
- * esm_encoder_check).  An id may stand in a row more than once.  A row without a usable entry is
- * not scored: its loss, its lse and its gradient are 0, whatever its logits are.
- * logits: device, float32 (logits_type ESM_FP32) or bfloat16 (ESM_BF16; other types:
- *   ESM_ERR_UNSUPPORTED) [T, vocab], rows logits_stride >= vocab elements apart; T and vocab of up to
- *   ESM_DISTILL_MAX each, vocab >= 1
- * teacher_ids, teacher_logits: device int32 and float32 [T, K], 1 <= K <= ESM_DISTILL_MAX_K
- * temperature: > 0, its square a normal float32 (about 1.1e-19 to 1.8e19)
- * token_loss: device float32 [T]; lse: device float32 [T] or NULL (the backward needs it);
- * loss_sum, count: device float32 and int32 scalars, each may be NULL: the sum of token_loss, in a
- *   fixed order, and the number of scored rows.  The workspace (the size query's bytes, 256-byte
- *   aligned) may be NULL when both are NULL.
- * T == 0 sets loss_sum and count to 0.  Sums are float32 whatever the logits' type. */
-#define ESM_DISTILL_MAX_K 256
-#define ESM_DISTILL_MAX (1 << 30)
-ESM_API esm_status esm_op_distill_loss_workspace_size(const esm_encoder_t* h, int total_tokens, int vocab,
-                                                      size_t* bytes);
-ESM_API esm_status esm_op_distill_loss(esm_encoder_t* h, const void* logits, esm_precision logits_type,
-                                       long long logits_stride, const int32_t* teacher_ids,
-                                       const float* teacher_logits, int K, int total_tokens, int vocab,
-                                       float temperature, float* token_loss, float* lse, float* loss_sum, int* count,
-                                       void* workspace, size_t workspace_bytes, esm_stream_t stream);
-
-/* d_logits = d(sum of token_loss / n) / d logits, n = *loss_count (device int32 scalar: the
- * forward's count, or the global batch's in data-parallel training; with n <= 0 every gradient is
- * 0) or 1 if loss_count is NULL.  lse: of esm_op_distill_loss for the same logits and temperature.
- * d_logits: of the logits' type, rows d_stride >= vocab elements apart; it may be the logits
- * themselves (then with the same stride).  Otherwise no value may be in both; rows of the two may
- * alternate in one buffer if their strides are the same (ESM_ERR_INVALID_ARG where this is broken).  Elements between
- * the rows are left as they are. */
-ESM_API esm_status esm_op_distill_loss_backward(esm_encoder_t* h, const void* logits, esm_precision logits_type,
-                                                long long logits_stride, const int32_t* teacher_ids,
-                                                const float* teacher_logits, int K, int total_tokens, int vocab,
-                                                float temperature, const float* lse, const int* loss_count,
-                                                void* d_logits, long long d_stride, esm_stream_t stream);
-
 /* ---- the residual stream of a training step: dropout, embedding, norms around a block ----
  * No counterpart on the pages, which only name the embedding: what a training step does between its
  * products and its attention.  rows, vocab and token counts of up to ESM_STREAM_MAX each.  float32
@@ -719,6 +556,180 @@ ESM_API esm_status esm_op_block_norm_backward(esm_encoder_t* h, const esm_block_
                                               const void* y, const float* stats, const float* d_x_out, const void* d_h,
                                               float* dx, void* dy, const esm_block_norm_grads* grads, int rows,
                                               int cols, void* workspace, size_t workspace_bytes, esm_stream_t stream);
+
+/* ---- FP8 delayed-scaling state (ESM_FP8_E4M3 handles) ----
+ * Layout, float32: for each layer l and each of the 8 quantised tensors k in the order
+ * {x_qkv, w_qkv, x_o, w_o, x_1, w_1, x_2, w_2}: scale[l][k] (num_layers*8 floats), then
+ * amax_history[l][k][amax_history_len] (newest first).  n is the number of floats in
+ * host_buf and must equal num_layers*8*(1 + amax_history_len).  Initial state: every
+ * scale 1, every history entry 0.  get synchronises the device. */
+ESM_API esm_status esm_encoder_get_fp8_state(const esm_encoder_t* h, float* host_buf, size_t n);
+ESM_API esm_status esm_encoder_set_fp8_state(esm_encoder_t* h, const float* host_buf, size_t n);
+
+/* ---- training: a forward that keeps its activations, and the backward pass ----
+ * The hotelren.com guide trains the packed model over cu_seqlens (section 3.2, the packed
+ * training loop; section 6, the training step with loss.backward()); the mlqm.cn walkthrough
+ * describes the same layer stack under training.  The pages do not write the backward
+ * out: it is the exact gradient of the forward above (chain rule through the final
+ * LayerNorm, every layer in reverse, and the embedding), with bf16 GEMM and attention
+ * operands and fp32 accumulation, reductions over tokens in a fixed order.
+ * ESM_BF16 handles with hidden <= 4096 only (others: ESM_ERR_UNSUPPORTED).
+ *
+ * Gradient buffers: device float32, same shapes as the weights ([out, in] for linear
+ * maps); the per-layer members point to HOST arrays of num_layers DEVICE pointers.
+ * Every buffer is overwritten (not accumulated into); 16-byte aligned. */
+typedef struct {
+  float* emb;                 /* [vocab, hidden]                                 */
+  float* const* ln1_g;
+  float* const* ln1_b;
+  float* const* w_qkv;        /* [3*hidden, hidden]                              */
+  float* const* b_qkv;
+  float* const* w_o;          /* [hidden, hidden]                                */
+  float* const* b_o;
+  float* const* ln2_g;
+  float* const* ln2_b;
+  float* const* w_1;          /* [ffn, hidden]                                   */
+  float* const* b_1;
+  float* const* w_2;          /* [hidden, ffn]                                   */
+  float* const* b_2;
+  float* lnf_g;               /* [hidden] (ignored if final_ln == 0)             */
+  float* lnf_b;
+} esm_grads;
+
+/* Bytes of the training buffer for up to max_tokens tokens: per layer the layer input and
+ * mid-layer residual (float32 [T, hidden]), the LayerNorm outputs, q|k|v after RoPE, the
+ * attention output (bf16), the attention log-sum-exp (float32 [heads, T]), fc1's
+ * pre-activation and GELU output (bf16 [T, ffn]); then the backward's scratch.  About
+ * 46 KB per token per layer for ESM-2 650M. */
+ESM_API esm_status esm_encoder_train_buffer_size(const esm_encoder_t* h, int max_tokens, size_t* bytes);
+
+/* The packed forward of esm_encoder_forward (same arguments, same hidden_out in bf16) that
+ * also keeps its activations in train_buf (device, 256-byte aligned, at least
+ * esm_encoder_train_buffer_size bytes).  total_tokens > 0.  The workspace and train_buf
+ * belong to the handle's next esm_encoder_backward: leave both untouched until then (another
+ * call of this handle with the same workspace withdraws that backward, which then returns
+ * ESM_ERR_INVALID_ARG).
+ * Errors as esm_encoder_forward; ESM_ERR_WORKSPACE for a short train_buf. */
+ESM_API esm_status esm_encoder_forward_train(esm_encoder_t* h, const esm_weights* w, const int32_t* token_ids,
+                                             const int32_t* cu_seqlens, int num_seqs, int total_tokens,
+                                             int max_seqlen, void* hidden_out, void* train_buf, size_t train_bytes,
+                                             void* workspace, size_t workspace_bytes, esm_stream_t stream);
+
+/* Dropout of the training forward, from the next esm_encoder_forward_train on: of the embedded rows, and of each
+ * layer's two block outputs (attention output projection, fc2) before they are added to the residual
+ * stream; NULL, or a p that rounds to none, for no dropout (the default).  With L layers the 2 L + 1 dropouts of a step
+ * have the offsets dropout->offset (embedding), + 1 + 2 l (layer l's attention block) and + 2 + 2 l
+ * (its MLP block): a program adds 2 L + 1 to the base between steps.  The struct is copied; the device memory that rng
+ * points to must stay valid, and unchanged between a forward and its backward, which uses the dropout that its forward
+ * ran with.  A block's output rows are rounded to bf16 before they are dropped.  ESM_BF16 handles (others:
+ * ESM_ERR_UNSUPPORTED); no other call of the handle drops anything. */
+ESM_API esm_status esm_encoder_set_dropout(esm_encoder_t* h, const esm_dropout* dropout);
+
+/* Gradients of a loss L with respect to every parameter, given d_hidden_out = dL/d(hidden_out)
+ * (device float32 [T, hidden], T of the last esm_encoder_forward_train on this handle).
+ * train_buf and workspace must be the ones that forward used (ESM_ERR_INVALID_ARG
+ * otherwise); weights as in that forward.  grads->emb receives emb_scale times the sum of
+ * the embedded rows' gradients per token id. */
+ESM_API esm_status esm_encoder_backward(esm_encoder_t* h, const esm_weights* w, const float* d_hidden_out,
+                                        const esm_grads* grads, void* train_buf, size_t train_bytes,
+                                        void* workspace, size_t workspace_bytes, esm_stream_t stream);
+
+/* Backward hooks (the kernels the backward uses, exposed for parity); bf16 operands,
+ * handles of precision ESM_BF16 or ESM_FP8_E4M3.
+ * esm_op_gemm_dgrad: out[M, K] = dY[M, N] W with dY device bf16 [M, N] and W device bf16
+ *   [N, K] (a weight, [out, in]); out device float32, or bf16 with out_bf16 != 0.
+ *   N % 64 == 0, K % 256 == 0, 16-byte aligned pointers.
+ * esm_op_gemm_wgrad: dW[N, K] = dY^T X summed over the M rows of dY (bf16 [M, N]) and X
+ *   (bf16 [M, K]); dW device float32.  N % 256 == 0, K % 256 == 0, any M.  The workspace
+ *   (esm_op_gemm_wgrad_workspace_size bytes, 256-byte aligned; NULL allowed, then the
+ *   token reduction is not split) holds split partial products, added in a fixed order. */
+ESM_API esm_status esm_op_gemm_dgrad(esm_encoder_t* h, const void* dY, const void* W, void* out, int out_bf16, int M,
+                                     int N, int K, esm_stream_t stream);
+ESM_API esm_status esm_op_gemm_wgrad_workspace_size(const esm_encoder_t* h, int N, int K, size_t* bytes);
+ESM_API esm_status esm_op_gemm_wgrad(esm_encoder_t* h, const void* dY, const void* X, float* dW, int M, int N, int K,
+                                     void* workspace, size_t workspace_bytes, esm_stream_t stream);
+
+/* LayerNorm backward over rows of x (device float32 [rows, cols], cols % 4 == 0, cols <= 4096): with
+ * dy = dL/dy (float32 [rows, cols]) and gamma in the parameter dtype,
+ *   dx = dres + dL/dx (dres may be NULL or equal to dx), dgamma = sum_rows dy xhat,
+ *   dbeta = sum_rows dy (float32 [cols]).  Workspace: the size query's bytes. */
+ESM_API esm_status esm_op_layernorm_backward_workspace_size(const esm_encoder_t* h, int rows, int cols,
+                                                            size_t* bytes);
+ESM_API esm_status esm_op_layernorm_backward(esm_encoder_t* h, const float* x, const void* gamma, const float* dy,
+                                             const float* dres, float* dx, float* dgamma, float* dbeta, int rows,
+                                             int cols, void* workspace, size_t workspace_bytes,
+                                             esm_stream_t stream);
+
+/* esm_op_attention (bf16, head_dim 64) that also writes lse (device float32 [heads, T],
+ * head-major): the natural-log softmax normaliser log sum_s exp(q_t . k_s / 8) of every query
+ * row.
+ * esm_op_attention_backward: from the same qkv (bf16 [T, 3*hidden], q | k | v as the
+ * attention read them), its output o (bf16 [T, hidden]), lse and d_o = dL/do (bf16
+ * [T, hidden]), writes dqkv = dL/d(q | k | v) (bf16 [T, 3*hidden]).  Workspace:
+ * esm_op_attention_backward_workspace_size bytes (the forward's work list plus float32
+ * scratch [heads, T] and [T, hidden]). */
+ESM_API esm_status esm_op_attention_train(esm_encoder_t* h, const void* qkv, const int32_t* cu_seqlens, int num_seqs,
+                                          int total_tokens, int max_seqlen, void* o, float* lse, void* workspace,
+                                          size_t workspace_bytes, esm_stream_t stream);
+ESM_API esm_status esm_op_attention_backward_workspace_size(const esm_encoder_t* h, int total_tokens, int num_seqs,
+                                                            size_t* bytes);
+ESM_API esm_status esm_op_attention_backward(esm_encoder_t* h, const void* qkv, const void* o, const float* lse,
+                                             const void* d_o, const int32_t* cu_seqlens, int num_seqs,
+                                             int total_tokens, int max_seqlen, void* dqkv, void* workspace,
+                                             size_t workspace_bytes, esm_stream_t stream);
+
+/* esm_op_attention_backward with a window (bf16, head_dim 64): dqkv = dL/d(q | k | v) from qkv, o
+ * and lse of esm_op_attention_window with the same window, and d_o = dL/do.  qkv, d_o, o and lse
+ * must be finite, and dqkv apart from qkv and d_o.  The float32 sums over key tiles behind dq, and
+ * only those, are added in no fixed order. */
+ESM_API esm_status esm_op_attention_window_backward(esm_encoder_t* h, const void* qkv, const void* o, const float* lse,
+                                                    const void* d_o, const int32_t* cu_seqlens, int num_seqs,
+                                                    int total_tokens, int max_seqlen, const esm_attn_window* window,
+                                                    void* dqkv, void* workspace, size_t workspace_bytes,
+                                                    esm_stream_t stream);
+
+/* ---- distillation from a teacher's top logits ----
+ * No counterpart on the pages.  For every token, K entries of a teacher's output are given: ids
+ * and logits (its K largest, say).  With temperature t, q = softmax(logits / t) over the
+ * vocabulary and p = softmax(teacher_logits / t) over the row's usable entries,
+ *   token_loss = t^2 sum_k p_k (log p_k - log q_{id_k}),   lse = log sum_v exp(logits_v / t),
+ *   d token_loss / d logits_v = t (q_v - sum_{k: id_k = v} p_k).
+ * An entry is usable if its id is in [0, vocab) and its logit is not -inf; id -1 marks an unused
+ * entry, any other id outside [0, vocab) is unused and latches ESM_ERR_TOKEN_RANGE (see
+ * esm_encoder_check).  An id may stand in a row more than once.  A row without a usable entry is
+ * not scored: its loss, its lse and its gradient are 0, whatever its logits are.
+ * logits: device, float32 (logits_type ESM_FP32) or bfloat16 (ESM_BF16; other types:
+ *   ESM_ERR_UNSUPPORTED) [T, vocab], rows logits_stride >= vocab elements apart; T and vocab of up to
+ *   ESM_DISTILL_MAX each, vocab >= 1
+ * teacher_ids, teacher_logits: device int32 and float32 [T, K], 1 <= K <= ESM_DISTILL_MAX_K
+ * temperature: > 0, its square a normal float32 (about 1.1e-19 to 1.8e19)
+ * token_loss: device float32 [T]; lse: device float32 [T] or NULL (the backward needs it);
+ * loss_sum, count: device float32 and int32 scalars, each may be NULL: the sum of token_loss, in a
+ *   fixed order, and the number of scored rows.  The workspace (the size query's bytes, 256-byte
+ *   aligned) may be NULL when both are NULL.
+ * T == 0 sets loss_sum and count to 0.  Sums are float32 whatever the logits' type. */
+#define ESM_DISTILL_MAX_K 256
+#define ESM_DISTILL_MAX (1 << 30)
+ESM_API esm_status esm_op_distill_loss_workspace_size(const esm_encoder_t* h, int total_tokens, int vocab,
+                                                      size_t* bytes);
+ESM_API esm_status esm_op_distill_loss(esm_encoder_t* h, const void* logits, esm_precision logits_type,
+                                       long long logits_stride, const int32_t* teacher_ids,
+                                       const float* teacher_logits, int K, int total_tokens, int vocab,
+                                       float temperature, float* token_loss, float* lse, float* loss_sum, int* count,
+                                       void* workspace, size_t workspace_bytes, esm_stream_t stream);
+
+/* d_logits = d(sum of token_loss / n) / d logits, n = *loss_count (device int32 scalar: the
+ * forward's count, or the global batch's in data-parallel training; with n <= 0 every gradient is
+ * 0) or 1 if loss_count is NULL.  lse: of esm_op_distill_loss for the same logits and temperature.
+ * d_logits: of the logits' type, rows d_stride >= vocab elements apart; it may be the logits
+ * themselves (then with the same stride).  Otherwise no value may be in both; rows of the two may
+ * alternate in one buffer if their strides are the same (ESM_ERR_INVALID_ARG where this is broken).  Elements between
+ * the rows are left as they are. */
+ESM_API esm_status esm_op_distill_loss_backward(esm_encoder_t* h, const void* logits, esm_precision logits_type,
+                                                long long logits_stride, const int32_t* teacher_ids,
+                                                const float* teacher_logits, int K, int total_tokens, int vocab,
+                                                float temperature, const float* lse, const int* loss_count,
+                                                void* d_logits, long long d_stride, esm_stream_t stream);
 
 /* ---- measurement hooks ----
  * Kernel classes of the forward: 0 QKV GEMM (+bias, RoPE), 1 attention, 2 output-projection

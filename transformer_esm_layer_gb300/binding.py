@@ -51,7 +51,7 @@ EXPORTS = ("esm_encoder_create", "esm_encoder_destroy", "esm_encoder_workspace_s
            "esm_op_attention_window_backward", "esm_op_distill_loss_workspace_size", "esm_op_distill_loss",
            "esm_op_distill_loss_backward", "esm_encoder_lm_head_distill_backward", "esm_op_dropout", "esm_op_embed",
            "esm_op_embed_backward_workspace_size", "esm_op_embed_backward", "esm_op_block_norm",
-           "esm_op_block_norm_backward_workspace_size", "esm_op_block_norm_backward")
+           "esm_op_block_norm_backward_workspace_size", "esm_op_block_norm_backward", "esm_encoder_set_dropout")
 STREAM_MAX = 1 << 30  # ESM_STREAM_MAX
 DISTILL_MAX = 1 << 30  # ESM_DISTILL_MAX
 PROFILE_CLASSES = ("gemm_qkv", "attention", "gemm_oproj", "gemm_fc1", "gemm_fc2", "layernorm", "other",
@@ -195,6 +195,7 @@ def load_library() -> ctypes.CDLL:
         "esm_op_distill_loss_workspace_size": (i32, [vp, i32, i32, ctypes.POINTER(sz)]),
         "esm_op_distill_loss": (i32, [vp, vp, i32, i64, vp, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp, sz, vp]),
         "esm_op_distill_loss_backward": (i32, [vp, vp, i32, i64, vp, vp, i32, i32, i32, f32, vp, vp, vp, i64, vp]),
+        "esm_encoder_set_dropout": (i32, [vp, _PD]),
         "esm_op_dropout": (i32, [vp, vp, i32, i64, vp, i64, vp, i32, i64, i32, i32, _PD, vp]),
         "esm_op_embed": (i32, [vp, vp, i32, vp, i32, i32, i32, f32, vp, _PD, vp, i32, i64, vp]),
         "esm_op_embed_backward_workspace_size": (i32, [vp, i32, i32, i32, ctypes.POINTER(sz)]),
@@ -941,6 +942,15 @@ class EsmEncoder:
                     "esm_encoder_lm_head")
 
     # ------------------------------------------------------------------ training
+    def set_dropout(self, dropout: Optional[Dropout] = None):
+        """esm_encoder_set_dropout: dropout of the embedding and of every block's output in forward_train
+        (and its backward); None for none.  A step uses 2 * num_layers + 1 offsets from dropout's on."""
+        where = "set_dropout"
+        _need(dropout is None or isinstance(dropout, Dropout), where, "dropout must be a Dropout or None")
+        self._raise(self.lib.esm_encoder_set_dropout(self.handle, None if dropout is None else dropout.struct),
+                    "esm_encoder_set_dropout")
+        self._dropout = dropout  # keeps rng's memory
+
     def train_buffer(self, max_tokens: int, device="cuda"):
         n = ctypes.c_size_t()
         self._raise(self.lib.esm_encoder_train_buffer_size(self.handle, max_tokens, ctypes.byref(n)),
@@ -959,6 +969,7 @@ class EsmEncoder:
                                                        _ptr(train_buf), train_buf.numel(), _ptr(workspace),
                                                        workspace.numel(), _stream_ptr(stream)),
                     "esm_encoder_forward_train")
+        self._train_dropout = getattr(self, "_dropout", None)  # the backward reads its rng
         return out
 
     def backward(self, weights: DeviceWeights, d_out, grads: "DeviceGrads", train_buf, workspace, stream=None):

@@ -73,6 +73,8 @@ struct esm_encoder {
   std::vector<uint8_t> layer_fp8;  // per layer: 1 = E4M3 GEMMs, 2 = NVFP4 GEMMs (FP8 handles only)
   AttnWindow window = kFullWindow;        // attention window of every layer
   AttnWindow train_window = kFullWindow;  // the window the last training forward ran with
+  esm_dropout dropout{};                  // of the training forward (rng NULL: none)
+  esm_dropout train_dropout{};            // the one the last training forward ran with
   float* d_fp8 = nullptr;        // scales [L*8] | history [L*8*len] | amax [L*8]
   float* d_fp4 = nullptr;        // NVFP4 tensor scales of the last forward [L*8] | amax [L*8]
   size_t fp8_floats = 0;
@@ -627,6 +629,33 @@ bool config_ok(const esm_config* c) {
 // ------------------------------------------------------------------ training (backward)
 // Buffer of a training forward: every activation the backward reads, per layer, plus the
 // backward's scratch.  Per-layer tensors are slabs of layers (x: layers + 1) of one size.
+// Above this vocabulary the embedding's gradient is summed from sorted tokens; up to it, without dropout, by a
+// table of sums in shared memory (128 columns of every id: 48 KB).
+constexpr int kTableVocab = 96;
+
+// The mask of a dropout that may be NULL; false if it is malformed.
+bool drop_mask(const esm_dropout* d, DropMask* m) {
+  *m = DropMask{nullptr, 0, 0, 1.f};
+  if (!d) return true;
+  if (!(d->p >= 0.0 && d->p <= 1.0) || !d->rng || !aligned(d->rng, 8)) return false;
+  const unsigned n = (unsigned)(d->p * 65536.0 + 0.5);
+  if (n == 0) return true;
+  m->rng = reinterpret_cast<const unsigned long long*>(d->rng);
+  m->offset = (unsigned long long)d->offset;
+  m->threshold = n;
+  m->scale = n >= 65536 ? 0.f : (float)(65536.0 / (65536 - n));
+  return true;
+}
+
+// The dropout of one place of an encoder's training step: 0 the embedding, 1 + 2 l layer l's attention block,
+// 2 + 2 l its MLP block.
+DropMask drop_site(const esm_dropout& d, int site) {
+  DropMask m;
+  drop_mask(d.rng ? &d : nullptr, &m);
+  m.offset += (unsigned long long)site;
+  return m;
+}
+
 struct TrainLayout {
   size_t tok, x, xmid, y1, qkv, o, lse, y2, z, u;                        // bases
   size_t sx, sy, sqkv, slse, sz;                                         // slab strides
@@ -673,7 +702,8 @@ TrainLayout train_layout(const esm_config& c, int Tm, const AttnWindow& win) {
   L.partial = take(4 * bwd_partial_floats((int)T, (int)widest));
   L.split_floats = (size_t)kMaxKSplit * std::max(f * d, 3 * d * d);
   L.split = take(4 * L.split_floats);
-  L.embp = take(4 * emb_bwd_partial_floats((int)T, c.vocab, (int)d));
+  const size_t sorted = embed_grad_workspace_bytes((int)T, c.vocab, (int)d);
+  L.embp = take(c.vocab > kTableVocab ? sorted : std::max(sorted, 4 * emb_bwd_partial_floats((int)T, c.vocab, (int)d)));
   L.total = off;
   return L;
 }
@@ -765,12 +795,52 @@ esm_status train_forward_impl(esm_encoder* h, const esm_weights* w, const int32_
   if (cudaMemsetAsync(pb.seg_id, 0, 4 * (size_t)T, st) != cudaSuccess) return ESM_ERR_CUDA;
   if (cudaMemcpyAsync(tb + R.tok, tok, 4 * (size_t)T, cudaMemcpyDeviceToDevice, st) != cudaSuccess) return ESM_ERR_CUDA;
   const int d = c.hidden, f = c.ffn;
+  const bool drop = h->dropout.rng != nullptr;
   {
     ProfScope _ps(h, P_OTHER, st, 3);
     launch_pack_index(cu, B, T, max_seqlen, c.max_positions, pb, h->d_err, st);
     launch_attn_worklist(B, L.max_items, kAttnQTileTc, pb, st);
-    launch_embed(tok, T, w->emb, false, c.vocab, d, c.emb_scale, reinterpret_cast<float*>(tb + R.x), h->d_err, st);
+    if (drop) {
+      EmbedArgs e{};
+      e.ids = tok;
+      e.table = w->emb;
+      e.table_bf16 = true;
+      e.out = tb + R.x;
+      e.out_stride = d;
+      e.tokens = T;
+      e.vocab = c.vocab;
+      e.cols = d;
+      e.scale = c.emb_scale;
+      e.mask = drop_site(h->dropout, 0);
+      e.err = h->d_err;
+      if (launch_embed_scaled(e, st) != cudaSuccess) return ESM_ERR_CUDA;
+    } else {
+      launch_embed(tok, T, w->emb, false, c.vocab, d, c.emb_scale, reinterpret_cast<float*>(tb + R.x), h->d_err, st);
+    }
   }
+  // With dropout, a block's last product leaves bf16 rows (in the workspace), and one pass drops them, adds them
+  // to the residual stream and takes the LayerNorm that follows (gamma NULL: none).
+  uint8_t* rows = static_cast<uint8_t*>(ws) + L.y;
+  auto add_block = [&](int site, const void* A, const void* W, const void* bias, int K, int cls, const float* from,
+                       float* to, const void* gamma, const void* beta, void* normed) -> esm_status {
+    const esm_status e = run_gemm(h, cls, ESM_EPI_QKV_ROPE, A, W, bias, rows, nullptr, T, d, K, false, Act::BF16, nullptr,
+                                  nullptr, nullptr, nullptr, st, 0);
+    if (e != ESM_OK) return e;
+    BlockNormArgs n{};
+    n.eps = c.ln_eps;
+    n.residual_scale = 1.f;
+    n.pre_gamma = gamma;
+    n.pre_beta = beta;
+    n.mask = drop_site(h->dropout, site);
+    n.rows = T;
+    n.cols = d;
+    n.y = rows;
+    n.x = from;
+    n.x_out = to;
+    n.h = normed;
+    ProfScope _ps(h, P_LN, st, 1);
+    return cuda_status(launch_block_norm(n, true, h->num_sms, st));
+  };
   for (int l = 0; l < c.num_layers; ++l) {
     float* x = reinterpret_cast<float*>(tb + R.x + R.sx * l);
     float* xmid = reinterpret_cast<float*>(tb + R.xmid + R.sx * l);
@@ -782,9 +852,10 @@ esm_status train_forward_impl(esm_encoder* h, const esm_weights* w, const int32_
     void* y2 = tb + R.y2 + R.sy * l;
     void* z = tb + R.z + R.sz * l;
     void* u = tb + R.u + R.sz * l;
-    PROF(h, P_LN, st, 1,
-         launch_layernorm(x, w->ln1_g[l], w->ln1_b[l], false, y1, Act::BF16, T, d, c.ln_eps, nullptr, nullptr, nullptr,
-                          nullptr, nullptr, st));
+    if (l == 0 || !drop)
+      PROF(h, P_LN, st, 1,
+           launch_layernorm(x, w->ln1_g[l], w->ln1_b[l], false, y1, Act::BF16, T, d, c.ln_eps, nullptr, nullptr, nullptr,
+                            nullptr, nullptr, st));
     s = run_gemm(h, P_QKV, ESM_EPI_QKV_ROPE, y1, w->w_qkv[l], w->b_qkv[l], qkv, pb.pos_id, T, 3 * d, d, false,
                  Act::BF16, nullptr, nullptr, nullptr, nullptr, st);
     if (s != ESM_OK) return s;
@@ -793,22 +864,37 @@ esm_status train_forward_impl(esm_encoder* h, const esm_weights* w, const int32_
       if ((s = run_attention(h, h->window, qkv, o, Act::BF16, T, L.max_items, pb, nullptr, nullptr, st, lse)) != ESM_OK)
         return s;
     }
-    s = run_gemm(h, P_OPROJ, ESM_EPI_RESIDUAL, o, w->w_o[l], w->b_o[l], xmid, nullptr, T, d, d, false, Act::F32,
-                 nullptr, nullptr, nullptr, nullptr, st, -1, x);
-    if (s != ESM_OK) return s;
-    PROF(h, P_LN, st, 1,
-         launch_layernorm(xmid, w->ln2_g[l], w->ln2_b[l], false, y2, Act::BF16, T, d, c.ln_eps, nullptr, nullptr,
-                          nullptr, nullptr, nullptr, st));
+    if (drop) {
+      s = add_block(1 + 2 * l, o, w->w_o[l], w->b_o[l], d, P_OPROJ, x, xmid, w->ln2_g[l], w->ln2_b[l], y2);
+      if (s != ESM_OK) return s;
+    } else {
+      s = run_gemm(h, P_OPROJ, ESM_EPI_RESIDUAL, o, w->w_o[l], w->b_o[l], xmid, nullptr, T, d, d, false, Act::F32,
+                   nullptr, nullptr, nullptr, nullptr, st, -1, x);
+      if (s != ESM_OK) return s;
+      PROF(h, P_LN, st, 1,
+           launch_layernorm(xmid, w->ln2_g[l], w->ln2_b[l], false, y2, Act::BF16, T, d, c.ln_eps, nullptr, nullptr,
+                            nullptr, nullptr, nullptr, st));
+    }
     // fc1: u = GELU(z) feeds fc2; the epilogue also keeps the pre-activation z for GELU'(z)
     s = run_gemm(h, P_FC1, ESM_EPI_GELU, y2, w->w_1[l], w->b_1[l], u, nullptr, T, f, d, false, Act::BF16, nullptr,
                  nullptr, nullptr, nullptr, st, -1, nullptr, z);
     if (s != ESM_OK) return s;
-    s = run_gemm(h, P_FC2, ESM_EPI_RESIDUAL, u, w->w_2[l], w->b_2[l], xnext, nullptr, T, d, f, false, Act::F32, nullptr,
-                 nullptr, nullptr, nullptr, st, -1, xmid);
+    if (drop) {
+      const bool last = l + 1 == c.num_layers;
+      const void* gamma = !last ? w->ln1_g[l + 1] : c.final_ln ? w->lnf_g : nullptr;
+      const void* beta = !last ? w->ln1_b[l + 1] : c.final_ln ? w->lnf_b : nullptr;
+      s = add_block(2 + 2 * l, u, w->w_2[l], w->b_2[l], f, P_FC2, xmid, xnext, gamma, beta,
+                    !last ? tb + R.y1 + R.sy * (l + 1) : c.final_ln ? out : nullptr);
+    } else {
+      s = run_gemm(h, P_FC2, ESM_EPI_RESIDUAL, u, w->w_2[l], w->b_2[l], xnext, nullptr, T, d, f, false, Act::F32, nullptr,
+                   nullptr, nullptr, nullptr, st, -1, xmid);
+    }
     if (s != ESM_OK) return s;
   }
   const float* xl = reinterpret_cast<const float*>(tb + R.x + R.sx * c.num_layers);
-  if (c.final_ln)
+  if (c.final_ln && drop && c.num_layers > 0)
+    ;  // (the last block's pass took it)
+  else if (c.final_ln)
     PROF(h, P_LN, st, 1,
          launch_layernorm(xl, w->lnf_g, w->lnf_b, false, out, Act::BF16, T, d, c.ln_eps, nullptr, nullptr, nullptr,
                           nullptr, nullptr, st));
@@ -818,6 +904,7 @@ esm_status train_forward_impl(esm_encoder* h, const esm_weights* w, const int32_
   h->train_B = B;
   h->train_items = L.max_items;
   h->train_window = h->window;
+  h->train_dropout = h->dropout;
   h->train_buf = train;
   h->train_ws = ws;
   return cuda_status(cudaGetLastError());
@@ -852,6 +939,26 @@ esm_status backward_impl(esm_encoder* h, const esm_weights* w, const float* d_ou
   } else if (cudaMemcpyAsync(dx, d_out, 4 * (size_t)T * d, cudaMemcpyDeviceToDevice, st) != cudaSuccess) {
     return ESM_ERR_CUDA;
   }
+  // The gradient of a block's output rows, as bf16 in dxb: dx, or dropped like the rows; and its bias's.
+  const bool drop = h->train_dropout.rng != nullptr;
+  auto block_rows = [&](int site, float* d_bias) -> esm_status {
+    if (!drop) {
+      PROF(h, P_OTHER, st, 2, launch_colsum(dx, false, T, d, d_bias, partial, dxb, st));
+      return ESM_OK;
+    }
+    DropoutArgs a{};
+    a.x = dx;
+    a.y = dxb;
+    a.y_bf16 = true;
+    a.x_stride = a.y_stride = d;
+    a.rows = T;
+    a.cols = d;
+    a.mask = drop_site(h->train_dropout, site);
+    ProfScope _ps(h, P_OTHER, st, 3);
+    if (launch_dropout(a, st) != cudaSuccess) return ESM_ERR_CUDA;
+    launch_colsum(dxb, true, T, d, d_bias, partial, nullptr, st);
+    return ESM_OK;
+  };
   for (int l = c.num_layers - 1; l >= 0; --l) {
     const float* x = reinterpret_cast<const float*>(tb + R.x + R.sx * l);
     const float* xmid = reinterpret_cast<const float*>(tb + R.xmid + R.sx * l);
@@ -863,7 +970,7 @@ esm_status backward_impl(esm_encoder* h, const esm_weights* w, const float* d_ou
     const void* z = tb + R.z + R.sz * l;
     const void* u = tb + R.u + R.sz * l;
     // ---- MLP block: x_{l+1} = xmid + GELU(LN2(xmid) W1^T + b1) W2^T + b2
-    PROF(h, P_OTHER, st, 2, launch_colsum(dx, false, T, d, g->b_2[l], partial, dxb, st));
+    if ((s = block_rows(2 + 2 * l, g->b_2[l])) != ESM_OK) return s;
     if ((s = run_wgrad(h, dxb, u, g->w_2[l], T, d, f, split, R.split_floats, st)) != ESM_OK) return s;
     // dz = (dx W2) * GELU'(z), in the input-gradient GEMM's epilogue
     if ((s = run_dgrad(h, dxb, w->w_2[l], dz, true, T, d, f, st, z)) != ESM_OK) return s;
@@ -874,7 +981,7 @@ esm_status backward_impl(esm_encoder* h, const esm_weights* w, const float* d_ou
          launch_ln_bwd(xmid, w->ln2_g[l], false, dy, dx, dx, g->ln2_g[l], g->ln2_b[l], partial, T, d, c.ln_eps,
                        st));
     // ---- attention block: xmid = x + Attn(LN1(x)) Wo^T + bo
-    PROF(h, P_OTHER, st, 2, launch_colsum(dx, false, T, d, g->b_o[l], partial, dxb, st));
+    if ((s = block_rows(1 + 2 * l, g->b_o[l])) != ESM_OK) return s;
     if ((s = run_wgrad(h, dxb, o, g->w_o[l], T, d, d, split, R.split_floats, st)) != ESM_OK) return s;
     if ((s = run_dgrad(h, dxb, w->w_o[l], dob, true, T, d, d, st)) != ESM_OK) return s;
     {
@@ -900,8 +1007,23 @@ esm_status backward_impl(esm_encoder* h, const esm_weights* w, const float* d_ou
     PROF(h, P_LN, st, 4,
          launch_ln_bwd(x, w->ln1_g[l], false, dy, dx, dx, g->ln1_g[l], g->ln1_b[l], partial, T, d, c.ln_eps, st));
   }
-  PROF(h, P_OTHER, st, 2,
-       launch_emb_bwd(dx, reinterpret_cast<const int32_t*>(tb + R.tok), T, d, c.vocab, c.emb_scale, embp, g->emb, st));
+  const int32_t* tok = reinterpret_cast<const int32_t*>(tb + R.tok);
+  if (drop || c.vocab > kTableVocab) {
+    EmbedArgs e{};
+    e.ids = tok;
+    e.out = dx;
+    e.out_stride = d;
+    e.d_table = g->emb;
+    e.tokens = T;
+    e.vocab = c.vocab;
+    e.cols = d;
+    e.scale = c.emb_scale;
+    e.mask = drop_site(h->train_dropout, 0);
+    e.err = h->d_err;
+    ProfScope _ps(h, P_OTHER, st, 3);
+    return cuda_status(launch_embed_grad(e, embp, h->num_sms, st));
+  }
+  PROF(h, P_OTHER, st, 2, launch_emb_bwd(dx, tok, T, d, c.vocab, c.emb_scale, embp, g->emb, st));
   return cuda_status(cudaGetLastError());
 }
 
@@ -1050,6 +1172,14 @@ esm_status esm_encoder_set_attention_window(esm_encoder_t* h, const esm_attn_win
   AttnWindow w = kFullWindow;
   if (window && !canonical_window(h, window, &w)) return ESM_ERR_INVALID_ARG;
   h->window = w;
+  return ESM_OK;
+}
+
+esm_status esm_encoder_set_dropout(esm_encoder_t* h, const esm_dropout* dropout) {
+  DropMask m;
+  if (!h || !drop_mask(dropout, &m)) return ESM_ERR_INVALID_ARG;
+  if (dropout && h->cfg.precision != ESM_BF16) return ESM_ERR_UNSUPPORTED;
+  h->dropout = m.rng ? *dropout : esm_dropout{};
   return ESM_OK;
 }
 
@@ -1808,20 +1938,6 @@ static bool apart(const Rows& a, const void* p, size_t n) { return !p || disjoin
 static bool stream_size(int n) { return n >= 0 && n <= ESM_STREAM_MAX; }
 static bool stream_type(esm_precision t) { return t == ESM_FP32 || t == ESM_BF16; }
 static int type_bytes(esm_precision t) { return t == ESM_FP32 ? 4 : 2; }
-
-// The mask of a dropout that may be NULL; false if it is malformed.
-static bool drop_mask(const esm_dropout* d, DropMask* m) {
-  *m = DropMask{nullptr, 0, 0, 1.f};
-  if (!d) return true;
-  if (!(d->p >= 0.0 && d->p <= 1.0) || !d->rng || !aligned(d->rng, 8)) return false;
-  const unsigned n = (unsigned)(d->p * 65536.0 + 0.5);
-  if (n == 0) return true;
-  m->rng = reinterpret_cast<const unsigned long long*>(d->rng);
-  m->offset = (unsigned long long)d->offset;
-  m->threshold = n;
-  m->scale = n >= 65536 ? 0.f : (float)(65536.0 / (65536 - n));
-  return true;
-}
 
 esm_status esm_op_dropout(esm_encoder_t* h, const void* x, esm_precision x_type, long long x_stride,
                           const void* residual, long long residual_stride, void* y, esm_precision y_type,
