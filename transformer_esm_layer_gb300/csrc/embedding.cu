@@ -25,40 +25,30 @@ __device__ __forceinline__ float token_scale(const EmbedArgs& a, int t) {
   return a.row_scale ? a.scale * __ldg(a.row_scale + t) : a.scale;
 }
 
-// Blocks of eight columns in the order of the tokens: a thread takes four of them, 256 apart, and has all its ids
-// and then all its rows on the way before it draws the first bits.  Rows on 16 bytes.
-constexpr int kBlocks = 1;
-
+// Blocks of eight columns in the order of the tokens, one to a thread: 64 warps an SM hide the way from the id to
+// the row (four blocks to a thread and half as many warps took 29 us where this takes 25).  Rows on 16 bytes.
 template <typename TE, typename TO>
 __global__ void __launch_bounds__(256, 8) embed_scaled_kernel(const EmbedArgs a, const FastDiv per_row, long long total) {
-  const PhiloxState ps = philox_state(a.mask);
-  const long long first = (long long)blockIdx.x * (256 * kBlocks) + threadIdx.x;
-  int t[kBlocks], col[kBlocks], id[kBlocks];
-  float f[kBlocks];
+  const long long b = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (b >= total) return;
+  const int t = total <= INT32_MAX ? (int)div_by((uint32_t)b, per_row) : (int)(b / per_row.d);
+  const int col = (int)(b - (long long)t * per_row.d) * 8, left = a.cols - col;
+  const int id = checked_id(a, t, col == 0);
+  Raw8<TE> x;
+  if (id >= 0) x.load(static_cast<const TE*>(a.table) + (long long)id * a.cols + col, left);
+  const float f = token_scale(a, t) * a.mask.scale;
+  Pairs v;
+  fill(v, 0.f);
+  if (id >= 0) {
+    x.get(v);
 #pragma unroll
-  for (int j = 0; j < kBlocks; ++j) {
-    const long long b = first + j * 256;
-    t[j] = total <= INT32_MAX ? (int)div_by((uint32_t)min(b, total), per_row) : (int)(b / per_row.d);
-    col[j] = (int)(b - (long long)t[j] * per_row.d) * 8;
-    id[j] = b < total ? checked_id(a, t[j], col[j] == 0) : -1;
-    f[j] = b < total ? token_scale(a, t[j]) * a.mask.scale : 0.f;
+    for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], f2_both(f));
+    if (a.mask.rng) {
+      const PhiloxState ps = philox_state(a.mask);
+      keep(drop_words(a.mask, ps, (unsigned long long)b), ps, v);
+    }
   }
-  Raw8<TE> x[kBlocks];
-#pragma unroll
-  for (int j = 0; j < kBlocks; ++j)
-    if (id[j] >= 0) x[j].load(static_cast<const TE*>(a.table) + (long long)id[j] * a.cols + col[j], a.cols - col[j]);
-#pragma unroll
-  for (int j = 0; j < kBlocks; ++j) {
-    const uint4 w = drop_words(a.mask, ps, (unsigned long long)(first + j * 256));
-    Pairs v;
-    x[j].get(v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], f2_both(f[j]));
-    if (id[j] < 0) fill(v, 0.f);
-    keep(w, ps, v);
-    if (first + j * 256 < total)
-      span_store<true>(static_cast<TO*>(a.out) + (long long)t[j] * a.out_stride + col[j], a.cols - col[j], 0, v);
-  }
+  span_store<true>(static_cast<TO*>(a.out) + (long long)t * a.out_stride + col, left, 0, v);
 }
 
 // Rows off 16-byte boundaries: one warp per 256 columns of a token.
@@ -87,8 +77,10 @@ __global__ void __launch_bounds__(256) embed_rows_kernel(const EmbedArgs a, cons
 template <bool VEC>
 __device__ __forceinline__ void add_token(const EmbedArgs& a, const PhiloxState& ps, const PhiloxKeys* keys, int t, int c0,
                                           int lane, float f, Pairs& g, Pairs& acc) {
-  const unsigned long long b = (unsigned long long)t * ((a.cols + 7) / 8) + c0 / 8 + lane;
-  keep(span_words<VEC>(a.mask, drop_words(a.mask, ps, keys, b), lane), ps, g);
+  if (a.mask.rng) {
+    const unsigned long long b = (unsigned long long)t * ((a.cols + 7) / 8) + c0 / 8 + lane;
+    keep(span_words<VEC>(a.mask, drop_words(a.mask, ps, keys, b), lane), ps, g);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] = f2_fma(g[i], f2_both(f), acc[i]);
 }
@@ -173,17 +165,29 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
     const int end = (int)min((long long)n, begin + stretch);
     for (int d = lane; d < bins; d += 32) mine[d] = 0;
     __syncwarp();
-    auto item = [&](int i) -> uint2 {  // an id of -1: none
+    auto item = [&](long long i) -> uint2 {  // an id of -1: none
       if (i >= end) return make_uint2(0xffffffffu, 0);
       if (pass) return __ldcg(src + i);
-      return make_uint2((uint32_t)checked_id(a, i, true), (uint32_t)i);
+      return make_uint2((uint32_t)checked_id(a, (int)i, true), (uint32_t)i);
     };
-    for (long long i0 = begin; i0 < end; i0 += 32) {
-      const uint2 v = item((int)i0 + lane);
-      const int d = v.x == 0xffffffffu ? kBins : (int)(v.x >> shift) & (bins - 1);
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+    // (the first two steps' items are kept for the second time round)
+    uint2 kept[2];
+    uint32_t kept_peers[2];
+    auto digit = [&](const uint2& v) { return v.x == 0xffffffffu ? kBins : (int)(v.x >> shift) & (bins - 1); };
+    auto count = [&](int d, uint32_t peers) {
       if (d < kBins && lane == __ffs(peers) - 1) mine[d] += __popc(peers);
       __syncwarp();
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) kept[i] = item(begin + 32 * i + lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      kept_peers[i] = __match_any_sync(0xffffffffu, digit(kept[i]));
+      count(digit(kept[i]), kept_peers[i]);
+    }
+    for (long long i0 = begin + 64; i0 < end; i0 += 32) {
+      const int d = digit(item(i0 + lane));
+      count(d, __match_any_sync(0xffffffffu, d));
     }
     __syncthreads();
     // counts of the warps before, and the block's: a warp per digit, a lane per warp's count
@@ -226,20 +230,26 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
     }
     if (tid < bins) start[tid] = lower + incl - total + before;
     __syncthreads();
-    for (long long i0 = begin; i0 < end; i0 += 32) {
-      const uint2 v = item((int)i0 + lane);
-      const int d = v.x == 0xffffffffu ? kBins : (int)(v.x >> shift) & (bins - 1);
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
-      const int ahead = __popc(peers & ((1u << lane) - 1));
+    const bool last = pass == s.passes - 1;
+    if (last) cluster_arrive();  // (this block has read the others' counts)
+    auto place = [&](const uint2& v, uint32_t peers) {
+      const int d = digit(v), ahead = __popc(peers & ((1u << lane) - 1));
       if (d < kBins) dst[start[d] + mine[d] + ahead] = v;
       __syncwarp();
       if (d < kBins && ahead == 0) mine[d] += __popc(peers);
       __syncwarp();
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) place(kept[i], kept_peers[i]);
+    for (long long i0 = begin + 64; i0 < end; i0 += 32) {
+      const uint2 v = item(i0 + lane);
+      place(v, __match_any_sync(0xffffffffu, digit(v)));
     }
     n = all;
-    __syncwarp();
-    // (also: no block counts again, or leaves, while another still reads its counts)
-    cluster_sync();
+    // the next pass reads what all blocks have placed; and none counts again, or leaves, while another still
+    // reads its counts
+    if (last) cluster_wait();
+    else cluster_sync();
   }
   if (rank == 0 && tid == 0) *s.valid = n;
 }
@@ -377,7 +387,7 @@ template <typename TE, typename TO>
 cudaError_t launch_lookup(const EmbedArgs& a, cudaStream_t st) {
   if (rows_on_16(a.table, a.cols, sizeof(TE)) && rows_on_16(a.out, a.out_stride, sizeof(TO))) {
     const int per_row = (a.cols + 7) / 8;
-    const long long total = (long long)a.tokens * per_row, grid = (total + 256 * kBlocks - 1) / (256 * kBlocks);
+    const long long total = (long long)a.tokens * per_row, grid = (total + 255) / 256;
     embed_scaled_kernel<TE, TO><<<(unsigned)grid, 256, 0, st>>>(a, fast_div(per_row), total);
   } else {
     const int spans = (a.cols + 255) / 256;
