@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_BLOCKS)
 // e = d_x_out + rstd_x g all of a row's sums
 //   S0 = sum g, S1 = sum g xh, S2 = sum c e, S3 = sum c, S4 = sum c xh, S5 = sum c yh e, S6 = sum c yh,
 //   S7 = sum c yh xh
-// are taken in one exchange:  sum c G = S2 - rstd_x (S0 S3 + S1 S4) / cols, and so on.
+// (S1, S5 and S7 for an RMS norm) are taken in one exchange:  sum c G = S2 - rstd_x (S0 S3 + S1 S4) / cols, and so on.
 // The parameters' gradients come of four column sums: d_h xh, d_h, and with q = keep scale G
 //   P = sum q yh, Q = sum q:  dgate = gamma_post P + beta_post Q, dgamma_post = gate P, dbeta_post = gate Q
 // (a gate of its own for every row goes into q instead, and its gradient is written row by row).
@@ -307,6 +307,20 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
   return total;
 }
 
+// Four sums: lanes 8 i to 8 i + 7 end with the total of value i.
+__device__ __forceinline__ float warp_sum4(float (&v)[4], int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float send = lane & 16 ? v[i] : v[i + 2], mine = lane & 16 ? v[i + 2] : v[i];
+    v[i] = mine + __shfl_xor_sync(0xffffffffu, send, 16);
+  }
+  const float send = lane & 8 ? v[0] : v[1], mine = lane & 8 ? v[1] : v[0];
+  float total = mine + __shfl_xor_sync(0xffffffffu, send, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  return total;
+}
+
 constexpr int kSums = 4;         // column sums: d_h xh, d_h, P, Q
 constexpr int kBwdWarps = 20;    // warps of a block
 
@@ -319,7 +333,7 @@ constexpr int kMaxGroups = 15;  // named barriers
 // once per block, into partial[block][kSums][cols].  The rows to come arrive by bulk copies, kStages of them per
 // group, which leaves the threads and the L1 out of it; gamma_pre and gate gamma_post stand in shared memory
 // as float32.
-template <typename T>
+template <typename T, bool RMS>
 __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     block_norm_bwd_kernel(const BlockNormArgs a, int W, int groups, float* __restrict__ partial) {
   extern __shared__ __align__(16) uint8_t smem[];  // vectors, column sums, the rows on their way
@@ -437,7 +451,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
         sx[k] = f2_fma(dh[k], xh[k], sx[k]);
         sd[k] = f2_add(dh[k], sd[k]);
         const uint64_t gg = f2_mul(dh[k], p[k]);
-        s2[0] = k ? f2_add(s2[0], gg) : gg;
+        if (!RMS) s2[0] = k ? f2_add(s2[0], gg) : gg;
         s2[1] = k ? f2_fma(gg, xh[k], s2[1]) : f2_mul(gg, xh[k]);
         e[k] = f2_fma(f2_both(st.w), gg, e[k]);
       }
@@ -462,43 +476,61 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
         const uint64_t ck = f2_mul(cg[k], kf[k]);
         yh[k] = f2_mul(f2_add(yh[k], f2_both(-st.x)), f2_both(st.y));
         const uint64_t ce = f2_mul(ck, e[k]), cyh = f2_mul(ck, yh[k]);
-        s2[2] = k ? f2_add(s2[2], ce) : ce;
-        s2[3] = k ? f2_add(s2[3], ck) : ck;
-        s2[4] = k ? f2_fma(ck, xh[k], s2[4]) : f2_mul(ck, xh[k]);
+        if (!RMS) {
+          s2[2] = k ? f2_add(s2[2], ce) : ce;
+          s2[3] = k ? f2_add(s2[3], ck) : ck;
+          s2[4] = k ? f2_fma(ck, xh[k], s2[4]) : f2_mul(ck, xh[k]);
+          s2[6] = k ? f2_add(s2[6], cyh) : cyh;
+        }
         s2[5] = k ? f2_fma(ce, yh[k], s2[5]) : f2_mul(ce, yh[k]);
-        s2[6] = k ? f2_add(s2[6], cyh) : cyh;
         s2[7] = k ? f2_fma(cyh, xh[k], s2[7]) : f2_mul(cyh, xh[k]);
       }
     } else {
       s2[2] = s2[3] = s2[4] = s2[5] = s2[6] = s2[7] = 0;
     }
+    // the row's sums over the group's warps: value i of a warp stands with its lanes `per` i and on
+    constexpr int kRowSums = RMS ? 4 : 8, per = 32 / kRowSums;
+    float total;
+    if constexpr (RMS) {
+      float v[4] = {f2_sum(s2[1]), f2_sum(s2[5]), f2_sum(s2[7]), 0.f};
+      total = warp_sum4(v, lane);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = f2_sum(s2[i]);
-    float total = warp_sum8(s, lane);
+      for (int i = 0; i < 8; ++i) s[i] = f2_sum(s2[i]);
+      total = warp_sum8(s, lane);
+    }
     if (W > 1) {
-      if (lane % 4 == 0) red[flip][warp][lane / 4] = total;
+      if (lane % per == 0) red[flip][warp][lane / per] = total;
       named_bar_sync(1 + group, 32 * W);
       total = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        if (i + (lane & 3) < W) total += red[flip][group * W + i + (lane & 3)][lane / 4];
-      total += __shfl_xor_sync(0xffffffffu, total, 2);
-      total += __shfl_xor_sync(0xffffffffu, total, 1);
+      for (int i = 0; i < 16; i += per)
+        if (i + lane % per < W) total += red[flip][group * W + i + lane % per][lane / per];
+#pragma unroll
+      for (int o = per / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
       flip ^= 1;
     } else {
       __syncwarp();
     }
     // the whole group has this row in its registers: the stage takes the next one
     if (w == 0 && lane == 0) arrive(row + kStages * step, stage);
+    float A = 0.f, B, m0 = 0.f, m1;
+    if constexpr (RMS) {
+      B = st.w * __shfl_sync(0xffffffffu, total, 0) * inv_n;
+      m1 = (__shfl_sync(0xffffffffu, total, per) - B * __shfl_sync(0xffffffffu, total, 2 * per)) * inv_n;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = __shfl_sync(0xffffffffu, total, 4 * i);
-    const float A = a.rms ? 0.f : st.w * s[0] * inv_n, B = st.w * s[1] * inv_n;
-    const float m0 = a.rms ? 0.f : (s[2] - A * s[3] - B * s[4]) * inv_n, m1 = (s[5] - A * s[6] - B * s[7]) * inv_n;
+      for (int i = 0; i < 8; ++i) s[i] = __shfl_sync(0xffffffffu, total, per * i);
+      A = st.w * s[0] * inv_n;
+      B = st.w * s[1] * inv_n;
+      m0 = (s[2] - A * s[3] - B * s[4]) * inv_n;
+      m1 = (s[5] - A * s[6] - B * s[7]) * inv_n;
+    }
     Pairs q, out;
     const size_t at = (size_t)row * (uint32_t)a.cols + c;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      e[k] = f2_fma(f2_both(-B), xh[k], f2_add(e[k], f2_both(-A)));  // now G
+      e[k] = f2_fma(f2_both(-B), xh[k], RMS ? e[k] : f2_add(e[k], f2_both(-A)));  // now G
       out[k] = f2_mul(f2_both(a.residual_scale), e[k]);
       q[k] = f2_mul(e[k], kf[k]);
     }
@@ -530,7 +562,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       sp[k] = f2_fma(q[k], yh[k], sp[k]);
       sq[k] = f2_add(q[k], sq[k]);
       out[k] = f2_mul(p[k], q[k]);
-      if (post) out[k] = f2_mul(f2_both(st.y), f2_fma(f2_both(-m1), yh[k], f2_add(out[k], f2_both(-m0))));
+      if (post) out[k] = f2_mul(f2_both(st.y), f2_fma(f2_both(-m1), yh[k], RMS ? out[k] : f2_add(out[k], f2_both(-m0))));
     }
     put_sum(2, sp);
     put_sum(3, sq);
@@ -545,12 +577,14 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   // the groups' sums are added in order
   __syncthreads();
   const float* all = reinterpret_cast<const float*>(smem + 2048 * W);
-  for (int i = threadIdx.x; i < kSums * a.cols; i += blockDim.x) {
-    const int s = i / a.cols, col = i - s * a.cols;
-    float v = 0.f;
-    for (int g = 0; g < groups; ++g)
-      v += all[((size_t)(2 * s + (col >> 2 & 1)) * blockDim.x + (g * W + (col >> 8)) * 32 + (col >> 3 & 31)) * 4 + (col & 3)];
-    partial[(size_t)blockIdx.x * kSums * a.cols + i] = v;
+  for (int col = threadIdx.x; col < a.cols; col += blockDim.x) {
+    const int place = (((col >> 2 & 1) * blockDim.x) + (col >> 8) * 32 + (col >> 3 & 31)) * 4 + (col & 3);
+#pragma unroll
+    for (int s = 0; s < kSums; ++s) {
+      float v = 0.f;
+      for (int g = 0; g < groups; ++g) v += all[place + (2 * s * blockDim.x + g * W * 32) * 4];
+      partial[((size_t)blockIdx.x * kSums + s) * a.cols + col] = v;
+    }
   }
 }
 
@@ -790,17 +824,17 @@ __global__ void __launch_bounds__(512, 1)
 }
 
 // The parameters' gradients from the blocks' column sums, in a fixed order: warp w of a block adds blocks
-// w, w + 16, ... of 32 columns, then the warps' sums are added in order.  Even blocks: the sums of pre, odd: of post.
+// w, w + 32, ... of 32 columns, then the warps' sums are added in order.  Even blocks: the sums of pre, odd: of post.
 template <typename T>
-__global__ void __launch_bounds__(512) block_norm_sums_kernel(const BlockNormArgs a, const float* __restrict__ partial,
+__global__ void __launch_bounds__(1024) block_norm_sums_kernel(const BlockNormArgs a, const float* __restrict__ partial,
                                                               int blocks) {
-  __shared__ float part[2][16][32];
+  __shared__ float part[2][32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, post = blockIdx.x & 1, c = (blockIdx.x >> 1) * 32 + lane;
   grid_dependency_wait();
   float s0 = 0.f, s1 = 0.f;
   if (c < a.cols) {
-#pragma unroll 4
-    for (int b = warp; b < blocks; b += 16) {
+#pragma unroll 5
+    for (int b = warp; b < blocks; b += 32) {
       const float* at = partial + ((size_t)b * kSums + 2 * post) * a.cols + c;
       s0 += __ldg(at);
       s1 += __ldg(at + a.cols);
@@ -811,7 +845,7 @@ __global__ void __launch_bounds__(512) block_norm_sums_kernel(const BlockNormArg
   __syncthreads();
   if (warp || c >= a.cols) return;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) {
+  for (int i = 1; i < 32; ++i) {
     s0 += part[0][i][lane];
     s1 += part[1][i][lane];
   }
@@ -877,13 +911,14 @@ cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num
   } else {
     s.groups = (int)std::min((size_t)s.groups, fits);
     const size_t smem = fixed + group * s.groups;
-    e = allow_smem(block_norm_bwd_kernel<T>, smem);
+    const auto kernel = a.rms ? block_norm_bwd_kernel<T, true> : block_norm_bwd_kernel<T, false>;
+    e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    block_norm_bwd_kernel<T><<<s.blocks, 32 * s.W * s.groups, smem, st>>>(a, s.W, s.groups, partial);
+    kernel<<<s.blocks, 32 * s.W * s.groups, smem, st>>>(a, s.W, s.groups, partial);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  return launch_after(block_norm_sums_kernel<T>, 2 * ((a.cols + 31) / 32), 512, st, a, (const float*)partial, s.blocks);
+  return launch_after(block_norm_sums_kernel<T>, 2 * ((a.cols + 31) / 32), 1024, st, a, (const float*)partial, s.blocks);
 }
 
 // W warps to a row of up to 4096 columns.  Registers for 800 threads an SM with bfloat16 blocks (80 each; 16384 x
