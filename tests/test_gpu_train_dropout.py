@@ -188,6 +188,21 @@ def test_the_backward_uses_its_forwards_dropout():
         assert rel_l2(to_np(b), to_np(a)) < 1e-5
 
 
+@pytest.mark.parametrize("vocab", [33, 300])
+@pytest.mark.parametrize("p", [0.0, 0.2])
+@pytest.mark.parametrize("bad", [-1, 300])
+def test_ids_out_of_range_are_reported(vocab, p, bad):
+    """With a dropout as without one: -1 is no token of an encoder's step."""
+    from transformer_esm_layer_gb300.binding import Dropout
+    s = _setup(vocab)
+    s["enc"].set_dropout(Dropout(p, _rng(), OFFSET))
+    s["t"][3] = bad
+    s["enc"].forward_train(s["dw"], s["t"], s["cu"], max(LENGTHS), s["tb"], s["ws"])
+    assert s["enc"].check_status() == 4  # ESM_ERR_TOKEN_RANGE
+    s["enc"].backward(s["dw"], s["d"], s["grads"], s["tb"], s["ws"])
+    assert torch.isfinite(s["grads"].emb).all()
+
+
 def test_refusals():
     import ctypes
 

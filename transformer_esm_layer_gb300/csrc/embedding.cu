@@ -13,11 +13,11 @@
 namespace esm {
 namespace {
 
-// An id that has a row, or -1; other ids latch ERRBIT_TOKEN.
+// An id that has a row, or -1; ids out of range latch ERRBIT_TOKEN.
 __device__ __forceinline__ int checked_id(const EmbedArgs& a, int t, bool report) {
   const int id = __ldg(a.ids + t);
   if (id >= 0 && id < a.vocab) return id;
-  if (id != -1 && report) latch_error(a.err, ERRBIT_TOKEN);
+  if (!(a.none && id == -1) && report) latch_error(a.err, ERRBIT_TOKEN);
   return -1;
 }
 

@@ -1985,6 +1985,7 @@ static bool embed_args(esm_encoder* h, const int32_t* ids, int tokens, int vocab
   a->vocab = vocab;
   a->cols = cols;
   a->scale = scale;
+  a->none = true;
   a->err = h->d_err;
   return true;
 }

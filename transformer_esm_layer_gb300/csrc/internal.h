@@ -345,12 +345,13 @@ cudaError_t launch_dropout(const DropoutArgs& a, cudaStream_t st);
 
 // Lookup: table (vocab x cols) -> out; gradient: out (= dL/d(out)) -> d_table.
 struct EmbedArgs {
-  const int32_t* ids;      // [tokens], -1: none
+  const int32_t* ids;      // [tokens]
   const float* row_scale;  // [tokens] or NULL
   const void* table;
   void* out;               // rows out_stride apart
   float* d_table;
   bool table_bf16, out_bf16, accumulate;
+  bool none;  // id -1 stands for no token (else it is out of range like any other)
   long long out_stride;
   int tokens, vocab, cols;
   float scale;
