@@ -558,6 +558,70 @@ def test_block_norm_misaligned(encs):
     _check_forward(x, y, x_out, h, stats, ref, _factors(50, cols, p), BF16)
 
 
+# aligned rows, rows off 16 bytes, wide rows of both kinds; several groups of warps to a block and one
+@pytest.mark.parametrize("rows,cols", [(1000, 64), (400, 1280), (37, 1283), (9, 4096), (5, 5120), (3, 8191)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("config", NORMS)
+def test_block_norm_backward_reads_no_absent_norms_stats(encs, rows, cols, dtype, config):
+    """The columns of stats of a norm that there is not may hold anything."""
+    enc = encs[dtype]
+    norm, gate, x, y, p, ref = _norm_case(dtype, rows, cols, config, 4)
+    post, pre = config[1], config[2]
+    d_x, d_h = _randn(_gen(1), rows, cols), _randn(_gen(2), rows, cols, dtype=dtype) if pre else None
+    x_out, stats = torch.empty_like(x), torch.empty(rows, 4, device="cuda")
+    enc.op_block_norm(norm, x, y, x_out, torch.empty_like(y) if pre else None, gate=gate, dropout=_drop(p), stats=stats)
+    results = []
+    for hold in (0.0, float("nan")):
+        st = stats.clone()
+        if not post:
+            st[:, :2] = hold
+        if not pre:
+            st[:, 2:] = hold
+        dx, dy = torch.empty_like(x), torch.empty_like(y)
+        grads = {k: torch.empty(cols, device="cuda") for k in ("post_gamma", "post_beta", "pre_gamma", "pre_beta")
+                 if ref[k] is not None}
+        enc.op_block_norm_backward(norm, x_out if pre else None, y, st, d_x, d_h, dx, dy, grads, gate=gate, dropout=_drop(p))
+        results.append([dx, dy] + list(grads.values()))
+    for a, b in zip(*results):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,cols", [(1000, 64), (400, 1280), (37, 1283), (9, 4096), (5, 5120), (3, 8191)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("config", [c for c in NORMS if c[6]])
+@pytest.mark.parametrize("hold", [float("nan"), float("inf")])
+def test_block_norm_backward_of_dropped_places(encs, rows, cols, dtype, config, hold):
+    """What d_x_out holds at a dropped place goes to dx there and nowhere else; without a norm after the block,
+    what y holds there goes nowhere."""
+    enc = encs[dtype]
+    norm, gate, x, y, p, ref = _norm_case(dtype, rows, cols, config, 5)
+    post, pre = config[1], config[2]
+    dropped = torch.from_numpy(_factors(rows, cols, p) == 0).cuda()
+    d_x, d_h = _randn(_gen(1), rows, cols), _randn(_gen(2), rows, cols, dtype=dtype) if pre else None
+    x_out, stats = torch.empty_like(x), torch.empty(rows, 4, device="cuda")
+    h = torch.empty_like(y) if pre else None
+    enc.op_block_norm(norm, x, y, x_out, h, gate=gate, dropout=_drop(p), stats=stats)
+    results = []
+    for there in (False, True):
+        d_xt, yt = d_x.clone(), y.clone()
+        if there:
+            d_xt[dropped] = hold
+            if not post:
+                yt[dropped] = hold
+                again = torch.empty_like(x)
+                enc.op_block_norm(norm, x, yt, again, h, gate=gate, dropout=_drop(p))
+                assert torch.equal(again, x_out)
+        dx, dy = torch.empty_like(x), torch.empty_like(y)
+        grads = {k: torch.empty(cols, device="cuda") for k in ("post_gamma", "post_beta", "pre_gamma", "pre_beta")
+                 if ref[k] is not None}
+        if gate is not None:
+            grads["gate"] = torch.empty(cols, device="cuda") if gate.dim() == 1 else torch.empty_like(gate)
+        enc.op_block_norm_backward(norm, x_out, yt, stats, d_xt, d_h, dx, dy, grads, gate=gate, dropout=_drop(p))
+        results.append([dx.masked_fill(dropped, 0.0), dy] + list(grads.values()))
+    for a, b in zip(*results):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
 def test_some_gradients_alone(encs):
     """Any of the parameters' gradients may be left out."""
     enc, cols = encs[BF16], 640

@@ -331,8 +331,8 @@ constexpr int kMaxGroups = 15;  // named barriers
 // its SM and takes a row per group and step; a lane owns eight columns of every row that its group takes, so
 // the four column sums stay with it (in shared memory: 32 registers fewer let 20 warps run, not 16) and leave
 // once per block, into partial[block][kSums][cols].  The rows to come arrive by bulk copies, kStages of them per
-// group, which leaves the threads and the L1 out of it; gamma_pre and gate gamma_post stand in shared memory
-// as float32.
+// group, which leaves the threads and the L1 out of it; gamma_pre and scale gate gamma_post stand in shared
+// memory as float32.
 template <typename T, bool RMS>
 __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     block_norm_bwd_kernel(const BlockNormArgs a, int W, int groups, float* __restrict__ partial) {
@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     const int at = ((i >> 8) * 2 + (i >> 2 & 1)) * 128 + (i >> 3 & 31) * 4 + (i & 3);
     auto value = [&](const void* p, float without) { return p ? ld1(static_cast<const T*>(p) + i) : without; };
     vf[at] = i < a.cols ? value(a.pre_gamma, 0.f) : 0.f;
-    vf[256 * W + at] = i < a.cols ? value(a.gate_rows ? nullptr : a.gate, 1.f) * value(a.post_gamma, 1.f) : 0.f;
+    vf[256 * W + at] =
+        i < a.cols ? a.mask.scale * value(a.gate_rows ? nullptr : a.gate, 1.f) * value(a.post_gamma, 1.f) : 0.f;
   }
   const ulonglong2* vectors = reinterpret_cast<const ulonglong2*>(smem) + w * 64 + lane;
   auto vector = [&](int v, Pairs& out) {
@@ -416,21 +417,22 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       alive = false;  // (the copy never came: nothing of this call is right, and nothing more is waited for)
       latch_error(a.err, ERRBIT_TIMEOUT);
     }
-    const float4 st = pre || post ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 st = pre || post ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!pre) st.w = 0.f;  // (no norm's columns may hold anything)
     const uint8_t* values = from + 16;
     auto row_f = [&](int i, Pairs& v) { ld8(reinterpret_cast<const float*>(values + i * f_bytes) + c, v); };
     auto row_t = [&](int i, Pairs& v) { ld8(reinterpret_cast<const T*>(values + 2 * f_bytes + i * t_bytes) + c, v); };
-    Pairs xh, e, yh, kf, p;
+    Pairs xh, e, yh, kept, p;
     float s[8];
-    // 0 or the dropout's scale, per element
-    fill(kf, a.mask.scale);
-    keep(drop_words(a.mask, ps, &keys, (unsigned long long)(uint32_t)row * per_row + (uint32_t)c / 8), ps, kf);
+    // all bits or none, per element: a dropped place is 0 whatever it holds
+    fill(kept, __uint_as_float(~0u));
+    keep(drop_words(a.mask, ps, &keys, (unsigned long long)(uint32_t)row * per_row + (uint32_t)c / 8), ps, kept);
     row_f(0, e);
     row_t(0, yh);
     if (partly && !active) {
       fill(e, 0.f);
       fill(yh, 0.f);
-      fill(kf, 0.f);
+      fill(kept, 0.f);
     }
     uint64_t s2[8];
     if (pre) {
@@ -473,9 +475,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint64_t ck = f2_mul(cg[k], kf[k]);
+        const uint64_t ck = cg[k] & kept[k];
         yh[k] = f2_mul(f2_add(yh[k], f2_both(-st.x)), f2_both(st.y));
-        const uint64_t ce = f2_mul(ck, e[k]), cyh = f2_mul(ck, yh[k]);
+        const uint64_t ce = f2_mul(ck, e[k] & kept[k]), cyh = f2_mul(ck, yh[k]);
         if (!RMS) {
           s2[2] = k ? f2_add(s2[2], ce) : ce;
           s2[3] = k ? f2_add(s2[3], ck) : ck;
@@ -532,15 +534,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     for (int k = 0; k < 4; ++k) {
       e[k] = f2_fma(f2_both(-B), xh[k], RMS ? e[k] : f2_add(e[k], f2_both(-A)));  // now G
       out[k] = f2_mul(f2_both(a.residual_scale), e[k]);
-      q[k] = f2_mul(e[k], kf[k]);
+      q[k] = e[k] & kept[k];  // (the dropout's scale comes with p)
     }
     if (active) st8(a.dx + at, out);
     vector(1, p);
     if (!post) {
-      // (y as it came: a dropped one adds nothing, whatever it holds)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        yh[k] = f2_pack(f2_lo(kf[k]) != 0.f ? f2_lo(yh[k]) : 0.f, f2_hi(kf[k]) != 0.f ? f2_hi(yh[k]) : 0.f);
+      for (int k = 0; k < 4; ++k) yh[k] &= kept[k];  // (y as it came)
     }
     if (a.gate_rows) {
       Pairs n, own_gate, beta;
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       if (a.post_beta && active) ld8(static_cast<const T*>(a.post_beta) + c, beta);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        n[k] = f2_mul(q[k], f2_fma(yh[k], p[k], beta[k]));
+        n[k] = f2_mul(q[k], f2_fma(yh[k], p[k], f2_mul(f2_both(a.mask.scale), beta[k])));
         q[k] = f2_mul(q[k], own_gate[k]);
       }
       if (a.d_gate && active) st8(static_cast<T*>(a.d_gate) + at, n);
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     for (int s = 0; s < kSums; ++s) {
       float v = 0.f;
       for (int g = 0; g < groups; ++g) v += all[place + (2 * s * blockDim.x + g * W * 32) * 4];
-      partial[((size_t)blockIdx.x * kSums + s) * a.cols + col] = v;
+      partial[((size_t)blockIdx.x * kSums + s) * a.cols + col] = s < 2 ? v : v * a.mask.scale;
     }
   }
 }
@@ -699,15 +699,18 @@ __global__ void __launch_bounds__(512, 1)
         fill(xh[g], 0.f);
       }
       if (post) {
-        Pairs c;
+        Pairs c, ek;  // (0 where they are dropped, whatever d_x_out holds there)
         factors(g, base, c);
         keep(words[g], ps, c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ek[k] = e[g][k];
+        keep(words[g], ps, ek);
 #pragma unroll
         for (int k = 0; k < 4; ++k) yh[g][k] = f2_mul(f2_add(yh[g][k], minus_y), ry);
         span_trim<VEC>(left, lane, yh[g]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint64_t ce = f2_mul(c[k], e[g][k]), cyh = f2_mul(c[k], yh[g][k]);
+          const uint64_t ce = f2_mul(c[k], ek[k]), cyh = f2_mul(c[k], yh[g][k]);
           s2[2] = f2_add(s2[2], ce);
           s2[3] = f2_add(s2[3], c[k]);
           s2[4] = f2_fma(c[k], xh[g][k], s2[4]);
@@ -781,6 +784,7 @@ __global__ void __launch_bounds__(512, 1)
         Pairs c;
         factors(g, base, c);
         keep(words[g], ps, c);
+        keep(words[g], ps, e[g]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           out[k] = f2_mul(ry, f2_fma(f2_both(-m1), yh[g][k], f2_fma(c[k], e[g][k], f2_both(-m0))));
