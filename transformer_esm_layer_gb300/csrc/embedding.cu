@@ -257,6 +257,7 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
 // Sums of 32 consecutive places of the sorted list and 256 columns by one warp.  An id whose tokens all lie
 // within the piece is written at once; of an id that goes on over the piece's border the piece keeps its part:
 // part[piece][0] for one that began before, part[piece][1] for one that begins here and goes on.
+// VEC: rows on 16 bytes and cols % 8 == 0.
 constexpr int kPiece = 32;
 
 template <typename TO, bool VEC>
@@ -464,7 +465,7 @@ size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols) {
 }
 
 cudaError_t launch_embed_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaStream_t st) {
-  const bool vec = rows_on_16(a.d_table, a.cols, 4) && rows_on_16(a.out, a.out_stride, a.out_bf16 ? 2 : 4);
+  const bool vec = a.cols % 8 == 0 && rows_on_16(a.d_table, a.cols, 4) && rows_on_16(a.out, a.out_stride, a.out_bf16 ? 2 : 4);
   if (a.out_bf16)
     return vec ? launch_grad<__nv_bfloat16, true>(a, workspace, num_sms, st)
                : launch_grad<__nv_bfloat16, false>(a, workspace, num_sms, st);
