@@ -356,8 +356,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   uint64_t* bars = full + group * kStages;
   if (threadIdx.x < groups * kStages) mbar_init(full + threadIdx.x, 1);
   fence_barrier_init();
+  bool alive = true;
   auto arrive = [&](int row, int stage) {  // (one thread of the group)
-    if (row >= a.rows) return;
+    if (row >= a.rows || !alive) return;
     const size_t at = (size_t)row * a.cols;
     uint8_t* to = ring + stage * stage_bytes;
     mbar_arrive_expect_tx(bars + stage, (pre || post ? 16 : 0) + (a.d_x_out ? f_bytes : 0) + t_bytes + (pre ? f_bytes + t_bytes : 0) +
@@ -407,14 +408,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   };
   const float inv_n = 1.f / (float)a.cols;
   const uint32_t per_row = (uint32_t)a.cols / 8;
-  bool alive = true;
   int flip = 0, stage = 0;
   const uint8_t* from = ring;
   uint32_t parity = 0;
   __syncthreads();
   for (int row = first; row < a.rows; row += step) {
     if (alive && !mbar_wait_warp(bars + stage, parity)) {
-      alive = false;  // (the copy never came: nothing of this call is right, and nothing more is waited for)
+      alive = false;  // (the copy never came: nothing of this call is right, and nothing more is copied)
       latch_error(a.err, ERRBIT_TIMEOUT);
     }
     float4 st = pre || post ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -573,6 +573,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       from = ring;
       parity ^= 1;
     }
+  }
+  if (!alive) {  // copies still on their way get as long again, whichever phase they belong to
+    for (int i = 0; i < 2 * kStages; ++i) mbar_wait_warp(bars + i / 2, i & 1);
   }
   // the groups' sums are added in order
   __syncthreads();
