@@ -55,6 +55,15 @@ def test_host_tensors_are_rejected_before_any_call():
         Dropout(0.1, torch.zeros(2, dtype=torch.int64))
 
 
+def test_the_steps_dropout_lies_on_the_steps_device():
+    enc = _NoDevice()
+    enc._dropout = object.__new__(Dropout)
+    enc._dropout._set(device=torch.device("cuda", 1))
+    tok, cu = torch.zeros(4, dtype=torch.int32), torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError, match="rng must be on"):
+        enc.forward_train(None, tok, cu, 4, None, None)
+
+
 def test_block_norm_parameters():
     g = torch.ones(8)
     with pytest.raises(ValueError, match="kind"):

@@ -962,6 +962,9 @@ class EsmEncoder:
         """esm_encoder_forward_train: the forward, keeping its activations in train_buf."""
         T = token_ids.numel()
         B = cu_seqlens.numel() - 1
+        drop = getattr(self, "_dropout", None)
+        _need(drop is None or drop.device == token_ids.device, "forward_train",
+              f"the dropout's rng must be on {token_ids.device}")
         if out is None:
             out = torch.empty(T, self.hidden, dtype=self.out_dtype, device=token_ids.device)
         self._raise(self.lib.esm_encoder_forward_train(self.handle, ctypes.byref(weights.struct), _ptr(token_ids),
@@ -969,7 +972,7 @@ class EsmEncoder:
                                                        _ptr(train_buf), train_buf.numel(), _ptr(workspace),
                                                        workspace.numel(), _stream_ptr(stream)),
                     "esm_encoder_forward_train")
-        self._train_dropout = getattr(self, "_dropout", None)  # the backward reads its rng
+        self._train_dropout = drop  # the backward reads its rng
         return out
 
     def backward(self, weights: DeviceWeights, d_out, grads: "DeviceGrads", train_buf, workspace, stream=None):
