@@ -622,6 +622,34 @@ def test_block_norm_backward_of_dropped_places(encs, rows, cols, dtype, config, 
         assert torch.isfinite(a).all() and torch.equal(a, b)
 
 
+@pytest.mark.parametrize("shift", [4, 8])
+def test_float32_rows_off_32_bytes(encs, shift):
+    """Float32 rows that start `shift` values into their buffer: the same results, wherever they lie."""
+    enc, rows, cols, V = encs[F32], 600, 264, 70
+    move = lambda t: torch.cat([torch.zeros(shift, device="cuda"), t.flatten()])[shift:].view_as(t)
+    g = _gen(3)
+    x, table, ids = _randn(g, rows, cols), _randn(g, V, cols), _tokens(g, rows, V)
+    for case in range(2):
+        at = move if case else (lambda t: t.clone())
+        y, out, dt = at(torch.empty_like(x)), at(torch.empty_like(x)), at(torch.empty_like(table))
+        enc.op_dropout(at(x), y, _drop(0.3), residual=at(2 * x))
+        enc.op_embed(ids, at(table), out, dropout=_drop(0.3))
+        enc.op_embed_backward(ids, at(x), dt, dropout=_drop(0.3))
+        few = at(torch.empty(33, cols, device="cuda"))
+        enc.op_embed_backward(ids % 33, at(x), few, dropout=_drop(0.3))
+        now = [y, out, dt, few]
+        if case:
+            assert all(torch.equal(a, b) for a, b in zip(now[:2], first[:2]))
+            for a, b in zip(now[2:], first[2:]):
+                torch.testing.assert_close(a, b, rtol=0, atol=64 * U * 64)  # up to 64 terms of some size 8 in another order
+        first = now
+    norm, gate, x, y, p, ref = _norm_case(F32, 50, cols, NORMS[0], 1)
+    x_out, h, stats = move(torch.empty_like(x)), move(torch.empty_like(y)), torch.empty(50, 4, device="cuda")
+    enc.op_block_norm(norm, move(x), move(y), x_out, h, gate=gate, dropout=_drop(p), stats=stats)
+    _check_forward(x, y, x_out, h, stats, ref, _factors(50, cols, p), F32)
+    _check_backward(enc, norm, gate, move(x), move(y), p, ref, move(x), move(y), F32)
+
+
 def test_some_gradients_alone(encs):
     """Any of the parameters' gradients may be left out."""
     enc, cols = encs[BF16], 640

@@ -112,7 +112,7 @@ __device__ __forceinline__ void row_moments(const Pairs (&z)[R][G], const BlockN
   }
 }
 
-// W = 0: the number of warps is blockDim.x / 32.  VEC: every row on 16 bytes and cols % 8 == 0.
+// W = 0: the number of warps is blockDim.x / 32.  VEC: every row's eights aligned and cols % 8 == 0.
 template <typename T, bool VEC, int W, int R, int G, int MAX_THREADS, int MIN_BLOCKS>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_BLOCKS)
     block_norm_kernel(const BlockNormArgs a, const RowShape shape) {
@@ -327,7 +327,7 @@ constexpr int kBwdWarps = 20;    // warps of a block
 constexpr int kStages = 2;
 constexpr int kMaxGroups = 15;  // named barriers
 
-// Rows on 16 bytes, cols % 8 == 0 and <= 4096.  A block of `groups` groups of W = ceil(cols / 256) warps stays on
+// Aligned eights, cols % 8 == 0 and <= 4096.  A block of `groups` groups of W = ceil(cols / 256) warps stays on
 // its SM and takes a row per group and step; a lane owns eight columns of every row that its group takes, so
 // the four column sums stay with it (in shared memory: 32 registers fewer let 20 warps run, not 16) and leave
 // once per block, into partial[block][kSums][cols].  The rows to come arrive by bulk copies, kStages of them per
@@ -347,9 +347,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   const int first = blockIdx.x * groups + group, step = gridDim.x * groups;  // (rows + 4 steps fit 32 bits)
   const PhiloxState ps = philox_state(a.mask);
   philox_keys(ps, &keys);
-  // a stage: the statistics, rows of d_x_out and x_out (float32), of y, d_h and the gate (T)
+  // a stage: the statistics, rows of d_x_out and x_out (float32), of y and d_h (T)
   const uint32_t f_bytes = (uint32_t)a.cols * 4, t_bytes = (uint32_t)a.cols * sizeof(T);
-  const uint32_t stage_bytes = 16 + 2 * f_bytes + (a.gate_rows ? 3 : 2) * t_bytes;
+  const uint32_t stage_bytes = 16 + 2 * f_bytes + 2 * t_bytes;
   // sum i of the lane's columns: its own 16 bytes at 2 i and 2 i + 1 blocks' widths
   float4* own_sums = reinterpret_cast<float4*>(smem + 2048 * W) + threadIdx.x;
   uint8_t* ring = smem + 2048 * W + (size_t)blockDim.x * (32 * kSums) + group * kStages * stage_bytes;
@@ -361,8 +361,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     if (row >= a.rows || !alive) return;
     const size_t at = (size_t)row * a.cols;
     uint8_t* to = ring + stage * stage_bytes;
-    mbar_arrive_expect_tx(bars + stage, (pre || post ? 16 : 0) + (a.d_x_out ? f_bytes : 0) + t_bytes + (pre ? f_bytes + t_bytes : 0) +
-                                            (a.gate_rows ? t_bytes : 0));
+    mbar_arrive_expect_tx(bars + stage, (pre || post ? 16 : 0) + (a.d_x_out ? f_bytes : 0) + t_bytes + (pre ? f_bytes + t_bytes : 0));
     if (pre || post) bulk_load(to, a.stats + 4 * (size_t)row, 16, bars + stage);
     to += 16;
     if (a.d_x_out) bulk_load(to, a.d_x_out + at, f_bytes, bars + stage);
@@ -370,7 +369,6 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     to += 2 * f_bytes;
     bulk_load(to, static_cast<const T*>(a.y) + at, t_bytes, bars + stage);
     if (pre) bulk_load(to + t_bytes, static_cast<const T*>(a.d_h) + at, t_bytes, bars + stage);
-    if (a.gate_rows) bulk_load(to + 2 * t_bytes, static_cast<const T*>(a.gate) + at, t_bytes, bars + stage);
   };
   __syncthreads();
   grid_dependency_launch();
@@ -413,6 +411,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
   uint32_t parity = 0;
   __syncthreads();
   for (int row = first; row < a.rows; row += step) {
+    Raw8<T> gate;  // (its row by the threads: in the ring it would take a group's room at 2560 columns)
+    if (a.gate_rows) gate.load(static_cast<const T*>(a.gate) + (size_t)row * (uint32_t)a.cols + (active ? c : 0), 8);
     if (alive && !mbar_wait_warp(bars + stage, parity)) {
       alive = false;  // (the copy never came: nothing of this call is right, and nothing more is copied)
       latch_error(a.err, ERRBIT_TIMEOUT);
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     float4 st = pre || post ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
     if (!pre) st.w = 0.f;  // (no norm's columns may hold anything)
     const uint8_t* values = from + 16;
-    auto row_f = [&](int i, Pairs& v) { ld8(reinterpret_cast<const float*>(values + i * f_bytes) + c, v); };
+    auto row_f = [&](int i, Pairs& v) { ld8_shared(reinterpret_cast<const float*>(values + i * f_bytes) + w * 256, lane, v); };
     auto row_t = [&](int i, Pairs& v) { ld8(reinterpret_cast<const T*>(values + 2 * f_bytes + i * t_bytes) + c, v); };
     Pairs xh, e, yh, kept, p;
     float s[8];
@@ -463,8 +463,6 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
       fill(xh, 0.f);
       s2[0] = s2[1] = 0;
     }
-    Raw8<T> gate;
-    if (a.gate_rows) gate.load(reinterpret_cast<const T*>(values + 2 * f_bytes + 2 * t_bytes) + (active ? c : 0), 8);
     if (post) {
       Pairs cg;
       vector(1, cg);
@@ -907,7 +905,7 @@ template <typename T>
 cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num_sms, cudaStream_t st) {
   BwdShape s = bwd_shape(a.rows, a.cols, num_sms);
   // a group's rows and sums, behind the vectors (1 KB more: lanes past a row's end read on behind it)
-  const size_t group = ((size_t)a.cols * (8 + (a.gate_rows ? 3 : 2) * sizeof(T)) + 16) * kStages + (size_t)1024 * kSums * s.W;
+  const size_t group = ((size_t)a.cols * (8 + 2 * sizeof(T)) + 16) * kStages + (size_t)1024 * kSums * s.W;
   const size_t fixed = 2048 * s.W + 1024, fits = (kSmemMax - fixed) / group;
   cudaError_t e;
   if (s.G == 2) {
@@ -971,21 +969,21 @@ cudaError_t launch_fwd(const BlockNormArgs& a, bool vec, int num_sms, cudaStream
   return cudaGetLastError();
 }
 
-// 16-byte accesses to every row and parameter
-bool all_on_16(const BlockNormArgs& a, bool bf16) {
+// a row's or parameter's eight values at a time
+bool all_on_eights(const BlockNormArgs& a, bool bf16) {
   const int es = bf16 ? 2 : 4, n = a.cols;
-  return rows_on_16(a.y, n, es) && rows_on_16(a.x, n, 4) && rows_on_16(a.x_out, n, 4) && rows_on_16(a.h, n, es) &&
-         rows_on_16(a.d_x_out, n, 4) && rows_on_16(a.d_h, n, es) && rows_on_16(a.dx, n, 4) && rows_on_16(a.dy, n, es) &&
-         rows_on_16(a.post_gamma, n, es) && rows_on_16(a.post_beta, n, es) && rows_on_16(a.pre_gamma, n, es) &&
-         rows_on_16(a.pre_beta, n, es) && rows_on_16(a.gate, n, es) &&
-         (!a.gate_rows || rows_on_16(a.d_gate, n, es));
+  return rows_on_eights(a.y, n, es) && rows_on_eights(a.x, n, 4) && rows_on_eights(a.x_out, n, 4) && rows_on_eights(a.h, n, es) &&
+         rows_on_eights(a.d_x_out, n, 4) && rows_on_eights(a.d_h, n, es) && rows_on_eights(a.dx, n, 4) && rows_on_eights(a.dy, n, es) &&
+         rows_on_eights(a.post_gamma, n, es) && rows_on_eights(a.post_beta, n, es) && rows_on_eights(a.pre_gamma, n, es) &&
+         rows_on_eights(a.pre_beta, n, es) && rows_on_eights(a.gate, n, es) &&
+         (!a.gate_rows || rows_on_eights(a.d_gate, n, es));
 }
 
 }  // namespace
 
 cudaError_t launch_block_norm(const BlockNormArgs& a, bool bf16, int num_sms, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
-  const bool vec = all_on_16(a, bf16);
+  const bool vec = all_on_eights(a, bf16);
   return bf16 ? launch_fwd<__nv_bfloat16>(a, vec, num_sms, st) : launch_fwd<float>(a, vec, num_sms, st);
 }
 
@@ -994,7 +992,7 @@ size_t block_norm_bwd_workspace_bytes(int rows, int cols, int num_sms) {
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, bool bf16, void* workspace, int num_sms, cudaStream_t st) {
-  const bool vec = all_on_16(a, bf16);
+  const bool vec = all_on_eights(a, bf16);
   float* partial = static_cast<float*>(workspace);
   return bf16 ? launch_bwd<__nv_bfloat16>(a, vec, partial, num_sms, st) : launch_bwd<float>(a, vec, partial, num_sms, st);
 }

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256, 4) dropout_kernel(const DropoutArgs a, co
   }
 }
 
-// Rows off 16-byte boundaries: one warp per 256 columns of a row.
+// Rows whose eights are not aligned: one warp per 256 columns of a row.
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(256) dropout_rows_kernel(const DropoutArgs a, const FastDiv spans, long long total) {
   const PhiloxState ps = philox_state(a.mask);
@@ -109,8 +109,8 @@ cudaError_t launch(const DropoutArgs& a, bool vec, bool dense, cudaStream_t st) 
 
 cudaError_t launch_dropout(const DropoutArgs& a, cudaStream_t st) {
   if (a.rows <= 0 || a.cols <= 0) return cudaSuccess;
-  const bool vec = rows_on_16(a.x, a.x_stride, a.x_bf16 ? 2 : 4) && rows_on_16(a.y, a.y_stride, a.y_bf16 ? 2 : 4) &&
-                   (!a.residual || rows_on_16(a.residual, a.res_stride, a.y_bf16 ? 2 : 4));
+  const bool vec = rows_on_eights(a.x, a.x_stride, a.x_bf16 ? 2 : 4) && rows_on_eights(a.y, a.y_stride, a.y_bf16 ? 2 : 4) &&
+                   (!a.residual || rows_on_eights(a.residual, a.res_stride, a.y_bf16 ? 2 : 4));
   const bool dense = a.cols % 8 == 0 && (a.rows == 1 || (a.x_stride == a.cols && a.y_stride == a.cols &&
                                                          (!a.residual || a.res_stride == a.cols)));
   if (a.x_bf16) return a.y_bf16 ? launch<__nv_bfloat16, __nv_bfloat16>(a, vec, dense, st) : launch<__nv_bfloat16, float>(a, vec, dense, st);

@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(256) embed_grad_join_kernel(const EmbedArgs a,
 
 template <typename TE, typename TO>
 cudaError_t launch_lookup(const EmbedArgs& a, cudaStream_t st) {
-  if (rows_on_16(a.table, a.cols, sizeof(TE)) && rows_on_16(a.out, a.out_stride, sizeof(TO))) {
+  if (rows_on_eights(a.table, a.cols, sizeof(TE)) && rows_on_eights(a.out, a.out_stride, sizeof(TO))) {
     const int per_row = (a.cols + 7) / 8;
     const long long total = (long long)a.tokens * per_row, grid = (total + 255) / 256;
     embed_scaled_kernel<TE, TO><<<(unsigned)grid, 256, 0, st>>>(a, fast_div(per_row), total);
@@ -465,7 +465,7 @@ size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols) {
 }
 
 cudaError_t launch_embed_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaStream_t st) {
-  const bool vec = a.cols % 8 == 0 && rows_on_16(a.d_table, a.cols, 4) && rows_on_16(a.out, a.out_stride, a.out_bf16 ? 2 : 4);
+  const bool vec = a.cols % 8 == 0 && rows_on_eights(a.d_table, a.cols, 4) && rows_on_eights(a.out, a.out_stride, a.out_bf16 ? 2 : 4);
   if (a.out_bf16)
     return vec ? launch_grad<__nv_bfloat16, true>(a, workspace, num_sms, st)
                : launch_grad<__nv_bfloat16, false>(a, workspace, num_sms, st);

@@ -328,9 +328,9 @@ cudaError_t launch_distill_loss(const DistillArgs& a, float* loss_sum, int* coun
 cudaError_t launch_distill_loss_backward(const DistillArgs& a, int num_sms, cudaStream_t st);
 
 // ---------------------------------------------------------------- dropout.cu, embedding.cu, block_norm.cu
-// True if rows `stride` elements of `es` bytes apart all start on 16-byte boundaries (NULL: true).
-inline bool rows_on_16(const void* p, long long stride, int es) {
-  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * es)) & 15) == 0 || p == nullptr;
+// True if rows `stride` elements of `es` bytes apart all start where eight elements are aligned (NULL: true).
+inline bool rows_on_eights(const void* p, long long stride, int es) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * es)) & (8 * es - 1)) == 0 || p == nullptr;
 }
 struct DropoutArgs {
   const void* x;
