@@ -250,6 +250,27 @@ def test_embed_backward_of_large_batches(enc, T, V, cols):
     assert torch.equal(table, again)  # the order goes by the ids alone
 
 
+@pytest.mark.parametrize("T,V,cols", [(513, 1, 8), (769, 64, 1283), (2000, 63, 12), (1025, 2, 520), (4097, 33, 1280)])
+@pytest.mark.parametrize("ids", ["any", "one", "none", "runs", "first"])
+@pytest.mark.parametrize("td", [F32, BF16])
+def test_embed_backward_of_few_ids(enc, T, V, cols, ids, td):
+    """Sums of chunks: ids that fill a chunk, that a chunk lacks, that change on and off its warps' borders."""
+    g = _gen(T + V)
+    t = {"any": torch.randint(-1, V, (T,), device="cuda", generator=g), "one": torch.full((T,), V - 1),
+         "none": torch.full((T,), -1), "runs": torch.arange(T) // 32 % V,
+         "first": torch.cat([torch.zeros(250, dtype=torch.long), torch.arange(T - 250) // 250 % V])}[ids].to(torch.int32).cuda()
+    d, rs, kept = _randn(g, T, cols, dtype=td), _randn(g, T), _randn(g, V, cols)
+    want, mag = S.embed_backward(t.cpu().numpy(), to_np(d), V, 1.0, to_np(rs), _factors(T, cols, 0.2))
+    most = int(torch.bincount(t[t >= 0], minlength=V).max()) if ids != "none" else 0
+    for accumulate in (False, True):
+        table = kept.clone() if accumulate else torch.full((V, cols), float("nan"), device="cuda")
+        enc.op_embed_backward(t, d, table, row_scale=rs, dropout=_drop(0.2), accumulate=accumulate)
+        before = to_np(kept) if accumulate else 0.0
+        _within(table, want + before, (most + 6) * U * (mag + np.abs(before)))
+    if ids == "none":
+        assert torch.equal(table, kept)
+
+
 @pytest.mark.parametrize("ids", ["one", "rising", "none", "last"])
 def test_embed_backward_of_uneven_ids(enc, ids):
     T, V, cols = 5000, 5000, 72

@@ -26,7 +26,7 @@ __device__ __forceinline__ float token_scale(const EmbedArgs& a, int t) {
 }
 
 // Blocks of eight columns in the order of the tokens, one to a thread: 64 warps an SM hide the way from the id to
-// the row (four blocks to a thread and half as many warps took 29 us where this takes 25).  Rows on 16 bytes.
+// the row (four blocks to a thread and half as many warps took 29 us where this takes 25).  Rows with aligned eights.
 template <typename TE, typename TO>
 __global__ void __launch_bounds__(256, 8) embed_scaled_kernel(const EmbedArgs a, const FastDiv per_row, long long total) {
   const long long b = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(256, 8) embed_scaled_kernel(const EmbedArgs a,
   span_store<true>(static_cast<TO*>(a.out) + (long long)t * a.out_stride + col, left, 0, v);
 }
 
-// Rows off 16-byte boundaries: one warp per 256 columns of a token.
+// Rows whose eights are not aligned: one warp per 256 columns of a token.
 template <typename TE, typename TO>
 __global__ void __launch_bounds__(256) embed_rows_kernel(const EmbedArgs a, const FastDiv spans, long long total) {
   const PhiloxState ps = philox_state(a.mask);
@@ -112,6 +112,195 @@ __global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedArgs a, cons
     }
   }
   span_store<VEC>(dst, left, lane, acc);
+}
+
+// Sums of `count` <= 32 places of a list sorted by id, lane l holding place l's (id, token) and factor, over 256
+// columns: leave(id, last, sums) takes each id's.  VEC: aligned eights and cols % 8 == 0.
+template <typename TO, bool VEC, typename Leave>
+__device__ __forceinline__ void sum_places(const EmbedArgs& a, const PhiloxState& ps, const PhiloxKeys* keys, int c0, int left,
+                                           int lane, const uint2& own, float own_scale, int count, Leave leave) {
+  constexpr int kAhead = 4;  // rows in flight
+  // bfloat16 rows leave registers for the masks of all four at once (16384 x 1280, 65 ids: 30.6 us, one by one 32.3)
+  constexpr bool kMasksAhead = VEC && sizeof(TO) == 2;
+  int id = (int)__shfl_sync(0xffffffffu, own.x, 0);
+  const bool active = 8 * lane < left;
+  Pairs acc;
+  fill(acc, 0.f);
+  using Row = std::conditional_t<VEC, Raw8<TO>, Pairs>;
+  for (int j0 = 0; j0 < count; j0 += kAhead) {
+    Row g[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      // (past the end: the last row once more, which is not added)
+      const int t = (int)__shfl_sync(0xffffffffu, own.y, min(j0 + j, count - 1));
+      const TO* row = static_cast<const TO*>(a.out) + (size_t)t * a.out_stride + c0;
+      if constexpr (VEC) g[j].load(row + (active ? 8 * lane : 0), 8);
+      else span_load<false>(row, left, lane, g[j]);
+    }
+    uint4 words[kMasksAhead ? kAhead : 1];
+    if (kMasksAhead && a.mask.rng) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const uint32_t t = __shfl_sync(0xffffffffu, own.y, min(j0 + j, count - 1));
+        words[j] = drop_words(a.mask, ps, keys, (unsigned long long)t * ((a.cols + 7) / 8) + c0 / 8 + lane);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int t = (int)__shfl_sync(0xffffffffu, own.y, j0 + j), v = (int)__shfl_sync(0xffffffffu, own.x, j0 + j);
+      const float f = __shfl_sync(0xffffffffu, own_scale, j0 + j);
+      if (j0 + j >= count) break;
+      if (v != id) {
+        leave(id, false, acc);
+        id = v;
+        fill(acc, 0.f);
+      }
+      Pairs p;
+      if constexpr (VEC) {
+        g[j].get(p);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = g[j][k];
+      }
+      if constexpr (kMasksAhead) {
+        if (a.mask.rng) keep(words[j], ps, p);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = f2_fma(p[k], f2_both(f), acc[k]);
+      } else {
+        add_token<VEC>(a, ps, keys, t, c0, lane, f, p, acc);
+      }
+    }
+  }
+  leave(id, true, acc);
+}
+
+// ---- the gradient of larger batches of few ids: chunks of 256 tokens, each sorted by its own block ----
+// A block sums a chunk's rows over 256 columns into part[chunk][id]; a second kernel adds the chunks.  Its eight
+// warps take 32 places each of the chunk's sorted list; an id that goes on over a warp's border leaves parts in
+// shared memory, which the warp in which it begins joins in order.
+constexpr int kChunk = 256, kChunkIds = 64, kChunkWarps = kChunk / 32;
+
+template <typename TO, bool VEC>
+__global__ void __launch_bounds__(kChunk, 3)
+    embed_grad_chunks_kernel(const EmbedArgs a, float* __restrict__ part, const FastDiv spans) {
+  __shared__ PhiloxKeys keys;
+  __shared__ int hist[kChunkWarps][kChunkIds];  // each warp's counts, then where its tokens of each id go
+  __shared__ int counts[kChunkIds], total;
+  __shared__ uint2 list[kChunk];  // (id, token)
+  __shared__ float scales[kChunk];
+  __shared__ ulonglong2 parts[kChunkWarps][2][2][32];  // as of the pieces below: a lane's eight columns in two halves
+  grid_dependency_launch();
+  const PhiloxState ps = philox_state(a.mask);
+  philox_keys(ps, &keys);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunk = (int)div_by(blockIdx.x, spans), c0 = (int)(blockIdx.x - chunk * spans.d) * 256, left = a.cols - c0;
+  for (int i = threadIdx.x; i < kChunkWarps * kChunkIds; i += kChunk) hist[i / kChunkIds][i % kChunkIds] = 0;
+  const int t = chunk * kChunk + threadIdx.x, my_id = t < a.tokens ? checked_id(a, t, c0 == 0) : -1;
+  const float my_scale = my_id >= 0 ? token_scale(a, t) * a.mask.scale : 0.f;
+  const uint32_t peers = __match_any_sync(0xffffffffu, my_id);
+  const int ahead = __popc(peers & ((1u << lane) - 1));
+  __syncthreads();
+  if (my_id >= 0 && ahead == 0) hist[warp][my_id] = __popc(peers);
+  __syncthreads();
+  if (warp == 0) {  // (two ids to a lane)
+    int own[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int w = 0; w < kChunkWarps; ++w) own[k] += hist[w][2 * lane + k];
+    int incl = own[0] + own[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    int at = incl - own[0] - own[1];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      counts[2 * lane + k] = own[k];
+#pragma unroll
+      for (int w = 0; w < kChunkWarps; ++w) {
+        const int c = hist[w][2 * lane + k];
+        hist[w][2 * lane + k] = at;
+        at += c;
+      }
+    }
+    if (lane == 31) total = incl;
+  }
+  __syncthreads();
+  if (my_id >= 0) {
+    const int place = hist[warp][my_id] + ahead;
+    list[place] = make_uint2((uint32_t)my_id, (uint32_t)t);
+    scales[place] = my_scale;
+  }
+  __syncthreads();
+  const int n = total, p0 = warp * 32, count = min(32, n - p0);
+  float* sums = part + (size_t)chunk * a.vocab * a.cols + c0;
+  if (count > 0) {
+    const uint2 own = lane < count ? list[p0 + lane] : make_uint2(0xffffffffu, 0);
+    const float own_scale = lane < count ? scales[p0 + lane] : 0.f;
+    const int before = p0 > 0 ? (int)list[p0 - 1].x : -1, after = p0 + 32 < n ? (int)list[p0 + 32].x : -1;
+    sum_places<TO, VEC>(a, ps, &keys, c0, left, lane, own, own_scale, count, [&](int id, bool last, Pairs& acc) {
+      const bool from_before = id == before, goes_on = last && id == after;
+      if (from_before || goes_on) {
+        parts[warp][from_before ? 0 : 1][0][lane] = make_ulonglong2(acc[0], acc[1]);
+        parts[warp][from_before ? 0 : 1][1][lane] = make_ulonglong2(acc[2], acc[3]);
+      } else {
+        span_store<VEC>(sums + (size_t)id * a.cols, left, lane, acc);
+      }
+    });
+  }
+  __syncthreads();
+  Pairs acc;
+  if (p0 + 32 < n) {
+    const uint32_t id = list[p0 + 31].x;
+    if (list[p0 + 32].x == id && !(p0 > 0 && list[p0 - 1].x == id)) {
+      fill(acc, 0.f);
+      for (int w = warp; w < kChunkWarps && (w == warp || (32 * w < n && list[32 * w].x == id)); ++w) {
+        const ulonglong2 lo = parts[w][w == warp][0][lane], hi = parts[w][w == warp][1][lane];
+        acc[0] = f2_add(acc[0], lo.x); acc[1] = f2_add(acc[1], lo.y);
+        acc[2] = f2_add(acc[2], hi.x); acc[3] = f2_add(acc[3], hi.y);
+      }
+      span_store<VEC>(sums + (size_t)id * a.cols, left, lane, acc);
+    }
+  }
+  fill(acc, 0.f);
+  for (int v = warp; v < a.vocab; v += kChunkWarps)
+    if (counts[v] == 0) span_store<VEC>(sums + (size_t)v * a.cols, left, lane, acc);
+}
+
+// d_table (+)= the chunks' sums: warp w of a block adds chunks w, w + 8, ... of 128 elements, then the warps' sums
+// are added in order.  VEC: four elements to a lane in one access.
+template <bool VEC>
+__global__ void __launch_bounds__(256) embed_grad_add_kernel(const EmbedArgs a, const float* __restrict__ part, int chunks) {
+  __shared__ float sums[8][128];
+  grid_dependency_wait();
+  const size_t n = (size_t)a.vocab * a.cols, first = (size_t)blockIdx.x * 128;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (VEC) {
+    if (first + 4 * lane < n) {
+#pragma unroll 8
+      for (int k = warp; k < chunks; k += 8) {
+        const float4 v = *reinterpret_cast<const float4*>(part + k * n + first + 4 * lane);
+        s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+      }
+    }
+  } else {
+#pragma unroll 2
+    for (int k = warp; k < chunks; k += 8)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (first + 4 * lane + e < n) s[e] += part[k * n + first + 4 * lane + e];
+  }
+  *reinterpret_cast<float4*>(&sums[warp][4 * lane]) = make_float4(s[0], s[1], s[2], s[3]);
+  __syncthreads();
+  if (threadIdx.x >= 128 || first + threadIdx.x >= n) return;
+  float v = a.accumulate ? a.d_table[first + threadIdx.x] : 0.f;
+  float own = sums[0][threadIdx.x];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) own += sums[w][threadIdx.x];
+  a.d_table[first + threadIdx.x] = v + own;
 }
 
 // ---- the gradient of larger batches: tokens sorted by id, then summed in pieces of 32 ----
@@ -257,14 +446,12 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
 // Sums of 32 consecutive places of the sorted list and 256 columns by one warp.  An id whose tokens all lie
 // within the piece is written at once; of an id that goes on over the piece's border the piece keeps its part:
 // part[piece][0] for one that began before, part[piece][1] for one that begins here and goes on.
-// VEC: rows on 16 bytes and cols % 8 == 0.
 constexpr int kPiece = 32;
 
 template <typename TO, bool VEC>
 __global__ void __launch_bounds__(32, 24)
     embed_grad_pieces_kernel(const EmbedArgs a, const uint2* __restrict__ list, const int* __restrict__ valid,
                              float* __restrict__ part, const FastDiv spans, long long total) {
-  constexpr int kAhead = 4;  // rows in flight
   __shared__ PhiloxKeys keys;
   const PhiloxState ps = philox_state(a.mask);
   philox_keys(ps, &keys);
@@ -280,11 +467,7 @@ __global__ void __launch_bounds__(32, 24)
   const uint2 own = lane < count ? list[p0 + lane] : make_uint2(0xffffffffu, 0);
   const float own_scale = lane < count ? token_scale(a, (int)own.y) * a.mask.scale : 0.f;
   const int before = p0 > 0 ? (int)list[p0 - 1].x : -1, after = p0 + kPiece < n ? (int)list[p0 + kPiece].x : -1;
-  int id = (int)__shfl_sync(0xffffffffu, own.x, 0);
-  const bool active = 8 * lane < left;
-  Pairs acc;
-  fill(acc, 0.f);
-  auto leave = [&](bool last) {
+  sum_places<TO, VEC>(a, ps, &keys, c0, left, lane, own, own_scale, count, [&](int id, bool last, Pairs& acc) {
     const bool from_before = id == before, goes_on = last && id == after;
     if (from_before || goes_on) {
       span_store<VEC>(part + ((size_t)piece * 2 + (from_before ? 0 : 1)) * a.cols + c0, left, lane, acc);
@@ -298,39 +481,7 @@ __global__ void __launch_bounds__(32, 24)
       for (int k = 0; k < 4; ++k) acc[k] = f2_add(acc[k], old[k]);
     }
     span_store<VEC>(dst, left, lane, acc);
-  };
-  using Row = std::conditional_t<VEC, Raw8<TO>, Pairs>;
-  for (int j0 = 0; j0 < count; j0 += kAhead) {
-    Row g[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      // (past the end: the last row once more, which is not added)
-      const int t = (int)__shfl_sync(0xffffffffu, own.y, min(j0 + j, count - 1));
-      const TO* row = static_cast<const TO*>(a.out) + (size_t)t * a.out_stride + c0;
-      if constexpr (VEC) g[j].load(row + (active ? 8 * lane : 0), 8);
-      else span_load<false>(row, left, lane, g[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int t = (int)__shfl_sync(0xffffffffu, own.y, j0 + j), v = (int)__shfl_sync(0xffffffffu, own.x, j0 + j);
-      const float f = __shfl_sync(0xffffffffu, own_scale, j0 + j);
-      if (j0 + j >= count) break;
-      if (v != id) {
-        leave(false);
-        id = v;
-        fill(acc, 0.f);
-      }
-      Pairs p;
-      if constexpr (VEC) {
-        g[j].get(p);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = g[j][k];
-      }
-      add_token<VEC>(a, ps, &keys, t, c0, lane, f, p, acc);
-    }
-  }
-  leave(true);
+  });
 }
 
 // Ids that cross borders: one block per piece in which such an id begins and 256 columns; its warps add
@@ -401,6 +552,10 @@ cudaError_t launch_lookup(const EmbedArgs& a, cudaStream_t st) {
 // Few tokens: a search through all of them for every id is one launch.
 bool direct(int tokens, int vocab) { return tokens <= 512 && (long long)vocab * tokens <= 1 << 18; }
 
+// Few ids: sums of every id per chunk of 256 tokens.
+bool by_chunks(int vocab) { return vocab <= kChunkIds; }
+int chunks_of(int tokens) { return (tokens + kChunk - 1) / kChunk; }
+
 struct GradWorkspace {
   size_t list[2], valid, part, total;
 };
@@ -422,6 +577,15 @@ cudaError_t launch_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaSt
   if (direct(a.tokens, a.vocab)) {
     embed_grad_kernel<TO, VEC><<<(unsigned)((spans * a.vocab + 7) / 8), 256, 0, st>>>(a, fast_div((uint32_t)spans), spans * a.vocab);
     return cudaGetLastError();
+  }
+  if (by_chunks(a.vocab)) {
+    float* part = static_cast<float*>(workspace);
+    const int chunks = chunks_of(a.tokens);
+    embed_grad_chunks_kernel<TO, VEC><<<(unsigned)(spans * chunks), kChunk, 0, st>>>(a, part, fast_div((uint32_t)spans));
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_after(embed_grad_add_kernel<VEC>, (unsigned)(((size_t)a.vocab * a.cols + 127) / 128), 256, st, a,
+                        (const float*)part, chunks);
   }
   const GradWorkspace w = grad_workspace(a.tokens, a.cols);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -461,7 +625,9 @@ cudaError_t launch_embed_scaled(const EmbedArgs& a, cudaStream_t st) {
 }
 
 size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols) {
-  return direct(tokens, vocab) ? 256 : grad_workspace(tokens, cols).total;
+  if (direct(tokens, vocab)) return 256;
+  if (by_chunks(vocab)) return ((size_t)chunks_of(tokens) * vocab * cols * 4 + 255) & ~size_t(255);
+  return grad_workspace(tokens, cols).total;
 }
 
 cudaError_t launch_embed_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaStream_t st) {
