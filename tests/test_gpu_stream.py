@@ -250,6 +250,23 @@ def test_embed_backward_of_large_batches(enc, T, V, cols):
     assert torch.equal(table, again)  # the order goes by the ids alone
 
 
+@pytest.mark.parametrize("T,V,cols", [(1, 8192, 8), (512, 1639, 1280), (511, 1638, 1280), (257, 33, 2056), (512, 3, 12)])
+@pytest.mark.parametrize("ids", ["any", "one", "none"])
+def test_embed_backward_of_few_tokens(enc, T, V, cols, ids):
+    """On both sides of the search's limits; a token count of zero clears the table or leaves it."""
+    g = _gen(T + V)
+    t = {"any": torch.randint(-1, V, (T,), device="cuda", generator=g), "one": torch.full((T,), V - 1),
+         "none": torch.full((T,), -1)}[ids].to(torch.int32).cuda()
+    d, kept = _randn(g, T, cols), _randn(g, V, cols)
+    want, mag = S.embed_backward(t.cpu().numpy(), to_np(d), V, 1.0, None, _factors(T, cols, 0.2))
+    for n in (T, 0):
+        for accumulate in (False, True):
+            table = kept.clone() if accumulate else torch.full((V, cols), float("nan"), device="cuda")
+            enc.op_embed_backward(t[:n], d[:n], table, dropout=_drop(0.2), accumulate=accumulate)
+            before = to_np(kept) if accumulate else 0.0
+            _within(table, (want if n else 0.0) + before, (n + 6) * U * ((mag if n else 0.0) + np.abs(before)))
+
+
 @pytest.mark.parametrize("T,V,cols", [(513, 1, 8), (769, 64, 1283), (2000, 63, 12), (1025, 2, 520), (4097, 33, 1280)])
 @pytest.mark.parametrize("ids", ["any", "one", "none", "runs", "first"])
 @pytest.mark.parametrize("td", [F32, BF16])

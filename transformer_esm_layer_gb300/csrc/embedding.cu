@@ -85,31 +85,49 @@ __device__ __forceinline__ void add_token(const EmbedArgs& a, const PhiloxState&
   for (int i = 0; i < 4; ++i) acc[i] = f2_fma(g[i], f2_both(f), acc[i]);
 }
 
-// One warp per id and 256 columns: it looks through all tokens, 32 at a time.
+// One block per id and 256 columns: its eight warps look through all tokens, 32 at a time in turn, and add the rows
+// that they find; their sums are then added in order.
 template <typename TO, bool VEC>
-__global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedArgs a, const FastDiv spans, long long total) {
+__global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedArgs a, const FastDiv spans) {
   __shared__ PhiloxKeys keys;
+  __shared__ ulonglong2 sums[8][2][32];  // a lane's eight columns in two halves
   const PhiloxState ps = philox_state(a.mask);
   philox_keys(ps, &keys);
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= total) return;
-  const int v = total <= INT32_MAX ? (int)div_by((uint32_t)i, spans) : (int)(i / spans.d);
-  const int c0 = (int)(i - (long long)v * spans.d) * 256, left = a.cols - c0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int v = (int)div_by(blockIdx.x, spans), c0 = (int)(blockIdx.x - v * spans.d) * 256, left = a.cols - c0;
   float* dst = a.d_table + (long long)v * a.cols + c0;
   Pairs acc;
   fill(acc, 0.f);
-  if (a.accumulate) span_load<VEC>(dst, left, lane, acc);
-  for (int t0 = 0; t0 < a.tokens; t0 += 32) {
+  bool any = false;
+  for (int t0 = 32 * warp; t0 < a.tokens; t0 += 256) {
     const int t = t0 + lane;
-    const int id = t < a.tokens ? checked_id(a, t, i == 0) : -1;
+    const int id = t < a.tokens ? checked_id(a, t, blockIdx.x == 0) : -1;
     for (uint32_t hit = __ballot_sync(0xffffffffu, id == v); hit; hit &= hit - 1) {
       const int m = t0 + __ffs(hit) - 1;
       Pairs g;
       span_load<VEC>(static_cast<const TO*>(a.out) + m * a.out_stride + c0, left, lane, g);
       add_token<VEC>(a, ps, &keys, m, c0, lane, token_scale(a, m) * a.mask.scale, g, acc);
+      any = true;
     }
+  }
+  sums[warp][0][lane] = make_ulonglong2(acc[0], acc[1]);
+  sums[warp][1][lane] = make_ulonglong2(acc[2], acc[3]);
+  any = __syncthreads_or(any);
+  if (warp || (a.accumulate && !any)) return;
+  fill(acc, 0.f);
+  if (any) {
+    if (a.accumulate) span_load<VEC>(dst, left, lane, acc);
+    Pairs total;
+    fill(total, 0.f);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const ulonglong2 lo = sums[w][0][lane], hi = sums[w][1][lane];
+      total[0] = f2_add(total[0], lo.x); total[1] = f2_add(total[1], lo.y);
+      total[2] = f2_add(total[2], hi.x); total[3] = f2_add(total[3], hi.y);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = f2_add(acc[k], total[k]);
   }
   span_store<VEC>(dst, left, lane, acc);
 }
@@ -549,10 +567,15 @@ cudaError_t launch_lookup(const EmbedArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Few tokens: a search through all of them for every id is one launch.
-bool direct(int tokens, int vocab) { return tokens <= 512 && (long long)vocab * tokens <= 1 << 18; }
+// Few tokens: a search through all of them for every id is one launch (1280 columns, 33 ids, 173 tokens: 2.6 us, of
+// which the worst, one id's alone, take 8; by chunks 8.2; 300 ids, 512 tokens: 4.6 us, sorted 15).  The blocks of ids
+// that are not met cost too: 1000 ids take 10 us, 2000 17, and sorted 16.
+bool direct(int tokens, int vocab, int cols) {
+  return tokens <= 512 && (long long)vocab * ((cols + 255) / 256) <= 8192;
+}
 
-// Few ids: sums of every id per chunk of 256 tokens.
+// Few ids: sums of every id per chunk of 256 tokens (16384 x 1280: 64 ids 28.5 us, sorted 33; with more ids what
+// the chunks leave grows, and what is saved shrinks).
 bool by_chunks(int vocab) { return vocab <= kChunkIds; }
 int chunks_of(int tokens) { return (tokens + kChunk - 1) / kChunk; }
 
@@ -574,8 +597,10 @@ GradWorkspace grad_workspace(int tokens, int cols) {
 template <typename TO, bool VEC>
 cudaError_t launch_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaStream_t st) {
   const long long spans = (a.cols + 255) / 256;
-  if (direct(a.tokens, a.vocab)) {
-    embed_grad_kernel<TO, VEC><<<(unsigned)((spans * a.vocab + 7) / 8), 256, 0, st>>>(a, fast_div((uint32_t)spans), spans * a.vocab);
+  if (a.tokens == 0)
+    return a.accumulate ? cudaSuccess : cudaMemsetAsync(a.d_table, 0, 4 * (size_t)a.vocab * a.cols, st);
+  if (direct(a.tokens, a.vocab, a.cols)) {
+    embed_grad_kernel<TO, VEC><<<(unsigned)(spans * a.vocab), 256, 0, st>>>(a, fast_div((uint32_t)spans));
     return cudaGetLastError();
   }
   if (by_chunks(a.vocab)) {
@@ -625,7 +650,7 @@ cudaError_t launch_embed_scaled(const EmbedArgs& a, cudaStream_t st) {
 }
 
 size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols) {
-  if (direct(tokens, vocab)) return 256;
+  if (direct(tokens, vocab, cols)) return 256;
   if (by_chunks(vocab)) return ((size_t)chunks_of(tokens) * vocab * cols * 4 + 255) & ~size_t(255);
   return grad_workspace(tokens, cols).total;
 }
