@@ -322,7 +322,10 @@ __device__ __forceinline__ float warp_sum4(float (&v)[4], int lane) {
 }
 
 constexpr int kSums = 4;         // column sums: d_h xh, d_h, P, Q
-constexpr int kBwdWarps = 20;    // warps of a block
+constexpr int kBwdWarps = 20;    // warps of a block at most
+// ... with rows of T: by the registers that a float32 block's values take, and its rows leave room for no more
+template <typename T>
+constexpr int kWarpsOf = sizeof(T) == 2 ? kBwdWarps : 16;
 
 constexpr int kStages = 2;
 constexpr int kMaxGroups = 15;  // named barriers
@@ -334,7 +337,7 @@ constexpr int kMaxGroups = 15;  // named barriers
 // group, which leaves the threads and the L1 out of it; gamma_pre and scale gate gamma_post stand in shared
 // memory as float32.
 template <typename T, bool RMS>
-__global__ void __launch_bounds__(32 * kBwdWarps, 1)
+__global__ void __launch_bounds__(32 * kWarpsOf<T>, 1)
     block_norm_bwd_kernel(const BlockNormArgs a, int W, int groups, float* __restrict__ partial) {
   extern __shared__ __align__(16) uint8_t smem[];  // vectors, column sums, the rows on their way
   __shared__ float red[2][kBwdWarps][8];           // the two latest rows' sums of every warp
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1)
     if (!pre) st.w = 0.f;  // (no norm's columns may hold anything)
     const uint8_t* values = from + 16;
     auto row_f = [&](int i, Pairs& v) { ld8_shared(reinterpret_cast<const float*>(values + i * f_bytes) + w * 256, lane, v); };
-    auto row_t = [&](int i, Pairs& v) { ld8(reinterpret_cast<const T*>(values + 2 * f_bytes + i * t_bytes) + c, v); };
+    auto row_t = [&](int i, Pairs& v) { ld8_shared(reinterpret_cast<const T*>(values + 2 * f_bytes + i * t_bytes) + w * 256, lane, v); };
     Pairs xh, e, yh, kept, p;
     float s[8];
     // all bits or none, per element: a dropped place is 0 whatever it holds
@@ -914,7 +917,7 @@ cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num
     s.groups = std::min(s.groups, 16 / s.W);
     e = vec ? launch_bwd_any<T, true, 1>(a, s, partial, st) : launch_bwd_any<T, false, 1>(a, s, partial, st);
   } else {
-    s.groups = (int)std::min((size_t)s.groups, fits);
+    s.groups = (int)std::min({(size_t)s.groups, fits, (size_t)(kWarpsOf<T> / s.W)});
     const size_t smem = fixed + group * s.groups;
     const auto kernel = a.rms ? block_norm_bwd_kernel<T, true> : block_norm_bwd_kernel<T, false>;
     e = allow_smem(kernel, smem);

@@ -179,8 +179,8 @@ __device__ __forceinline__ void st8(__nv_bfloat16* p, const Pairs& v) {
 // that eight lanes meet all banks.
 __device__ __forceinline__ void ld8_shared(const float* p, int lane, Pairs& v) {
   const bool upper = lane & 4;
-  const ulonglong2* at = reinterpret_cast<const ulonglong2*>(p + 8 * lane);
-  const ulonglong2 f = at[upper], s = at[!upper];
+  const int at = 8 * lane + (lane & 4);
+  const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(p + at), s = *reinterpret_cast<const ulonglong2*>(p + (at ^ 4));
   v[0] = upper ? s.x : f.x; v[1] = upper ? s.y : f.y; v[2] = upper ? f.x : s.x; v[3] = upper ? f.y : s.y;
 }
 __device__ __forceinline__ void ld8_shared(const __nv_bfloat16* p, int lane, Pairs& v) { ld8(p + 8 * lane, v); }
