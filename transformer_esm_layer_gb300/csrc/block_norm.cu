@@ -6,7 +6,9 @@
 //
 // Bound by memory: 12 bytes an element forward and 18 backward with bfloat16 blocks (the residual
 // stream and its gradient are float32).  So every value is read and written once, a row's statistics and
-// sums never leave the SM, and the rows to come are copied into shared memory while this one is worked on.
+// sums never leave the SM.  16384 x 1280 with two LayerNorms, gate and dropout: forward 46.3 us, 5.4 TB/s (the same
+// five streams copied without arithmetic: 39.5 us), backward 73.7 us, 5.1 TB/s; without the dropout 44.3 and 68: the
+// instructions of masks, sums and statistics are what keeps them off the memory's rate.
 #include <algorithm>
 #include <type_traits>
 
@@ -19,7 +21,7 @@ namespace {
 // ---- forward ----
 // A block takes R rows, W warps to each; a warp holds G spans of 256 columns, eight of each to a lane.  Rows
 // come as blocks of the grid, not in a loop: the SM holds 25 to 40 warps whose loads, sums and stores interleave
-// by themselves (blocks that stay, with rows copied ahead by the threads, took 60 us where this takes 49.5).
+// by themselves (blocks that stay, with rows copied ahead by the threads, took 60 us where this took 49.5).
 // Up to 2048 columns G = 1, and R = 2 where there are rows enough: the parameters are read and unpacked once
 // for both, the generator's round keys are shared, and one barrier serves both rows' sums.
 struct RowShape {
@@ -321,18 +323,18 @@ __device__ __forceinline__ float warp_sum4(float (&v)[4], int lane) {
   return total;
 }
 
-constexpr int kSums = 4;         // column sums: d_h xh, d_h, P, Q
-constexpr int kBwdWarps = 20;    // warps of a block at most
-// ... with rows of T: by the registers that a float32 block's values take, and its rows leave room for no more
+constexpr int kSums = 4;        // column sums: d_h xh, d_h, P, Q
+constexpr int kBwdWarps = 20;   // warps of a block at most
+constexpr int kStages = 2;      // rows of a group on their way (three were no faster)
+constexpr int kMaxGroups = 15;  // named barriers
+// The same with blocks of T: 96 registers are enough for bfloat16 ones (16384 x 1280: 73.7 us, 16 warps 81), float32 ones
+// spill (84.8 us with 16 warps and 128 registers, 117 with 20).
 template <typename T>
 constexpr int kWarpsOf = sizeof(T) == 2 ? kBwdWarps : 16;
 
-constexpr int kStages = 2;
-constexpr int kMaxGroups = 15;  // named barriers
-
 // Aligned eights, cols % 8 == 0 and <= 4096.  A block of `groups` groups of W = ceil(cols / 256) warps stays on
 // its SM and takes a row per group and step; a lane owns eight columns of every row that its group takes, so
-// the four column sums stay with it (in shared memory: 32 registers fewer let 20 warps run, not 16) and leave
+// the four column sums stay with it (in shared memory, which frees 32 registers) and leave
 // once per block, into partial[block][kSums][cols].  The rows to come arrive by bulk copies, kStages of them per
 // group, which leaves the threads and the L1 out of it; gamma_pre and scale gate gamma_post stand in shared
 // memory as float32.
@@ -592,12 +594,13 @@ __global__ void __launch_bounds__(32 * kWarpsOf<T>, 1)
   }
 }
 
-// Any alignment, and rows of up to 8192 columns: the same sums, rows read where they are used and parameters
-// from the L1; a lane owns 8 G columns, G = 2 with its column sums in shared memory.
+// Any alignment, and rows of up to 8192 columns: the same sums, rows read where they are used (the next one is
+// brought into the L2) and parameters from the L1; a lane owns 8 G columns, G = 2 with its column sums in shared
+// memory.  One row a block at a time, then: 4096 x 5120 179 us, 2560 x 8192 148, 16384 x 1283 238.
 template <typename T, bool VEC, int G>
 __global__ void __launch_bounds__(512, 1)
     block_norm_bwd_any_kernel(const BlockNormArgs a, int W, int groups, float* __restrict__ partial) {
-  extern __shared__ float sums[];          // [kSums][cols]
+  extern __shared__ __align__(16) float sums[];  // [kSums][cols], or each lane's own
   __shared__ float red[2][kBwdWarps][8];  // the two latest rows' sums of every warp
   grid_dependency_launch();
   __shared__ PhiloxKeys keys;
@@ -607,13 +610,15 @@ __global__ void __launch_bounds__(512, 1)
   const long long first = (long long)blockIdx.x * groups + group, step = (long long)gridDim.x * groups;
   const PhiloxState ps = philox_state(a.mask);
   philox_keys(ps, &keys);
-  const int own_left = a.cols - w * 256;
+  const int own_left = a.cols - w * 256 * G;
   auto load = [&](const void* p, size_t at, int left, Pairs& out) { span_load<VEC>(static_cast<const T*>(p) + at, left, lane, out); };
+  // G = 2: sum i of a lane's eight columns of its span g, in two halves
+  auto own_sums = [&](int i, int g) { return reinterpret_cast<ulonglong2*>(sums) + ((i * G + g) * W + w) * 64 + lane; };
   Pairs acc[G == 1 ? kSums : 1];
 #pragma unroll
   for (int i = 0; i < (G == 1 ? kSums : 1); ++i) fill(acc[i], 0.f);
   if constexpr (G > 1) {
-    for (int i = threadIdx.x; i < kSums * a.cols; i += blockDim.x) sums[i] = 0.f;
+    for (int i = threadIdx.x; i < kSums * G * W * 256; i += blockDim.x) sums[i] = 0.f;
   }
   __syncthreads();
   const float inv_n = 1.f / (float)a.cols;
@@ -628,6 +633,29 @@ __global__ void __launch_bounds__(512, 1)
   for (long long row = first; row < a.rows; row += step) {
     const float4 st = next;
     next = statistics(row + step);
+    // the next row into the L2
+    if (VEC && w == 0 && lane == 0 && row + step < a.rows) {
+      const size_t at = (size_t)(row + step) * a.cols;
+      const uint32_t t_bytes = (uint32_t)a.cols * sizeof(T);
+      if (a.d_x_out) bulk_prefetch(a.d_x_out + at, 4 * (uint32_t)a.cols);
+      if (pre) bulk_prefetch(a.x_out + at, 4 * (uint32_t)a.cols);
+      bulk_prefetch(static_cast<const T*>(a.y) + at, t_bytes);
+      if (pre) bulk_prefetch(static_cast<const T*>(a.d_h) + at, t_bytes);
+      if (a.gate_rows) bulk_prefetch(static_cast<const T*>(a.gate) + at, t_bytes);
+    }
+    if (!VEC && row + step < a.rows) {
+      const size_t at = (size_t)(row + step) * a.cols + w * 256 * G;
+      constexpr int kLine = 128 / sizeof(T);
+      if (32 * lane < min(256 * G, own_left)) {
+        if (a.d_x_out) prefetch_l2(a.d_x_out + at + 32 * lane);
+        if (pre) prefetch_l2(a.x_out + at + 32 * lane);
+      }
+      if (kLine * lane < min(256 * G, own_left)) {
+        prefetch_l2(static_cast<const T*>(a.y) + at + kLine * lane);
+        if (pre) prefetch_l2(static_cast<const T*>(a.d_h) + at + kLine * lane);
+        if (a.gate_rows) prefetch_l2(static_cast<const T*>(a.gate) + at + kLine * lane);
+      }
+    }
     const uint64_t minus_x = f2_both(-st.z), rx = f2_both(st.w), minus_y = f2_both(-st.x), ry = f2_both(st.y);
     Pairs xh[G], e[G], yh[G];
     uint4 words[G];
@@ -637,14 +665,12 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[i][k] = f2_add(acc[i][k], v[k]);
       } else {
-        const int c0 = (g * W + w) * 256;
-        float* to = sums + (size_t)i * a.cols + c0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int p = span_col<VEC>(lane, 2 * k), q = span_col<VEC>(lane, 2 * k + 1);
-          if (c0 + p < a.cols) to[p] += f2_lo(v[k]);
-          if (c0 + q < a.cols) to[q] += f2_hi(v[k]);
-        }
+        ulonglong2* to = own_sums(i, g);
+        ulonglong2 lo = to[0], hi = to[32];
+        lo.x = f2_add(lo.x, v[0]); lo.y = f2_add(lo.y, v[1]);
+        hi.x = f2_add(hi.x, v[2]); hi.y = f2_add(hi.y, v[3]);
+        to[0] = lo;
+        to[32] = hi;
       }
     };
     auto add_product = [&](int g, int i, const Pairs& v, const Pairs& by) {
@@ -824,11 +850,19 @@ __global__ void __launch_bounds__(512, 1)
       }
       __syncthreads();
     }
+    for (int i = threadIdx.x; i < kSums * a.cols; i += blockDim.x)
+      partial[(size_t)blockIdx.x * kSums * a.cols + i] = sums[i];
   } else {
-    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSums; ++i)
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int c0 = (g * W + w) * 256;
+        const ulonglong2 lo = own_sums(i, g)[0], hi = own_sums(i, g)[32];
+        const Pairs v = {lo.x, lo.y, hi.x, hi.y};
+        span_store<VEC>(partial + ((size_t)blockIdx.x * kSums + i) * a.cols + c0, a.cols - c0, lane, v);
+      }
   }
-  for (int i = threadIdx.x; i < kSums * a.cols; i += blockDim.x)
-    partial[(size_t)blockIdx.x * kSums * a.cols + i] = sums[i];
 }
 
 // The parameters' gradients from the blocks' column sums, in a fixed order: warp w of a block adds blocks
@@ -897,7 +931,7 @@ cudaError_t allow_smem(Kernel k, size_t smem) {
 
 template <typename T, bool VEC, int G>
 cudaError_t launch_bwd_any(const BlockNormArgs& a, const BwdShape& s, float* partial, cudaStream_t st) {
-  const size_t smem = sizeof(float) * kSums * a.cols;
+  const size_t smem = sizeof(float) * kSums * (G == 1 ? a.cols : G * s.W * 256);
   const cudaError_t e = allow_smem(block_norm_bwd_any_kernel<T, VEC, G>, smem);
   if (e != cudaSuccess) return e;
   block_norm_bwd_any_kernel<T, VEC, G><<<s.blocks, 32 * s.W * s.groups, smem, st>>>(a, s.W, s.groups, partial);
@@ -913,7 +947,7 @@ cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num
   cudaError_t e;
   if (s.G == 2) {
     e = vec ? launch_bwd_any<T, true, 2>(a, s, partial, st) : launch_bwd_any<T, false, 2>(a, s, partial, st);
-  } else if (!vec || a.cols % 8 || fits == 0) {
+  } else if (!vec || fits == 0) {
     s.groups = std::min(s.groups, 16 / s.W);
     e = vec ? launch_bwd_any<T, true, 1>(a, s, partial, st) : launch_bwd_any<T, false, 1>(a, s, partial, st);
   } else {
@@ -929,8 +963,8 @@ cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num
   return launch_after(block_norm_sums_kernel<T>, 2 * ((a.cols + 31) / 32), 1024, st, a, (const float*)partial, s.blocks);
 }
 
-// W warps to a row of up to 4096 columns.  Registers for 800 threads an SM with bfloat16 blocks (80 each; 16384 x
-// 1280: 49.5 us, with 64 registers 52, with 104 56) and for 640 with float32 ones (68.6 us, with 80 registers 82).
+// W warps to a row of up to 4096 columns.  Registers for 800 threads an SM with bfloat16 blocks (72 each; 16384 x
+// 1280: 46.3 us, for 640 threads 53.9, for 960 48.7) and for 640 with float32 ones (55.7 us, for 512 64.2).
 template <typename T, int W>
 void launch_fwd_as(const BlockNormArgs& a, const RowShape& s, int spans, int num_sms, cudaStream_t st) {
   constexpr int kThreads = 32 * W, kBlocks = std::min(24, (sizeof(T) == 2 ? 800 : 640) / kThreads);
@@ -945,18 +979,22 @@ void launch_fwd_as(const BlockNormArgs& a, const RowShape& s, int spans, int num
 template <typename T>
 cudaError_t launch_fwd(const BlockNormArgs& a, bool vec, int num_sms, cudaStream_t st) {
   const int spans = (a.cols + 255) / 256;
-  const bool by_width = vec && a.cols % 8 == 0 && spans <= 16;
-  const int G = by_width && spans > 8 ? 2 : 1, W = (spans + G - 1) / G;
+  const bool by_width = vec && spans <= 16;
+  const int G = vec && spans > 8 ? 2 : 1, W = (spans + G - 1) / G;
   RowShape s;
   s.inv_cols = 1.f / (float)a.cols;
   s.last = (float)(a.cols - 256 * G * (W - 1));
   s.inv_last = 1.f / s.last;
   if (!by_width) {
     const unsigned rows = (unsigned)a.rows;
-    const int threads = 32 * spans;
-    if (vec && a.cols % 8 == 0) block_norm_kernel<T, true, 0, 1, 1, 1024, 1><<<rows, threads, 0, st>>>(a, s);
-    else if (spans <= 8) block_norm_kernel<T, false, 0, 1, 1, 256, 4><<<rows, threads, 0, st>>>(a, s);
-    else block_norm_kernel<T, false, 0, 1, 1, 1024, 1><<<rows, threads, 0, st>>>(a, s);
+    if (vec) {
+      // (4096 x 5120: 57 us, 2560 x 8192: 63; a span a warp, one block an SM: 102 and 100)
+      block_norm_kernel<T, true, 0, 1, 2, 512, 2><<<rows, 32 * W, 0, st>>>(a, s);
+    } else if (spans <= 8) {
+      block_norm_kernel<T, false, 0, 1, 1, 256, 4><<<rows, 32 * W, 0, st>>>(a, s);
+    } else {
+      block_norm_kernel<T, false, 0, 1, 1, 1024, 1><<<rows, 32 * W, 0, st>>>(a, s);
+    }
     return cudaGetLastError();
   }
   switch (W) {
@@ -972,7 +1010,7 @@ cudaError_t launch_fwd(const BlockNormArgs& a, bool vec, int num_sms, cudaStream
   return cudaGetLastError();
 }
 
-// a row's or parameter's eight values at a time
+// A row's or parameter's eight values at a time (cols % 8 == 0 is part of it).
 bool all_on_eights(const BlockNormArgs& a, bool bf16) {
   const int es = bf16 ? 2 : 4, n = a.cols;
   return rows_on_eights(a.y, n, es) && rows_on_eights(a.x, n, 4) && rows_on_eights(a.x_out, n, 4) && rows_on_eights(a.h, n, es) &&
