@@ -3,7 +3,9 @@
 //   d_table[v] (+)= scale * sum over t with id_t = v of row_scale[t] * keep(t, c) * drop_scale * d_out[t]
 // The sums run in a fixed order, so results do not depend on scheduling.
 //
-// Bound by memory: the rows met and the output; for the gradient d_out and the table's rows.
+// Bound by memory: the rows met and the output; for the gradient d_out and the table's rows.  16384 tokens x 1280:
+// lookup in 50021 float32 rows 25.2 us (4.5 TB/s of the bytes that it cannot do without); gradient of 33 ids 26.7 us, of
+// 50021 64.2 us, of which 38 clear the table.
 #include <algorithm>
 #include <type_traits>
 
@@ -327,7 +329,8 @@ __global__ void __launch_bounds__(256) embed_grad_add_kernel(const EmbedArgs a, 
 // list; per pass it counts its digits (lanes with equal digits find each other by match, so one lane writes
 // each count and no atomics order anything), the blocks exchange their counts through distributed shared
 // memory, and every warp then knows where each of its digits goes.  Up to 8 bits per pass: one pass for
-// 256 ids, two for 65536.  The rest of the grid meanwhile clears d_table.
+// 256 ids, two for 65536 (16384 tokens: 15.7 us alone).  The rest of the grid meanwhile clears d_table (rows that the
+// sort may not name left to the sums' launch: 69 us and more where all of it takes 66).
 constexpr int kSortBlocks = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 8, kBins = 1 << kDigitBits;
 
