@@ -267,7 +267,8 @@ def test_embed_backward_of_few_tokens(enc, T, V, cols, ids):
             _within(table, (want if n else 0.0) + before, (n + 6) * U * ((mag if n else 0.0) + np.abs(before)))
 
 
-@pytest.mark.parametrize("T,V,cols", [(513, 1, 8), (769, 64, 1283), (2000, 63, 12), (1025, 2, 520), (4097, 33, 1280)])
+@pytest.mark.parametrize("T,V,cols", [(513, 1, 8), (769, 64, 1283), (2000, 63, 12), (1025, 2, 520), (4097, 33, 1280),
+                                      (16384, 33, 1280), (9000, 64, 1283), (40000, 9, 520)])
 @pytest.mark.parametrize("ids", ["any", "one", "none", "runs", "first"])
 @pytest.mark.parametrize("td", [F32, BF16])
 def test_embed_backward_of_few_ids(enc, T, V, cols, ids, td):

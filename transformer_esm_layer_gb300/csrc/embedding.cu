@@ -4,8 +4,8 @@
 // The sums run in a fixed order, so results do not depend on scheduling.
 //
 // Bound by memory: the rows met and the output; for the gradient d_out and the table's rows.  16384 tokens x 1280:
-// lookup in 50021 float32 rows 25.2 us (4.5 TB/s of the bytes that it cannot do without); gradient of 33 ids 26.7 us, of
-// 50021 64.2 us, of which 38 clear the table.
+// lookup in 50021 float32 rows 25.2 us (4.5 TB/s of the bytes that it cannot do without); gradient of 33 ids 24.7 us (14.5
+// without the dropout, 5.8 TB/s: the rest is its masks' instructions), of 50021 64.2 us, of which 38 clear the table.
 #include <algorithm>
 #include <type_traits>
 
@@ -135,13 +135,12 @@ __global__ void __launch_bounds__(256) embed_grad_kernel(const EmbedArgs a, cons
 }
 
 // Sums of `count` <= 32 places of a list sorted by id, lane l holding place l's (id, token) and factor, over 256
-// columns: leave(id, last, sums) takes each id's.  VEC: aligned eights and cols % 8 == 0.
-template <typename TO, bool VEC, typename Leave>
+// columns: leave(id, last, sums) takes each id's.  VEC: aligned eights and cols % 8 == 0.  MASKS_AHEAD: the masks of four
+// rows at once while they are on their way, for 16 registers more.
+template <typename TO, bool VEC, bool MASKS_AHEAD, typename Leave>
 __device__ __forceinline__ void sum_places(const EmbedArgs& a, const PhiloxState& ps, const PhiloxKeys* keys, int c0, int left,
                                            int lane, const uint2& own, float own_scale, int count, Leave leave) {
   constexpr int kAhead = 4;  // rows in flight
-  // bfloat16 rows leave registers for the masks of all four at once (16384 x 1280, 65 ids: 30.6 us, one by one 32.3)
-  constexpr bool kMasksAhead = VEC && sizeof(TO) == 2;
   int id = (int)__shfl_sync(0xffffffffu, own.x, 0);
   const bool active = 8 * lane < left;
   Pairs acc;
@@ -157,8 +156,8 @@ __device__ __forceinline__ void sum_places(const EmbedArgs& a, const PhiloxState
       if constexpr (VEC) g[j].load(row + (active ? 8 * lane : 0), 8);
       else span_load<false>(row, left, lane, g[j]);
     }
-    uint4 words[kMasksAhead ? kAhead : 1];
-    if (kMasksAhead && a.mask.rng) {
+    uint4 words[MASKS_AHEAD ? kAhead : 1];
+    if (MASKS_AHEAD && a.mask.rng) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const uint32_t t = __shfl_sync(0xffffffffu, own.y, min(j0 + j, count - 1));
@@ -182,7 +181,7 @@ __device__ __forceinline__ void sum_places(const EmbedArgs& a, const PhiloxState
 #pragma unroll
         for (int k = 0; k < 4; ++k) p[k] = g[j][k];
       }
-      if constexpr (kMasksAhead) {
+      if constexpr (MASKS_AHEAD) {
         if (a.mask.rng) keep(words[j], ps, p);
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[k] = f2_fma(p[k], f2_both(f), acc[k]);
@@ -194,15 +193,15 @@ __device__ __forceinline__ void sum_places(const EmbedArgs& a, const PhiloxState
   leave(id, true, acc);
 }
 
-// ---- the gradient of larger batches of few ids: chunks of 256 tokens, each sorted by its own block ----
+// ---- the gradient of larger batches of few ids: chunks of up to 256 tokens, each sorted by its own block ----
 // A block sums a chunk's rows over 256 columns into part[chunk][id]; a second kernel adds the chunks.  Its eight
-// warps take 32 places each of the chunk's sorted list; an id that goes on over a warp's border leaves parts in
+// warps take up to 32 places each of the chunk's sorted list; an id that goes on over a warp's border leaves parts in
 // shared memory, which the warp in which it begins joins in order.
-constexpr int kChunk = 256, kChunkIds = 64, kChunkWarps = kChunk / 32;
+constexpr int kChunk = 256, kShortChunk = 64, kChunkIds = 64, kChunkWarps = kChunk / 32;
 
 template <typename TO, bool VEC>
 __global__ void __launch_bounds__(kChunk, 3)
-    embed_grad_chunks_kernel(const EmbedArgs a, float* __restrict__ part, const FastDiv spans) {
+    embed_grad_chunks_kernel(const EmbedArgs a, float* __restrict__ part, const FastDiv spans, int length) {
   __shared__ PhiloxKeys keys;
   __shared__ int hist[kChunkWarps][kChunkIds];  // each warp's counts, then where its tokens of each id go
   __shared__ int counts[kChunkIds], total;
@@ -215,7 +214,8 @@ __global__ void __launch_bounds__(kChunk, 3)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = (int)div_by(blockIdx.x, spans), c0 = (int)(blockIdx.x - chunk * spans.d) * 256, left = a.cols - c0;
   for (int i = threadIdx.x; i < kChunkWarps * kChunkIds; i += kChunk) hist[i / kChunkIds][i % kChunkIds] = 0;
-  const int t = chunk * kChunk + threadIdx.x, my_id = t < a.tokens ? checked_id(a, t, c0 == 0) : -1;
+  const int t = chunk * length + threadIdx.x;
+  const int my_id = (int)threadIdx.x < length && t < a.tokens ? checked_id(a, t, c0 == 0) : -1;
   const float my_scale = my_id >= 0 ? token_scale(a, t) * a.mask.scale : 0.f;
   const uint32_t peers = __match_any_sync(0xffffffffu, my_id);
   const int ahead = __popc(peers & ((1u << lane) - 1));
@@ -254,13 +254,17 @@ __global__ void __launch_bounds__(kChunk, 3)
     scales[place] = my_scale;
   }
   __syncthreads();
-  const int n = total, p0 = warp * 32, count = min(32, n - p0);
+  // (four places to a step of a warp)
+  const int n = total, per = (n + 4 * kChunkWarps - 1) / (4 * kChunkWarps) * 4, p0 = warp * per, end = p0 + per;
+  const int count = min(per, n - p0);
   float* sums = part + (size_t)chunk * a.vocab * a.cols + c0;
   if (count > 0) {
     const uint2 own = lane < count ? list[p0 + lane] : make_uint2(0xffffffffu, 0);
     const float own_scale = lane < count ? scales[p0 + lane] : 0.f;
-    const int before = p0 > 0 ? (int)list[p0 - 1].x : -1, after = p0 + 32 < n ? (int)list[p0 + 32].x : -1;
-    sum_places<TO, VEC>(a, ps, &keys, c0, left, lane, own, own_scale, count, [&](int id, bool last, Pairs& acc) {
+    const int before = p0 > 0 ? (int)list[p0 - 1].x : -1, after = end < n ? (int)list[end].x : -1;
+    // (masks ahead with float32 rows: 30 us for 25)
+    constexpr bool kMasksAhead = VEC && sizeof(TO) == 2;
+    sum_places<TO, VEC, kMasksAhead>(a, ps, &keys, c0, left, lane, own, own_scale, count, [&](int id, bool last, Pairs& acc) {
       const bool from_before = id == before, goes_on = last && id == after;
       if (from_before || goes_on) {
         parts[warp][from_before ? 0 : 1][0][lane] = make_ulonglong2(acc[0], acc[1]);
@@ -272,11 +276,11 @@ __global__ void __launch_bounds__(kChunk, 3)
   }
   __syncthreads();
   Pairs acc;
-  if (p0 + 32 < n) {
-    const uint32_t id = list[p0 + 31].x;
-    if (list[p0 + 32].x == id && !(p0 > 0 && list[p0 - 1].x == id)) {
+  if (end < n) {
+    const uint32_t id = list[end - 1].x;
+    if (list[end].x == id && !(p0 > 0 && list[p0 - 1].x == id)) {
       fill(acc, 0.f);
-      for (int w = warp; w < kChunkWarps && (w == warp || (32 * w < n && list[32 * w].x == id)); ++w) {
+      for (int w = warp; w < kChunkWarps && (w == warp || (per * w < n && list[per * w].x == id)); ++w) {
         const ulonglong2 lo = parts[w][w == warp][0][lane], hi = parts[w][w == warp][1][lane];
         acc[0] = f2_add(acc[0], lo.x); acc[1] = f2_add(acc[1], lo.y);
         acc[2] = f2_add(acc[2], hi.x); acc[3] = f2_add(acc[3], hi.y);
@@ -488,7 +492,8 @@ __global__ void __launch_bounds__(32, 24)
   const uint2 own = lane < count ? list[p0 + lane] : make_uint2(0xffffffffu, 0);
   const float own_scale = lane < count ? token_scale(a, (int)own.y) * a.mask.scale : 0.f;
   const int before = p0 > 0 ? (int)list[p0 - 1].x : -1, after = p0 + kPiece < n ? (int)list[p0 + kPiece].x : -1;
-  sum_places<TO, VEC>(a, ps, &keys, c0, left, lane, own, own_scale, count, [&](int id, bool last, Pairs& acc) {
+  // (65536 x 1280, 65 ids: masks ahead 91.5 us, one by one 94.7; in bfloat16 84 and 106)
+  sum_places<TO, VEC, VEC>(a, ps, &keys, c0, left, lane, own, own_scale, count, [&](int id, bool last, Pairs& acc) {
     const bool from_before = id == before, goes_on = last && id == after;
     if (from_before || goes_on) {
       span_store<VEC>(part + ((size_t)piece * 2 + (from_before ? 0 : 1)) * a.cols + c0, left, lane, acc);
@@ -618,10 +623,21 @@ bool direct(int tokens, int vocab, int cols) {
   return tokens <= 512 && (long long)vocab * ((cols + 255) / 256) <= 8192;
 }
 
-// Few ids: sums of every id per chunk of 256 tokens (16384 x 1280: 64 ids 28.5 us, sorted 33; with more ids what
-// the chunks leave grows, and what is saved shrinks).
+// Few ids: sums of every id per chunk (16384 x 1280: 64 ids 26.5 us, sorted 31; 65536 tokens 88.7 and 91.5: what the
+// chunks leave grows with the ids).
 bool by_chunks(int vocab) { return vocab <= kChunkIds; }
-int chunks_of(int tokens) { return (tokens + kChunk - 1) / kChunk; }
+// Tokens of a chunk: as many as give every SM three blocks, up to 256 (16384 x 1280, 33 ids: 192 tokens 24.8 us, 256 26.7;
+// 2000 tokens 9.0 and 13.4).
+int chunk_length(int tokens, int cols, int num_sms) {
+  const long long blocks = 3ll * num_sms, spans = (cols + 255) / 256;
+  const long long even = (tokens * spans + blocks - 1) / blocks;
+  return (int)std::min((long long)kChunk, std::max((long long)kShortChunk, (even + 31) / 32 * 32));
+}
+// Chunks of any batch of up to `tokens`.
+long long most_chunks(int tokens, int cols, int num_sms) {
+  const long long spans = (cols + 255) / 256, wave = (3ll * num_sms + spans - 1) / spans;
+  return std::max((tokens + kChunk - 1ll) / kChunk, std::min((tokens + kShortChunk - 1ll) / kShortChunk, wave));
+}
 
 struct GradWorkspace {
   size_t list[2], valid, part, total;
@@ -649,8 +665,9 @@ cudaError_t launch_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaSt
   }
   if (by_chunks(a.vocab)) {
     float* part = static_cast<float*>(workspace);
-    const int chunks = chunks_of(a.tokens);
-    embed_grad_chunks_kernel<TO, VEC><<<(unsigned)(spans * chunks), kChunk, 0, st>>>(a, part, fast_div((uint32_t)spans));
+    const int length = chunk_length(a.tokens, a.cols, num_sms), chunks = (a.tokens + length - 1) / length;
+    embed_grad_chunks_kernel<TO, VEC><<<(unsigned)(spans * chunks), kChunk, 0, st>>>(a, part, fast_div((uint32_t)spans),
+                                                                                     length);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_after(embed_grad_add_kernel<VEC>, (unsigned)(((size_t)a.vocab * a.cols + 127) / 128), 256, st, a,
@@ -693,9 +710,9 @@ cudaError_t launch_embed_scaled(const EmbedArgs& a, cudaStream_t st) {
   return a.out_bf16 ? launch_lookup<float, bf16>(a, st) : launch_lookup<float, float>(a, st);
 }
 
-size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols) {
+size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols, int num_sms) {
   if (direct(tokens, vocab, cols)) return 256;
-  if (by_chunks(vocab)) return ((size_t)chunks_of(tokens) * vocab * cols * 4 + 255) & ~size_t(255);
+  if (by_chunks(vocab)) return ((size_t)most_chunks(tokens, cols, num_sms) * vocab * cols * 4 + 255) & ~size_t(255);
   return grad_workspace(tokens, cols).total;
 }
 

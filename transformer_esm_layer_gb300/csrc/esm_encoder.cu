@@ -665,7 +665,7 @@ struct TrainLayout {
 
 constexpr int kMaxKSplit = 8;
 
-TrainLayout train_layout(const esm_config& c, int Tm, const AttnWindow& win) {
+TrainLayout train_layout(const esm_config& c, int Tm, const AttnWindow& win, int num_sms) {
   TrainLayout L{};
   const size_t T = Tm > 0 ? Tm : 1, d = c.hidden, f = c.ffn, H = c.heads, nl = c.num_layers > 0 ? c.num_layers : 0;
   L.sx = align256(4 * T * d);
@@ -702,7 +702,7 @@ TrainLayout train_layout(const esm_config& c, int Tm, const AttnWindow& win) {
   L.partial = take(4 * bwd_partial_floats((int)T, (int)widest));
   L.split_floats = (size_t)kMaxKSplit * std::max(f * d, 3 * d * d);
   L.split = take(4 * L.split_floats);
-  const size_t sorted = embed_grad_workspace_bytes((int)T, c.vocab, (int)d);
+  const size_t sorted = embed_grad_workspace_bytes((int)T, c.vocab, (int)d, num_sms);
   L.embp = take(c.vocab > kTableVocab ? sorted : std::max(sorted, 4 * emb_bwd_partial_floats((int)T, c.vocab, (int)d)));
   L.total = off;
   return L;
@@ -788,7 +788,7 @@ esm_status train_forward_impl(esm_encoder* h, const esm_weights* w, const int32_
   esm_status s = check_ws(h, T, B, ws, ws_bytes, &L);
   if (s != ESM_OK) return s;
   const esm_config& c = h->cfg;
-  const TrainLayout R = train_layout(c, T, h->window);
+  const TrainLayout R = train_layout(c, T, h->window, h->num_sms);
   uint8_t* tb = static_cast<uint8_t*>(train);
   PackBuffers pb = pack_buffers(ws, L);
   if (cudaMemsetAsync(pb.pos_id, 0, 4 * (size_t)T, st) != cudaSuccess) return ESM_ERR_CUDA;
@@ -915,7 +915,7 @@ esm_status backward_impl(esm_encoder* h, const esm_weights* w, const float* d_ou
   const esm_config& c = h->cfg;
   const int T = h->train_T, d = c.hidden, f = c.ffn, H = c.heads;
   const AttnWindow& win = h->train_window;
-  const TrainLayout R = train_layout(c, T, win);
+  const TrainLayout R = train_layout(c, T, win, h->num_sms);
   const WsLayout L = h->layout(T, h->train_B);
   PackBuffers pb = pack_buffers(ws, L);
   uint8_t* tb = static_cast<uint8_t*>(train);
@@ -2012,7 +2012,7 @@ esm_status esm_op_embed(esm_encoder_t* h, const int32_t* ids, int tokens, const 
 
 esm_status esm_op_embed_backward_workspace_size(const esm_encoder_t* h, int tokens, int vocab, int cols, size_t* bytes) {
   if (!h || !bytes || !embed_sizes(tokens, vocab, cols)) return ESM_ERR_INVALID_ARG;
-  *bytes = embed_grad_workspace_bytes(tokens, vocab, cols);
+  *bytes = embed_grad_workspace_bytes(tokens, vocab, cols, h->num_sms);
   return ESM_OK;
 }
 
@@ -2026,7 +2026,7 @@ esm_status esm_op_embed_backward(esm_encoder_t* h, const int32_t* ids, int token
   if (!embed_args(h, ids, tokens, vocab, cols, scale, row_scale, dropout, d_out, d_type, d_stride, &a) || !d_table ||
       !aligned(d_table, 4))
     return ESM_ERR_INVALID_ARG;
-  const size_t need = embed_grad_workspace_bytes(tokens, vocab, cols);
+  const size_t need = embed_grad_workspace_bytes(tokens, vocab, cols, h->num_sms);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ESM_ERR_WORKSPACE;
   const Rows rd{d_out, d_stride, tokens, cols, type_bytes(d_type)}, rt{d_table, cols, vocab, cols, 4};
   if (!rows_apart(rt, rd) || !apart(rt, tokens ? ids : nullptr, 4 * (size_t)tokens) ||
@@ -2167,7 +2167,7 @@ esm_status esm_op_block_norm_backward(esm_encoder_t* h, const esm_block_norm* no
 esm_status esm_encoder_train_buffer_size(const esm_encoder_t* h, int max_tokens, size_t* bytes) {
   if (!h || !bytes || max_tokens < 0) return ESM_ERR_INVALID_ARG;
   if (h->cfg.precision != ESM_BF16 || h->cfg.hidden > 4096) return ESM_ERR_UNSUPPORTED;
-  *bytes = train_layout(h->cfg, max_tokens, h->window).total;
+  *bytes = train_layout(h->cfg, max_tokens, h->window, h->num_sms).total;
   return ESM_OK;
 }
 
@@ -2180,7 +2180,7 @@ esm_status esm_encoder_forward_train(esm_encoder_t* h, const esm_weights* w, con
   if (!token_ids || !cu_seqlens || !hidden_out || !aligned(hidden_out, 16)) return ESM_ERR_INVALID_ARG;
   if (max_seqlen <= 0 || max_seqlen > h->cfg.max_positions) return ESM_ERR_INVALID_ARG;
   if (!weights_ok(h, w)) return ESM_ERR_INVALID_ARG;
-  if (!train_buf || !aligned(train_buf, 256) || train_bytes < train_layout(h->cfg, total_tokens, h->window).total)
+  if (!train_buf || !aligned(train_buf, 256) || train_bytes < train_layout(h->cfg, total_tokens, h->window, h->num_sms).total)
     return ESM_ERR_WORKSPACE;
   h->train_buf = nullptr;  // valid again only once this forward is fully enqueued
   return train_forward_impl(h, w, token_ids, cu_seqlens, num_seqs, total_tokens, max_seqlen, hidden_out, train_buf,
@@ -2194,7 +2194,7 @@ esm_status esm_encoder_backward(esm_encoder_t* h, const esm_weights* w, const fl
   if (h->cfg.precision != ESM_BF16) return ESM_ERR_UNSUPPORTED;
   if (!weights_ok(h, w) || !grads_ok(h, grads)) return ESM_ERR_INVALID_ARG;
   if (h->train_T <= 0 || train_buf != h->train_buf || workspace != h->train_ws) return ESM_ERR_INVALID_ARG;
-  if (train_bytes < train_layout(h->cfg, h->train_T, h->train_window).total) return ESM_ERR_WORKSPACE;
+  if (train_bytes < train_layout(h->cfg, h->train_T, h->train_window, h->num_sms).total) return ESM_ERR_WORKSPACE;
   if (workspace_bytes < h->layout(h->train_T, h->train_B).total) return ESM_ERR_WORKSPACE;
   return backward_impl(h, w, d_hidden_out, grads, train_buf, workspace, reinterpret_cast<cudaStream_t>(stream));
 }

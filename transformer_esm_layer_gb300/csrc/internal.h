@@ -359,7 +359,7 @@ struct EmbedArgs {
   unsigned* err;
 };
 cudaError_t launch_embed_scaled(const EmbedArgs& a, cudaStream_t st);
-size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols);
+size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols, int num_sms);
 cudaError_t launch_embed_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaStream_t st);
 
 // Norm after a block, dropout, gate, residual and norm before the next (cols <= ESM_BLOCK_NORM_MAX_COLS).
