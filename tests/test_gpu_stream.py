@@ -365,6 +365,17 @@ def test_embed_strided_rows(enc):
         _within(grad, want, 90 * U * mag)
 
 
+def test_embed_backward_of_no_tokens_in_wide_rows(enc):
+    """Shapes that no token count takes to the search still have a workspace for none."""
+    for V, cols in ((3, 800_000), (9000, 264)):
+        ids, d = torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, cols, device="cuda")
+        table = torch.full((V, cols), float("nan"), device="cuda")
+        enc.op_embed_backward(ids, d, table)
+        assert (table == 0).all()
+        enc.op_embed_backward(ids, d, table.fill_(2.0), accumulate=True)
+        assert (table == 2).all()
+
+
 def test_embed_of_nothing(enc):
     none = torch.empty(0, dtype=torch.int32, device="cuda")
     table, out = _randn(_gen(1), 9, 16), torch.empty(0, 16, device="cuda")

@@ -711,7 +711,7 @@ cudaError_t launch_embed_scaled(const EmbedArgs& a, cudaStream_t st) {
 }
 
 size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols, int num_sms) {
-  if (direct(tokens, vocab, cols)) return 256;
+  if (tokens == 0 || direct(tokens, vocab, cols)) return 256;
   if (by_chunks(vocab)) return ((size_t)most_chunks(tokens, cols, num_sms) * vocab * cols * 4 + 255) & ~size_t(255);
   return grad_workspace(tokens, cols).total;
 }
