@@ -501,7 +501,7 @@ ESM_API esm_status esm_op_embed(esm_encoder_t* h, const int32_t* ids, int tokens
  * dropout(d_out[t]), added to what d_table holds if accumulate != 0 (a tied table's other part).
  * d_table: device float32 [vocab, cols], every row written; d_out: device, d_type (ESM_FP32 or ESM_BF16),
  * rows d_stride >= cols elements apart; the rest as in the forward.  Every element's sum runs over its
- * tokens in an order that the ids alone determine.  Workspace: the size query's bytes, 256-byte aligned, of this call
+ * tokens in an order that the ids and the sizes determine.  Workspace: the size query's bytes, 256-byte aligned, of this call
  * alone while it runs. */
 ESM_API esm_status esm_op_embed_backward_workspace_size(const esm_encoder_t* h, int tokens, int vocab, int cols,
                                                         size_t* bytes);

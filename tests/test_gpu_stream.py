@@ -247,10 +247,11 @@ def test_embed_backward_of_large_batches(enc, T, V, cols):
     _within(table, want, (counts + 6) * U * mag)
     again = torch.empty_like(table)
     enc.op_embed_backward(ids, d, again)
-    assert torch.equal(table, again)  # the order goes by the ids alone
+    assert torch.equal(table, again)  # the order goes by the ids and the sizes
 
 
-@pytest.mark.parametrize("T,V,cols", [(1, 8192, 8), (512, 1639, 1280), (511, 1638, 1280), (257, 33, 2056), (512, 3, 12)])
+@pytest.mark.parametrize("T,V,cols", [(1, 8192, 8), (512, 1639, 1280), (511, 1638, 1280), (257, 33, 2056), (512, 3, 12),
+                                      (256, 33, 264), (512, 65, 264), (513, 65, 264)])
 @pytest.mark.parametrize("ids", ["any", "one", "none"])
 def test_embed_backward_of_few_tokens(enc, T, V, cols, ids):
     """On both sides of the search's limits; a token count of zero clears the table or leaves it."""

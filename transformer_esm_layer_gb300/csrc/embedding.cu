@@ -616,16 +616,15 @@ cudaError_t launch_lookup(const EmbedArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Few tokens: a search through all of them for every id is one launch (1280 columns, 33 ids, 173 tokens: 2.6 us, of
-// which the worst, one id's alone, take 8; by chunks 8.2; 300 ids, 512 tokens: 4.6 us, sorted 15).  The blocks of ids
-// that are not met cost too: 1000 ids take 10 us, 2000 17, and sorted 16.
-bool direct(int tokens, int vocab, int cols) {
-  return tokens <= 512 && (long long)vocab * ((cols + 255) / 256) <= 8192;
-}
-
 // Few ids: sums of every id per chunk (16384 x 1280: 64 ids 26.5 us, sorted 31; 65536 tokens 88.7 and 91.5: what the
 // chunks leave grows with the ids).
 bool by_chunks(int vocab) { return vocab <= kChunkIds; }
+// Few tokens: a search through all of them for every id is one launch.  1280 columns, us with ids at random and all
+// the same: 33 ids, 173 tokens 2.8 and 8.3, by chunks 5.2 and 5.5; 512 tokens 3.7 and 14.9, by chunks 5.5 and 5.6; 300 ids,
+// 512 tokens 4.6 and 15, sorted 15 and 14.  The blocks of ids that are not met cost too: 1000 ids take 10, 2000 17, sorted 16.
+bool direct(int tokens, int vocab, int cols) {
+  return tokens <= (by_chunks(vocab) ? 256 : 512) && (long long)vocab * ((cols + 255) / 256) <= 8192;
+}
 // Tokens of a chunk: as many as give every SM three blocks, up to 256 (16384 x 1280, 33 ids: 192 tokens 24.8 us, 256 26.7;
 // 2000 tokens 9.0 and 13.4).
 int chunk_length(int tokens, int cols, int num_sms) {
