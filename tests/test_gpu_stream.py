@@ -495,6 +495,14 @@ def test_block_norm_backward(encs, rows, cols, dtype, config):
     _check_backward(encs[dtype], norm, gate, x, y, p, ref, d_x, d_h, dtype)
 
 
+@pytest.mark.parametrize("rows,cols", [(500, 4104), (700, 5120), (470, 8192), (471, 6400), (460, 4096), (309, 3592)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("config", NORMS)
+def test_block_norm_backward_of_wide_rows(encs, rows, cols, dtype, config):
+    """Several rows to a block, and more of them than are on their way at once."""
+    test_block_norm_backward(encs, rows, cols, dtype, config)
+
+
 def _check_backward(enc, norm, gate, x, y, p, ref, d_x, d_h, dtype, **kw):
     rows, cols = y.shape
     f = _factors(rows, cols, p)
