@@ -541,7 +541,8 @@ ESM_API esm_status esm_op_block_norm(esm_encoder_t* h, const esm_block_norm* nor
  * when there is no pre): dx (float32 [rows, cols]; may be d_x_out), dy (activation dtype; may be d_h or y)
  * and the parameters' gradients, each of which may be NULL: float32 [cols], summed over the rows; with
  * gate_rows the gate's is [rows, cols] in the activation dtype.  A gradient of a parameter that is NULL must be NULL.
- * x_out and stats are not read for pre if there is none (x_out may be NULL then).  rows == 0 sets the
+ * x_out and stats are not read for pre if there is none (x_out may be NULL then).  What d_x_out holds at a dropped
+ * place reaches dx there and nothing else.  rows == 0 sets the
  * parameters' gradients to 0.  Workspace as above. */
 typedef struct {
   float* post_gamma;

@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<T>, 1)
     if (row >= a.rows || !alive) return;
     const size_t at = (size_t)row * a.cols;
     uint8_t* to = ring + stage * stage_bytes;
-    mbar_arrive_expect_tx(bars + stage, (pre || post ? 16 : 0) + (a.d_x_out ? f_bytes : 0) + t_bytes + (pre ? f_bytes + t_bytes : 0));
+    mbar_arrive_expect_tx(bars + stage, (pre || post ? 16 : 0) + (a.d_x_out ? f_bytes : 0) + t_bytes +
+                                            (pre ? f_bytes + t_bytes : 0));
     if (pre || post) bulk_load(to, a.stats + 4 * (size_t)row, 16, bars + stage);
     to += 16;
     if (a.d_x_out) bulk_load(to, a.d_x_out + at, f_bytes, bars + stage);
@@ -426,7 +427,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<T>, 1)
     if (!pre) st.w = 0.f;  // (no norm's columns may hold anything)
     const uint8_t* values = from + 16;
     auto row_f = [&](int i, Pairs& v) { ld8_shared(reinterpret_cast<const float*>(values + i * f_bytes) + w * 256, lane, v); };
-    auto row_t = [&](int i, Pairs& v) { ld8_shared(reinterpret_cast<const T*>(values + 2 * f_bytes + i * t_bytes) + w * 256, lane, v); };
+    auto row_t = [&](int i, Pairs& v) {
+      ld8_shared(reinterpret_cast<const T*>(values + 2 * f_bytes + i * t_bytes) + w * 256, lane, v);
+    };
     Pairs xh, e, yh, kept, p;
     float s[8];
     // all bits or none, per element: a dropped place is 0 whatever it holds
@@ -611,7 +614,9 @@ __global__ void __launch_bounds__(512, 1)
   const PhiloxState ps = philox_state(a.mask);
   philox_keys(ps, &keys);
   const int own_left = a.cols - w * 256 * G;
-  auto load = [&](const void* p, size_t at, int left, Pairs& out) { span_load<VEC>(static_cast<const T*>(p) + at, left, lane, out); };
+  auto load = [&](const void* p, size_t at, int left, Pairs& out) {
+    span_load<VEC>(static_cast<const T*>(p) + at, left, lane, out);
+  };
   // G = 2: sum i of a lane's eight columns of its span g, in two halves
   auto own_sums = [&](int i, int g) { return reinterpret_cast<ulonglong2*>(sums) + ((i * G + g) * W + w) * 64 + lane; };
   Pairs acc[G == 1 ? kSums : 1];
@@ -1012,12 +1017,13 @@ cudaError_t launch_fwd(const BlockNormArgs& a, bool vec, int num_sms, cudaStream
 
 // A row's or parameter's eight values at a time (cols % 8 == 0 is part of it).
 bool all_on_eights(const BlockNormArgs& a, bool bf16) {
-  const int es = bf16 ? 2 : 4, n = a.cols;
-  return rows_on_eights(a.y, n, es) && rows_on_eights(a.x, n, 4) && rows_on_eights(a.x_out, n, 4) && rows_on_eights(a.h, n, es) &&
-         rows_on_eights(a.d_x_out, n, 4) && rows_on_eights(a.d_h, n, es) && rows_on_eights(a.dx, n, 4) && rows_on_eights(a.dy, n, es) &&
-         rows_on_eights(a.post_gamma, n, es) && rows_on_eights(a.post_beta, n, es) && rows_on_eights(a.pre_gamma, n, es) &&
-         rows_on_eights(a.pre_beta, n, es) && rows_on_eights(a.gate, n, es) &&
-         (!a.gate_rows || rows_on_eights(a.d_gate, n, es));
+  const int es = bf16 ? 2 : 4;
+  for (const void* p : {a.y, (const void*)a.h, a.d_h, (const void*)a.dy, a.post_gamma, a.post_beta, a.pre_gamma, a.pre_beta,
+                        a.gate, a.gate_rows ? (const void*)a.d_gate : nullptr})
+    if (!rows_on_eights(p, a.cols, es)) return false;
+  for (const float* p : {a.x, (const float*)a.x_out, a.d_x_out, (const float*)a.dx})
+    if (!rows_on_eights(p, a.cols, 4)) return false;
+  return true;
 }
 
 }  // namespace

@@ -115,8 +115,9 @@ cudaError_t launch_dropout(const DropoutArgs& a, cudaStream_t st) {
                    (!a.residual || rows_on_eights(a.residual, a.res_stride, a.y_bf16 ? 2 : 4));
   const bool dense = a.cols % 8 == 0 && (a.rows == 1 || (a.x_stride == a.cols && a.y_stride == a.cols &&
                                                          (!a.residual || a.res_stride == a.cols)));
-  if (a.x_bf16) return a.y_bf16 ? launch<__nv_bfloat16, __nv_bfloat16>(a, vec, dense, st) : launch<__nv_bfloat16, float>(a, vec, dense, st);
-  return a.y_bf16 ? launch<float, __nv_bfloat16>(a, vec, dense, st) : launch<float, float>(a, vec, dense, st);
+  using bf16 = __nv_bfloat16;
+  if (a.x_bf16) return a.y_bf16 ? launch<bf16, bf16>(a, vec, dense, st) : launch<bf16, float>(a, vec, dense, st);
+  return a.y_bf16 ? launch<float, bf16>(a, vec, dense, st) : launch<float, float>(a, vec, dense, st);
 }
 
 }  // namespace esm

@@ -207,7 +207,9 @@ struct Raw8 {
     if (left >= 8) {
       if constexpr (sizeof(T) == 4) {
         asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w) : "l"(p));
+                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y),
+                       "=r"(v[1].z), "=r"(v[1].w)
+                     : "l"(p));
         return;
       }
 #pragma unroll

@@ -4,8 +4,9 @@
 // The sums run in a fixed order, so results do not depend on scheduling.
 //
 // Bound by memory: the rows met and the output; for the gradient d_out and the table's rows.  16384 tokens x 1280:
-// lookup in 50021 float32 rows 25.2 us (4.5 TB/s of the bytes that it cannot do without); gradient of 33 ids 24.7 us (14.5
-// without the dropout, 5.8 TB/s: the rest is its masks' instructions), of 50021 64.2 us, of which 38 clear the table.
+// lookup in 50021 float32 rows 25.2 us (4.5 TB/s of the bytes that it cannot do without); gradient of 33 ids 24.7 us
+// (14.5 without the dropout, 5.8 TB/s: the rest is its masks' instructions), of 50021 64.2 us, of which 38 clear the
+// table.
 #include <algorithm>
 #include <type_traits>
 
@@ -620,13 +621,14 @@ cudaError_t launch_lookup(const EmbedArgs& a, cudaStream_t st) {
 // chunks leave grows with the ids).
 bool by_chunks(int vocab) { return vocab <= kChunkIds; }
 // Few tokens: a search through all of them for every id is one launch.  1280 columns, us with ids at random and all
-// the same: 33 ids, 173 tokens 2.8 and 8.3, by chunks 5.2 and 5.5; 512 tokens 3.7 and 14.9, by chunks 5.5 and 5.6; 300 ids,
-// 512 tokens 4.6 and 15, sorted 15 and 14.  The blocks of ids that are not met cost too: 1000 ids take 10, 2000 17, sorted 16.
+// the same: 33 ids, 173 tokens 2.8 and 8.3, by chunks 5.2 and 5.5; 512 tokens 3.7 and 14.9, by chunks 5.5 and 5.6;
+// 300 ids, 512 tokens 4.6 and 15, sorted 15 and 14.  The blocks of ids that are not met cost too: 1000 ids take 10,
+// 2000 17, sorted 16.
 bool direct(int tokens, int vocab, int cols) {
   return tokens <= (by_chunks(vocab) ? 256 : 512) && (long long)vocab * ((cols + 255) / 256) <= 8192;
 }
-// Tokens of a chunk: as many as give every SM three blocks, up to 256 (16384 x 1280, 33 ids: 192 tokens 24.8 us, 256 26.7;
-// 2000 tokens 9.0 and 13.4).
+// Tokens of a chunk: as many as give every SM three blocks, up to 256 (16384 x 1280, 33 ids: 192 tokens 24.8 us, 256
+// 26.7; 2000 tokens 9.0 and 13.4).
 int chunk_length(int tokens, int cols, int num_sms) {
   const long long blocks = 3ll * num_sms, spans = (cols + 255) / 256;
   const long long even = (tokens * spans + blocks - 1) / blocks;
@@ -692,8 +694,8 @@ cudaError_t launch_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaSt
   embed_sort_kernel<<<kSortBlocks + clear, kSortThreads, 0, st>>>(a, s);
   const long long pieces = (a.tokens + kPiece - 1) / kPiece;
   // (each launch may start while the one before it still runs, and waits for it where it needs its results)
-  cudaError_t e = launch_after(embed_grad_pieces_kernel<TO, VEC>, (unsigned)(spans * pieces), 32, st, a, (const uint2*)s.list, (const int*)s.valid, part,
-                               fast_div((uint32_t)spans), spans * pieces);
+  cudaError_t e = launch_after(embed_grad_pieces_kernel<TO, VEC>, (unsigned)(spans * pieces), 32, st, a,
+                               (const uint2*)s.list, (const int*)s.valid, part, fast_div((uint32_t)spans), spans * pieces);
   if (e != cudaSuccess) return e;
   const unsigned join = (unsigned)std::min((spans * pieces + 7) / 8, (long long)num_sms * 32);
   return launch_after(embed_grad_join_kernel<VEC>, join, 256, st, a, (const uint2*)s.list, (const int*)s.valid,
@@ -716,7 +718,8 @@ size_t embed_grad_workspace_bytes(int tokens, int vocab, int cols, int num_sms) 
 }
 
 cudaError_t launch_embed_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaStream_t st) {
-  const bool vec = a.cols % 8 == 0 && rows_on_eights(a.d_table, a.cols, 4) && rows_on_eights(a.out, a.out_stride, a.out_bf16 ? 2 : 4);
+  const bool vec =
+      a.cols % 8 == 0 && rows_on_eights(a.d_table, a.cols, 4) && rows_on_eights(a.out, a.out_stride, a.out_bf16 ? 2 : 4);
   if (a.out_bf16)
     return vec ? launch_grad<__nv_bfloat16, true>(a, workspace, num_sms, st)
                : launch_grad<__nv_bfloat16, false>(a, workspace, num_sms, st);
