@@ -542,8 +542,7 @@ ESM_API esm_status esm_op_block_norm(esm_encoder_t* h, const esm_block_norm* nor
  * and the parameters' gradients, each of which may be NULL: float32 [cols], summed over the rows; with
  * gate_rows the gate's is [rows, cols] in the activation dtype.  A gradient of a parameter that is NULL must be NULL.
  * x_out and stats are not read for pre if there is none (x_out may be NULL then).  What d_x_out holds at a dropped
- * place reaches dx there and nothing else.  rows == 0 sets the
- * parameters' gradients to 0.  Workspace as above. */
+ * place reaches dx there and nothing else.  rows == 0 sets the parameters' gradients to 0.  Workspace as above. */
 typedef struct {
   float* post_gamma;
   float* post_beta;
