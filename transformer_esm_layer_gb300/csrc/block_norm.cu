@@ -928,16 +928,18 @@ BwdShape bwd_shape(int rows, int cols, int num_sms) {
 
 constexpr size_t kSmemMax = 227 * 1024 - 2048;  // (the rest: static shared memory)
 
-// Lets a kernel have `smem` bytes of dynamic shared memory.
+// Lets a kernel have `smem` bytes of dynamic shared memory.  The limit belongs to the kernel, for all host threads: it
+// is always set to `most`, what any shape may need, so that no call lowers it under another's launch.
 template <typename Kernel>
-cudaError_t allow_smem(Kernel k, size_t smem) {
-  return smem <= 40 * 1024 ? cudaSuccess : cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+cudaError_t allow_smem(Kernel k, size_t smem, size_t most) {
+  return smem <= 40 * 1024 ? cudaSuccess : cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
 }
 
 template <typename T, bool VEC, int G>
 cudaError_t launch_bwd_any(const BlockNormArgs& a, const BwdShape& s, float* partial, cudaStream_t st) {
   const size_t smem = sizeof(float) * kSums * (G == 1 ? a.cols : G * s.W * 256);
-  const cudaError_t e = allow_smem(block_norm_bwd_any_kernel<T, VEC, G>, smem);
+  constexpr size_t kMost = sizeof(float) * kSums * (G == 1 ? 16 * 256 : ESM_BLOCK_NORM_MAX_COLS);
+  const cudaError_t e = allow_smem(block_norm_bwd_any_kernel<T, VEC, G>, smem, kMost);
   if (e != cudaSuccess) return e;
   block_norm_bwd_any_kernel<T, VEC, G><<<s.blocks, 32 * s.W * s.groups, smem, st>>>(a, s.W, s.groups, partial);
   return cudaGetLastError();
@@ -959,7 +961,7 @@ cudaError_t launch_bwd(const BlockNormArgs& a, bool vec, float* partial, int num
     s.groups = (int)std::min({(size_t)s.groups, fits, (size_t)(kWarpsOf<T> / s.W)});
     const size_t smem = fixed + group * s.groups;
     const auto kernel = a.rms ? block_norm_bwd_kernel<T, true> : block_norm_bwd_kernel<T, false>;
-    e = allow_smem(kernel, smem);
+    e = allow_smem(kernel, smem, kSmemMax);
     if (e != cudaSuccess) return e;
     kernel<<<s.blocks, 32 * s.W * s.groups, smem, st>>>(a, s.W, s.groups, partial);
     e = cudaGetLastError();
