@@ -81,3 +81,47 @@ def test_block_norm_backward(kind, precision, narrow, wide):
         return enc.lib.esm_op_block_norm_backward, args, [dx, dy, d_post, d_pre]
 
     _side_by_side([make(narrow), make(wide)])
+
+
+def _head(precision, hidden, vocab, seed):
+    from transformer_esm_layer_gb300.binding import DeviceLmHead, EsmEncoder
+    g = synth.Geometry(num_layers=1, hidden=hidden, heads=hidden // 64, ffn=512, vocab=vocab)
+    emb = synth.model_weights(g, seed, precision)["emb"]
+    return EsmEncoder.from_geometry(g, precision), DeviceLmHead(synth.lm_head_weights(g, seed, precision, emb), precision)
+
+
+@pytest.mark.parametrize("precision,narrow,wide", [("bf16", (256, 33), (1280, 33)), ("bf16", (512, 60), (1280, 64)),
+                                                   ("fp32", (576, 20), (768, 33))])
+def test_lm_head(precision, narrow, wide):
+    T, keep = 5, []
+
+    def make(hidden, vocab):
+        enc, head = _head(precision, hidden, vocab, hidden)
+        h = torch.randn(T, hidden, device="cuda").to(enc.out_dtype)
+        logits, ws, stream = torch.zeros(T, vocab, device="cuda"), enc.lm_head_workspace(T), torch.cuda.Stream()
+        keep.append((enc, head, h, ws, stream))
+        args = (enc.handle, ctypes.byref(head.struct), h.data_ptr(), T, None, logits.data_ptr(), None, None, None,
+                ws.data_ptr(), ws.numel(), stream.cuda_stream)
+        return enc.lib.esm_encoder_lm_head, args, [logits]
+
+    _side_by_side([make(*narrow), make(*wide)])
+
+
+@pytest.mark.parametrize("narrow,wide", [(20, 33), (33, 64)])
+def test_lm_head_backward(narrow, wide):
+    from transformer_esm_layer_gb300.binding import LM_HEAD_NAMES, EsmLmHeadGrads
+    T, keep = 5, []
+
+    def make(vocab):
+        enc, head = _head("bf16", 256, vocab, vocab)
+        h = torch.randn(T, 256, device="cuda").bfloat16()
+        targets = torch.arange(T, device="cuda", dtype=torch.int32)
+        d_h, ws = torch.zeros(T, 256, device="cuda"), enc.lm_head_backward_workspace(T)
+        grads = [torch.zeros(tuple(head.t[k].shape), device="cuda") for k in LM_HEAD_NAMES]
+        gs, stream = EsmLmHeadGrads(*[t.data_ptr() for t in grads]), torch.cuda.Stream()
+        keep.append((enc, head, h, targets, gs, ws, stream))
+        args = (enc.handle, ctypes.byref(head.struct), h.data_ptr(), T, targets.data_ptr(), d_h.data_ptr(), ctypes.byref(gs),
+                None, None, None, ws.data_ptr(), ws.numel(), stream.cuda_stream)
+        return enc.lib.esm_encoder_lm_head_backward, args, [d_h, *grads]
+
+    _side_by_side([make(narrow), make(wide)])

@@ -297,6 +297,7 @@ void reduce_chunks(const float* partial, int chunks, size_t stride, size_t n, fl
 }
 
 constexpr int kLnRowsPerBlock = 64;
+constexpr int kLnBwdSmem = 192 * 1024;  // a block's slices of column sums at most
 
 size_t bwd_partial_floats(int rows, int cols) {
   const int blocks = rows <= 0 ? 1 : (rows + kLnRowsPerBlock - 1) / kLnRowsPerBlock;
@@ -319,7 +320,7 @@ LnBwdGrid ln_bwd_grid(int rows, int cols) {
         cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || num_sms <= 0)
       num_sms = 148;
   }
-  const int warps = std::max(1, std::min(8, (int)(196608 / (8 * (size_t)cols))));
+  const int warps = std::max(1, std::min(8, (int)(kLnBwdSmem / (8 * (size_t)cols))));
   const size_t smem = (size_t)warps * 2 * cols * sizeof(float);
   const int n4 = (cols / 4 + 31) / 32;
   const int per_sm = (n4 <= 10 && 2 * (smem + 1024) <= 227 * 1024) ? 2 : 1;  // the kernel's launch bounds
@@ -332,13 +333,14 @@ LnBwdGrid ln_bwd_grid(int rows, int cols) {
 template <int N4, bool XBF16>
 cudaError_t ln_bwd_launch(const void* x, const void* gamma, bool gf32, const float* dy, const float* dres, float* dx,
                           float* partial, int rows, int cols, float eps, cudaStream_t st) {
-  const int warps = std::max(1, std::min(8, (int)(196608 / (8 * (size_t)cols))));
+  const int warps = std::max(1, std::min(8, (int)(kLnBwdSmem / (8 * (size_t)cols))));
   const size_t smem = (size_t)warps * 2 * cols * sizeof(float);
-  static size_t configured = 0;
-  if (smem > 48 * 1024 && smem > configured) {
-    cudaError_t e = cudaFuncSetAttribute(ln_bwd_kernel<N4, XBF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (the limit is for all host threads: always the most of any row, so that no call lowers it under another's launch)
+  static bool configured = false;
+  if (smem > 48 * 1024 && !configured) {
+    cudaError_t e = cudaFuncSetAttribute(ln_bwd_kernel<N4, XBF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLnBwdSmem);
     if (e != cudaSuccess) return e;
-    configured = smem;
+    configured = true;
   }
   const LnBwdGrid g = ln_bwd_grid(rows, cols);
   ln_bwd_kernel<N4, XBF16><<<g.blocks, 32 * warps, smem, st>>>(x, gamma, gf32, dy, dres, dx, partial, rows, cols,

@@ -258,6 +258,12 @@ __global__ void __launch_bounds__(128) lm_logits_mma_kernel(const __nv_bfloat16*
   }
 }
 
+// The kernels' limits of dynamic shared memory belong to all host threads: each is always set to the most that its
+// kernel may need, so that no call lowers it under another's launch.
+constexpr int kMmaSmemMost = 227 * 1024;     // lm_logits_mma_kernel
+constexpr int kLogitsSmemMost = 200 * 1024;  // lm_logits_kernel
+constexpr int kMaxVocab = 64;
+
 // Table row pitch of lm_logits_mma_kernel: 2 d bytes rounded up to 64 (mod 512).
 int lm_mma_row_bytes(int d) { return 2 * d + (((64 - 2 * d) % 512) + 512) % 512; }
 
@@ -266,7 +272,7 @@ void launch_mma_nb(int num_sms, const void* z, const void* emb, const void* bias
                    const int32_t* targets, float* logits, float* token_loss, unsigned* err, cudaStream_t st) {
   const int rb = lm_mma_row_bytes(d);
   const size_t smem = (size_t)8 * NB * rb;
-  cudaFuncSetAttribute(lm_logits_mma_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaFuncSetAttribute(lm_logits_mma_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmemMost);
   const int per_sm = smem <= 110 * 1024 ? 2 : 1;
   const int warps = 4, groups = (T + 15) / 16;
   int grid = std::min(num_sms * per_sm, (groups + warps - 1) / warps);
@@ -447,14 +453,15 @@ cudaError_t launch_lm_backward_from_dlogits(const float* dl, const void* emb, co
                                             int V, float* dz, float* demb, float* dbias, float* partial,
                                             cudaStream_t st) {
   const size_t smem = sizeof(float) * (size_t)V * (kDzCols + kDzTStride);
-  cudaFuncSetAttribute(lm_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr int kMost = sizeof(float) * kMaxVocab * (kDzCols + kDzTStride);
+  cudaFuncSetAttribute(lm_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   lm_dz_kernel<<<dim3((d + kDzCols - 1) / kDzCols, (T + kDzTok - 1) / kDzTok), 256, smem, st>>>(
       dl, static_cast<const __nv_bfloat16*>(emb), T, d, V, dz);
   const int chunks = (T + kLmChunkRows - 1) / kLmChunkRows;
   float* pe = partial;
   float* pb = partial + (size_t)chunks * V * d;
   const size_t smem2 = sizeof(float) * (size_t)kLmChunkRows * V;
-  cudaFuncSetAttribute(lm_demb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem2);
+  // (up to 32 KB: no limit to raise)
   lm_demb_kernel<<<dim3((d + 127) / 128, chunks), 256, smem2, st>>>(dl, z, T, d, V, kLmChunkRows, pe, pb);
   reduce_chunks(pe, chunks, (size_t)V * d, (size_t)V * d, 1.f, demb, st);
   reduce_chunks(pb, chunks, (size_t)V, (size_t)V, 1.f, dbias, st);
@@ -478,15 +485,15 @@ size_t lm_logits_smem_bytes(int vocab, int hidden, bool bf16) { return (size_t)v
 template <bool BF16, int NU>
 void launch_nu(int grid, size_t smem, const void* z, const void* emb, const void* bias, int T, int d, int V,
                const int32_t* targets, float* logits, float* token_loss, unsigned* err, cudaStream_t st) {
-  cudaFuncSetAttribute(lm_logits_kernel<BF16, NU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaFuncSetAttribute(lm_logits_kernel<BF16, NU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLogitsSmemMost);
   lm_logits_kernel<BF16, NU><<<grid, 256, smem, st>>>(z, emb, bias, T, d, V, targets, logits, token_loss, err);
 }
 
 // false when the table does not fit shared memory or the row is too long for the register plan
 bool lm_logits_supported(int vocab, int hidden, bool bf16) {
   const int per = bf16 ? 8 : 4;
-  return vocab >= 1 && vocab <= 64 && hidden % per == 0 && hidden / per <= 16 * 32 &&
-         lm_logits_smem_bytes(vocab, hidden, bf16) <= 200 * 1024;
+  return vocab >= 1 && vocab <= kMaxVocab && hidden % per == 0 && hidden / per <= 16 * 32 &&
+         lm_logits_smem_bytes(vocab, hidden, bf16) <= kLogitsSmemMost;
 }
 
 cudaError_t launch_lm_logits(const void* z, bool bf16, const void* emb, const void* bias, int T, int d, int V,
@@ -495,7 +502,7 @@ cudaError_t launch_lm_logits(const void* z, bool bf16, const void* emb, const vo
   const size_t smem = lm_logits_smem_bytes(V, d, bf16);
   const int nb = (V + 7) / 8;
   if (T > 0 && bf16 && d % 128 == 0 && nb >= 1 && nb <= 8 &&
-      (size_t)8 * nb * lm_mma_row_bytes(d) <= 227 * 1024) {
+      (size_t)8 * nb * lm_mma_row_bytes(d) <= kMmaSmemMost) {
     switch (nb) {
       case 1: launch_mma_nb<1>(num_sms, z, emb, bias, T, d, V, targets, logits, token_loss, err, st); break;
       case 2: launch_mma_nb<2>(num_sms, z, emb, bias, T, d, V, targets, logits, token_loss, err, st); break;
