@@ -925,3 +925,31 @@ def test_refusals(enc):
     with pytest.raises(EsmError, match="UNSUPPORTED"):
         enc.op_block_norm(BlockNorm(), wide, wide.to(BF16), torch.empty_like(wide))
     enc.check()
+
+
+@pytest.mark.parametrize("T,V", [(8, 33), (600, 33), (600, 100)])  # a search, chunks, a sort
+def test_embed_backward_workspace_lies_apart(enc, T, V):
+    from transformer_esm_layer_gb300.binding import EsmError
+    cols = 16
+    need = enc.op_embed_backward_workspace(T, V, cols).numel()
+    buf = torch.zeros(need + 2 ** 18, dtype=torch.uint8, device="cuda")
+    ws, table = buf[:need], torch.zeros(V, cols, device="cuda")
+    new = dict(ids=torch.zeros(T, dtype=torch.int32, device="cuda"), d_out=torch.ones(T, cols, device="cuda"),
+               row_scale=torch.ones(T, device="cuda"), rng=_rng())
+    for name, t in new.items():
+        for at, taken in ((0, False), (need - 16, False), (need, True)):
+            inside = buf[at:at + t.nbytes].view(t.dtype).view(t.shape)
+            inside.copy_(t)
+            s = {**new, name: inside}
+
+            def call():
+                enc.op_embed_backward(s["ids"], s["d_out"], table, row_scale=s["row_scale"], dropout=_drop(0.1, rng=s["rng"]),
+                                      workspace=ws)
+            if taken:
+                call()
+                assert torch.isfinite(table).all()
+                continue
+            with pytest.raises(EsmError, match="INVALID_ARG"):
+                call()
+                pytest.fail(f"{name} at {at} was taken")
+    enc.check()

@@ -2033,6 +2033,11 @@ esm_status esm_op_embed_backward(esm_encoder_t* h, const int32_t* ids, int token
       !apart(rt, tokens ? row_scale : nullptr, 4 * (size_t)tokens) || !apart(rt, a.mask.rng, 16) ||
       !apart(rt, workspace, need))
     return ESM_ERR_INVALID_ARG;
+  // the workspace is written while the inputs are still read
+  const auto inside = [&](const void* p, size_t n) { return p && n && !disjoint(workspace, need, p, n); };
+  if (inside(d_out, rd.bytes()) || inside(ids, 4 * (size_t)tokens) || inside(row_scale, 4 * (size_t)tokens) ||
+      inside(a.mask.rng, 16))
+    return ESM_ERR_INVALID_ARG;
   if (workspace == h->train_ws) h->train_buf = nullptr;  // as check_ws: the pending backward's index is overwritten
   a.d_table = d_table;
   a.accumulate = accumulate != 0;
