@@ -466,7 +466,7 @@ ESM_API esm_status esm_op_gemm_nvfp4(esm_encoder_t* h, esm_epilogue epi, const u
  * word first), the output word (c % 8) / 2, its lower half for even c and its upper half for odd.
  * With n = p * 65536 rounded to a whole number (halves up), the element is kept if u >= n and then multiplied by
  * 65536 / (65536 - n); others become 0 whatever they hold (n = 65536: all of them).
- * A NULL esm_dropout*, or n = 0, is no dropout. */
+ * A NULL esm_dropout*, or n = 0, is no dropout (rng may then be anything, NULL too). */
 typedef struct {
   const int64_t* rng; /* device int64 [2], 8-byte aligned: seed, base */
   int64_t offset;
@@ -621,8 +621,8 @@ ESM_API esm_status esm_encoder_forward_train(esm_encoder_t* h, const esm_weights
  * have the offsets dropout->offset (embedding), + 1 + 2 l (layer l's attention block) and + 2 + 2 l
  * (its MLP block): a program adds 2 L + 1 to the base between steps.  The struct is copied; the device memory that rng
  * points to must stay valid, and unchanged between a forward and its backward, which uses the dropout that its forward
- * ran with.  A block's output rows are rounded to bf16 before they are dropped.  ESM_BF16 handles (others:
- * ESM_ERR_UNSUPPORTED); no other call of the handle drops anything. */
+ * ran with.  A block's output rows are rounded to bf16 before they are dropped.  ESM_BF16 handles (a dropout on
+ * others: ESM_ERR_UNSUPPORTED); no other call of the handle drops anything. */
 ESM_API esm_status esm_encoder_set_dropout(esm_encoder_t* h, const esm_dropout* dropout);
 
 /* Gradients of a loss L with respect to every parameter, given d_hidden_out = dL/d(hidden_out)

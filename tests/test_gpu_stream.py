@@ -953,3 +953,23 @@ def test_embed_backward_workspace_lies_apart(enc, T, V):
                 call()
                 pytest.fail(f"{name} at {at} was taken")
     enc.check()
+
+
+def test_no_dropout_needs_no_generator(enc, encs):
+    """A p that rounds to none is no dropout, whatever rng is, in every call that takes one."""
+    from transformer_esm_layer_gb300 import binding
+    lib, h = enc.lib, enc.handle
+    x = _randn(_gen(30), 5, 64)
+    y = torch.empty_like(x)
+    for p in (0.0, 2.0 ** -18):
+        for rng in (None, 4, _rng().data_ptr()):  # (4: not even aligned)
+            none = binding.EsmDropout(rng, 3, p)
+            y.fill_(float("nan"))
+            assert lib.esm_op_dropout(h, x.data_ptr(), 0, 64, None, 0, y.data_ptr(), 0, 64, 5, 64, none, None) == 0
+            assert torch.equal(x, y)
+            for e in encs.values():
+                assert lib.esm_encoder_set_dropout(e.handle, none) == 0
+    for bad in (binding.EsmDropout(None, 0, 0.1), binding.EsmDropout(4, 0, 0.1), binding.EsmDropout(None, 0, -0.1),
+                binding.EsmDropout(None, 0, float("nan")), binding.EsmDropout(None, 0, 1.5)):
+        assert lib.esm_op_dropout(h, x.data_ptr(), 0, 64, None, 0, y.data_ptr(), 0, 64, 5, 64, bad, None) == 1
+        assert lib.esm_encoder_set_dropout(h, bad) == 1

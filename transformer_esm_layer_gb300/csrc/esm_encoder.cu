@@ -637,9 +637,10 @@ constexpr int kTableVocab = 96;
 bool drop_mask(const esm_dropout* d, DropMask* m) {
   *m = DropMask{nullptr, 0, 0, 1.f};
   if (!d) return true;
-  if (!(d->p >= 0.0 && d->p <= 1.0) || !d->rng || !aligned(d->rng, 8)) return false;
+  if (!(d->p >= 0.0 && d->p <= 1.0)) return false;
   const unsigned n = (unsigned)(d->p * 65536.0 + 0.5);
   if (n == 0) return true;
+  if (!d->rng || !aligned(d->rng, 8)) return false;
   m->rng = reinterpret_cast<const unsigned long long*>(d->rng);
   m->offset = (unsigned long long)d->offset;
   m->threshold = n;
@@ -1178,7 +1179,7 @@ esm_status esm_encoder_set_attention_window(esm_encoder_t* h, const esm_attn_win
 esm_status esm_encoder_set_dropout(esm_encoder_t* h, const esm_dropout* dropout) {
   DropMask m;
   if (!h || !drop_mask(dropout, &m)) return ESM_ERR_INVALID_ARG;
-  if (dropout && h->cfg.precision != ESM_BF16) return ESM_ERR_UNSUPPORTED;
+  if (m.rng && h->cfg.precision != ESM_BF16) return ESM_ERR_UNSUPPORTED;
   h->dropout = m.rng ? *dropout : esm_dropout{};
   return ESM_OK;
 }
