@@ -217,3 +217,21 @@ def test_refusals():
     for precision in ("fp32", "fp8"):
         with pytest.raises(EsmError, match="UNSUPPORTED"):
             EsmEncoder.from_geometry(g, precision).set_dropout(Dropout(0.1, _rng()))
+
+
+def _dropped(T, d, p, site, x):
+    return S.dropout_factors(T, d, p, SEED, BASE, OFFSET + site) * x.astype(np.float64)
+
+
+@pytest.mark.parametrize("p", [0.1, 0.5, 1.0])
+def test_bias_gradients_are_sums_of_float32_rows(p):
+    """Without a final LayerNorm the last block's rows get the dropped d_out itself, so the gradient of its bias
+    is their sum: products by a rounded factor (two roundings each) and at most T additions of float32."""
+    from transformer_esm_layer_gb300.binding import Dropout
+    s = _setup(final_ln=False, layers=1)
+    s["enc"].set_dropout(Dropout(p, _rng(), OFFSET))
+    _step(s)
+    T, d = s["d_out"].shape
+    terms = _dropped(T, d, p, 2, s["d_out"])
+    bound = (T + 2) * 2.0 ** -24 * np.abs(terms).sum(0)
+    assert (np.abs(to_np(s["grads"].layers[0]["b_2"]) - terms.sum(0)) <= bound).all()

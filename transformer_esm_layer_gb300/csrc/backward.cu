@@ -201,6 +201,43 @@ __global__ void __launch_bounds__(128) colsum_kernel(const void* __restrict__ sr
   *reinterpret_cast<float4*>(partial + (size_t)chunk * cols + 4 * c4) = a;
 }
 
+// The same of the rows behind a dropout: copy holds scale * keep * src as bfloat16, the sums are of the float32 values
+// before that rounding.  Eight columns per thread, one call of the generator; four rows' loads ahead of their masks.
+__global__ void __launch_bounds__(64) colsum_drop_kernel(const float* __restrict__ src, const DropMask mask, int rows,
+                                                         int cols, int chunk_rows, float* __restrict__ partial,
+                                                         __nv_bfloat16* __restrict__ copy) {
+  __shared__ PhiloxKeys keys;
+  const PhiloxState ps = philox_state(mask);
+  philox_keys(ps, &keys);
+  __syncthreads();
+  const int c8 = blockIdx.x * blockDim.x + threadIdx.x;  // columns 8 c8 .. 8 c8 + 7
+  const int chunk = blockIdx.y;
+  if (8 * c8 >= cols) return;
+  const int r0 = chunk * chunk_rows, r1 = min(rows, r0 + chunk_rows);
+  const uint64_t scale = f2_both(mask.scale);
+  constexpr int kAhead = 4;
+  Pairs a;
+  fill(a, 0.f);
+  for (int r = r0; r < r1; r += kAhead) {
+    Raw8<float> raw[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) raw[j].load(src + (size_t)min(r + j, r1 - 1) * cols + 8 * c8, 8);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (r + j >= r1) break;
+      Pairs v;
+      raw[j].get(v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], scale);
+      keep(drop_words(mask, ps, &keys, (unsigned long long)(r + j) * ((uint32_t)cols / 8) + c8), ps, v);
+      st8(copy + (size_t)(r + j) * cols + 8 * c8, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = f2_add(a[i], v[i]);
+    }
+  }
+  st8(partial + (size_t)chunk * cols + 8 * c8, a);
+}
+
 // out[i] = scale * sum_k partial[k * stride + i] in a fixed order: a block owns 32
 // consecutive i; warp w of kReduceWarps adds the chunks k = w, w + kReduceWarps, ... (lane =
 // i, coalesced), then the warp sums are added in warp order.  The sums have few columns
@@ -390,6 +427,15 @@ void launch_colsum(const void* src, bool bf16_in, int rows, int cols, float* out
   if (bf16_in) colsum_kernel<true><<<grid, 128, 0, st>>>(src, rows, cols, kChunkRows, partial, nullptr);
   else colsum_kernel<false><<<grid, 128, 0, st>>>(src, rows, cols, kChunkRows, partial, copy);
   reduce_chunks(partial, chunks, (size_t)cols, cols, 1.f, out, st);
+}
+
+cudaError_t launch_colsum_dropped(const float* src, const DropMask& mask, int rows, int cols, float* out, float* partial,
+                                  __nv_bfloat16* copy, cudaStream_t st) {
+  if (rows <= 0) return cudaMemsetAsync(out, 0, sizeof(float) * cols, st);
+  const int chunks = chunks_for(rows);
+  colsum_drop_kernel<<<dim3((cols / 8 + 63) / 64, chunks), 64, 0, st>>>(src, mask, rows, cols, kChunkRows, partial, copy);
+  reduce_chunks(partial, chunks, (size_t)cols, cols, 1.f, out, st);
+  return cudaGetLastError();
 }
 
 void launch_reduce_splits(const float* partial, int splits, size_t n, float* out, cudaStream_t st) {

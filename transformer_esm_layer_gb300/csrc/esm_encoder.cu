@@ -940,24 +940,13 @@ esm_status backward_impl(esm_encoder* h, const esm_weights* w, const float* d_ou
   } else if (cudaMemcpyAsync(dx, d_out, 4 * (size_t)T * d, cudaMemcpyDeviceToDevice, st) != cudaSuccess) {
     return ESM_ERR_CUDA;
   }
-  // The gradient of a block's output rows, as bf16 in dxb: dx, or dropped like the rows; and its bias's.
+  // The gradient of a block's output rows, as bf16 in dxb: dx, or dropped like the rows; and its bias's, the sum
+  // of the same rows in fp32.
   const bool drop = h->train_dropout.rng != nullptr;
   auto block_rows = [&](int site, float* d_bias) -> esm_status {
-    if (!drop) {
-      PROF(h, P_OTHER, st, 2, launch_colsum(dx, false, T, d, d_bias, partial, dxb, st));
-      return ESM_OK;
-    }
-    DropoutArgs a{};
-    a.x = dx;
-    a.y = dxb;
-    a.y_bf16 = true;
-    a.x_stride = a.y_stride = d;
-    a.rows = T;
-    a.cols = d;
-    a.mask = drop_site(h->train_dropout, site);
-    ProfScope _ps(h, P_OTHER, st, 3);
-    if (launch_dropout(a, st) != cudaSuccess) return ESM_ERR_CUDA;
-    launch_colsum(dxb, true, T, d, d_bias, partial, nullptr, st);
+    ProfScope _ps(h, P_OTHER, st, 2);
+    if (drop) return cuda_status(launch_colsum_dropped(dx, drop_site(h->train_dropout, site), T, d, d_bias, partial, dxb, st));
+    launch_colsum(dx, false, T, d, d_bias, partial, dxb, st);
     return ESM_OK;
   };
   for (int l = c.num_layers - 1; l >= 0; --l) {

@@ -275,6 +275,10 @@ void launch_ln_bwd(const float* x, const void* gamma, bool gf32, const float* dy
 // rows as bf16.  partial: bwd_partial_floats(rows, cols) / 2 floats.  cols % 4 == 0.
 void launch_colsum(const void* src, bool bf16_in, int rows, int cols, float* out, float* partial, __nv_bfloat16* copy,
                    cudaStream_t st);
+// out[c] = sum_r of the dropped src[r][c], summed in fp32; copy: the dropped rows as bf16.  cols % 8 == 0, src, copy and
+// partial (as above) on 32 bytes.
+cudaError_t launch_colsum_dropped(const float* src, const DropMask& mask, int rows, int cols, float* out, float* partial,
+                                  __nv_bfloat16* copy, cudaStream_t st);
 // out[i] = scale * sum_k partial[k * stride + i] over k = 0..chunks-1, in index order.
 void reduce_chunks(const float* partial, int chunks, size_t stride, size_t n, float scale, float* out, cudaStream_t st);
 // LayerNorm backward of a bf16 input x (no residual gradient added): dx, dgamma, dbeta.
