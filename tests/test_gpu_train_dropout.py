@@ -25,7 +25,7 @@ def _built():
     ensure_built()
 
 
-def _reference(w, tok, heads, d_out, final_ln, p):
+def _reference(w, tok, heads, d_out, final_ln, p, lengths=LENGTHS):
     """Output and gradients: hidden states in packed order, a dict of parameter gradients."""
     T, d = len(tok), w["emb"].shape[1]
     L = len(w["layers"])
@@ -40,7 +40,7 @@ def _reference(w, tok, heads, d_out, final_ln, p):
         return torch.nn.functional.layer_norm(x, (d,), g, b, 1e-5)
 
     dh = d // heads
-    pos = torch.cat([torch.arange(n) for n in LENGTHS]).double()
+    pos = torch.cat([torch.arange(n) for n in lengths]).double()
     ang = pos[:, None] * 10000.0 ** (-torch.arange(dh // 2).double() * 2 / dh)
     cos, sin = torch.cos(ang)[:, None], torch.sin(ang)[:, None]
 
@@ -54,7 +54,7 @@ def _reference(w, tok, heads, d_out, final_ln, p):
         qq, kk, vv = (m.view(T, heads, dh) for m in qkv.chunk(3, 1))
         qq, kk = rope(qq), rope(kk)
         out, start = [], 0
-        for n in LENGTHS:
+        for n in lengths:
             i = slice(start, start + n)
             att = torch.softmax(torch.einsum("qhd,khd->hqk", qq[i], kk[i]) / dh ** 0.5, -1)
             out.append(torch.einsum("hqk,khd->qhd", att, vv[i]).reshape(n, d))
@@ -235,3 +235,37 @@ def test_bias_gradients_are_sums_of_float32_rows(p):
     terms = _dropped(T, d, p, 2, s["d_out"])
     bound = (T + 2) * 2.0 ** -24 * np.abs(terms).sum(0)
     assert (np.abs(to_np(s["grads"].layers[0]["b_2"]) - terms.sum(0)) <= bound).all()
+
+
+# The embedding's gradient goes by size: up to 256 tokens (512 of more than 64 ids) a search through them, above by
+# chunks of tokens up to 64 ids, by a sort above; the latter two keep partial sums and lists in the train buffer.
+LONGER = {"chunks": [300, 37, 211, 1, 402], "sort": [300, 37, 211, 1, 402, 5]}
+
+
+@pytest.mark.parametrize("how,vocab,p", [("chunks", 33, 0.1), ("chunks", 64, 0.3), ("sort", 65, 0.1), ("sort", 96, 0.2),
+                                         ("sort", 97, 0.0), ("sort", 300, 0.0), ("sort", 300, 0.2)])
+@pytest.mark.parametrize("room", [0, 777])  # tokens that the buffers are made for beyond the batch
+def test_longer_steps_against_autograd(how, vocab, p, room):
+    from transformer_esm_layer_gb300.binding import DeviceGrads, DeviceWeights, Dropout, EsmEncoder, packed_inputs
+    lengths = LONGER[how]
+    T = sum(lengths)
+    g = synth.Geometry(num_layers=1, hidden=256, heads=4, ffn=512, vocab=vocab)
+    w = synth.model_weights(g, 15, "bf16")
+    rng = np.random.default_rng(16)
+    tok = rng.integers(0, vocab, T).astype(np.int32)
+    d_out = rng.standard_normal((T, g.hidden)).astype(np.float32)
+    enc = EsmEncoder.from_geometry(g, "bf16")
+    enc.set_dropout(Dropout(p, _rng(), OFFSET))
+    t, cu = packed_inputs(tok, lengths)
+    tb = enc.train_buffer(T + room)
+    guarded = torch.full((tb.numel() + 2 ** 20,), 0x5A, dtype=torch.uint8, device="cuda")
+    s = dict(grads=DeviceGrads(g, 1))
+    dw, ws, tb = DeviceWeights(w, "bf16"), enc.workspace(T + room, len(lengths)), guarded[:tb.numel()]
+    for x in s["grads"].tensors():
+        x.fill_(float("nan"))
+    h = enc.forward_train(dw, t, cu, max(lengths), tb, ws)
+    enc.backward(dw, torch.from_numpy(d_out).cuda(), s["grads"], tb, ws)
+    enc.check()
+    assert (guarded[tb.numel():] == 0x5A).all()  # nothing behind the buffer was written
+    want, P = _reference(w, tok, 4, d_out, True, p, lengths)
+    _compare(s, h, P, want, True)
