@@ -460,7 +460,8 @@ ESM_API esm_status esm_op_gemm_nvfp4(esm_encoder_t* h, esm_epilogue epi, const u
 /* Dropout by a counter-based generator.  The mask is a function of (rng[0], rng[1] + offset, row,
  * column): the backward draws it again, and nothing is stored.  rng is read when the kernels run, so
  * a captured graph draws new masks when the program writes another base between replays; offset tells
- * the dropouts of one step apart.
+ * the dropouts of one step apart: two of the same offset and width drop the same places, and the base
+ * has to move past every offset of a step before the next one.
  * Element (r, c) of [rows, cols] has 16 bits u: of Philox4x32-10 with key rng[0] (lower word first)
  * and counter (b, o), b = r * ceil(cols / 8) + c / 8 and o = rng[1] + offset modulo 2^64 (each lower
  * word first), the output word (c % 8) / 2, its lower half for even c and its upper half for odd.
@@ -619,7 +620,8 @@ ESM_API esm_status esm_encoder_forward_train(esm_encoder_t* h, const esm_weights
  * layer's two block outputs (attention output projection, fc2) before they are added to the residual
  * stream; NULL, or a p that rounds to none, for no dropout (the default).  With L layers the 2 L + 1 dropouts of a step
  * have the offsets dropout->offset (embedding), + 1 + 2 l (layer l's attention block) and + 2 + 2 l
- * (its MLP block): a program adds 2 L + 1 to the base between steps.  The struct is copied; the device memory that rng
+ * (its MLP block): a program adds 2 L + 1 to the base between steps, more if it has dropouts of its own behind these
+ * offsets.  The struct is copied; the device memory that rng
  * points to must stay valid, and unchanged between a forward and its backward, which uses the dropout that its forward
  * ran with.  A block's output rows are rounded to bf16 before they are dropped.  ESM_BF16 handles (a dropout on
  * others: ESM_ERR_UNSUPPORTED); no other call of the handle drops anything. */

@@ -375,7 +375,8 @@ class Dropout(_Frozen):
 
     ``rng``: int64 CUDA tensor (seed, base), read when a kernel runs: a training program adds to the
     base every step (in place, on the device), and captured graphs see it.  ``offset`` tells the
-    dropouts of one step apart.  Give the same object to a forward call and its backward."""
+    dropouts of one step apart: give the same object to a forward call and its backward, another one
+    to every other dropout, and let the base move past all offsets of a step."""
 
     __slots__ = ("p", "rng", "offset", "device", "struct")
 
