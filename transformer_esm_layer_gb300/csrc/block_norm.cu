@@ -20,8 +20,9 @@ namespace {
 
 // ---- forward ----
 // A block takes R rows, W warps to each; a warp holds G spans of 256 columns, eight of each to a lane.  Rows
-// come as blocks of the grid, not in a loop: the SM holds 25 to 40 warps whose loads, sums and stores interleave
-// by themselves (blocks that stay, with rows copied ahead by the threads, took 60 us where this took 49.5).
+// come as blocks of the grid, not in a loop: the launch bounds keep 21 to 25 warps on the SM (14 to 20 with float32
+// blocks), whose loads, sums and stores interleave by themselves (blocks that stay, with rows copied ahead by the
+// threads, took 60 us where this took 49.5).
 // Up to 2048 columns G = 1, and R = 2 where there are rows enough: the parameters are read and unpacked once
 // for both, the generator's round keys are shared, and one barrier serves both rows' sums.
 struct RowShape {
@@ -332,9 +333,10 @@ constexpr int kMaxGroups = 15;  // named barriers
 template <typename T>
 constexpr int kWarpsOf = sizeof(T) == 2 ? kBwdWarps : 16;
 
-// Aligned eights, cols % 8 == 0 and <= 4096.  A block of `groups` groups of W = ceil(cols / 256) warps stays on
-// its SM and takes a row per group and step; a lane owns eight columns of every row that its group takes, so
-// the four column sums stay with it (in shared memory, which frees 32 registers) and leave
+// Aligned eights, cols % 8 == 0 and a group's rows and sums in shared memory: cols <= 4096, float32 <= 4088 (at 4096 the
+// kernel below: 5120 rows 131 us; 5130 of 4088 columns by this one 99).  A block of `groups` groups of
+// W = ceil(cols / 256) warps stays on its SM and takes a row per group and step; a lane owns eight columns of every row
+// that its group takes, so the four column sums stay with it (in shared memory, which frees 32 registers) and leave
 // once per block, into partial[block][kSums][cols].  The rows to come arrive by bulk copies, kStages of them per
 // group, which leaves the threads and the L1 out of it; gamma_pre and scale gate gamma_post stand in shared
 // memory as float32.
@@ -599,7 +601,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<T>, 1)
 
 // Any alignment, and rows of up to 8192 columns: the same sums, rows read where they are used (the next one is
 // brought into the L2) and parameters from the L1; a lane owns 8 G columns, G = 2 with its column sums in shared
-// memory.  One row a block at a time, then: 4096 x 5120 179 us, 2560 x 8192 148, 16384 x 1283 238.
+// memory.  One row a block at a time, then: 4096 x 5120 180 us, 2560 x 8192 150, 16384 x 1283 243, all far from the
+// memory's time (56.5): a row's loads, sums and second reads of its parameters follow one another with nothing of the
+// next row in shared memory, and 128 registers spill 72 to 136 bytes.
 template <typename T, bool VEC, int G>
 __global__ void __launch_bounds__(512, 1)
     block_norm_bwd_any_kernel(const BlockNormArgs a, int W, int groups, float* __restrict__ partial) {
@@ -995,7 +999,8 @@ cudaError_t launch_fwd(const BlockNormArgs& a, bool vec, int num_sms, cudaStream
   if (!by_width) {
     const unsigned rows = (unsigned)a.rows;
     if (vec) {
-      // (4096 x 5120: 57 us, 2560 x 8192: 63; a span a warp, one block an SM: 102 and 100)
+      // (4096 x 5120: 58 us, 2560 x 8192: 64; a span a warp, one block an SM: 102 and 100.  64 registers spill 112 bytes,
+      // 392 with float32 blocks, which take 88 and 96)
       block_norm_kernel<T, true, 0, 1, 2, 512, 2><<<rows, 32 * W, 0, st>>>(a, s);
     } else if (spans <= 8) {
       block_norm_kernel<T, false, 0, 1, 1, 256, 4><<<rows, 32 * W, 0, st>>>(a, s);

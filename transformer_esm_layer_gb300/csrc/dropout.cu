@@ -3,7 +3,9 @@
 // The gradient is the same call on dy.
 //
 // Bound by memory: x (and the residual) read once, y written once.  16384 x 5120 in bfloat16: 54.7 us, 6.1 TB/s,
-// 92 % of a copy's rate; the generator's issue slots, some two thirds of all, hide behind it.
+// 92 % of a copy's rate; the generator's issue slots, some two thirds of all, hide behind it.  The launch bound fits
+// bfloat16; with float32 operands the aligned kernel spills 108 to 360 bytes: bfloat16 to float32 81 us (floor 75), float32
+// to bfloat16 92 (75), float32 to float32 157 (100).
 #include <algorithm>
 
 #include "dropout.cuh"

@@ -4,9 +4,9 @@
 // The sums run in a fixed order, so results do not depend on scheduling.
 //
 // Bound by memory: the rows met and the output; for the gradient d_out and the table's rows.  16384 tokens x 1280:
-// lookup in 50021 float32 rows 25.2 us (4.5 TB/s of the bytes that it cannot do without); gradient of 33 ids 24.7 us
-// (14.5 without the dropout, 5.8 TB/s: the rest is its masks' instructions), of 50021 64.2 us, of which 38 clear the
-// table.
+// lookup in 50021 float32 rows 25.2 us (4.5 TB/s of the bytes that it cannot do without); gradient of 33 ids 24.7 us,
+// 22.0 without the dropout (3.8 TB/s; 16 where d_out still lies in the L2: the sort of a chunk before its first row's
+// load and the second kernel over the chunks' sums are not hidden), of 50021 64.2 us, of which 38 clear the table.
 #include <algorithm>
 #include <type_traits>
 
@@ -334,7 +334,8 @@ __global__ void __launch_bounds__(256) embed_grad_add_kernel(const EmbedArgs a, 
 // list; per pass it counts its digits (lanes with equal digits find each other by match, so one lane writes
 // each count and no atomics order anything), the blocks exchange their counts through distributed shared
 // memory, and every warp then knows where each of its digits goes.  Up to 8 bits per pass: one pass for
-// 256 ids, two for 65536 (16384 tokens: 15.7 us alone).  The rest of the grid meanwhile clears d_table (rows that the
+// 256 ids, two for 65536 (16384 tokens: 15.7 us alone; it grows with the tokens, as eight SMs take them: a gradient of
+// 65536 tokens of 300 ids takes 46 us at 128 columns, 62 at 480).  The rest of the grid meanwhile clears d_table (rows that the
 // sort may not name left to the sums' launch: 69 us and more where all of it takes 66).
 constexpr int kSortBlocks = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 8, kBins = 1 << kDigitBits;
@@ -685,7 +686,7 @@ cudaError_t launch_grad(const EmbedArgs& a, void* workspace, int num_sms, cudaSt
   s.passes = (bits + kDigitBits - 1) / kDigitBits;
   s.digit_bits = (bits + s.passes - 1) / s.passes;
   float* part = reinterpret_cast<float*>(ws + w.part);
-  int clear = 0;  // blocks that clear d_table: a few KB each at least
+  int clear = 0;  // blocks that clear d_table: one per 128 KB, in clusters of eight, up to two an SM
   if (!a.accumulate) {
     const size_t bytes = 4 * (size_t)a.vocab * a.cols;
     clear = (int)std::min((bytes + (1 << 17) - 1) >> 17, (size_t)num_sms * 2);

@@ -627,10 +627,8 @@ bool config_ok(const esm_config* c) {
 }
 
 // ------------------------------------------------------------------ training (backward)
-// Buffer of a training forward: every activation the backward reads, per layer, plus the
-// backward's scratch.  Per-layer tensors are slabs of layers (x: layers + 1) of one size.
-// Above this vocabulary the embedding's gradient is summed from sorted tokens; up to it, without dropout, by a
-// table of sums in shared memory (128 columns of every id: 48 KB).
+// Up to this vocabulary, and without dropout, the step's embedding gradient is a table of sums in shared memory (128
+// columns of every id: 48 KB); otherwise launch_embed_grad takes it, by the number of tokens and ids.
 constexpr int kTableVocab = 96;
 
 // The mask of a dropout that may be NULL; false if it is malformed.
@@ -657,6 +655,8 @@ DropMask drop_site(const esm_dropout& d, int site) {
   return m;
 }
 
+// Buffer of a training forward: every activation the backward reads, per layer, plus the
+// backward's scratch.  Per-layer tensors are slabs of layers (x: layers + 1) of one size.
 struct TrainLayout {
   size_t tok, x, xmid, y1, qkv, o, lse, y2, z, u;                        // bases
   size_t sx, sy, sqkv, slse, sz;                                         // slab strides
